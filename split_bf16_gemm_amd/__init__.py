@@ -5,11 +5,16 @@ fp32) result, K cut into split_k slices whose partials the last-arriving
 slice adds in slice order.  The work runs in the HIP kernels of
 ``_lib/liblowm.so`` (C ABI in ``include/lowm.h``); this package only loads and
 calls them.
+
+Beside the GEMM stand the operators of a decode step around it (C ABI in
+``include/lowm_ops.h``): residual_norm and quantize_rows.
 """
 from .binding import (MAX_BATCH, BwProbe, GemmDesc, Library, LowmError, Tactic,
                       batched_workspace_bytes, counter_bytes, gemm, gemm_batched, load,
                       make_workspace, pick_split_k, tactic, workspace_bytes)
+from .ops import quantize_rows, residual_norm
 
 __all__ = ["MAX_BATCH", "BwProbe", "GemmDesc", "Library", "LowmError", "Tactic",
            "batched_workspace_bytes", "counter_bytes", "gemm", "gemm_batched", "load",
-           "make_workspace", "pick_split_k", "tactic", "workspace_bytes"]
+           "make_workspace", "pick_split_k", "quantize_rows", "residual_norm", "tactic",
+           "workspace_bytes"]

@@ -1,0 +1,380 @@
+// ops_norm.hip -- the residual norm at a block's border and the row quantiser
+// (include/lowm_ops.h) for gfx950.
+//
+//   p = N(y) w_post ;  r' = a r + b g p ;  x = N(r') w_pre ;  q = rint(x / s)
+//
+// Each element is read once and written once: a row stays in the registers of
+// the group of lanes that owns it (8 elements per lane and step), and its sums
+// (the two norms' and, for int8, the largest magnitude) are the only values
+// that cross lanes, in fp32.  Bound by HBM for many rows (8 bytes an element
+// with bf16 everywhere) and by latency for few: one load's round trip, then a
+// reduction per norm.
+#include "ops_common.cuh"
+
+namespace lowm {
+namespace {
+
+// Centred, twice: two sums a norm; and the largest magnitude.
+[[maybe_unused]] constexpr int kMaxReductions = 5;
+
+struct NormArgs {
+  lowm_residual_norm_args u;
+};
+
+// Sums over the group of G lanes that shares a row.  A group larger than a
+// wavefront joins its wavefronts' sums through LDS, each reduction in a slot
+// of its own, so one barrier per reduction is enough.
+template <int G>
+struct Group {
+  static constexpr int kWavesPer = G / kWave;
+  float* lds;      // [reductions][kWavesPer]
+  int at = 0;
+
+  __device__ __forceinline__ float sum(float v) {
+    v = wave_sum(v);
+    if constexpr (kWavesPer > 1) {
+      float* slot = lds + kWavesPer * at++;
+      if ((threadIdx.x & (kWave - 1)) == 0) slot[threadIdx.x / kWave] = v;
+      __syncthreads();
+      v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWavesPer; ++w) v += slot[w];
+    }
+    return v;
+  }
+  __device__ __forceinline__ uint32_t umax(uint32_t v) {
+    v = wave_umax(v);
+    if constexpr (kWavesPer > 1) {
+      uint32_t* slot = reinterpret_cast<uint32_t*>(lds) + kWavesPer * at++;
+      if ((threadIdx.x & (kWave - 1)) == 0) slot[threadIdx.x / kWave] = v;
+      __syncthreads();
+      v = 0;
+#pragma unroll
+      for (int w = 0; w < kWavesPer; ++w) v = slot[w] > v ? slot[w] : v;
+    }
+    return v;
+  }
+};
+
+// The elements of a row that a lane owns: with VEC, V runs of 8 consecutive
+// ones, G lanes apart; otherwise 8 V single ones, G apart.
+template <int G, int V, bool VEC>
+struct Row {
+  int lane, D;
+  __device__ __forceinline__ int at(int v, int i) const {
+    return VEC ? (v * G + lane) * 8 + i : (v * 8 + i) * G + lane;
+  }
+  __device__ __forceinline__ bool has(int v, int i) const { return at(v, i) < D; }
+
+  __device__ __forceinline__ void load(const void* p, int64_t base, bool f32, float fill,
+                                       float (&x)[V][8]) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[v][i] = fill;
+        if (has(v, 0)) load8(p, base + at(v, 0), f32, x[v]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[v][i] = has(v, i) ? load1(p, base + at(v, i), f32) : fill;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(void* p, int64_t base, bool f32,
+                                        const float (&x)[V][8]) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (VEC) {
+        if (has(v, 0)) store8(p, base + at(v, 0), f32, x[v]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (has(v, i)) store1(p, base + at(v, i), f32, x[v][i]);
+      }
+    }
+  }
+};
+
+// x -> N(x), without weights.  Elements past the row's end are zero on entry
+// and are left out of the centred sum; their values on exit are not used.
+template <int G, int V, bool VEC>
+__device__ __forceinline__ void normalise(const Row<G, V, VEC>& row, Group<G>& grp, bool center,
+                                          float eps, float (&x)[V][8]) {
+  const float inv_d = 1.0f / (float)row.D;
+  if (center) {
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += x[v][i];
+    const float mean = grp.sum(s) * inv_d;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[v][i] = row.has(v, i) ? x[v][i] - mean : 0.f;
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += x[v][i] * x[v][i];
+  const float k = 1.0f / sqrtf(grp.sum(s) * inv_d + eps);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[v][i] *= k;
+}
+
+// Row to int8: s = max|x| / 127 and q = rint(x / s), both with the correctly
+// rounded divide, so that q is the same number on any machine.  The magnitudes
+// are compared as bit patterns: a NaN or an infinity then comes out on top
+// instead of being passed over, and gives the row the scale NaN.
+template <int G, int V, bool VEC>
+__device__ __forceinline__ void quantise(const Row<G, V, VEC>& row, Group<G>& grp,
+                                         const float (&x)[V][8], int8_t* q, int64_t base,
+                                         float* scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = __builtin_bit_cast(uint32_t, x[v][i]) & 0x7fffffffu;
+      if (row.has(v, i)) top = b > top ? b : top;
+    }
+  top = grp.umax(top);
+  const bool finite = top < 0x7f800000u;
+  const float s = __builtin_bit_cast(float, top) / 127.0f;
+  if (row.lane == 0) *scale = finite ? s : __builtin_nanf("");
+  const bool some = finite && s > 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    int n[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // A scale in the subnormals can be rounded far enough that a quotient
+      // passes 127: such a value is held at 127.
+      const float t = some ? rintf(x[v][i] / s) : 0.f;
+      n[i] = (int)fminf(fmaxf(t, -127.f), 127.f);
+    }
+    if constexpr (VEC) {
+      ops_u32x2 w;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        w[h] = (uint32_t)(n[4 * h] & 255) | (uint32_t)(n[4 * h + 1] & 255) << 8 |
+               (uint32_t)(n[4 * h + 2] & 255) << 16 | (uint32_t)n[4 * h + 3] << 24;
+      if (row.has(v, 0)) *reinterpret_cast<ops_u32x2*>(q + base + row.at(v, 0)) = w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (row.has(v, i)) q[base + row.at(v, i)] = (int8_t)n[i];
+    }
+  }
+}
+
+// Threads of a workgroup whose rows belong to groups of G lanes.
+constexpr int group_threads(int G) { return G < 256 ? 256 : G; }
+
+template <int G, int V, bool VEC>
+__global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(NormArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const lowm_residual_norm_args& u = a.u;
+  __shared__ float lds[kMaxReductions * (G / kWave)];
+  const int64_t m = (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
+  // Whole wavefronts leave here, and only where no group spans two of them.
+  if (m >= u.M) return;
+  const Row<G, V, VEC> row{(int)threadIdx.x % G, u.D};
+  Group<G> grp{lds};
+
+  float p[V][8], r[V][8], w[V][8], g[V][8];
+  row.load(u.y, m * u.ld_y, u.y_type == LOWM_F32, 0.f, p);
+  row.load(u.r, m * u.ld_r, u.r_type == LOWM_F32, 0.f, r);
+  const bool post = u.flags & LOWM_NORM_POST, center = u.flags & LOWM_NORM_CENTER;
+  // what multiplies the branch: b * gate * w_post
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[v][i] = 1.f;
+  if (post && u.w_post) row.load(u.w_post, 0, u.w_type == LOWM_F32, 0.f, g);
+  if (u.gate) {
+    if (u.gate_col) {
+      row.load(u.gate, m * u.gate_row, u.gate_type == LOWM_F32, 0.f, w);
+    } else {
+      const float one = load1(u.gate, m * u.gate_row, u.gate_type == LOWM_F32);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[v][i] = one;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[v][i] *= w[v][i];
+  }
+  const bool pre = !(u.flags & LOWM_NORM_NO_PRE);
+  const bool weigh = pre && u.w_pre;
+  if (weigh) row.load(u.w_pre, 0, u.w_type == LOWM_F32, 0.f, w);
+
+  if (post) normalise(row, grp, center, u.eps, p);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = u.residual_scale * r[v][i] + u.branch_scale * (g[v][i] * p[v][i]);
+      r[v][i] = row.has(v, i) ? t : 0.f;
+    }
+  row.store(u.r_out, m * u.ld_r_out, u.r_type == LOWM_F32, r);
+  if (!pre) return;
+  normalise(row, grp, center, u.eps, r);
+  if (weigh) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[v][i] *= w[v][i];
+  }
+  if (u.x_type == LOWM_I8)
+    quantise(row, grp, r, static_cast<int8_t*>(u.x), m * u.ld_x, u.x_scale + m);
+  else
+    row.store(u.x, m * u.ld_x, false, r);
+#endif
+}
+
+struct QuantArgs {
+  const void* x;
+  int8_t* q;
+  float* scale;
+  int64_t ld;
+  int M, D, f32;
+};
+
+template <int G, int V, bool VEC>
+__global__ __launch_bounds__(group_threads(G)) void quantize_rows_kernel(QuantArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ float lds[kMaxReductions * (G / kWave)];
+  const int64_t m = (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
+  if (m >= a.M) return;
+  const Row<G, V, VEC> row{(int)threadIdx.x % G, a.D};
+  Group<G> grp{lds};
+  float x[V][8];
+  row.load(a.x, m * a.ld, a.f32 != 0, 0.f, x);
+  quantise(row, grp, x, a.q, m * (int64_t)a.D, a.scale + m);
+#endif
+}
+
+// The group of lanes for rows of D elements: a wavefront up to 512 elements,
+// a workgroup of 256 lanes up to 2048 of them in one run per lane and 4096 in
+// two, then 1024 lanes with up to four runs (two for the norm, whose four
+// operands stay in registers).
+template <template <int, int, bool> class K, bool VEC, int VMAX, typename A>
+int launch_rows(const A& a, int M, int D, hipStream_t stream) {
+  auto go = [&](auto fn, int G) {
+    const int per = group_threads(G) / G;
+    void* args[] = {const_cast<A*>(&a)};
+    return launched(hipLaunchKernel(reinterpret_cast<const void*>(fn),
+                                    dim3((unsigned)((M + per - 1) / per)),
+                                    dim3(group_threads(G)), args, 0, stream));
+  };
+  if (D <= 512) return go(K<64, 1, VEC>::fn(), 64);
+  if (D <= 2048) return go(K<256, 1, VEC>::fn(), 256);
+  if (D <= 4096) return go(K<256, 2, VEC>::fn(), 256);
+  if (D <= 8192) return go(K<1024, 1, VEC>::fn(), 1024);
+  if constexpr (VMAX > 2) {
+    if (D > 16384) return go(K<1024, 4, VEC>::fn(), 1024);
+  }
+  return go(K<1024, 2, VEC>::fn(), 1024);
+}
+template <int G, int V, bool VEC>
+struct NormK {
+  static auto fn() { return &residual_norm_kernel<G, V, VEC>; }
+};
+template <int G, int V, bool VEC>
+struct QuantK {
+  static auto fn() { return &quantize_rows_kernel<G, V, VEC>; }
+};
+
+bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+bool real_type(int t) { return t == LOWM_BF16 || t == LOWM_F32; }
+
+int residual_norm(const lowm_residual_norm_args* u, hipStream_t stream) {
+  if (!u || u->M < 0 || u->D < 1) return LOWM_ERR_INVALID_ARG;
+  if (u->M == 0) return LOWM_OK;
+  if (!u->y || !u->r || !u->r_out) return LOWM_ERR_INVALID_ARG;
+  const bool pre = !(u->flags & LOWM_NORM_NO_PRE);
+  const bool i8 = pre && u->x_type == LOWM_I8;
+  if (u->flags & ~(LOWM_NORM_POST | LOWM_NORM_NO_PRE | LOWM_NORM_CENTER))
+    return LOWM_ERR_INVALID_ARG;
+  if (!real_type(u->y_type) || !real_type(u->r_type) || !real_type(u->w_type) ||
+      !real_type(u->gate_type))
+    return LOWM_ERR_INVALID_ARG;
+  if (pre && (!u->x || (u->x_type != LOWM_BF16 && u->x_type != LOWM_I8) || u->ld_x < u->D))
+    return LOWM_ERR_INVALID_ARG;
+  if (i8 && !u->x_scale) return LOWM_ERR_INVALID_ARG;
+  if (u->ld_y < u->D || u->ld_r < u->D || u->ld_r_out < u->D) return LOWM_ERR_INVALID_ARG;
+  if (u->gate && (u->gate_row < 0 || (u->gate_col != 0 && u->gate_col != 1)))
+    return LOWM_ERR_INVALID_ARG;
+  if (u->D > LOWM_NORM_MAX_D) return LOWM_ERR_UNSUPPORTED;
+  const int yb = type_bytes(u->y_type), rb = type_bytes(u->r_type), wb = type_bytes(u->w_type),
+            gb = type_bytes(u->gate_type), xb = type_bytes(u->x_type);
+  if (!aligned(u->y, yb) || !aligned(u->r, rb) || !aligned(u->r_out, rb) ||
+      !aligned(u->w_post, wb) || !aligned(u->w_pre, wb) || !aligned(u->gate, gb) ||
+      (pre && !aligned(u->x, xb)) || (i8 && !aligned(u->x_scale, 4)))
+    return LOWM_ERR_UNSUPPORTED;
+  const int64_t M = u->M, D = u->D;
+  const bool inplace = u->r_out == u->r && u->ld_r_out == u->ld_r;
+  const Span y = span_of(u->y, M, D, u->ld_y, yb), r = span_of(u->r, M, D, u->ld_r, rb),
+             ro = span_of(u->r_out, M, D, u->ld_r_out, rb),
+             w0 = span_of(u->w_post, 1, D, D, wb), w1 = span_of(u->w_pre, 1, D, D, wb),
+             g = span_of(u->gate, M, u->gate_col ? D : 1, u->gate_row, gb),
+             x = span_of(pre ? u->x : nullptr, M, D, u->ld_x, xb),
+             xs = span_of(i8 ? u->x_scale : nullptr, 1, M, M, 4);
+  const Span in[] = {y, w0, w1, g}, out[] = {ro, x, xs};
+  for (const Span& o : out)
+    for (const Span& s : in)
+      if (meet(o, s)) return LOWM_ERR_INVALID_ARG;
+  if ((!inplace && meet(ro, r)) || meet(x, r) || meet(xs, r) || meet(ro, x) || meet(ro, xs) ||
+      meet(x, xs))
+    return LOWM_ERR_INVALID_ARG;
+  // Whole 16-byte vectors (8-byte ones of int8) need every row to start on
+  // one and D to be a whole number of runs of 8.
+  bool vec = D % 8 == 0 && u->ld_y % 8 == 0 && u->ld_r % 8 == 0 && u->ld_r_out % 8 == 0 &&
+             aligned(u->y, 16) && aligned(u->r, 16) && aligned(u->r_out, 16) &&
+             aligned(u->w_post, 16) && aligned(u->w_pre, 16);
+  if (pre) vec = vec && u->ld_x % 8 == 0 && aligned(u->x, i8 ? 8 : 16);
+  if (u->gate && u->gate_col) vec = vec && u->gate_row % 8 == 0 && aligned(u->gate, 16);
+  const NormArgs a{*u};
+  return vec ? launch_rows<NormK, true, 2>(a, u->M, u->D, stream)
+             : launch_rows<NormK, false, 2>(a, u->M, u->D, stream);
+}
+
+int quantize_rows(const void* x, int x_type, int64_t ld, int M, int K, void* q, float* scale,
+                  hipStream_t stream) {
+  if (M < 0 || K < 1 || ld < K || !real_type(x_type)) return LOWM_ERR_INVALID_ARG;
+  if (M == 0) return LOWM_OK;
+  if (!x || !q || !scale) return LOWM_ERR_INVALID_ARG;
+  if (K > LOWM_QUANTIZE_MAX_K) return LOWM_ERR_UNSUPPORTED;
+  const int xb = type_bytes(x_type);
+  if (!aligned(x, xb) || !aligned(scale, 4)) return LOWM_ERR_UNSUPPORTED;
+  const Span xs = span_of(x, M, K, ld, xb), qs = span_of(q, M, K, K, 1),
+             ss = span_of(scale, 1, M, M, 4);
+  if (meet(xs, qs) || meet(xs, ss) || meet(qs, ss)) return LOWM_ERR_INVALID_ARG;
+  const QuantArgs a{x, static_cast<int8_t*>(q), scale, ld, M, K, x_type == LOWM_F32};
+  const bool vec = K % 8 == 0 && ld % 8 == 0 && aligned(x, 16) && aligned(q, 8);
+  return vec ? launch_rows<QuantK, true, 4>(a, M, K, stream)
+             : launch_rows<QuantK, false, 4>(a, M, K, stream);
+}
+
+}  // namespace
+}  // namespace lowm
+
+extern "C" {
+
+int lowm_residual_norm(const lowm_residual_norm_args* args, void* stream) {
+  return lowm::residual_norm(args, static_cast<hipStream_t>(stream));
+}
+
+int lowm_quantize_rows(const void* x, int x_type, int64_t ld_x, int M, int K, void* q,
+                       float* scale, void* stream) {
+  return lowm::quantize_rows(x, x_type, ld_x, M, K, q, scale, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,195 @@
+"""The operators that stand next to the low-M GEMM in a decode step, over the
+C ABI of include/lowm_ops.h.
+
+Argument checks and marshalling only: every step runs in the HIP kernels of
+liblowm.so, on the caller's current stream (or ``stream``), asynchronously and
+without allocating beyond the outputs a caller does not pass.  There is no
+fallback: when the library is not built, or a call fails, this raises.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import binding
+
+BF16, F32, I8 = 0, 1, 2
+_TYPES = {torch.bfloat16: BF16, torch.float32: F32, torch.int8: I8}
+NORM_POST, NORM_NO_PRE, NORM_CENTER = 1, 2, 4
+
+_vp, _i, _l, _f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+
+class ResidualNormArgs(ctypes.Structure):
+    _fields_ = [("y", _vp), ("r", _vp), ("r_out", _vp), ("x", _vp), ("x_scale", _vp),
+                ("w_post", _vp), ("w_pre", _vp), ("gate", _vp),
+                ("ld_y", _l), ("ld_r", _l), ("ld_r_out", _l), ("ld_x", _l),
+                ("gate_row", _l), ("gate_col", _l), ("M", _i), ("D", _i),
+                ("y_type", _i), ("r_type", _i), ("w_type", _i), ("gate_type", _i),
+                ("x_type", _i), ("flags", _i),
+                ("residual_scale", _f), ("branch_scale", _f), ("eps", _f)]
+
+
+_lib = None
+
+
+def library() -> binding.Library:
+    """liblowm.so with the operators' entry points declared."""
+    global _lib
+    if _lib is None:
+        lib = binding.load()
+        c = lib.lib
+        c.lowm_residual_norm.argtypes = [_vp, _vp]
+        c.lowm_quantize_rows.argtypes = [_vp, _i, _l, _i, _i, _vp, _vp, _vp]
+        _lib = lib
+    return _lib
+
+
+def _stream(stream, device) -> int:
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    return stream.cuda_stream
+
+
+def _check(rc: int):
+    if rc:
+        library().check(rc)
+
+
+def _need(ok: bool, what: str, error=ValueError):
+    if not ok:
+        raise error(what)
+
+
+def _rows(name: str, t: torch.Tensor, shape, types) -> int:
+    """The row pitch of a GPU tensor [M, D] with contiguous rows."""
+    if t.dtype not in types:
+        raise TypeError(f"{name} must be one of {[str(x) for x in types]}, not {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape and tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    m, d = t.shape
+    sm, sd = t.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name} must have contiguous rows (stride {sd})")
+    return sm if m > 1 and sm >= d else _pitch(name, m, d, sm)
+
+
+def _pitch(name, m, d, sm) -> int:
+    if m > 1 and sm < d:
+        raise ValueError(f"{name}'s rows overlap (row stride {sm} of {d} elements)")
+    return d
+
+
+def _dense(name: str, t: torch.Tensor, shape, dtype, device=None):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous GPU tensor of shape {tuple(shape)}")
+
+
+_REAL = (torch.bfloat16, torch.float32)
+
+
+def residual_norm(y: torch.Tensor, residual: torch.Tensor, *, post_norm: bool = True,
+                  post_weight: Optional[torch.Tensor] = None,
+                  pre_norm: bool = True, pre_weight: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, branch_scale: float = 1.0,
+                  residual_scale: float = 1.0, eps: float = 1e-6, center: bool = False,
+                  quantize: bool = False, residual_out: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, scale_out: Optional[torch.Tensor] = None,
+                  stream=None):
+    """(r', x, scale) at the border between two blocks:
+
+        p  = norm(y) * post_weight                 (y itself without post_norm)
+        r' = residual_scale * residual + branch_scale * gate * p
+        x  = norm(r') * pre_weight                 (None without pre_norm)
+
+    y and residual [M, D], bf16 or fp32 each; r' has the residual's type (pass
+    ``residual_out=residual`` to update it in place); x is bf16, or with
+    ``quantize`` int8 rows with fp32 ``scale`` [M] (else None), as gemm_i8 takes
+    them.  gate: [D], [M, 1] or [M, D].  norm: root mean square, or with
+    ``center`` also the mean taken off."""
+    ld_r = _rows("residual", residual, None, _REAL)
+    shape = residual.shape
+    ld_y = _rows("y", y, shape, _REAL)
+    M, D = shape
+    dev = residual.device
+    if residual_out is None:
+        residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
+    flags = (NORM_POST if post_norm else 0) | (NORM_CENTER if center else 0)
+    a = ResidualNormArgs(y=y.data_ptr(), r=residual.data_ptr(), r_out=residual_out.data_ptr(),
+                         ld_y=ld_y, ld_r=ld_r,
+                         ld_r_out=_rows("residual_out", residual_out, shape, (residual.dtype,)),
+                         M=M, D=D, y_type=_TYPES[y.dtype], r_type=_TYPES[residual.dtype],
+                         residual_scale=residual_scale, branch_scale=branch_scale, eps=eps)
+    wtype = None
+    if post_norm and post_weight is not None:
+        wtype = post_weight.dtype
+        _need(wtype in _REAL, "post_weight must be bf16 or fp32", TypeError)
+        _dense("post_weight", post_weight, (D,), wtype)
+        a.w_post = post_weight.data_ptr()
+    if pre_norm and pre_weight is not None:
+        _need(wtype in (None, pre_weight.dtype) and pre_weight.dtype in _REAL,
+              "post_weight and pre_weight must both be bf16 or both fp32", TypeError)
+        wtype = pre_weight.dtype
+        _dense("pre_weight", pre_weight, (D,), wtype)
+        a.w_pre = pre_weight.data_ptr()
+    if wtype is not None:
+        a.w_type = _TYPES[wtype]
+    if gate is not None:
+        _need(gate.dtype in _REAL, "gate must be bf16 or fp32", TypeError)
+        _need(gate.is_cuda, "gate must be on the GPU")
+        if gate.dim() == 1 and gate.shape[0] == D:
+            row, col = 0, gate.stride(0)
+        elif gate.dim() == 2 and gate.shape[0] in (1, M) and gate.shape[1] in (1, D):
+            row = gate.stride(0) if gate.shape[0] == M and M > 1 else 0
+            col = gate.stride(1) if gate.shape[1] == D and D > 1 else 0
+        else:
+            raise ValueError(f"gate has shape {tuple(gate.shape)}: not [{D}], [{M}, 1] or "
+                             f"[{M}, {D}]")
+        if D == 1:
+            col = 0
+        _need(col in (0, 1) and row >= 0, "gate must have contiguous rows")
+        a.gate, a.gate_type, a.gate_row, a.gate_col = (gate.data_ptr(), _TYPES[gate.dtype], row,
+                                                       col)
+    if pre_norm:
+        want = torch.int8 if quantize else torch.bfloat16
+        if out is None:
+            out = torch.empty(shape, dtype=want, device=dev)
+        a.ld_x = _rows("out", out, shape, (want,))
+        a.x, a.x_type = out.data_ptr(), I8 if quantize else BF16
+        if quantize:
+            if scale_out is None:
+                scale_out = torch.empty(M, dtype=torch.float32, device=dev)
+            _dense("scale_out", scale_out, (M,), torch.float32)
+            a.x_scale = scale_out.data_ptr()
+    else:
+        _need(not quantize, "quantize needs pre_norm")
+        flags |= NORM_NO_PRE
+        out = None
+    a.flags = flags
+    _check((_lib or library()).lib.lowm_residual_norm(ctypes.byref(a), _stream(stream, dev)))
+    return residual_out, out, scale_out if quantize else None
+
+
+def quantize_rows(x: torch.Tensor, *, out: Optional[torch.Tensor] = None,
+                  scale_out: Optional[torch.Tensor] = None, stream=None):
+    """(q, scale): int8 rows q = rint(x / scale), scale = max|x| / 127 per row
+    (fp32), of x [M, K] bf16 or fp32.  A row with an infinity or a NaN gets the
+    scale NaN."""
+    ld = _rows("x", x, None, _REAL)
+    M, K = x.shape
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    if scale_out is None:
+        scale_out = torch.empty(M, dtype=torch.float32, device=x.device)
+    _dense("out", out, (M, K), torch.int8)
+    _dense("scale_out", scale_out, (M,), torch.float32)
+    _check((_lib or library()).lib.lowm_quantize_rows(
+        x.data_ptr(), _TYPES[x.dtype], ld, M, K, out.data_ptr(), scale_out.data_ptr(),
+        _stream(stream, x.device)))
+    return out, scale_out
