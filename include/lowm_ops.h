@@ -96,6 +96,59 @@ int lowm_residual_norm(const lowm_residual_norm_args* args, void* stream);
 int lowm_quantize_rows(const void* x, int x_type, int64_t ld_x, int M, int K, void* q,
                        float* scale, void* stream);
 
+/*
+ * Log probabilities of given tokens.  For each of M rows of V logits, with
+ * m = max_v l[v], S = sum_v e^(l[v] - m) and log p[v] = l[v] - m - log S:
+ *
+ *     logprob = log p[token]
+ *     entropy = -sum_v p[v] log p[v] = log S - (sum_v e^(l[v]-m) (l[v]-m)) / S
+ *     rank    = how many logits are greater than the token's
+ *     top_logprob, top_id [top_n]: the largest log p, in order; equal ones by id
+ *
+ * in fp32, from one pass over the logits.  A logit of -infinity is a masked
+ * token: its probability is 0 and it is never an alternative.  Alternatives
+ * past the last unmasked one have log p -infinity and id -1.  A row with
+ * nothing unmasked has logprob -infinity, entropy 0, rank 0 and no alternatives.
+ * A token outside 0 .. V-1 has logprob NaN and rank -1.  A row with a NaN or
+ * a +infinity has no distribution: logprob, entropy and every top_logprob are
+ * NaN and every top_id is -1.  The rank goes by comparison (a NaN is greater
+ * than nothing, and nothing than it).
+ *
+ * logits bf16 or fp32, rows ld elements apart (>= V); tokens int64 or int32
+ * [M]; logprob, entropy fp32 [M]; rank int32 [M]; top_logprob fp32 and top_id
+ * int32 [M, top_n] (unused with top_n 0, at most LOWM_LOGPROBS_MAX_TOP).
+ * logits must not overlap an output or the workspace.  The workspace needs no
+ * clearing, holds nothing between calls, and may be NULL where
+ * lowm_token_logprobs_workspace_bytes is 0.
+ */
+#define LOWM_LOGPROBS_MAX_TOP 32
+typedef struct lowm_token_logprobs_args {
+    const void* logits;
+    const void* tokens;
+    float* logprob;
+    float* entropy;
+    int32_t* rank;
+    float* top_logprob;
+    int32_t* top_id;
+    void* workspace;
+    size_t workspace_bytes;
+    int64_t ld;
+    int32_t M, V, top_n;
+    int32_t logits_type;    /* LOWM_BF16 or LOWM_F32 */
+    int32_t tokens_bytes;   /* 8 (int64) or 4 (int32) */
+} lowm_token_logprobs_args;
+
+/* Bytes of workspace a call needs (0 for arguments it would reject).
+ * Host-only. */
+size_t lowm_token_logprobs_workspace_bytes(int M, int V, int top_n);
+
+/* Errors: NULL operand, M < 0, V < 1, ld < V, top_n < 0, an unknown type,
+ * overlap: LOWM_ERR_INVALID_ARG; top_n > LOWM_LOGPROBS_MAX_TOP, V > 2^30, a
+ * pointer not aligned to its element (the workspace: to 16 bytes):
+ * LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
+ * LOWM_ERR_WORKSPACE.  M == 0 does nothing. */
+int lowm_token_logprobs(const lowm_token_logprobs_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,7 +15,7 @@ namespace lowm {
 namespace {
 
 // Centred, twice: two sums a norm; and the largest magnitude.
-[[maybe_unused]] constexpr int kMaxReductions = 5;
+constexpr int kMaxReductions = 5;
 
 struct NormArgs {
   lowm_residual_norm_args u;
@@ -177,7 +177,6 @@ constexpr int group_threads(int G) { return G < 256 ? 256 : G; }
 
 template <int G, int V, bool VEC>
 __global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(NormArgs a) {
-#if defined(__HIP_DEVICE_COMPILE__)
   const lowm_residual_norm_args& u = a.u;
   __shared__ float lds[kMaxReductions * (G / kWave)];
   const int64_t m = (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
@@ -236,7 +235,6 @@ __global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(NormArg
     quantise(row, grp, r, static_cast<int8_t*>(u.x), m * u.ld_x, u.x_scale + m);
   else
     row.store(u.x, m * u.ld_x, false, r);
-#endif
 }
 
 struct QuantArgs {
@@ -249,7 +247,6 @@ struct QuantArgs {
 
 template <int G, int V, bool VEC>
 __global__ __launch_bounds__(group_threads(G)) void quantize_rows_kernel(QuantArgs a) {
-#if defined(__HIP_DEVICE_COMPILE__)
   __shared__ float lds[kMaxReductions * (G / kWave)];
   const int64_t m = (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
   if (m >= a.M) return;
@@ -258,7 +255,6 @@ __global__ __launch_bounds__(group_threads(G)) void quantize_rows_kernel(QuantAr
   float x[V][8];
   row.load(a.x, m * a.ld, a.f32 != 0, 0.f, x);
   quantise(row, grp, x, a.q, m * (int64_t)a.D, a.scale + m);
-#endif
 }
 
 // The group of lanes for rows of D elements: a wavefront up to 512 elements,

@@ -3,7 +3,8 @@ C ABI of include/lowm_ops.h.
 
 Argument checks and marshalling only: every step runs in the HIP kernels of
 liblowm.so, on the caller's current stream (or ``stream``), asynchronously and
-without allocating beyond the outputs a caller does not pass.  There is no
+without allocating beyond the outputs and workspaces a caller does not pass
+(those belong to the stream the call runs on).  There is no
 fallback: when the library is not built, or a call fails, this raises.
 """
 from __future__ import annotations
@@ -32,6 +33,13 @@ class ResidualNormArgs(ctypes.Structure):
                 ("residual_scale", _f), ("branch_scale", _f), ("eps", _f)]
 
 
+class TokenLogprobsArgs(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("tokens", _vp), ("logprob", _vp), ("entropy", _vp),
+                ("rank", _vp), ("top_logprob", _vp), ("top_id", _vp), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t), ("ld", _l), ("M", _i), ("V", _i),
+                ("top_n", _i), ("logits_type", _i), ("tokens_bytes", _i)]
+
+
 _lib = None
 
 
@@ -43,6 +51,9 @@ def library() -> binding.Library:
         c = lib.lib
         c.lowm_residual_norm.argtypes = [_vp, _vp]
         c.lowm_quantize_rows.argtypes = [_vp, _i, _l, _i, _i, _vp, _vp, _vp]
+        c.lowm_token_logprobs.argtypes = [_vp, _vp]
+        c.lowm_token_logprobs_workspace_bytes.argtypes = [_i, _i, _i]
+        c.lowm_token_logprobs_workspace_bytes.restype = ctypes.c_size_t
         _lib = lib
     return _lib
 
@@ -51,6 +62,15 @@ def _stream(stream, device) -> int:
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised tensor that belongs to the stream its kernel runs on, so
+    that its memory is not handed on while that kernel may still use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _check(rc: int):
@@ -119,7 +139,7 @@ def residual_norm(y: torch.Tensor, residual: torch.Tensor, *, post_norm: bool = 
     M, D = shape
     dev = residual.device
     if residual_out is None:
-        residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
+        residual_out = _empty(shape, residual.dtype, dev, stream)
     flags = (NORM_POST if post_norm else 0) | (NORM_CENTER if center else 0)
     a = ResidualNormArgs(y=y.data_ptr(), r=residual.data_ptr(), r_out=residual_out.data_ptr(),
                          ld_y=ld_y, ld_r=ld_r,
@@ -159,12 +179,12 @@ def residual_norm(y: torch.Tensor, residual: torch.Tensor, *, post_norm: bool = 
     if pre_norm:
         want = torch.int8 if quantize else torch.bfloat16
         if out is None:
-            out = torch.empty(shape, dtype=want, device=dev)
+            out = _empty(shape, want, dev, stream)
         a.ld_x = _rows("out", out, shape, (want,))
         a.x, a.x_type = out.data_ptr(), I8 if quantize else BF16
         if quantize:
             if scale_out is None:
-                scale_out = torch.empty(M, dtype=torch.float32, device=dev)
+                scale_out = _empty((M,), torch.float32, dev, stream)
             _dense("scale_out", scale_out, (M,), torch.float32)
             a.x_scale = scale_out.data_ptr()
     else:
@@ -184,12 +204,58 @@ def quantize_rows(x: torch.Tensor, *, out: Optional[torch.Tensor] = None,
     ld = _rows("x", x, None, _REAL)
     M, K = x.shape
     if out is None:
-        out = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        out = _empty((M, K), torch.int8, x.device, stream)
     if scale_out is None:
-        scale_out = torch.empty(M, dtype=torch.float32, device=x.device)
+        scale_out = _empty((M,), torch.float32, x.device, stream)
     _dense("out", out, (M, K), torch.int8)
     _dense("scale_out", scale_out, (M,), torch.float32)
     _check((_lib or library()).lib.lowm_quantize_rows(
         x.data_ptr(), _TYPES[x.dtype], ld, M, K, out.data_ptr(), scale_out.data_ptr(),
         _stream(stream, x.device)))
     return out, scale_out
+
+
+def make_token_logprobs_workspace(M: int, V: int, top_n: int = 0,
+                                  device="cuda") -> Optional[torch.Tensor]:
+    """The workspace of token_logprobs for these sizes (None where it needs none)."""
+    n = library().lib.lowm_token_logprobs_workspace_bytes(M, V, top_n)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int = 0, *,
+                   workspace: Optional[torch.Tensor] = None, outs=None, stream=None):
+    """(logprob [M], entropy [M], rank [M], top_logprob [M, top_n], top_id [M, top_n]) of
+    logits [M, V] (bf16 or fp32; -inf masks a token) and the given tokens [M] (int64 or int32).
+
+    logprob and entropy are those of softmax(logits); rank counts the logits greater than the
+    token's; the alternatives are the top_n most likely tokens, equal ones by id, -1 past the last
+    unmasked one.  fp32 and int32 outputs (``outs``: five tensors to write into)."""
+    ld = _rows("logits", logits, None, _REAL)
+    M, V = logits.shape
+    dev = logits.device
+    if tokens.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"tokens must be int64 or int32, not {tokens.dtype}")
+    _dense("tokens", tokens, (M,), tokens.dtype)
+    if outs is None:
+        outs = tuple(_empty(s, t, dev, stream)
+                     for s, t in (((M,), torch.float32), ((M,), torch.float32),
+                                  ((M,), torch.int32), ((M, top_n), torch.float32),
+                                  ((M, top_n), torch.int32)))
+    else:
+        for name, t, shape, dtype in zip(
+                ("logprob", "entropy", "rank", "top_logprob", "top_id"), outs,
+                ((M,), (M,), (M,), (M, top_n), (M, top_n)),
+                (torch.float32, torch.float32, torch.int32, torch.float32, torch.int32)):
+            _dense(name, t, shape, dtype)
+    lib = (_lib or library()).lib
+    if workspace is None:
+        need = lib.lowm_token_logprobs_workspace_bytes(M, V, top_n)
+        workspace = _empty((need,), torch.uint8, dev, stream) if need else None
+    a = TokenLogprobsArgs(
+        logits.data_ptr(), tokens.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(),
+        outs[2].data_ptr(), outs[3].data_ptr(), outs[4].data_ptr(),
+        0 if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        ld, M, V, top_n, _TYPES[logits.dtype], tokens.element_size())
+    _check(lib.lowm_token_logprobs(ctypes.byref(a), _stream(stream, dev)))
+    return tuple(outs)

@@ -1,0 +1,230 @@
+"""token_logprobs against its formulas in 64 bits.
+
+Tolerances, with u = 2^-24 and d = l - m: e^d carries the rounding of d and of
+its scaling and the exponential's own, (3|d| + 2) u; a sum adds at most 16
+terms a chunk of 4096, a rescaling a chunk (4 u) and under 64 more; log p adds
+the roundings of two subtractions and a logarithm.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+import split_bf16_gemm_amd as sbg
+from split_bf16_gemm_amd import ops
+
+U = 2.0 ** -24
+BF16, F32 = torch.bfloat16, torch.float32
+INF, NAN = float("inf"), float("nan")
+
+
+def reference(x, tok, n):
+    """fp64 logprob, entropy, rank, alternatives, and the bounds of both sums."""
+    M, V = x.shape
+    x = x.double()
+    m = x.amax(1, keepdim=True)
+    d = x - m
+    e = torch.exp(d)
+    S = e.sum(1, keepdim=True)
+    held = torch.where(e > 0, d, 0)
+    lp = d - torch.log(S)
+    H = (torch.log(S) - (e * held).sum(1, keepdim=True) / S)[:, 0]
+    mine = lp.gather(1, tok[:, None])[:, 0]
+    rank = (x > x.gather(1, tok[:, None])).sum(1)
+    val, ids = torch.sort(x, dim=1, descending=True, stable=True)
+    val, ids = val[:, :n], ids[:, :n]
+    if ids.shape[1] < n:
+        pad = n - ids.shape[1]
+        val = torch.cat([val, torch.full((M, pad), -INF, dtype=val.dtype)], 1)
+        ids = torch.cat([ids, torch.full((M, pad), -1)], 1)
+    ids = torch.where(val == -INF, -1, ids)
+    top = val - m - torch.log(S)
+    p = e / S
+    mean_d = (p * held.abs()).sum(1, keepdim=True)
+    mean_d2 = (p * held ** 2).sum(1, keepdim=True)
+    steps = V / 4096 * 20 + 120
+    s_err = U * (3 * mean_d + steps)
+    lp_err = s_err + 4 * U * (torch.log(S) + 1)
+    H_err = (s_err * (1 + mean_d) + U * (3 * mean_d2 + steps * mean_d)
+             + 4 * U * (torch.log(S) + mean_d + 1))[:, 0]
+    return mine, H, rank, top, ids, lp_err, H_err
+
+
+def judge(x, tok, n, got):
+    mine, H, rank, top, ids, lp_err, H_err = reference(x, tok, n)
+    lp, ent, rk, tl, ti = (t.cpu() for t in got)
+    assert torch.equal(rk.long(), rank) and torch.equal(ti.long(), ids)
+    assert lp.dtype == ent.dtype == tl.dtype == F32
+
+    def near(a, b, err):
+        a = a.double()
+        fin = b.isfinite()
+        assert torch.equal(a[~fin], b[~fin])
+        bound = (err + 3 * U * torch.where(fin, b, 0).abs())[fin]
+        assert ((a - b)[fin].abs() <= bound).all(), ((a - b)[fin].abs() / bound).max()
+
+    near(lp, mine, lp_err[:, 0])
+    near(ent, H, H_err)
+    near(tl, top, lp_err.expand_as(top))
+
+
+def logits(g, M, V, dtype, std=3.0):
+    return (torch.randn(M, V, generator=g) * std).to(dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,V", [(1, 1), (1, 7), (3, 300), (1, 4097), (2, 49152), (1, 131072),
+                                 (5, 50001), (64, 8193), (300, 5000), (1030, 1000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [0, 1, 20, 32])
+def test_token_logprobs(M, V, dtype, n):
+    g = torch.Generator().manual_seed(M * 7919 + V + n)
+    x = logits(g, M, V, dtype)
+    tok = torch.randint(0, V, (M,), generator=g)
+    if V > 40:
+        x[:, torch.randperm(V, generator=g)[:V // 7]] = -INF
+    ttype = torch.int32 if n == 1 else torch.int64
+    got = sbg.token_logprobs(x.cuda(), tok.to(ttype).cuda(), n)
+    torch.cuda.synchronize()
+    judge(x, tok, n, got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("start", [0, 1, 2, 5])
+@pytest.mark.parametrize("M", [2, 1100])
+def test_strided_rows_of_any_alignment(dtype, start, M):
+    g = torch.Generator().manual_seed(start)
+    V, ld = 4111, 4123
+    wide = torch.full((M, ld), INF, dtype=dtype)     # what lies beside a row would show
+    wide[:, start:start + V] = logits(g, M, V, dtype)
+    x = wide[:, start:start + V]
+    tok = torch.randint(0, V, (M,), generator=g)
+    got = sbg.token_logprobs(wide.cuda()[:, start:start + V], tok.cuda(), 6)
+    torch.cuda.synchronize()
+    judge(x, tok, 6, got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 3, 1200])
+@pytest.mark.parametrize("n", [5, 32])
+@pytest.mark.parametrize("kind", ["equal", "rising", "falling", "few_left", "one_left", "zeros",
+                                  "two_values", "far", "lowest"])
+def test_rows_that_fill_the_candidates(M, n, kind):
+    V = 9001
+    g = torch.Generator().manual_seed(n)
+    if kind == "equal":
+        x = torch.full((M, V), 2.5)
+    elif kind == "rising":
+        x = torch.arange(V).float().repeat(M, 1) / 64
+    elif kind == "falling":
+        x = -torch.arange(V).float().repeat(M, 1) / 64
+    elif kind in ("few_left", "one_left"):
+        x = torch.full((M, V), -INF)
+        for i in range(M):
+            keep = torch.randperm(V, generator=g)[:1 if kind == "one_left" else 17]
+            x[i, keep] = torch.randn(len(keep), generator=g)
+    elif kind == "zeros":
+        x = torch.zeros(M, V)
+        x[:, ::2] = -0.0
+    elif kind == "two_values":
+        x = torch.randint(0, 2, (M, V), generator=g).float()
+    elif kind == "far":
+        x = logits(g, M, V, F32) + 30000
+    else:
+        x = torch.full((M, V), torch.finfo(F32).min)
+        x[:, 1234] = -1.0
+    tok = torch.randint(0, V, (M,), generator=g)
+    for dtype in (BF16, F32):
+        y = x.to(dtype)
+        if kind == "lowest" and dtype == BF16:
+            y = y.clamp(min=torch.finfo(BF16).min)
+        got = sbg.token_logprobs(y.cuda(), tok.cuda(), n)
+        torch.cuda.synchronize()
+        judge(y, tok, n, got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [6, 1200])
+def test_rows_without_a_distribution(M):
+    V, n = 20000, 4
+    g = torch.Generator().manual_seed(1)
+    x = logits(g, M, V, F32)
+    x[1] = -INF
+    x[2, 19999] = NAN
+    x[3, 0] = INF
+    x[4, 77] = -NAN
+    tok = torch.randint(0, V, (M,), generator=g)
+    tok[5] = V
+    tok[0] = -1
+    lp, ent, rank, tl, ti = (t.cpu() for t in sbg.token_logprobs(x.cuda(), tok.cuda(), n))
+    assert lp[1] == -INF and ent[1] == 0 and rank[1] == 0
+    assert (tl[1] == -INF).all() and (ti[1] == -1).all()
+    for r in (2, 3, 4):
+        assert lp[r].isnan() and ent[r].isnan() and tl[r].isnan().all() and (ti[r] == -1).all()
+        assert rank[r] == (x[r] > x[r, tok[r]]).sum()
+    for r in (0, 5):
+        assert lp[r].isnan() and rank[r] == -1 and ent[r].isfinite() and tl[r].isfinite().all()
+        assert torch.equal(ti[r].long(), torch.sort(x[r], descending=True, stable=True).indices[:n])
+
+
+@pytest.mark.gpu
+def test_same_bits_each_time_and_in_a_graph():
+    g = torch.Generator().manual_seed(2)
+    x, tok = logits(g, 3, 50001, BF16).cuda(), torch.randint(0, 50001, (3,), generator=g).cuda()
+    ws = sbg.make_token_logprobs_workspace(3, 50001, 20)
+    outs = sbg.token_logprobs(x, tok, 20, workspace=ws)
+    outs = tuple(torch.zeros_like(t) for t in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sbg.token_logprobs(x, tok, 20, workspace=ws, outs=outs)
+    side = torch.cuda.Stream()
+    for i in range(3):
+        x.copy_(logits(g, 3, 50001, BF16))
+        want = sbg.token_logprobs(x, tok, 20)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        again = sbg.token_logprobs(x, tok, 20, stream=side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(again, want))
+
+
+# -- refusals ------------------------------------------------------------------------------------
+BASE = dict(logits=0x10000000, tokens=0x20000000, logprob=0x21000000, entropy=0x22000000,
+            rank=0x23000000, top_logprob=0x24000000, top_id=0x25000000, workspace=0x26000000,
+            workspace_bytes=1 << 20, ld=5000, M=2, V=5000, top_n=5, logits_type=0, tokens_bytes=8)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(logits=None), -1), (dict(tokens=None), -1), (dict(logprob=None), -1),
+    (dict(entropy=None), -1), (dict(rank=None), -1), (dict(top_id=None), -1),
+    (dict(top_logprob=None), -1), (dict(M=-1), -1), (dict(V=0), -1), (dict(ld=4999), -1),
+    (dict(top_n=-1), -1), (dict(logits_type=2), -1), (dict(tokens_bytes=2), -1),
+    (dict(entropy=0x21000004), -1), (dict(logprob=0x10000000), -1), (dict(top_id=0x26000000), -1),
+    (dict(top_n=33), -2), (dict(V=(1 << 30) + 1, ld=1 << 31), -2), (dict(logits=0x10000001), -2),
+    (dict(logits=0x10000002, logits_type=1), -2), (dict(tokens=0x20000004), -2),
+    (dict(rank=0x23000002), -2), (dict(workspace=0x26000008), -2),
+    (dict(workspace=None), -3), (dict(workspace_bytes=64), -3), (dict(M=0, logits=None), 0)])
+def test_refuses(kw, code):
+    a = ops.TokenLogprobsArgs(**{**BASE, **kw})
+    assert ops.library().lib.lowm_token_logprobs(ctypes.byref(a), None) == code
+
+
+def test_workspace_bytes():
+    f = ops.library().lib.lowm_token_logprobs_workspace_bytes
+    assert f(2048, 49152, 5) == 0                    # enough rows: no row is cut
+    assert f(1, 49152, 5) == 12 * (16 + 5 * 8)
+    assert f(1, 4096, 5) == 0 and f(1, 4097, 0) == 2 * 16
+    assert f(0, 5, 5) == f(1, 0, 5) == f(1, 5, 33) == f(1, 5, -1) == 0
+
+
+def test_python_checks():
+    x = torch.zeros(2, 8, dtype=BF16)
+    for bad in (lambda: sbg.token_logprobs(x, torch.zeros(2, dtype=torch.int64)),
+                lambda: sbg.token_logprobs(x.half(), torch.zeros(2, dtype=torch.int64))):
+        with pytest.raises((ValueError, TypeError)):
+            bad()
