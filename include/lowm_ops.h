@@ -97,6 +97,40 @@ int lowm_quantize_rows(const void* x, int x_type, int64_t ld_x, int M, int K, vo
                        float* scale, void* stream);
 
 /*
+ * C[m][n] = (sum_k A[m][k] W[n][k]) * a_scale[m] * w_scale[n], the sum exact in
+ * int32, scaled in fp32 and rounded once.  A [M, K] int8 with a_scale [M], or
+ * bf16, which the call quantises per row as lowm_quantize_rows does (a row with
+ * an infinity or a NaN gives a row of NaN); W [N, K] int8 with w_scale [N]; C
+ * [M, N] bf16 or fp32; scales fp32.  All dense row-major; 1 <= M <= LOWM_MAX_M.
+ * With a bf16 A, `workspace` holds the quantised rows:
+ * lowm_gemm_i8_workspace_bytes, no clearing needed; one per call in flight.
+ */
+typedef struct lowm_gemm_i8_args {
+    const void* A;
+    const void* W;
+    const float* a_scale;   /* only for an int8 A */
+    const float* w_scale;
+    void* C;
+    void* workspace;
+    size_t workspace_bytes;
+    int32_t M, N, K;
+    int32_t a_type;         /* LOWM_I8 or LOWM_BF16 */
+    int32_t c_type;         /* LOWM_BF16 or LOWM_F32 */
+} lowm_gemm_i8_args;
+
+/* Bytes of workspace for a bf16 A (0 for sizes the call would reject).
+ * Host-only. */
+size_t lowm_gemm_i8_workspace_bytes(int M, int N, int K);
+
+/* Errors: NULL operand, a size < 1, an unknown type, an output or workspace
+ * that overlaps another operand: LOWM_ERR_INVALID_ARG; M > LOWM_MAX_M, K not a
+ * multiple of 16, K > 131056 (> LOWM_QUANTIZE_MAX_K for a bf16 A), A, W or the
+ * workspace not 16-byte aligned, another pointer not aligned to its element:
+ * LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
+ * LOWM_ERR_WORKSPACE. */
+int lowm_gemm_i8(const lowm_gemm_i8_args* args, void* stream);
+
+/*
  * Log probabilities of given tokens.  For each of M rows of V logits, with
  * m = max_v l[v], S = sum_v e^(l[v] - m) and log p[v] = l[v] - m - log S:
  *

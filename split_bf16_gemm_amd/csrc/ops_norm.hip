@@ -342,6 +342,9 @@ int residual_norm(const lowm_residual_norm_args* u, hipStream_t stream) {
              : launch_rows<NormK, false, 2>(a, u->M, u->D, stream);
 }
 
+}  // namespace
+
+// (The int8 product calls this too.)
 int quantize_rows(const void* x, int x_type, int64_t ld, int M, int K, void* q, float* scale,
                   hipStream_t stream) {
   if (M < 0 || K < 1 || ld < K || !real_type(x_type)) return LOWM_ERR_INVALID_ARG;
@@ -359,7 +362,6 @@ int quantize_rows(const void* x, int x_type, int64_t ld, int M, int K, void* q, 
              : launch_rows<QuantK, false, 4>(a, M, K, stream);
 }
 
-}  // namespace
 }  // namespace lowm
 
 extern "C" {

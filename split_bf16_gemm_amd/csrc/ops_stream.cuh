@@ -1,0 +1,133 @@
+// ops_stream.cuh -- one wavefront's product of a few rows with 16*NB weight rows
+// over a stretch of the inner dimension, both operands streamed through an LDS
+// ring of the wavefront's own.  Shared by the operators that read weights once
+// (the int8 product, the experts' products).
+//
+// Bytes are all this file knows of the element type: a step is one 128-byte
+// line of every row, two matrix instructions of 64 bytes each.  A line goes
+// straight into LDS in whole requests (8 rows x 128 B), its 16-byte pieces
+// rotated by row/2 so that the matrix layout's reads of 16 rows fall in
+// distinct banks.  There is no barrier in the loop: a slot is refilled only
+// after the wavefront's own reads of it have completed.
+#pragma once
+
+#include "lowm_kernels.cuh"
+#include "ops_common.cuh"
+
+namespace lowm {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+// What pieces past a row's end read instead: they then add nothing.
+__device__ const u32x4 kZeroPiece = {0u, 0u, 0u, 0u};
+
+__device__ __forceinline__ f32x4 stream_mfma(u32x4 a, u32x4 b, f32x4 c) { return mfma(a, b, c); }
+__device__ __forceinline__ i32x4 stream_mfma(u32x4 a, u32x4 b, i32x4 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                               __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+// See mfma_settle (lowm_kernels.cuh): wait states between the last matrix
+// instruction and the first read of its result on every path.
+template <int N>
+__device__ __forceinline__ void stream_settle(f32x4 (&acc)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+a"(acc[i]));
+}
+template <int N>
+__device__ __forceinline__ void stream_settle(i32x4 (&acc)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+a"(acc[i]));
+}
+
+// NB blocks of 16 weight rows, MB blocks of 16 activation rows, R ring slots.
+template <int NB, int MB, int R>
+struct StreamShape {
+  static constexpr int kPP = 68;                 // u32x4 per piece of 8 rows (1088 B)
+  static constexpr int G = 2 * (NB + MB);        // pieces, and loads, per step
+  static constexpr int kSlot = G * kPP;          // u32x4 per slot
+  static constexpr int kRing = R * kSlot;        // u32x4 per wavefront
+  static_assert(R >= 2 && (R - 1) * G <= 63, "the wait counter is 6 bits");
+};
+
+// Lane's row within a piece of 8 and its 16-byte piece of the row's line.
+__device__ __forceinline__ int stream_row(int lane) { return lane >> 3; }
+__device__ __forceinline__ int stream_piece(int lane) { return ((lane & 7) - (lane >> 4)) & 7; }
+
+// acc[j * MB + b] += rows of block b times weight rows of block j over P steps.
+// src[t]: this lane's 16 bytes of piece t in the first step (pieces 0 .. 2NB-1
+// weight rows, then activation rows); left: bytes from there to the row's end,
+// the same for every t.  Every address up to the row's end must be readable;
+// none past it is read.
+template <int NB, int MB, int R, typename Acc>
+__device__ __forceinline__ void stream_tile(u32x4* ring, const uint8_t* (&src)[2 * (NB + MB)],
+                                            int left, int P, Acc (&acc)[NB * MB]) {
+  using SH = StreamShape<NB, MB, R>;
+  constexpr int G = SH::G, kPP = SH::kPP;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int g = lane >> 4, l16 = lane & 15;
+  // Lane 7 of each 8-row piece's row 0 holds the line's last 16 bytes: a step is
+  // whole when they are inside.
+  const int line = __builtin_amdgcn_readfirstlane(left);   // lane 0: piece 0
+  int rpos[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    rpos[c] = (l16 >> 3) * kPP + (l16 & 7) * 8 + ((4 * c + g + ((l16 & 7) >> 1)) & 7);
+
+  auto issue = [&](u32x4* slot, int p) {
+    const int at = p * 128;
+    const bool whole = line - at >= 128;
+    static_for<G>([&](auto t_c) {
+      constexpr int t = decltype(t_c)::value;
+      const uint8_t* from = src[t] + at;
+      if (!whole) from = left - at >= 16 ? from : reinterpret_cast<const uint8_t*>(&kZeroPiece);
+      __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)(slot + t * kPP),
+                                       16, 0, t < 2 * NB ? kStreamAux : 0);
+    });
+    pin_issue();
+  };
+  auto multiply = [&](const u32x4* slot) {
+    u32x4 v[2 * (NB + MB)];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int t = 0; t < NB + MB; ++t)
+        v[c * (NB + MB) + t] = lds_read_opaque(slot + 2 * t * kPP + rpos[c]);
+    lds_wait(v);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+          acc[j * MB + b] =
+              stream_mfma(v[c * (NB + MB) + NB + b], v[c * (NB + MB) + j], acc[j * MB + b]);
+  };
+
+  u32x4* const end = ring + SH::kRing;
+  u32x4 *fill = ring, *use = ring;
+  auto next = [&](u32x4* s) { return s + SH::kSlot == end ? ring : s + SH::kSlot; };
+  for (int p = 0; p < R - 1 && p < P; ++p) {
+    issue(fill, p);
+    fill = next(fill);
+  }
+  int p = 0;
+  for (; p + R - 1 < P; ++p) {
+    // steps p .. p+R-2 are in flight; step p has landed when R-2 are
+    wait_vmcnt<(R - 2) * G>();
+    issue(fill, p + R - 1);        // into the slot step p-1 was read from
+    fill = next(fill);
+    multiply(use);
+    use = next(use);
+  }
+  static_for<R - 1>([&](auto i_c) {
+    constexpr int younger = R - 2 - decltype(i_c)::value;   // steps after this one
+    if (P - p == younger + 1) {
+      wait_vmcnt<younger * G>();
+      multiply(use);
+      use = next(use);
+      ++p;
+    }
+  });
+}
+
+}  // namespace lowm

@@ -33,6 +33,12 @@ class ResidualNormArgs(ctypes.Structure):
                 ("residual_scale", _f), ("branch_scale", _f), ("eps", _f)]
 
 
+class GemmI8Args(ctypes.Structure):
+    _fields_ = [("A", _vp), ("W", _vp), ("a_scale", _vp), ("w_scale", _vp), ("C", _vp),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("M", _i), ("N", _i),
+                ("K", _i), ("a_type", _i), ("c_type", _i)]
+
+
 class TokenLogprobsArgs(ctypes.Structure):
     _fields_ = [("logits", _vp), ("tokens", _vp), ("logprob", _vp), ("entropy", _vp),
                 ("rank", _vp), ("top_logprob", _vp), ("top_id", _vp), ("workspace", _vp),
@@ -51,6 +57,9 @@ def library() -> binding.Library:
         c = lib.lib
         c.lowm_residual_norm.argtypes = [_vp, _vp]
         c.lowm_quantize_rows.argtypes = [_vp, _i, _l, _i, _i, _vp, _vp, _vp]
+        c.lowm_gemm_i8.argtypes = [_vp, _vp]
+        c.lowm_gemm_i8_workspace_bytes.argtypes = [_i, _i, _i]
+        c.lowm_gemm_i8_workspace_bytes.restype = ctypes.c_size_t
         c.lowm_token_logprobs.argtypes = [_vp, _vp]
         c.lowm_token_logprobs_workspace_bytes.argtypes = [_i, _i, _i]
         c.lowm_token_logprobs_workspace_bytes.restype = ctypes.c_size_t
@@ -213,6 +222,55 @@ def quantize_rows(x: torch.Tensor, *, out: Optional[torch.Tensor] = None,
         x.data_ptr(), _TYPES[x.dtype], ld, M, K, out.data_ptr(), scale_out.data_ptr(),
         _stream(stream, x.device)))
     return out, scale_out
+
+
+def make_gemm_i8_workspace(M: int, N: int, K: int, device="cuda") -> Optional[torch.Tensor]:
+    """The workspace of gemm_i8 with a bf16 A of these sizes (None for sizes it rejects)."""
+    n = library().lib.lowm_gemm_i8_workspace_bytes(M, N, K)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def gemm_i8(A: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, *,
+            a_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            out_dtype: torch.dtype = torch.bfloat16,
+            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """(A @ W.T) * a_scale[:, None] * w_scale on the GPU, W [N, K] int8 with w_scale [N].
+
+    A [M, K], M <= 64: int8 with a_scale [M] (as quantize_rows or residual_norm give them), or
+    bf16, quantised per row within the call (``workspace``: make_gemm_i8_workspace)."""
+    if A.dim() != 2 or W.dim() != 2 or A.shape[1] != W.shape[1]:
+        raise ValueError(f"shapes {tuple(A.shape)} and {tuple(W.shape)} do not chain")
+    M, K = A.shape
+    N = W.shape[0]
+    dev = A.device
+    given = A.dtype == torch.int8
+    if not given and A.dtype != torch.bfloat16:
+        raise TypeError(f"A must be int8 or bfloat16, not {A.dtype}")
+    _dense("A", A, (M, K), A.dtype)
+    _dense("W", W, (N, K), torch.int8)
+    _dense("w_scale", w_scale, (N,), torch.float32)
+    if out is None:
+        out = _empty((M, N), out_dtype, dev, stream)
+    if out.dtype not in _REAL:
+        raise TypeError(f"the output must be bf16 or fp32, not {out.dtype}")
+    _dense("out", out, (M, N), out.dtype)
+    lib = (_lib or library()).lib
+    a = GemmI8Args(A.data_ptr(), W.data_ptr(), None, w_scale.data_ptr(), out.data_ptr(), None, 0,
+                   M, N, K, I8 if given else BF16, _TYPES[out.dtype])
+    if given:
+        _need(a_scale is not None, "an int8 A needs a_scale")
+        _dense("a_scale", a_scale, (M,), torch.float32)
+        a.a_scale = a_scale.data_ptr()
+    else:
+        _need(a_scale is None, "a bf16 A takes no a_scale")
+        if workspace is None:
+            need = lib.lowm_gemm_i8_workspace_bytes(M, N, K)
+            workspace = _empty((need,), torch.uint8, dev, stream) if need else None
+        if workspace is not None:
+            a.workspace = workspace.data_ptr()
+            a.workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib.lowm_gemm_i8(ctypes.byref(a), _stream(stream, dev)))
+    return out
 
 
 def make_token_logprobs_workspace(M: int, V: int, top_n: int = 0,
