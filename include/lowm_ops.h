@@ -131,6 +131,61 @@ size_t lowm_gemm_i8_workspace_bytes(int M, int N, int K);
 int lowm_gemm_i8(const lowm_gemm_i8_args* args, void* stream);
 
 /*
+ * A mixture-of-experts layer for T <= LOWM_MOE_MAX_T tokens:
+ *
+ *     l[t][e] = sum_d x[t][d] router[e][d]
+ *     s       = softmax over e of l[t], or with LOWM_MOE_SIGMOID 1 / (1 + e^-l)
+ *     the top_k experts of token t: the largest l, or with a bias the largest
+ *         s + bias[e]; equal ones by e
+ *     gate    = s of the chosen, divided by their sum unless LOWM_MOE_NO_RENORM,
+ *         times routed_scale
+ *     h       = silu(x[t] . w13[e][i]) * (x[t] . w13[e][I + i])    i < I
+ *     out[t]  = sum over the chosen of gate * (h . w2[e][d])
+ *
+ * x, out [T, D], router [E, D], w13 [E, 2I, D] (gate rows, then up rows), w2
+ * [E, D, I] bf16, all dense; bias fp32 [E] or NULL.  Sums are fp32; h is
+ * rounded to bf16 between the two products (the matrix units' input type) and
+ * out once.  ids (int32) and gates (fp32) [T, top_k], the chosen experts in
+ * order, are written where not NULL.  The same inputs give the same bits.
+ *
+ * The workspace (lowm_moe_workspace_bytes, 256-byte aligned) is zeroed once
+ * before its first use; every call that completes leaves what must be zero so,
+ * for any sizes.  One workspace per call in flight.  lowm_workspace_status of
+ * the GEMM reads it too, with N = D + 16.
+ */
+#define LOWM_MOE_MAX_T 64
+#define LOWM_MOE_MAX_E 256
+#define LOWM_MOE_MAX_K 16
+#define LOWM_MOE_SIGMOID 1
+#define LOWM_MOE_NO_RENORM 2
+typedef struct lowm_moe_args {
+    const void* x;
+    const void* router;
+    const float* bias;
+    const void* w13;
+    const void* w2;
+    void* out;
+    int32_t* ids;
+    float* gates;
+    void* workspace;
+    size_t workspace_bytes;
+    int32_t T, D, I, E, top_k;
+    int32_t flags;
+    float routed_scale;
+} lowm_moe_args;
+
+/* Bytes of workspace a call needs (0 for sizes it would reject).  Host-only. */
+size_t lowm_moe_workspace_bytes(int T, int D, int I, int E, int top_k);
+
+/* Errors: NULL operand, a size < 1, top_k > E, an unknown flag, overlap of an
+ * output or the workspace with another operand: LOWM_ERR_INVALID_ARG; T, E or
+ * top_k past its limit, D or I not a multiple of 8 or past 65536, an operand
+ * not 16-byte (ids, gates, bias: 4-byte, workspace: 256-byte) aligned:
+ * LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
+ * LOWM_ERR_WORKSPACE.  T == 0 does nothing. */
+int lowm_moe(const lowm_moe_args* args, void* stream);
+
+/*
  * Log probabilities of given tokens.  For each of M rows of V logits, with
  * m = max_v l[v], S = sum_v e^(l[v] - m) and log p[v] = l[v] - m - log S:
  *

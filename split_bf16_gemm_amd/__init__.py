@@ -8,16 +8,17 @@ calls them.
 
 Beside the GEMM stand the operators of a decode step around it (C ABI in
 ``include/lowm_ops.h``): residual_norm, quantize_rows,
-gemm_i8 and token_logprobs.
+gemm_i8, moe and token_logprobs.
 """
 from .binding import (MAX_BATCH, BwProbe, GemmDesc, Library, LowmError, Tactic,
                       batched_workspace_bytes, counter_bytes, gemm, gemm_batched, load,
                       make_workspace, pick_split_k, tactic, workspace_bytes)
-from .ops import (gemm_i8, make_gemm_i8_workspace, make_token_logprobs_workspace, quantize_rows,
-                  residual_norm, token_logprobs)
+from .ops import (gemm_i8, make_gemm_i8_workspace, make_moe_workspace,
+                  make_token_logprobs_workspace, moe, quantize_rows, residual_norm,
+                  token_logprobs)
 
 __all__ = ["MAX_BATCH", "BwProbe", "GemmDesc", "Library", "LowmError", "Tactic",
            "batched_workspace_bytes", "counter_bytes", "gemm", "gemm_batched", "gemm_i8", "load",
-           "make_gemm_i8_workspace", "make_token_logprobs_workspace", "make_workspace",
-           "pick_split_k", "quantize_rows", "residual_norm", "tactic", "token_logprobs",
-           "workspace_bytes"]
+           "make_gemm_i8_workspace", "make_moe_workspace", "make_token_logprobs_workspace",
+           "make_workspace", "moe", "pick_split_k", "quantize_rows", "residual_norm", "tactic",
+           "token_logprobs", "workspace_bytes"]

@@ -39,7 +39,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 GEMM_SOURCES = ["lowm_host.hip", "lowm_inst_bf16.hip", "lowm_inst_f32.hip",
                 "lowm_inst_push.hip"]
 # the operators of include/lowm_ops.h
-OPS_SOURCES = ["ops_norm.hip", "ops_logprob.hip", "ops_i8.hip"]
+OPS_SOURCES = ["ops_norm.hip", "ops_logprob.hip", "ops_i8.hip", "ops_moe.hip"]
 TARGETS = {
     "liblowm.so": (GEMM_SOURCES + OPS_SOURCES, []),
     "liblowm_stress.so": (GEMM_SOURCES, ["-DLOWM_STRESS"]),

@@ -94,19 +94,43 @@ __device__ __forceinline__ void store1(void* base, int64_t at, bool f32, float v
     static_cast<__bf16*>(base)[at] = static_cast<__bf16>(v);
 }
 
-// Reductions over the wavefront; every lane gets the result.
+// Reductions over the wavefront by data-parallel moves within the vector unit
+// (four shifts within rows of 16 lanes, then two broadcasts across rows); lanes
+// a move does not reach take the operation's neutral 0.  Every lane gets the
+// result, the last lane's.  All 64 lanes must be active.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t lane_move(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <typename Op>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, Op op) {
+  v = op(v, lane_move<0x111, 0xf>(v));   // row_shr 1, 2, 4, 8
+  v = op(v, lane_move<0x112, 0xf>(v));
+  v = op(v, lane_move<0x114, 0xf>(v));
+  v = op(v, lane_move<0x118, 0xf>(v));
+  v = op(v, lane_move<0x142, 0xa>(v));   // row_bcast 15 into rows 1 and 3
+  v = op(v, lane_move<0x143, 0xc>(v));   // row_bcast 31 into rows 2 and 3
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+  return __builtin_bit_cast(
+      float, wave_reduce(__builtin_bit_cast(uint32_t, v), [](uint32_t a, uint32_t b) {
+        return __builtin_bit_cast(
+            uint32_t, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+      }));
 }
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-#pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) {
-    const uint32_t o = __shfl_xor(v, off);
-    v = o > v ? o : v;
-  }
-  return v;
+  return wave_reduce(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+// fp32 bits as unsigned integers in the order of their values: -0 as +0, any
+// NaN above +infinity; never 0.
+__device__ __forceinline__ uint32_t order(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
+  return x != x ? 0xffffffffu : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __builtin_bit_cast(float, o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
 }  // namespace lowm

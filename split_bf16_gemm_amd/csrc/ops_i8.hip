@@ -15,8 +15,6 @@ namespace lowm {
 int quantize_rows(const void* x, int x_type, int64_t ld, int M, int K, void* q, float* scale,
                   hipStream_t stream);
 
-namespace {
-
 struct I8Args {
   const uint8_t* A;
   const uint8_t* W;
@@ -103,6 +101,8 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_kernel(I8Args a) {
   }
 #endif
 }
+
+namespace {
 
 template <int MB, int NB>
 const void* kernel_of() {

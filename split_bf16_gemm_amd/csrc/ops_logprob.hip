@@ -41,14 +41,6 @@ struct Part {
 };
 __host__ __device__ constexpr size_t part_bytes(int n) { return sizeof(Part) + 8 * (size_t)n; }
 
-// fp32 bits as unsigned integers in the order of their values (-0 as +0).
-__device__ __forceinline__ uint32_t order(float x) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float value_of(uint32_t o) {
-  return __builtin_bit_cast(float, o & 0x80000000u ? o & 0x7fffffffu : ~o);
-}
 __device__ __forceinline__ uint64_t key_of(float x, int id) {
   return (uint64_t)order(x) << 32 | (uint32_t)~id;
 }
@@ -74,10 +66,7 @@ struct Sums {
 };
 
 __device__ __forceinline__ Sums wave_join(Sums a) {
-  float m = a.m;
-#pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-  a.to(m);
+  a.to(value_of(wave_umax(order(a.m))));
   a.s = wave_sum(a.s);
   a.t = wave_sum(a.t);
   return a;

@@ -1,0 +1,721 @@
+// ops_moe.hip -- a mixture-of-experts layer for a few tokens
+// (include/lowm_ops.h) for gfx950.
+//
+// With few tokens the layer is a stream of weights: every expert that some
+// token chose is read once, 6 D I bytes, against a few rows of activations.
+// Three kernels:
+//   route  l = x router^T by expert tiles and stretches of D; the last workgroup
+//          to arrive adds the stretches, picks each token's experts and sorts the
+//          (token, expert) pairs by expert into segments of up to 16 rows, the
+//          matrix instructions' height;
+//   up     one workgroup per segment and 16 columns of h: 16 gate and 16 up rows;
+//   down   one workgroup per 16 output columns walks the segments as one long
+//          inner dimension, cut evenly over its wavefronts (and, for a narrow D,
+//          over several workgroups), and adds gate * result to the pair's token.
+// A segment's weights are all that its workgroups read from HBM; a further
+// segment of the same expert finds them in the caches.  No atomic adds, no
+// order that changes: equal inputs give equal bits.
+#include "ops_stream.cuh"
+
+namespace lowm {
+
+constexpr int kMaxT = LOWM_MOE_MAX_T;
+constexpr int kMaxE = LOWM_MOE_MAX_E;
+constexpr int kMaxK = LOWM_MOE_MAX_K;
+constexpr int kSegRows = 16;
+constexpr int kCols = 16;                 // columns of h, and of the output, per workgroup
+constexpr int kMaxDownSplits = 8;
+constexpr int kMaxSize = 65536;
+
+struct Segment {
+  int expert, first, rows, unused;        // pairs first .. first + rows - 1
+};
+struct Pair {
+  int token;
+  float gate;
+};
+
+// The workspace: arrival counters (one 256-byte line each: count, fault word)
+// and exchange slots, zero between calls, then what one call's kernels hand on.
+// The first part has one place and size for all calls, so that a call never
+// finds another size's leavings where its zeros have to be.
+constexpr size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+constexpr size_t kCounterBytes = 256 * (1 + (size_t)kMaxSize / kCols);
+constexpr size_t kRouteSlots = 256 * (size_t)kMaxE;              // most splits * T, times E
+constexpr size_t kDownSlots = 512 * (size_t)kMaxT * kCols;       // most tiles * splits, times the tile
+constexpr size_t kRouteAt = kCounterBytes;
+constexpr size_t kDownAt = kRouteAt + 4 * kRouteSlots;
+constexpr size_t kListsAt = kDownAt + 4 * kDownSlots;
+
+struct Layout {
+  int route_splits, down_splits, max_segments;
+  size_t pairs, h, bytes;
+};
+
+static Layout layout_of(int T, int D, int I, int E, int K) {
+  Layout l{};
+  const int steps = (2 * D + 127) / 128;
+  // Router: a stretch of D of at least a step per wavefront, and no more
+  // stretches than the last workgroup adds quickly (splits * T <= 256).
+  const int most = T <= 8 ? 16 : T <= 32 ? 8 : 4;
+  l.route_splits = steps / kWaves < most ? (steps / kWaves < 1 ? 1 : steps / kWaves) : most;
+  // Down: enough workgroups for 256 CUs (tiles * splits < 512).
+  const int tiles = (D + kCols - 1) / kCols;
+  l.down_splits = 1;
+  while (l.down_splits < kMaxDownSplits && tiles * l.down_splits < 256) l.down_splits *= 2;
+  const int pairs = T * K, active = pairs < E ? pairs : E;
+  // sum of ceil(n / 16) over the active experts, each with 1 <= n <= T pairs
+  l.max_segments = T <= kSegRows ? active : (pairs + (kSegRows - 1) * active) / kSegRows;
+  l.pairs = kListsAt + up256(16 + sizeof(Segment) * (size_t)l.max_segments);
+  l.h = l.pairs + up256(sizeof(Pair) * (size_t)pairs);
+  l.bytes = l.h + up256((size_t)2 * pairs * I);
+  return l;
+}
+
+struct MoeArgs {
+  const uint8_t* x;
+  const uint8_t* router;
+  const float* bias;
+  const uint8_t* w13;
+  const uint8_t* w2;
+  __bf16* out;
+  int* ids;
+  float* gates;
+  uint32_t* counters;                     // [1 + tiles], 64 words apart; 0 is the router's
+  uint32_t* route_slots;                  // [route_splits][T][E]
+  uint32_t* down_slots;                   // [tiles][down_splits][T][kCols]
+  int* lists;                             // number of segments, 3 unused, then the segments
+  Pair* pairs;
+  uint8_t* h;                             // [T * top_k, I] bf16, in the pairs' order
+  int T, D, I, E, top_k, flags;
+  float routed_scale;
+  int route_splits, down_splits;
+};
+
+// Exchange between workgroups: a slot holds the complement of an fp32 value's
+// bits, so zero means "not there yet", and each is written once per call; the
+// reader waits for it, whatever order the counter and the slots become visible
+// in.  The wait is bounded: a slot that stays zero sets the line's fault word.
+__device__ __forceinline__ float take_slot(uint32_t* slot, uint32_t w, uint32_t* line) {
+  if (w == 0u) {
+    const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
+    while ((w = load_slot(slot)) == 0u) {
+      if (__builtin_amdgcn_s_memrealtime() - t0 > kFoldPollTicks) {
+        store_slot(line + kFaultWord, 1u);
+        break;
+      }
+      __builtin_amdgcn_s_sleep(4);
+    }
+  }
+  store_slot(slot, 0u);
+  return dec_partial(w);
+}
+
+// Whether this workgroup is the last of `total` to arrive at the line; the
+// last one sets the count back to zero.
+__device__ __forceinline__ bool arrive_last(uint32_t* line, int total, int* lds) {
+  if (threadIdx.x == 0) {
+    const uint32_t before =
+        __hip_atomic_fetch_add(line, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *lds = before == (uint32_t)(total - 1);
+    if (*lds) store_slot(line, 0u);
+  }
+  __syncthreads();
+  return *lds != 0;
+}
+
+// ---------------------------------------------------------------------------
+// route
+// ---------------------------------------------------------------------------
+template <int MB>
+struct RouteShape {
+  static constexpr int R = MB == 4 ? 3 : 4;   // what LDS holds
+  using S = StreamShape<1, MB, R>;
+  static constexpr int kRings = kWaves * S::kRing * 16;
+  static constexpr int kLogits = 4 * kMaxT * kMaxE;
+  static constexpr int lds_bytes = kRings > kLogits ? kRings : kLogits;
+};
+
+__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+
+// One token's experts, by one wavefront: lane l holds experts l, l + 64, ...
+__device__ __forceinline__ void pick_experts(const MoeArgs& a, int t, const float* logits,
+                                             int (*chosen)[kMaxK], float (*gates)[kMaxK]) {
+  const int lane = threadIdx.x & (kWave - 1);
+  constexpr int kPer = kMaxE / kWave;
+  float l[kPer];
+  float m = -__builtin_inff();
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int e = lane + kWave * j;
+    l[j] = e < a.E ? logits[t * a.E + e] : -__builtin_inff();
+    m = fmaxf(m, l[j]);
+  }
+  m = value_of(wave_umax(order(m)));
+  const bool sig = a.flags & LOWM_MOE_SIGMOID, renorm = !(a.flags & LOWM_MOE_NO_RENORM);
+  float all = 1.f;
+  if (!sig) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (lane + kWave * j < a.E) s += expf(l[j] - m);
+    all = wave_sum(s);
+  }
+  auto score = [&](float v) { return sig ? sigmoid(v) : expf(v - m) / all; };
+  uint32_t o[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int e = lane + kWave * j;
+    o[j] = e < a.E ? order(a.bias ? score(l[j]) + a.bias[e] : l[j]) : 0u;
+  }
+  float sum = 0.f, mine = 0.f;
+  int my_id = 0;
+  for (int i = 0; i < a.top_k; ++i) {
+    uint32_t top = o[0];
+#pragma unroll
+    for (int j = 1; j < kPer; ++j) top = o[j] > top ? o[j] : top;
+    top = wave_umax(top);
+    // the lowest id among equals: the first j, then the first lane
+    int e = -1;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint64_t at = __ballot(o[j] == top);
+      if (e < 0 && at) e = kWave * j + __builtin_ctzll(at);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (lane + kWave * j == e) o[j] = 0u;
+    const float s = score(logits[t * a.E + e]);
+    sum += s;
+    if (lane == i) {
+      mine = s;
+      my_id = e;
+    }
+  }
+  if (lane < a.top_k) {
+    const float gate = (renorm ? mine / sum : mine) * a.routed_scale;
+    chosen[t][lane] = my_id;
+    gates[t][lane] = gate;
+    if (a.ids) a.ids[t * a.top_k + lane] = my_id;
+    if (a.gates) a.gates[t * a.top_k + lane] = gate;
+  }
+}
+
+// The pairs in order of expert, then token, and their segments.  Each expert's
+// tokens are the bits of a mask, so a pair's place is a count of bits below.
+__device__ __forceinline__ void sort_pairs(const MoeArgs& a, const int (*chosen)[kMaxK],
+                                           const float (*gates)[kMaxK], uint32_t (*mask)[2],
+                                           uint32_t* starts) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int pairs = a.T * a.top_k;
+  for (int p = tid; p < pairs; p += kThreads) {
+    const int t = p / a.top_k;
+    atomicOr(&mask[chosen[t][p % a.top_k]][t >> 5], 1u << (t & 31));
+  }
+  __syncthreads();
+  // thread e: expert e's pairs (low half) and segments (high half), summed over
+  // the experts before it
+  const int rows = __popc(mask[tid][0]) + __popc(mask[tid][1]);
+  const uint32_t own = (uint32_t)rows | (uint32_t)((rows + kSegRows - 1) / kSegRows) << 16;
+  uint32_t before = own;
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const uint32_t v = __shfl_up(before, off);
+    if (lane >= off) before += v;
+  }
+  __shared__ uint32_t ends[kWaves];
+  if (lane == kWave - 1) ends[wave] = before;
+  __syncthreads();
+  uint32_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) before += ends[w];
+    total += ends[w];
+  }
+  before -= own;
+  starts[tid] = before & 0xffffu;
+  Segment* segments = reinterpret_cast<Segment*>(a.lists + 4);
+  for (int s = 0; s * kSegRows < rows; ++s)
+    segments[(before >> 16) + s] =
+        Segment{tid, (int)(before & 0xffffu) + s * kSegRows,
+                rows - s * kSegRows < kSegRows ? rows - s * kSegRows : kSegRows, 0};
+  if (tid == 0) a.lists[0] = (int)(total >> 16);
+  __syncthreads();
+  for (int p = tid; p < pairs; p += kThreads) {
+    const int t = p / a.top_k, e = chosen[t][p % a.top_k];
+    const uint32_t lo = mask[e][0], hi = mask[e][1];
+    const int below = t < 32 ? __popc(lo & ((1u << t) - 1u))
+                             : __popc(lo) + __popc(hi & ((1u << (t - 32)) - 1u));
+    a.pairs[starts[e] + below] = Pair{t, gates[t][p % a.top_k]};
+  }
+}
+static_assert(kMaxE == kThreads, "sort_pairs has a thread for every expert");
+
+template <int MB>
+__global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  using SH = RouteShape<MB>;
+  constexpr int G = SH::S::G;
+  __shared__ u32x4 lds[SH::lds_bytes / 16];
+  __shared__ int chosen[kMaxT][kMaxK];
+  __shared__ float gates[kMaxT][kMaxK];
+  __shared__ uint32_t mask[kMaxE][2];
+  __shared__ uint32_t starts[kMaxE];
+  __shared__ int last;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int g = lane >> 4, l16 = lane & 15;
+  const int split = blockIdx.x % a.route_splits;
+  const int e0 = blockIdx.x / a.route_splits * 16;
+
+  // this wavefront's part of D: stretches in order, wavefronts in order in each
+  const int steps = (2 * a.D + 127) / 128;
+  const int parts = a.route_splits * kWaves, part = split * kWaves + wave;
+  const int s0 = steps * part / parts, P = steps * (part + 1) / parts - s0;
+  const int k0 = s0 * 128 + stream_piece(lane) * 16;
+  f32x4 acc[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (P > 0) {
+    const uint8_t* src[G];
+#pragma unroll
+    for (int t = 0; t < G; ++t) {
+      int r = 8 * (t < 2 ? t : t - 2) + stream_row(lane);
+      if (t < 2) {
+        r = e0 + r < a.E ? e0 + r : a.E - 1;
+        src[t] = a.router + (size_t)r * a.D * 2 + k0;
+      } else {
+        r = r < a.T ? r : a.T - 1;
+        src[t] = a.x + (size_t)r * a.D * 2 + k0;
+      }
+    }
+    stream_tile<1, MB, SH::R>(lds + wave * SH::S::kRing, src, 2 * a.D - k0, P, acc);
+  }
+  stream_settle(acc);
+  f32x4* sums = reinterpret_cast<f32x4*>(lds);
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < MB; ++b) sums[(wave * MB + b) * kWave + lane] = acc[b];
+  __syncthreads();
+  if (wave < MB && e0 + l16 < a.E) {
+    f32x4 v = sums[wave * kWave + lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      const f32x4 o = sums[(w * MB + wave) * kWave + lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += o[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 16 * wave + 4 * g + i;
+      if (t < a.T)
+        store_slot(a.route_slots + ((size_t)split * a.T + t) * a.E + e0 + l16, enc_partial(v[i]));
+    }
+  }
+  if (!arrive_last(a.counters, gridDim.x, &last)) return;
+
+  // The last workgroup: logits in order of the stretches, summed in 64 bits so
+  // that experts next to the border are told apart as well as fp32 can.
+  float* logits = reinterpret_cast<float*>(lds);
+  const int cells = a.T * a.E;
+  for (int c = threadIdx.x; c < cells; c += kThreads) {
+    double v = 0.0;
+    uint32_t w[16];
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+      if (s < a.route_splits) w[s] = load_slot(a.route_slots + (size_t)s * cells + c);
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+      if (s < a.route_splits)
+        v += (double)take_slot(a.route_slots + (size_t)s * cells + c, w[s], a.counters);
+    logits[c] = (float)v;
+  }
+  mask[threadIdx.x][0] = mask[threadIdx.x][1] = 0u;
+  __syncthreads();
+  for (int t = wave; t < a.T; t += kWaves) pick_experts(a, t, logits, chosen, gates);
+  __syncthreads();
+  sort_pairs(a, chosen, gates, mask, starts);
+#endif
+}
+
+// ---------------------------------------------------------------------------
+// up
+// ---------------------------------------------------------------------------
+struct UpShape {
+  static constexpr int R = 3;
+  using S = StreamShape<2, 1, R>;
+  static constexpr int kRings = kWaves * S::kRing * 16;
+};
+
+__global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int G = UpShape::S::G;
+  __shared__ u32x4 lds[UpShape::kRings / 16];
+  const int tiles = (a.I + kCols - 1) / kCols;
+  const int seg = blockIdx.x / tiles, i0 = blockIdx.x % tiles * kCols;
+  if (seg >= a.lists[0]) return;
+  const Segment s = reinterpret_cast<const Segment*>(a.lists + 4)[seg];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+
+  const int steps = (2 * a.D + 127) / 128;
+  const int s0 = steps * wave / kWaves, P = steps * (wave + 1) / kWaves - s0;
+  const int k0 = s0 * 128 + stream_piece(lane) * 16;
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  if (P > 0) {
+    const uint8_t* w = a.w13 + (size_t)s.expert * 4 * a.I * a.D + k0;
+    const uint8_t* src[G];
+#pragma unroll
+    for (int t = 0; t < G; ++t) {
+      // 16 gate rows, the 16 up rows of the same columns, then the segment's tokens
+      int r = 8 * (t & 1) + stream_row(lane);
+      if (t < 4) {
+        r = i0 + r < a.I ? i0 + r : a.I - 1;
+        src[t] = w + (size_t)(t < 2 ? r : a.I + r) * a.D * 2;
+      } else {
+        r = r < s.rows ? r : s.rows - 1;
+        src[t] = a.x + (size_t)a.pairs[s.first + r].token * a.D * 2 + k0;
+      }
+    }
+    stream_tile<2, 1, UpShape::R>(lds + wave * UpShape::S::kRing, src, 2 * a.D - k0, P, acc);
+  }
+  stream_settle(acc);
+  f32x4* sums = reinterpret_cast<f32x4*>(lds);
+  __syncthreads();
+  sums[(wave * 2) * kWave + lane] = acc[0];
+  sums[(wave * 2 + 1) * kWave + lane] = acc[1];
+  __syncthreads();
+  // wavefront i takes row 4 g + i of lane group g
+  float gate = 0.f, up = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    gate += reinterpret_cast<const float*>(sums + (w * 2) * kWave + lane)[wave];
+    up += reinterpret_cast<const float*>(sums + (w * 2 + 1) * kWave + lane)[wave];
+  }
+  const int row = 4 * (lane >> 4) + wave, i = i0 + (lane & 15);
+  if (row < s.rows && i < a.I)
+    reinterpret_cast<__bf16*>(a.h)[(size_t)(s.first + row) * a.I + i] =
+        static_cast<__bf16>(gate * sigmoid(gate) * up);
+#endif
+}
+
+// ---------------------------------------------------------------------------
+// down
+// ---------------------------------------------------------------------------
+struct DownShape {
+  static constexpr int R = 6;
+  using S = StreamShape<1, 1, R>;
+  static constexpr int kRings = kWaves * S::kRing * 16;
+};
+
+// LDS accesses the compiler does not see, for tables read while loads into LDS
+// are in flight (it would wait for all of those first).
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+__device__ __forceinline__ ops_u32x2 lds_read8_opaque(const void* p) {
+  ops_u32x2 v;
+  asm volatile("ds_read_b64 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(v) : "v"(lds_address(p)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void lds_add_opaque(float* p, float v) {
+  asm volatile("ds_add_f32 %0, %1" : : "v"(lds_address(p)), "v"(v) : "memory");
+}
+
+// The segments' steps as one sequence: step q is step q mod n of segment q / n.
+__global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  using S = DownShape::S;
+  constexpr int R = DownShape::R, G = S::G, kPP = S::kPP;
+  extern __shared__ u32x4 dyn[];
+  __shared__ u32x4 rings[DownShape::kRings / 16];
+  __shared__ int last;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int g = lane >> 4, l16 = lane & 15;
+  const int split = blockIdx.x % a.down_splits, tile = blockIdx.x / a.down_splits;
+  const int n0 = tile * kCols;
+  const int segments = a.lists[0], n_pairs = a.T * a.top_k;
+
+  // dynamic LDS: the segments, the pairs, each wavefront's [T][kCols] sums
+  Segment* segs = reinterpret_cast<Segment*>(dyn);
+  Pair* pairs = reinterpret_cast<Pair*>(segs + segments);
+  float* sums = reinterpret_cast<float*>(pairs + (n_pairs + 1) / 2 * 2);
+  for (int i = threadIdx.x; i < segments; i += kThreads)
+    segs[i] = reinterpret_cast<const Segment*>(a.lists + 4)[i];
+  for (int i = threadIdx.x; i < n_pairs; i += kThreads) pairs[i] = a.pairs[i];
+  const int cells = a.T * kCols;
+  for (int i = threadIdx.x; i < kWaves * cells; i += kThreads) sums[i] = 0.f;
+  __syncthreads();
+
+  const int per = (2 * a.I + 127) / 128;               // steps of a segment
+  const int steps = segments * per;
+  const int parts = a.down_splits * kWaves, part = split * kWaves + wave;
+  const int q0 = (int)((int64_t)steps * part / parts);
+  const int q1 = (int)((int64_t)steps * (part + 1) / parts);
+  const int P = q1 - q0;
+  u32x4* ring = rings + wave * S::kRing;
+  float* mine = sums + wave * cells;
+
+  const int piece = stream_piece(lane) * 16, qr = stream_row(lane);
+  int rpos[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    rpos[c] = (l16 >> 3) * kPP + (l16 & 7) * 8 + ((4 * c + g + ((l16 & 7) >> 1)) & 7);
+  // this tile's rows of w2 within an expert
+  size_t wrow[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int n = n0 + 8 * t + qr;
+    wrow[t] = (size_t)(n < a.D ? n : a.D - 1) * a.I * 2 + piece;
+  }
+
+  auto segment_at = [&](int s) {
+    u32x4 v[1] = {lds_read_opaque(reinterpret_cast<const u32x4*>(segs + s))};
+    lds_wait(v);
+    Segment out;
+    const uint32_t e = v[0][0], f = v[0][1], r = v[0][2];
+    out.expert = __builtin_amdgcn_readfirstlane((int)e);
+    out.first = __builtin_amdgcn_readfirstlane((int)f);
+    out.rows = __builtin_amdgcn_readfirstlane((int)r);
+    out.unused = 0;
+    return out;
+  };
+  // the next step to load
+  int ls = per > 0 ? q0 / per : 0, lk = q0 - ls * per;
+  const uint8_t* src[G];
+  auto point = [&]() {
+    const Segment s = segment_at(ls);
+    const uint8_t* w = a.w2 + (size_t)s.expert * a.D * a.I * 2;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) src[t] = w + wrow[t];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      int r = 8 * t + qr;
+      r = r < s.rows ? r : s.rows - 1;
+      src[2 + t] = a.h + (size_t)(s.first + r) * a.I * 2 + piece;
+    }
+  };
+  int loaded = 0;
+  auto issue = [&](u32x4* slot) {
+    const int at = lk * 128;
+    const bool whole = 2 * a.I - at >= 128;
+    static_for<G>([&](auto t_c) {
+      constexpr int t = decltype(t_c)::value;
+      const uint8_t* from = src[t] + at;
+      if (!whole)
+        from = 2 * a.I - piece - at >= 16 ? from : reinterpret_cast<const uint8_t*>(&kZeroPiece);
+      __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)(slot + t * kPP),
+                                       16, 0, t < 2 ? kStreamAux : 0);
+    });
+    pin_issue();
+    ++loaded;
+    if (++lk == per) {
+      lk = 0;
+      ++ls;
+      if (loaded < P) point();
+    }
+  };
+  f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+  int us = ls, uk = lk, used = 0;                        // the next step to use
+  auto flush = [&]() {
+    stream_settle(acc);
+    const Segment s = segment_at(us);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * g + i;
+      const ops_u32x2 p = lds_read8_opaque(pairs + s.first + (row < s.rows ? row : 0));
+      const uint32_t token = p[0], gate_bits = p[1];
+      const float gate = __builtin_bit_cast(float, gate_bits);
+      const float v = acc[0][i];
+      if (row < s.rows) lds_add_opaque(mine + token * kCols + l16, gate * v);
+    }
+    acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  auto multiply = [&](const u32x4* slot) {
+    u32x4 v[4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) v[2 * c + t] = lds_read_opaque(slot + 2 * t * kPP + rpos[c]);
+    lds_wait(v);
+    acc[0] = mfma(v[1], v[0], acc[0]);
+    acc[0] = mfma(v[3], v[2], acc[0]);
+    ++used;
+    if (++uk == per || used == P) {
+      flush();
+      uk = 0;
+      ++us;
+    }
+  };
+
+  u32x4* const end = ring + S::kRing;
+  u32x4 *fill = ring, *use = ring;
+  auto next = [&](u32x4* s) { return s + S::kSlot == end ? ring : s + S::kSlot; };
+  if (P > 0) point();
+  for (int p = 0; p < R - 1 && p < P; ++p) {
+    issue(fill);
+    fill = next(fill);
+  }
+  int p = 0;
+  for (; p + R - 1 < P; ++p) {
+    wait_vmcnt<(R - 2) * G>();
+    issue(fill);
+    fill = next(fill);
+    multiply(use);
+    use = next(use);
+  }
+  static_for<R - 1>([&](auto i_c) {
+    constexpr int younger = R - 2 - decltype(i_c)::value;
+    if (P - p == younger + 1) {
+      wait_vmcnt<younger * G>();
+      multiply(use);
+      use = next(use);
+      ++p;
+    }
+  });
+  wait_lgkmcnt0();
+  __syncthreads();
+
+  // The wavefronts' sums in order; then, with several workgroups to a tile, the
+  // workgroups' in order, by the last to arrive.
+  constexpr int kMine = kMaxT * kCols / kThreads;
+  float v[kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int c = threadIdx.x + j * kThreads;
+    v[j] = 0.f;
+    if (c < cells) {
+      v[j] = sums[c];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v[j] += sums[w * cells + c];
+    }
+  }
+  if (a.down_splits > 1) {
+    uint32_t* slots = a.down_slots + (size_t)tile * a.down_splits * cells;
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int c = threadIdx.x + j * kThreads;
+      if (c < cells) store_slot(slots + (size_t)split * cells + c, enc_partial(v[j]));
+    }
+    uint32_t* line = a.counters + (size_t)(1 + tile) * kCtrStride;
+    if (!arrive_last(line, a.down_splits, &last)) return;
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int c = threadIdx.x + j * kThreads;
+      if (c < cells) {
+        uint32_t w[kMaxDownSplits];
+#pragma unroll
+        for (int r = 0; r < kMaxDownSplits; ++r)
+          if (r < a.down_splits) w[r] = load_slot(slots + (size_t)r * cells + c);
+        float sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < kMaxDownSplits; ++r)
+          if (r < a.down_splits) {
+            const float part_sum = take_slot(slots + (size_t)r * cells + c, w[r], line);
+            sum = r == 0 ? part_sum : sum + part_sum;
+          }
+        v[j] = sum;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int c = threadIdx.x + j * kThreads;
+    const int n = n0 + c % kCols;
+    if (c < cells && n < a.D) a.out[(size_t)(c / kCols) * a.D + n] = static_cast<__bf16>(v[j]);
+  }
+#endif
+}
+
+namespace {
+
+bool moe_sizes(int T, int D, int I, int E, int K) {
+  return T >= 1 && T <= kMaxT && D >= 8 && D % 8 == 0 && D <= kMaxSize && I >= 8 && I % 8 == 0 &&
+         I <= kMaxSize && E >= 1 && E <= kMaxE && K >= 1 && K <= kMaxK && K <= E;
+}
+
+int moe(const lowm_moe_args* u, hipStream_t stream) {
+  if (!u || u->T < 0 || u->D < 1 || u->I < 1 || u->E < 1 || u->top_k < 1 || u->top_k > u->E)
+    return LOWM_ERR_INVALID_ARG;
+  if (u->flags & ~(LOWM_MOE_SIGMOID | LOWM_MOE_NO_RENORM)) return LOWM_ERR_INVALID_ARG;
+  if (u->T == 0) return LOWM_OK;
+  if (!u->x || !u->router || !u->w13 || !u->w2 || !u->out) return LOWM_ERR_INVALID_ARG;
+  const int T = u->T, D = u->D, I = u->I, E = u->E, K = u->top_k;
+  if (!moe_sizes(T, D, I, E, K)) return LOWM_ERR_UNSUPPORTED;
+  const Layout l = layout_of(T, D, I, E, K);
+  if (!u->workspace || u->workspace_bytes < l.bytes) return LOWM_ERR_WORKSPACE;
+  if (((uintptr_t)u->x | (uintptr_t)u->router | (uintptr_t)u->w13 | (uintptr_t)u->w2 |
+       (uintptr_t)u->out) & 15 ||
+      ((uintptr_t)u->bias | (uintptr_t)u->ids | (uintptr_t)u->gates) & 3 ||
+      (uintptr_t)u->workspace & 255)
+    return LOWM_ERR_UNSUPPORTED;
+  const Span in[] = {span_of(u->x, T, D, D, 2), span_of(u->router, E, D, D, 2),
+                     span_of(u->bias, 1, E, E, 4), span_of(u->w13, E, 2ll * I * D, 2ll * I * D, 2),
+                     span_of(u->w2, E, (int64_t)I * D, (int64_t)I * D, 2)};
+  const Span out[] = {span_of(u->out, T, D, D, 2), span_of(u->ids, T, K, K, 4),
+                      span_of(u->gates, T, K, K, 4),
+                      span_of(u->workspace, 1, (int64_t)l.bytes, (int64_t)l.bytes, 1)};
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& s : in)
+      if (meet(out[i], s)) return LOWM_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return LOWM_ERR_INVALID_ARG;
+  }
+  char* ws = static_cast<char*>(u->workspace);
+  MoeArgs a{};
+  a.x = static_cast<const uint8_t*>(u->x);
+  a.router = static_cast<const uint8_t*>(u->router);
+  a.bias = u->bias;
+  a.w13 = static_cast<const uint8_t*>(u->w13);
+  a.w2 = static_cast<const uint8_t*>(u->w2);
+  a.out = static_cast<__bf16*>(u->out);
+  a.ids = u->ids;
+  a.gates = u->gates;
+  a.counters = reinterpret_cast<uint32_t*>(ws);
+  a.route_slots = reinterpret_cast<uint32_t*>(ws + kRouteAt);
+  a.down_slots = reinterpret_cast<uint32_t*>(ws + kDownAt);
+  a.lists = reinterpret_cast<int*>(ws + kListsAt);
+  a.pairs = reinterpret_cast<Pair*>(ws + l.pairs);
+  a.h = reinterpret_cast<uint8_t*>(ws + l.h);
+  a.T = T;
+  a.D = D;
+  a.I = I;
+  a.E = E;
+  a.top_k = K;
+  a.flags = u->flags;
+  a.routed_scale = u->routed_scale;
+  a.route_splits = l.route_splits;
+  a.down_splits = l.down_splits;
+  void* args[] = {&a};
+  const void* route[] = {reinterpret_cast<const void*>(&moe_route_kernel<1>),
+                         reinterpret_cast<const void*>(&moe_route_kernel<2>),
+                         reinterpret_cast<const void*>(&moe_route_kernel<3>),
+                         reinterpret_cast<const void*>(&moe_route_kernel<4>)};
+  auto go = [&](const void* fn, size_t grid, size_t lds) {
+    return launched(hipLaunchKernel(fn, dim3((unsigned)grid), dim3(kThreads), args, lds, stream));
+  };
+  int rc = go(route[(T - 1) / 16], (size_t)((E + 15) / 16) * l.route_splits, 0);
+  if (rc == LOWM_OK)
+    rc = go(reinterpret_cast<const void*>(&moe_up_kernel),
+            (size_t)l.max_segments * ((I + kCols - 1) / kCols), 0);
+  const size_t lds = sizeof(Segment) * (size_t)l.max_segments +
+                     sizeof(Pair) * (size_t)((T * K + 1) / 2 * 2) +
+                     sizeof(float) * kWaves * (size_t)T * kCols;
+  if (rc == LOWM_OK)
+    rc = go(reinterpret_cast<const void*>(&moe_down_kernel),
+            (size_t)((D + kCols - 1) / kCols) * l.down_splits, lds);
+  return rc;
+}
+
+}  // namespace
+}  // namespace lowm
+
+extern "C" {
+
+size_t lowm_moe_workspace_bytes(int T, int D, int I, int E, int top_k) {
+  return lowm::moe_sizes(T, D, I, E, top_k) ? lowm::layout_of(T, D, I, E, top_k).bytes : 0;
+}
+
+int lowm_moe(const lowm_moe_args* args, void* stream) {
+  return lowm::moe(args, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

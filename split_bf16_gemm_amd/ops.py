@@ -19,6 +19,7 @@ from . import binding
 BF16, F32, I8 = 0, 1, 2
 _TYPES = {torch.bfloat16: BF16, torch.float32: F32, torch.int8: I8}
 NORM_POST, NORM_NO_PRE, NORM_CENTER = 1, 2, 4
+MOE_SIGMOID, MOE_NO_RENORM = 1, 2
 
 _vp, _i, _l, _f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
@@ -37,6 +38,13 @@ class GemmI8Args(ctypes.Structure):
     _fields_ = [("A", _vp), ("W", _vp), ("a_scale", _vp), ("w_scale", _vp), ("C", _vp),
                 ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("M", _i), ("N", _i),
                 ("K", _i), ("a_type", _i), ("c_type", _i)]
+
+
+class MoeArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("router", _vp), ("bias", _vp), ("w13", _vp), ("w2", _vp),
+                ("out", _vp), ("ids", _vp), ("gates", _vp), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t), ("T", _i), ("D", _i), ("I", _i),
+                ("E", _i), ("top_k", _i), ("flags", _i), ("routed_scale", _f)]
 
 
 class TokenLogprobsArgs(ctypes.Structure):
@@ -60,6 +68,9 @@ def library() -> binding.Library:
         c.lowm_gemm_i8.argtypes = [_vp, _vp]
         c.lowm_gemm_i8_workspace_bytes.argtypes = [_i, _i, _i]
         c.lowm_gemm_i8_workspace_bytes.restype = ctypes.c_size_t
+        c.lowm_moe.argtypes = [_vp, _vp]
+        c.lowm_moe_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
+        c.lowm_moe_workspace_bytes.restype = ctypes.c_size_t
         c.lowm_token_logprobs.argtypes = [_vp, _vp]
         c.lowm_token_logprobs_workspace_bytes.argtypes = [_i, _i, _i]
         c.lowm_token_logprobs_workspace_bytes.restype = ctypes.c_size_t
@@ -271,6 +282,60 @@ def gemm_i8(A: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, *,
             a.workspace_bytes = workspace.numel() * workspace.element_size()
     _check(lib.lowm_gemm_i8(ctypes.byref(a), _stream(stream, dev)))
     return out
+
+
+def make_moe_workspace(T: int, D: int, I: int, E: int, top_k: int,
+                       device="cuda") -> Optional[torch.Tensor]:
+    """A zeroed workspace of moe for these sizes (None for sizes it rejects); it also serves
+    any other sizes that need no more bytes, one call at a time."""
+    n = library().lib.lowm_moe_workspace_bytes(T, D, I, E, top_k)
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
+def moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, top_k: int, *,
+        score: str = "softmax", bias: Optional[torch.Tensor] = None, renormalize: bool = True,
+        routed_scale: float = 1.0, workspace: torch.Tensor, out: Optional[torch.Tensor] = None,
+        ids_out: Optional[torch.Tensor] = None, gates_out: Optional[torch.Tensor] = None,
+        stream=None):
+    """(out [T, D], ids [T, top_k], gates [T, top_k]) of a mixture-of-experts layer for T <= 64
+    tokens x [T, D]: router [E, D], w13 [E, 2I, D] (gate rows, then up rows), w2 [E, D, I], all
+    contiguous bf16.
+
+    Each token takes the top_k experts with the largest router logits, or with a ``bias`` [E]
+    (fp32) the largest score + bias; its gates are their scores ("softmax" over the experts or
+    "sigmoid"), divided by their sum with ``renormalize``, times ``routed_scale``; out is the
+    gated sum of w2 (silu(w13_gate x) * (w13_up x)).  workspace: make_moe_workspace."""
+    if x.dim() != 2 or router.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("x and router must have two dimensions, w13 and w2 three")
+    T, D = x.shape
+    E, _, I = w2.shape
+    for name, t, shape in (("x", x, (T, D)), ("router", router, (E, D)),
+                           ("w13", w13, (E, 2 * I, D)), ("w2", w2, (E, D, I))):
+        _dense(name, t, shape, torch.bfloat16)
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', not {score!r}")
+    dev = x.device
+    if out is None:
+        out = _empty((T, D), torch.bfloat16, dev, stream)
+    if ids_out is None:
+        ids_out = _empty((T, top_k), torch.int32, dev, stream)
+    if gates_out is None:
+        gates_out = _empty((T, top_k), torch.float32, dev, stream)
+    _dense("out", out, (T, D), torch.bfloat16)
+    _dense("ids_out", ids_out, (T, top_k), torch.int32)
+    _dense("gates_out", gates_out, (T, top_k), torch.float32)
+    if bias is not None:
+        _dense("bias", bias, (E,), torch.float32)
+    if workspace is None or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("moe needs a zeroed workspace on the GPU (make_moe_workspace)")
+    a = MoeArgs(x.data_ptr(), router.data_ptr(), None if bias is None else bias.data_ptr(),
+                w13.data_ptr(), w2.data_ptr(), out.data_ptr(), ids_out.data_ptr(),
+                gates_out.data_ptr(), workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), T, D, I, E, top_k,
+                (MOE_SIGMOID if score == "sigmoid" else 0)
+                | (0 if renormalize else MOE_NO_RENORM), routed_scale)
+    _check((_lib or library()).lib.lowm_moe(ctypes.byref(a), _stream(stream, dev)))
+    return out, ids_out, gates_out
 
 
 def make_token_logprobs_workspace(M: int, V: int, top_n: int = 0,
