@@ -7,11 +7,14 @@
 //   m' = max(m, l) ;  S' = S e^(m-m') + e^(l-m') ;  T' = (T + S (m-m')) e^(m-m') + ...
 //   log p = l - m - log S ;  entropy = log S - T / S
 //
-// so nothing overflows and the logits are read once.  The alternatives are kept
-// as a sorted list of 64-bit keys (the logit's bits in an order that integers
-// compare, then the complement of its id, so equal logits go by id and no two
-// keys are equal); a later chunk only adds what passes the list's last key.
-// Bound by HBM for many rows (2 or 4 bytes a logit against some 13 vector
+// so nothing overflows and the logits are read once.  The alternatives cost the
+// pass nothing: each lane's running maximum is its greatest logit, the top_n-th
+// of them bounds the row's top_n-th from below, and only the few lanes whose
+// maximum passes the bound have their logits read again (from the caches).
+// What passes is sorted by a 64-bit key: the logit's bits in an order that
+// integers compare, then the complement of its id, so equal logits go by id and
+// no two keys are equal.
+// Bound by HBM for many rows (2 or 4 bytes a logit against some 12 vector
 // instructions); few rows are cut into up to kMaxSplits pieces, joined by a
 // second small kernel.
 #include "ops_common.cuh"
@@ -22,8 +25,8 @@ namespace {
 constexpr int kTh = 256;                 // threads of a workgroup
 constexpr int kW = kTh / kWave;
 constexpr int kPerThread = 16;           // logits a thread takes from a chunk
-constexpr int kChunk = kTh * kPerThread;
-constexpr int kCap = 512;                // candidates a chunk may add at once
+constexpr int kCap = kTh;                // keys that are sorted
+constexpr int kPiece = 4096;             // least logits of a piece of a row
 constexpr int kMaxSplits = 32;
 constexpr int kMaxTop = LOWM_LOGPROBS_MAX_TOP;
 constexpr uint32_t kMasked = 0x007fffffu;   // order() of -infinity
@@ -72,92 +75,61 @@ __device__ __forceinline__ Sums wave_join(Sums a) {
   return a;
 }
 
-struct Shared {
-  uint64_t list[2][kMaxTop];             // the best so far, greatest first; 0: none
-  uint64_t buf[kCap];
-  uint64_t best[kW];
-  uint32_t thr[kW];
-  int count[3];
-  Sums sums[kW];
-};
-
-// Greatest key of the workgroup; every thread gets it.
-__device__ __forceinline__ uint64_t group_max(uint64_t v, uint64_t* lds) {
-#pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) {
-    const uint64_t o = __shfl_xor(v, off);
-    v = o > v ? o : v;
-  }
-  __syncthreads();
-  if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
-  __syncthreads();
-  v = lds[0];
-#pragma unroll
-  for (int w = 1; w < kW; ++w) v = lds[w] > v ? lds[w] : v;
-  return v;
+// The greatest bound that what is at or above t passes.  Below +0 lie the bits
+// of -0, which order() never gives: the bound is taken further down there, so
+// that +0 compares as greater than it.
+__device__ __forceinline__ uint32_t below(uint32_t t) {
+  return t == 0x80000000u ? 0x7f7fffffu : t - 1;
 }
 
-// The n greatest of list[0..n) and buf[0..count), in order, into next[0..n).
-// All keys but the empty ones differ, so each key's place is the number of
-// greater ones.  Barriers on both sides are the caller's.
-__device__ __forceinline__ void merge_lists(const uint64_t* list, const uint64_t* buf, int count,
-                                            int n, uint64_t* next) {
-  for (int i = threadIdx.x; i < count + n; i += kTh) {
-    const uint64_t key = i < n ? list[i] : buf[i - n];
-    int place = 0;
-    if (key) {
-      for (int j = 0; j < n; ++j) place += list[j] > key;
-      for (int j = 0; j < count; ++j) place += buf[j] > key;
-      if (place < n) next[place] = key;
-    }
-  }
-}
-
-// An order() that at least n of the workgroup's logits are above, at least thr:
-// of each wavefront's 64 lanes' own greatest logits the n-th, to 16 bits, and
-// the best of the wavefronts' bounds.  (n <= 32, so there always are n.)
-__device__ __forceinline__ uint32_t chunk_bound(float most, int n, uint32_t thr, uint32_t* lds) {
+// An order() that at least n of the wavefront's logits are above: the n-th of
+// its 64 lanes' own greatest logits, to 16 bits.  (n <= 32, so there always are n.)
+__device__ __forceinline__ uint32_t wave_bound(float most, int n) {
   const uint32_t o = order(most);
   uint32_t t = 0;
   for (int bit = 31; bit >= 16; --bit) {
     const uint32_t more = t | 1u << bit;
     if (__popcll(__ballot(o >= more)) >= n) t = more;
   }
-  // Above t - 1.  Below +0 lie the bits of -0, which order() never gives: the
-  // next bound down is taken there, so that +0 compares as greater than it.
-  t = t == 0x80000000u ? 0x7f7fffffu : t - 1;
-  if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = t;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kW; ++w) thr = lds[w] > thr ? lds[w] : thr;
-  return thr;
+  t = below(t);
+  return t > kMasked ? t : kMasked;
 }
 
+// The logits in 16 bytes.
 template <typename T>
 struct Raw;
 template <>
 struct Raw<float> {
-  static constexpr int kPer = 4;         // logits in 16 bytes
-  static constexpr uint32_t kMask = 0xff800000u;
+  static constexpr int kPer = 4;
+  static constexpr uint32_t kMask = 0xff800000u;         // -infinity throughout
   __device__ static __forceinline__ float get(const ops_u32x4& w, int i) {
     const uint32_t bits = w[i];          // a bit cast of w[i] itself reads element 0
     return __builtin_bit_cast(float, bits);
   }
-  __device__ static __forceinline__ void set(ops_u32x4& w, int i, uint32_t bits) { w[i] = bits; }
-  using Word = uint32_t;
 };
 template <>
 struct Raw<uint16_t> {
   static constexpr int kPer = 8;
-  static constexpr uint32_t kMask = 0xff80u;
+  static constexpr uint32_t kMask = 0xff80ff80u;
   __device__ static __forceinline__ float get(const ops_u32x4& w, int i) {
     return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
   }
-  __device__ static __forceinline__ void set(ops_u32x4& w, int i, uint32_t bits) {
-    w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | bits << 16 : (w[i / 2] & 0xffff0000u) | bits;
-  }
-  using Word = uint16_t;
 };
+
+// The sums' part of N logits of each lane; the greatest of them is `most`.
+template <int N>
+__device__ __forceinline__ void add_logits(Sums& sum, int& above, const float (&x)[N], float most,
+                                           float token_logit) {
+  sum.to(fmaxf(sum.m, most));
+  const float m = sum.m == kNone ? 0.f : sum.m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float d = x[i] - m, e = exp_of(d);
+    sum.s += e;                          // a NaN logit shows here
+    sum.t += e * held(d);
+    above += x[i] > token_logit;
+  }
+}
 
 // What a row's sums come to, by one thread.
 __device__ __forceinline__ void finish_row(const lowm_token_logprobs_args& u, int64_t row,
@@ -194,8 +166,15 @@ __device__ __forceinline__ bool token_of(const lowm_token_logprobs_args& u, int6
 template <typename T>
 __global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
   using R = Raw<T>;
-  constexpr int kRuns = kPerThread / R::kPer;
-  __shared__ Shared sh;
+  constexpr int kRuns = kPerThread / R::kPer;   // of 16 bytes
+  __shared__ uint64_t keys[kCap];
+  __shared__ uint64_t list[kMaxTop];
+  __shared__ uint64_t best[kW];
+  __shared__ Sums sums[kW];
+  __shared__ int totals[kW];
+  __shared__ uint32_t bounds[kW];
+  __shared__ int lanes[kTh];
+  __shared__ int n_lanes, n_keys;
   const lowm_token_logprobs_args& u = a.u;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int64_t row = blockIdx.x / a.splits;
@@ -203,42 +182,34 @@ __global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
   const int first = piece * a.per;                       // this piece: [first, first + len)
   const int len = first + a.per < u.V ? a.per : u.V - first;
   const T* src = static_cast<const T*>(u.logits) + row * u.ld + first;
-  // Logits between the 16-byte boundary below src and src: run j holds the
-  // logits [j * kPer - off, (j + 1) * kPer - off) of the piece.
-  const int off = (int)(((uintptr_t)src & 15) / sizeof(T));
-  const int chunks = (len + off + kChunk - 1) / kChunk;
-  const int n = u.top_n;
+  // Whole 16-byte runs between the first and the last 16-byte boundary in the
+  // piece, and up to 2 (kPer - 1) single logits beside them.
+  const int gap = (int)((16 - ((uintptr_t)src & 15)) & 15) / (int)sizeof(T);
+  const int head = gap < len ? gap : len;
+  const int runs = (len - head) / R::kPer;
+  const int chunks = (runs + kTh * kRuns - 1) / (kTh * kRuns);
+  const ops_u32x4* body = reinterpret_cast<const ops_u32x4*>(src + head);
 
-  float token_logit;
-  const bool token_ok = token_of(u, row, &token_logit);
-
-  if (tid < 3) sh.count[tid] = 0;
-  if (tid < kMaxTop) sh.list[0][tid] = sh.list[1][tid] = 0;
-  __syncthreads();
-
-  auto at = [&](int c, int r) { return (c * kChunk + (r * kTh + tid) * R::kPer) - off; };
+  auto run_at = [&](int c, int r) { return (c * kRuns + r) * kTh + tid; };
   auto fetch = [&](int c, ops_u32x4 (&w)[kRuns]) {
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) {
-      const int e = at(c, r);
-      if (e >= 0 && e + R::kPer <= len) {
-        w[r] = *reinterpret_cast<const ops_u32x4*>(src + e);
-      } else {
-#pragma unroll
-        for (int i = 0; i < R::kPer; ++i)
-          R::set(w[r], i,
-                 e + i >= 0 && e + i < len
-                     ? (uint32_t) reinterpret_cast<const typename R::Word*>(src)[e + i]
-                     : R::kMask);
-      }
+      w[r] = ops_u32x4{R::kMask, R::kMask, R::kMask, R::kMask};
+      const int j = run_at(c, r);
+      if (j < runs) w[r] = body[j];
     }
   };
 
-  Sums sum{kNone, 0.f, 0.f};
-  int above = 0;                         // of the wavefront
-  int cur = 0;                           // which list is the current one
   ops_u32x4 w[kRuns], ahead[kRuns];
   fetch(0, w);
+  float token_logit;
+  const bool token_ok = token_of(u, row, &token_logit);
+  Sums sum{kNone, 0.f, 0.f};
+  int above = 0;
+  const int n = u.top_n;
+  if (tid == 0) n_lanes = n_keys = 0;
+  if (tid < kMaxTop) list[tid] = 0;
+
   for (int c = 0; c < chunks; ++c) {
     if (c + 1 < chunks) fetch(c + 1, ahead);
     float x[kPerThread];
@@ -246,110 +217,105 @@ __global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
     for (int r = 0; r < kRuns; ++r)
 #pragma unroll
       for (int i = 0; i < R::kPer; ++i) x[r * R::kPer + i] = R::get(w[r], i);
-
     float most = x[0];
 #pragma unroll
     for (int i = 1; i < kPerThread; ++i) most = fmaxf(most, x[i]);
-    sum.to(fmaxf(sum.m, most));
-    const float m = sum.m == kNone ? 0.f : sum.m;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const float d = x[i] - m, e = exp_of(d);
-      sum.s += e;                        // a NaN logit shows here
-      sum.t += e * held(d);
-      above += __popcll(__ballot(x[i] > token_logit));
-    }
-
-    if (n > 0) {
-      const uint64_t* list = sh.list[cur];
-      int* count = &sh.count[c % 3];
-      // The third of the counters is cleared here for the next chunk: every
-      // thread has passed the barrier after which the last reads of it ended.
-      if (tid == 0) sh.count[(c + 1) % 3] = 0;
-      // A candidate's order() is above thr: that of the list's last key (an
-      // equal logit further on has a greater id, so it comes after it).
-      uint32_t thr = (uint32_t)(list[n - 1] >> 32);
-      thr = thr > kMasked ? thr : kMasked;
-      bool tried = false;
-      if (c == 0) {
-        thr = chunk_bound(most, n, thr, sh.thr);
-        tried = true;
-      }
-      int found;
-      while (true) {
-        const float bar = value_of(thr);
-        if (most > bar) {
-#pragma unroll
-          for (int i = 0; i < kPerThread; ++i)
-            if (x[i] > bar) {
-              const int to = atomicAdd(count, 1);
-              if (to < kCap)
-                sh.buf[to] = key_of(x[i], first + at(c, i / R::kPer) + i % R::kPer);
-            }
-        }
-        __syncthreads();
-        found = *count;
-        if (found <= kCap) break;
-        // Too many: raise the bound by this chunk's own, or, where that does
-        // not do (many equal logits), take the chunk's greatest one by one.
-        __syncthreads();
-        if (tid == 0) *count = 0;
-        if (!tried) {
-          thr = chunk_bound(most, n, thr, sh.thr);
-          tried = true;
-          continue;
-        }
-        uint64_t last = ~0ull;
-        for (int k = 0; k < n; ++k) {
-          uint64_t mine = 0;
-#pragma unroll
-          for (int i = 0; i < kPerThread; ++i)
-            if (x[i] > kNone) {
-              const uint64_t key = key_of(x[i], first + at(c, i / R::kPer) + i % R::kPer);
-              if (key < last && key > mine) mine = key;
-            }
-          last = group_max(mine, sh.best);
-          if (tid == 0) sh.buf[k] = last;      // 0 once there are none left
-        }
-        __syncthreads();
-        found = n;
-        break;
-      }
-      if (found > 0) {
-        uint64_t* next = sh.list[cur ^ 1];
-        if (tid < n) next[tid] = 0;
-        __syncthreads();
-        merge_lists(list, sh.buf, found, n, next);
-        __syncthreads();
-        cur ^= 1;
-      }
-    }
+    add_logits(sum, above, x, most, token_logit);
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) w[r] = ahead[r];
   }
+  const float most = sum.m;              // of the lane's runs
+  // The single logits beside the runs, one for each of the first lanes.
+  const int tail = head + runs * R::kPer;
+  const int single = tid < head ? tid : tail + tid - head;
+  float x1[1] = {kNone};
+  if (wave == 0) {
+    if (single < len) x1[0] = load1(src, single, sizeof(T) == 4);
+    add_logits(sum, above, x1, x1[0], token_logit);
+  }
 
   sum = wave_join(sum);
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) above += __shfl_xor(above, o);
   if (lane == 0) {
-    sh.sums[wave] = sum;
-    sh.thr[wave] = (uint32_t)above;
+    sums[wave] = sum;
+    totals[wave] = above;
+  }
+  if (n > 0) {
+    const uint32_t own = wave_bound(most, n);
+    if (lane == 0) bounds[wave] = own;
   }
   __syncthreads();
-  Sums all = sh.sums[0];
-  int total = (int)sh.thr[0];
+  if (n > 0) {
+    uint32_t thr = bounds[0];
+#pragma unroll
+    for (int v = 1; v < kW; ++v) thr = bounds[v] > thr ? bounds[v] : thr;
+    const float bar = value_of(thr);
+    if (most > bar) lanes[atomicAdd(&n_lanes, 1)] = tid;
+    auto add = [&](float v, int e) {
+      if (v > bar) {
+        const int to = atomicAdd(&n_keys, 1);
+        if (to < kCap) keys[to] = key_of(v, first + e);
+      }
+    };
+    if (wave == 0) add(x1[0], single);
+    __syncthreads();
+    const int per_lane = (runs + kTh - 1) / kTh, tasks = n_lanes * per_lane;
+    for (int q = tid; q < tasks; q += kTh) {
+      const int j = q % per_lane * kTh + lanes[q / per_lane];
+      if (j < runs) {
+        const ops_u32x4 again = body[j];
+#pragma unroll
+        for (int i = 0; i < R::kPer; ++i) add(R::get(again, i), head + j * R::kPer + i);
+      }
+    }
+    __syncthreads();
+    int count = n_keys;
+    if (count > kCap) {
+      // More equal logits at the bound than there is room for: the greatest
+      // keys one by one, each from the whole piece.
+      uint64_t last = ~0ull;
+      for (int k = 0; k < n && last; ++k) {
+        uint64_t mine = 0;
+        for (int e = tid; e < len; e += kTh) {
+          const float v = load1(src, e, sizeof(T) == 4);
+          const uint64_t key = key_of(v, first + e);
+          if (v > kNone && key < last && key > mine) mine = key;
+        }
+        const uint32_t hi = wave_umax((uint32_t)(mine >> 32));
+        const uint32_t lo = wave_umax((uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
+        __syncthreads();
+        if (lane == 0) best[wave] = (uint64_t)hi << 32 | lo;
+        __syncthreads();
+        last = best[0];
+#pragma unroll
+        for (int v = 1; v < kW; ++v) last = best[v] > last ? best[v] : last;
+        if (tid == 0) list[k] = last;
+      }
+    } else if (tid < count) {            // a key's place is the number of greater ones
+      const uint64_t key = keys[tid];
+      int place = 0;
+      for (int j = 0; j < count; ++j) place += keys[j] > key;
+      if (place < n) list[place] = key;
+    }
+    __syncthreads();
+  }
+  Sums all = sums[0];
+  int total = totals[0];
 #pragma unroll
   for (int v = 1; v < kW; ++v) {
-    Sums o = sh.sums[v];
+    Sums o = sums[v];
     const float m = fmaxf(all.m, o.m);
     all.to(m);
     o.to(m);
     all.s += o.s;
     all.t += o.t;
-    total += (int)sh.thr[v];
+    total += totals[v];
   }
   if (a.splits > 1) {
     char* part = static_cast<char*>(u.workspace) + (size_t)blockIdx.x * part_bytes(n);
     if (tid == 0) *reinterpret_cast<Part*>(part) = Part{all.m, all.s, all.t, total};
-    if (tid < n) reinterpret_cast<uint64_t*>(part + sizeof(Part))[tid] = sh.list[cur][tid];
+    if (tid < n) reinterpret_cast<uint64_t*>(part + sizeof(Part))[tid] = list[tid];
     return;
   }
   float log_s = 0.f;
@@ -358,10 +324,9 @@ __global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
     if (tid == 0) finish_row(u, row, all, total, token_logit, token_ok, &log_s, &bad);
     log_s = __shfl(log_s, 0);
     bad = __shfl((int)bad, 0);
-    if (tid < n) finish_top(u, row, tid, sh.list[cur][tid], all.m, log_s, bad);
+    if (tid < n) finish_top(u, row, tid, list[tid], all.m, log_s, bad);
   }
 }
-
 // Joins a row's pieces.  Each piece's keys are in order, so the greatest of the
 // pieces' last keys bounds the row's n-th from below.
 __global__ __launch_bounds__(kTh) void token_logprobs_join_kernel(LogprobArgs a) {
@@ -428,9 +393,9 @@ __global__ __launch_bounds__(kTh) void token_logprobs_join_kernel(LogprobArgs a)
 }
 
 // Pieces of a row: enough that the rows' pieces number 1024 (four workgroups
-// per CU), each at least a chunk long.
+// per CU), each at least kPiece long.
 int splits_of(int M, int V) {
-  const int want = (1024 + M - 1) / M, most = (V + kChunk - 1) / kChunk;
+  const int want = (1024 + M - 1) / M, most = (V + kPiece - 1) / kPiece;
   const int s = want < most ? want : most;
   return s < kMaxSplits ? s : kMaxSplits;
 }

@@ -4,10 +4,10 @@
 // With few tokens the layer is a stream of weights: every expert that some
 // token chose is read once, 6 D I bytes, against a few rows of activations.
 // Three kernels:
-//   route  l = x router^T by expert tiles and stretches of D; the last workgroup
-//          to arrive adds the stretches, picks each token's experts and sorts the
-//          (token, expert) pairs by expert into segments of up to 16 rows, the
-//          matrix instructions' height;
+//   route  l = x router^T by tiles of 16 experts and 16 tokens; the last workgroup
+//          to arrive picks each token's experts and sorts the (token, expert)
+//          pairs by expert into segments of up to 16 rows, the matrix
+//          instructions' height;
 //   up     one workgroup per segment and 16 columns of h: 16 gate and 16 up rows;
 //   down   one workgroup per 16 output columns walks the segments as one long
 //          inner dimension, cut evenly over its wavefronts (and, for a narrow D,
@@ -41,24 +41,19 @@ struct Pair {
 // finds another size's leavings where its zeros have to be.
 constexpr size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 constexpr size_t kCounterBytes = 256 * (1 + (size_t)kMaxSize / kCols);
-constexpr size_t kRouteSlots = 256 * (size_t)kMaxE;              // most splits * T, times E
+constexpr size_t kRouteSlots = (size_t)kMaxT * kMaxE;
 constexpr size_t kDownSlots = 512 * (size_t)kMaxT * kCols;       // most tiles * splits, times the tile
 constexpr size_t kRouteAt = kCounterBytes;
 constexpr size_t kDownAt = kRouteAt + 4 * kRouteSlots;
 constexpr size_t kListsAt = kDownAt + 4 * kDownSlots;
 
 struct Layout {
-  int route_splits, down_splits, max_segments;
+  int down_splits, max_segments;
   size_t pairs, h, bytes;
 };
 
 static Layout layout_of(int T, int D, int I, int E, int K) {
   Layout l{};
-  const int steps = (2 * D + 127) / 128;
-  // Router: a stretch of D of at least a step per wavefront, and no more
-  // stretches than the last workgroup adds quickly (splits * T <= 256).
-  const int most = T <= 8 ? 16 : T <= 32 ? 8 : 4;
-  l.route_splits = steps / kWaves < most ? (steps / kWaves < 1 ? 1 : steps / kWaves) : most;
   // Down: enough workgroups for 256 CUs (tiles * splits < 512).
   const int tiles = (D + kCols - 1) / kCols;
   l.down_splits = 1;
@@ -82,14 +77,14 @@ struct MoeArgs {
   int* ids;
   float* gates;
   uint32_t* counters;                     // [1 + tiles], 64 words apart; 0 is the router's
-  uint32_t* route_slots;                  // [route_splits][T][E]
+  uint32_t* route_slots;                  // [T][E]
   uint32_t* down_slots;                   // [tiles][down_splits][T][kCols]
   int* lists;                             // number of segments, 3 unused, then the segments
   Pair* pairs;
   uint8_t* h;                             // [T * top_k, I] bf16, in the pairs' order
   int T, D, I, E, top_k, flags;
   float routed_scale;
-  int route_splits, down_splits;
+  int down_splits;
 };
 
 // Exchange between workgroups: a slot holds the complement of an fp32 value's
@@ -127,13 +122,15 @@ __device__ __forceinline__ bool arrive_last(uint32_t* line, int total, int* lds)
 // ---------------------------------------------------------------------------
 // route
 // ---------------------------------------------------------------------------
-template <int MB>
+// 16 wavefronts cut D between them, so that a tile's few weights come in one
+// round trip and no sum has to cross workgroups.
+constexpr int kRouteWaves = 16;
+constexpr int kRouteThreads = kRouteWaves * kWave;
 struct RouteShape {
-  static constexpr int R = MB == 4 ? 3 : 4;   // what LDS holds
-  using S = StreamShape<1, MB, R>;
-  static constexpr int kRings = kWaves * S::kRing * 16;
-  static constexpr int kLogits = 4 * kMaxT * kMaxE;
-  static constexpr int lds_bytes = kRings > kLogits ? kRings : kLogits;
+  static constexpr int R = 2;
+  using S = StreamShape<1, 1, R>;
+  static constexpr int kRings = kRouteWaves * S::kRing * 16;
+  static_assert(kRings >= 4 * kMaxT * kMaxE, "the logits fit where the rings were");
 };
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
@@ -168,7 +165,6 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, int t, const floa
     const int e = lane + kWave * j;
     o[j] = e < a.E ? order(a.bias ? score(l[j]) + a.bias[e] : l[j]) : 0u;
   }
-  float sum = 0.f, mine = 0.f;
   int my_id = 0;
   for (int i = 0; i < a.top_k; ++i) {
     uint32_t top = o[0];
@@ -185,13 +181,10 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, int t, const floa
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
       if (lane + kWave * j == e) o[j] = 0u;
-    const float s = score(logits[t * a.E + e]);
-    sum += s;
-    if (lane == i) {
-      mine = s;
-      my_id = e;
-    }
+    if (lane == i) my_id = e;
   }
+  const float mine = lane < a.top_k ? score(logits[t * a.E + my_id]) : 0.f;
+  const float sum = wave_sum(mine);
   if (lane < a.top_k) {
     const float gate = (renorm ? mine / sum : mine) * a.routed_scale;
     chosen[t][lane] = my_id;
@@ -208,14 +201,16 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, const int (*chosen)
                                            uint32_t* starts) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int pairs = a.T * a.top_k;
-  for (int p = tid; p < pairs; p += kThreads) {
+  for (int p = tid; p < pairs; p += kRouteThreads) {
     const int t = p / a.top_k;
     atomicOr(&mask[chosen[t][p % a.top_k]][t >> 5], 1u << (t & 31));
   }
+  __shared__ uint32_t ends[kMaxE / kWave];
   __syncthreads();
   // thread e: expert e's pairs (low half) and segments (high half), summed over
   // the experts before it
-  const int rows = __popc(mask[tid][0]) + __popc(mask[tid][1]);
+  const bool one = tid < kMaxE;
+  const int rows = one ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
   const uint32_t own = (uint32_t)rows | (uint32_t)((rows + kSegRows - 1) / kSegRows) << 16;
   uint32_t before = own;
 #pragma unroll
@@ -223,25 +218,26 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, const int (*chosen)
     const uint32_t v = __shfl_up(before, off);
     if (lane >= off) before += v;
   }
-  __shared__ uint32_t ends[kWaves];
-  if (lane == kWave - 1) ends[wave] = before;
+  if (one && lane == kWave - 1) ends[wave] = before;
   __syncthreads();
-  uint32_t total = 0;
+  if (one) {
+    uint32_t total = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += ends[w];
-    total += ends[w];
+    for (int w = 0; w < kMaxE / kWave; ++w) {
+      if (w < wave) before += ends[w];
+      total += ends[w];
+    }
+    before -= own;
+    starts[tid] = before & 0xffffu;
+    Segment* segments = reinterpret_cast<Segment*>(a.lists + 4);
+    for (int s = 0; s * kSegRows < rows; ++s)
+      segments[(before >> 16) + s] =
+          Segment{tid, (int)(before & 0xffffu) + s * kSegRows,
+                  rows - s * kSegRows < kSegRows ? rows - s * kSegRows : kSegRows, 0};
+    if (tid == 0) a.lists[0] = (int)(total >> 16);
   }
-  before -= own;
-  starts[tid] = before & 0xffffu;
-  Segment* segments = reinterpret_cast<Segment*>(a.lists + 4);
-  for (int s = 0; s * kSegRows < rows; ++s)
-    segments[(before >> 16) + s] =
-        Segment{tid, (int)(before & 0xffffu) + s * kSegRows,
-                rows - s * kSegRows < kSegRows ? rows - s * kSegRows : kSegRows, 0};
-  if (tid == 0) a.lists[0] = (int)(total >> 16);
   __syncthreads();
-  for (int p = tid; p < pairs; p += kThreads) {
+  for (int p = tid; p < pairs; p += kRouteThreads) {
     const int t = p / a.top_k, e = chosen[t][p % a.top_k];
     const uint32_t lo = mask[e][0], hi = mask[e][1];
     const int below = t < 32 ? __popc(lo & ((1u << t) - 1u))
@@ -249,89 +245,77 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, const int (*chosen)
     a.pairs[starts[e] + below] = Pair{t, gates[t][p % a.top_k]};
   }
 }
-static_assert(kMaxE == kThreads, "sort_pairs has a thread for every expert");
 
-template <int MB>
-__global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using SH = RouteShape<MB>;
+  using SH = RouteShape;
   constexpr int G = SH::S::G;
-  __shared__ u32x4 lds[SH::lds_bytes / 16];
+  __shared__ u32x4 lds[SH::kRings / 16];
   __shared__ int chosen[kMaxT][kMaxK];
   __shared__ float gates[kMaxT][kMaxK];
   __shared__ uint32_t mask[kMaxE][2];
   __shared__ uint32_t starts[kMaxE];
   __shared__ int last;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int g = lane >> 4, l16 = lane & 15;
-  const int split = blockIdx.x % a.route_splits;
-  const int e0 = blockIdx.x / a.route_splits * 16;
+  const int tiles = (a.E + 15) / 16;
+  const int e0 = blockIdx.x % tiles * 16, t0 = blockIdx.x / tiles * 16;
 
-  // this wavefront's part of D: stretches in order, wavefronts in order in each
   const int steps = (2 * a.D + 127) / 128;
-  const int parts = a.route_splits * kWaves, part = split * kWaves + wave;
-  const int s0 = steps * part / parts, P = steps * (part + 1) / parts - s0;
+  const int s0 = steps * wave / kRouteWaves, P = steps * (wave + 1) / kRouteWaves - s0;
   const int k0 = s0 * 128 + stream_piece(lane) * 16;
-  f32x4 acc[MB];
-#pragma unroll
-  for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
   if (P > 0) {
     const uint8_t* src[G];
 #pragma unroll
     for (int t = 0; t < G; ++t) {
-      int r = 8 * (t < 2 ? t : t - 2) + stream_row(lane);
+      int r = 8 * (t & 1) + stream_row(lane);
       if (t < 2) {
         r = e0 + r < a.E ? e0 + r : a.E - 1;
         src[t] = a.router + (size_t)r * a.D * 2 + k0;
       } else {
-        r = r < a.T ? r : a.T - 1;
+        r = t0 + r < a.T ? t0 + r : a.T - 1;
         src[t] = a.x + (size_t)r * a.D * 2 + k0;
       }
     }
-    stream_tile<1, MB, SH::R>(lds + wave * SH::S::kRing, src, 2 * a.D - k0, P, acc);
+    stream_tile<1, 1, SH::R>(lds + wave * SH::S::kRing, src, 2 * a.D - k0, P, acc);
   }
   stream_settle(acc);
   f32x4* sums = reinterpret_cast<f32x4*>(lds);
   __syncthreads();
-#pragma unroll
-  for (int b = 0; b < MB; ++b) sums[(wave * MB + b) * kWave + lane] = acc[b];
+  sums[wave * kWave + lane] = acc[0];
+  mask[threadIdx.x % kMaxE][threadIdx.x / kMaxE & 1] = 0u;
   __syncthreads();
-  if (wave < MB && e0 + l16 < a.E) {
-    f32x4 v = sums[wave * kWave + lane];
+  // Wavefront i adds row 4 g + i of lane group g, in 64 bits so that experts next
+  // to the border are told apart as well as fp32 can.
+  if (wave < 4) {
+    double v = 0.0;
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-      const f32x4 o = sums[(w * MB + wave) * kWave + lane];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += o[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * wave + 4 * g + i;
-      if (t < a.T)
-        store_slot(a.route_slots + ((size_t)split * a.T + t) * a.E + e0 + l16, enc_partial(v[i]));
-    }
+    for (int w = 0; w < kRouteWaves; ++w)
+      v += (double)reinterpret_cast<const float*>(sums + w * kWave + lane)[wave];
+    const int t = t0 + 4 * (lane >> 4) + wave, e = e0 + (lane & 15);
+    if (t < a.T && e < a.E) store_slot(a.route_slots + t * a.E + e, enc_partial((float)v));
   }
   if (!arrive_last(a.counters, gridDim.x, &last)) return;
 
-  // The last workgroup: logits in order of the stretches, summed in 64 bits so
-  // that experts next to the border are told apart as well as fp32 can.
+  // The last workgroup has every logit before it.
   float* logits = reinterpret_cast<float*>(lds);
   const int cells = a.T * a.E;
-  for (int c = threadIdx.x; c < cells; c += kThreads) {
-    double v = 0.0;
-    uint32_t w[16];
+  constexpr int kAtOnce = 4;
+  for (int c0 = threadIdx.x; c0 < cells; c0 += kAtOnce * kRouteThreads) {
+    uint32_t w[kAtOnce];
 #pragma unroll
-    for (int s = 0; s < 16; ++s)
-      if (s < a.route_splits) w[s] = load_slot(a.route_slots + (size_t)s * cells + c);
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int c = c0 + j * kRouteThreads;
+      w[j] = load_slot(a.route_slots + (c < cells ? c : c0));
+    }
 #pragma unroll
-    for (int s = 0; s < 16; ++s)
-      if (s < a.route_splits)
-        v += (double)take_slot(a.route_slots + (size_t)s * cells + c, w[s], a.counters);
-    logits[c] = (float)v;
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int c = c0 + j * kRouteThreads;
+      if (c < cells) logits[c] = take_slot(a.route_slots + c, w[j], a.counters);
+    }
   }
-  mask[threadIdx.x][0] = mask[threadIdx.x][1] = 0u;
   __syncthreads();
-  for (int t = wave; t < a.T; t += kWaves) pick_experts(a, t, logits, chosen, gates);
+  for (int t = wave; t < a.T; t += kRouteWaves) pick_experts(a, t, logits, chosen, gates);
   __syncthreads();
   sort_pairs(a, chosen, gates, mask, starts);
 #endif
@@ -682,17 +666,13 @@ int moe(const lowm_moe_args* u, hipStream_t stream) {
   a.top_k = K;
   a.flags = u->flags;
   a.routed_scale = u->routed_scale;
-  a.route_splits = l.route_splits;
   a.down_splits = l.down_splits;
   void* args[] = {&a};
-  const void* route[] = {reinterpret_cast<const void*>(&moe_route_kernel<1>),
-                         reinterpret_cast<const void*>(&moe_route_kernel<2>),
-                         reinterpret_cast<const void*>(&moe_route_kernel<3>),
-                         reinterpret_cast<const void*>(&moe_route_kernel<4>)};
-  auto go = [&](const void* fn, size_t grid, size_t lds) {
-    return launched(hipLaunchKernel(fn, dim3((unsigned)grid), dim3(kThreads), args, lds, stream));
+  auto go = [&](const void* fn, size_t grid, size_t lds, int threads = kThreads) {
+    return launched(hipLaunchKernel(fn, dim3((unsigned)grid), dim3(threads), args, lds, stream));
   };
-  int rc = go(route[(T - 1) / 16], (size_t)((E + 15) / 16) * l.route_splits, 0);
+  int rc = go(reinterpret_cast<const void*>(&moe_route_kernel),
+              (size_t)((E + 15) / 16) * ((T + 15) / 16), 0, kRouteThreads);
   if (rc == LOWM_OK)
     rc = go(reinterpret_cast<const void*>(&moe_up_kernel),
             (size_t)l.max_segments * ((I + kCols - 1) / kCols), 0);
