@@ -102,9 +102,15 @@ int lowm_quantize_rows(const void* x, int x_type, int64_t ld_x, int M, int K, vo
  * bf16, which the call quantises per row as lowm_quantize_rows does (a row with
  * an infinity or a NaN gives a row of NaN); W [N, K] int8 with w_scale [N]; C
  * [M, N] bf16 or fp32; scales fp32.  All dense row-major; 1 <= M <= LOWM_MAX_M.
- * With a bf16 A, `workspace` holds the quantised rows:
- * lowm_gemm_i8_workspace_bytes, no clearing needed; one per call in flight.
+ *
+ * The workspace (lowm_gemm_i8_workspace_bytes, 256-byte aligned) holds the
+ * quantised rows of a bf16 A and the partial sums where K is split over
+ * workgroups.  It is zeroed once before its first use; every call that completes
+ * leaves what must be zero so, for any sizes.  One workspace per call in flight.
+ * An int8 A may come without one (NULL): K is then not split.
+ * lowm_workspace_status reads it, with N = LOWM_I8_STATUS_N.
  */
+#define LOWM_I8_STATUS_N 8192
 typedef struct lowm_gemm_i8_args {
     const void* A;
     const void* W;
@@ -118,15 +124,14 @@ typedef struct lowm_gemm_i8_args {
     int32_t c_type;         /* LOWM_BF16 or LOWM_F32 */
 } lowm_gemm_i8_args;
 
-/* Bytes of workspace for a bf16 A (0 for sizes the call would reject).
- * Host-only. */
+/* Bytes of workspace (0 for sizes the call would reject).  Host-only. */
 size_t lowm_gemm_i8_workspace_bytes(int M, int N, int K);
 
 /* Errors: NULL operand, a size < 1, an unknown type, an output or workspace
  * that overlaps another operand: LOWM_ERR_INVALID_ARG; M > LOWM_MAX_M, K not a
- * multiple of 16, K > 131056 (> LOWM_QUANTIZE_MAX_K for a bf16 A), A, W or the
- * workspace not 16-byte aligned, another pointer not aligned to its element:
- * LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
+ * multiple of 16, K > 131056 (> LOWM_QUANTIZE_MAX_K for a bf16 A), A or W not
+ * 16-byte, the workspace not 256-byte aligned, another pointer not aligned to
+ * its element: LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
  * LOWM_ERR_WORKSPACE. */
 int lowm_gemm_i8(const lowm_gemm_i8_args* args, void* stream);
 

@@ -5,9 +5,15 @@
 //
 // The sum is exact (int8 products in int32), so no order of it changes a bit;
 // it is scaled in fp32 and rounded once to the output's type.  Bound by HBM:
-// the N K bytes of W are read once.  Each workgroup takes 16*NB rows of W, its
-// wavefronts a stretch of K each (ops_stream.cuh), and adds their sums through
-// LDS.
+// the N K bytes of W are read once, the M K of A by every workgroup from the
+// caches.  Two kinds of workgroup:
+//   stretch  16*NB rows of W, its four wavefronts a stretch of K each
+//            (ops_stream.cuh), their sums added through LDS;
+//   panel    128*NB rows of W, 16*NB to each of eight wavefronts, all of K for
+//            each, with one panel of A per step for all of them: more rows of W
+//            for each byte of A read.
+// Where they are too few for the CUs, K is split over several workgroups whose
+// int32 sums the last to arrive adds.
 #include "ops_stream.cuh"
 
 namespace lowm {
@@ -21,32 +27,118 @@ struct I8Args {
   const float* a_scale;
   const float* w_scale;
   void* C;
-  int M, N, K, f32;
+  uint32_t* lines;                        // [tiles] counter lines
+  uint32_t* slots;                        // [tiles][splits][blocks][64][4]
+  int M, N, K, f32, splits;
 };
 
-template <int MB, int NB, int R>
+constexpr int kI8MaxSplits = 4;
+
+// Tile and split of this workgroup.  The grid is round_up(tiles, 8) * splits; a
+// tile's splits share their index modulo 8, so they run on one XCD.
+__device__ __forceinline__ void i8_place(const I8Args& a, int& tile, int& split) {
+  const int row = blockIdx.x / kXcds;
+  tile = blockIdx.x % kXcds + kXcds * (row / a.splits);
+  split = row % a.splits;
+}
+// The split's steps [s0, s0 + P) of 128 bytes, of this part of `parts`.
+__device__ __forceinline__ void i8_steps(const I8Args& a, int part, int parts, int& s0, int& P) {
+  const int steps = (a.K + 127) / 128;
+  s0 = (int)((int64_t)steps * part / parts);
+  P = (int)((int64_t)steps * (part + 1) / parts) - s0;
+}
+
+// A sum in a slot: never zero, since a sum of K <= 131056 products of magnitude
+// at most 2^14 is above -2^31.
+__device__ __forceinline__ uint32_t i8_encode(int v) { return (uint32_t)v ^ 0x80000000u; }
+__device__ __forceinline__ int i8_decode(uint32_t w) { return (int)(w ^ 0x80000000u); }
+
+// Row 4 g + i of block b, column n: element i of v.
+__device__ __forceinline__ void i8_store(const I8Args& a, const i32x4& v, int b, int n, int g) {
+  if (n >= a.N) return;
+  const float sw = a.w_scale[n];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = 16 * b + 4 * g + i;
+    if (m >= a.M) continue;
+    const int sum = v[i];
+    // int32 to fp32 rounds a sum past 2^24 by half a step of fp32.
+    const float c = (float)sum * a.a_scale[m] * sw;
+    const size_t at = (size_t)m * a.N + n;
+    if (a.f32)
+      static_cast<float*>(a.C)[at] = c;
+    else
+      static_cast<__bf16*>(a.C)[at] = static_cast<__bf16>(c);
+  }
+}
+
+// The splits' sums of a tile.  Thread by thread: v[j] is block first + j * step of
+// the tile's `blocks`.  Returns whether this workgroup, the last to arrive, now
+// holds the whole sums.
+template <int NV>
+__device__ __forceinline__ bool i8_join(const I8Args& a, i32x4 (&v)[NV], int tile, int split,
+                                        int blocks, int first, int step, int* lds) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const size_t per = (size_t)blocks * kWave * 4;
+  uint32_t* slots = a.slots + (size_t)tile * a.splits * per;
+  auto slot = [&](int s, int j, int i) {
+    return slots + s * per + ((size_t)(first + j * step) * kWave + lane) * 4 + i;
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (first + j * step < blocks) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store_slot(slot(split, j, i), i8_encode(v[j][i]));
+    }
+  uint32_t* line = a.lines + (size_t)tile * kCtrStride;
+  if (!arrive_last(line, a.splits, lds)) return false;
+  uint32_t w[NV][kI8MaxSplits][4];       // every load before the first use
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int s = 0; s < kI8MaxSplits; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (s < a.splits && first + j * step < blocks) w[j][s][i] = load_slot(slot(s, j, i));
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (first + j * step < blocks) {
+      v[j] = i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < kI8MaxSplits; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (s < a.splits) v[j][i] += i8_decode(take_slot(slot(s, j, i), w[j][s][i], line));
+    }
+  return true;
+}
+
+template <int AP, int NB, int R>
 struct I8Shape {
-  using S = StreamShape<NB, MB, R>;
-  static constexpr int kBlocks = NB * MB;
+  using S = StreamShape<NB, AP, R>;
+  static constexpr int kBlocks = NB * S::MB;
   static constexpr int kRings = kWaves * S::kRing * 16;                  // bytes
   static constexpr int kSums = kWaves * kBlocks * kWave * 16;
   static constexpr int lds_bytes = kRings > kSums ? kRings : kSums;
-  static constexpr bool valid = (R - 1) * S::G <= 63 && lds_bytes <= 160 * 1024;
+  static constexpr bool valid = S::valid && lds_bytes <= 160 * 1024 - 64;
 };
 
-template <int MB, int NB, int R>
-__global__ __launch_bounds__(kThreads) void gemm_i8_kernel(I8Args a) {
+template <int AP, int NB, int R>
+__global__ __launch_bounds__(kThreads) void gemm_i8_stretch_kernel(I8Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using SH = I8Shape<MB, NB, R>;
-  constexpr int G = SH::S::G;
+  using SH = I8Shape<AP, NB, R>;
+  constexpr int G = SH::S::G, MB = SH::S::MB;
   __shared__ u32x4 lds[SH::lds_bytes / 16];
+  __shared__ int last;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int g = lane >> 4, l16 = lane & 15;
-  const int n0 = blockIdx.x * 16 * NB;
+  int tile, split;
+  i8_place(a, tile, split);
+  const int n0 = tile * 16 * NB;
+  if (n0 >= a.N) return;                  // the grid's padding
 
-  const int steps = (a.K + 127) / 128, per = (steps + kWaves - 1) / kWaves;
-  const int s0 = wave * per;
-  const int P = steps - s0 < per ? steps - s0 : per;
+  int s0, P;
+  i8_steps(a, split * kWaves + wave, a.splits * kWaves, s0, P);
   const int k0 = s0 * 128 + stream_piece(lane) * 16;
   i32x4 acc[SH::kBlocks];
 #pragma unroll
@@ -65,82 +157,258 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_kernel(I8Args a) {
         src[t] = a.A + (size_t)r * a.K + k0;
       }
     }
-    stream_tile<NB, MB, R>(lds + wave * SH::S::kRing, src, a.K - k0, P, acc);
+    stream_tile<NB, AP, R>(lds + wave * SH::S::kRing, src, a.K - k0, P, acc);
   }
   stream_settle(acc);
 
-  // Sum i of block q from wavefront w at sums[((w * kBlocks + q) * 64 + lane)][i].
+  // Wavefront w's block q at sums[(w * kBlocks + q) * 64 + lane]; wavefront w adds
+  // up blocks w, w + 4, ...
   i32x4* sums = reinterpret_cast<i32x4*>(lds);
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < SH::kBlocks; ++q) sums[(wave * SH::kBlocks + q) * kWave + lane] = acc[q];
   __syncthreads();
+  constexpr int NV = (SH::kBlocks + kWaves - 1) / kWaves;
+  i32x4 v[NV];
 #pragma unroll
-  for (int q0 = 0; q0 < SH::kBlocks; q0 += kWaves) {
-    const int q = q0 + wave;
-    if (q >= SH::kBlocks) break;
-    i32x4 v = sums[q * kWave + lane];
+  for (int j = 0; j < NV; ++j) {
+    const int q = wave + j * kWaves;
+    v[j] = i32x4{0, 0, 0, 0};
+    if (q < SH::kBlocks) {
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) v += sums[(w * SH::kBlocks + q) * kWave + lane];
-    const int n = n0 + 16 * (q / MB) + l16;
-    if (n >= a.N) continue;
-    const float sw = a.w_scale[n];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = 16 * (q % MB) + 4 * g + i;
-      if (m >= a.M) continue;
-      const int sum = v[i];
-      // int32 to fp32 rounds a sum past 2^24 by half a step of fp32.
-      const float c = (float)sum * a.a_scale[m] * sw;
-      const size_t at = (size_t)m * a.N + n;
-      if (a.f32)
-        static_cast<float*>(a.C)[at] = c;
-      else
-        static_cast<__bf16*>(a.C)[at] = static_cast<__bf16>(c);
+      for (int w = 0; w < kWaves; ++w) v[j] += sums[(w * SH::kBlocks + q) * kWave + lane];
     }
   }
+  if (a.splits > 1 && !i8_join(a, v, tile, split, SH::kBlocks, wave, kWaves, &last)) return;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int q = wave + j * kWaves;
+    if (q < SH::kBlocks) i8_store(a, v[j], q % MB, n0 + 16 * (q / MB) + l16, g);
+  }
+#endif
+}
+
+// A step's slot of the panel kernel: the panel's pieces, one to a wavefront, then
+// each wavefront's 2*NB pieces of W.
+constexpr int kPanelWaves = 8;
+template <int AP, int NB, int R>
+struct I8Panel {
+  static constexpr int MB = (AP + 1) / 2;
+  static constexpr int kPP = 68;
+  static constexpr int kSlot = (2 * MB + 2 * NB * kPanelWaves) * kPP;
+  static constexpr int lds_bytes = R * kSlot * 16;
+  static constexpr bool valid =
+      R >= 2 && (R - 1) * (1 + 2 * NB) <= 63 && lds_bytes <= 160 * 1024 - 64;
+  static_assert(AP <= kPanelWaves, "a piece to a wavefront");
+  
+};
+
+// The loop of one wavefront; MINE: whether it loads a piece of the panel (its
+// waits count that load too).
+template <int AP, int NB, int R, bool MINE>
+__device__ __forceinline__ void i8_panel_loop(const I8Args& a, u32x4* lds, int n0, int P,
+                                              i32x4 (&acc)[NB * ((AP + 1) / 2)]) {
+  using SH = I8Panel<AP, NB, R>;
+  constexpr int G = 2 * NB + (MINE ? 1 : 0), kPP = SH::kPP, MB = SH::MB;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int g = lane >> 4, l16 = lane & 15;
+  const int k0 = stream_piece(lane) * 16, left = a.K - k0;
+  const int line = __builtin_amdgcn_readfirstlane(left);
+  const int my_w = (2 * MB + wave * 2 * NB) * kPP;       // within a slot
+  const uint8_t* src[G];
+#pragma unroll
+  for (int t = 0; t < G; ++t) {
+    if (t < 2 * NB) {
+      const int r = n0 + 8 * t + stream_row(lane);
+      src[t] = a.W + (size_t)(r < a.N ? r : a.N - 1) * a.K + k0;
+    } else {
+      const int r = 8 * wave + stream_row(lane);
+      src[t] = a.A + (size_t)(r < a.M ? r : a.M - 1) * a.K + k0;
+    }
+  }
+  int rpos[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    rpos[c] = (l16 >> 3) * kPP + (l16 & 7) * 8 + ((4 * c + g + ((l16 & 7) >> 1)) & 7);
+
+  auto issue = [&](u32x4* slot, int p) {
+    const int at = p * 128;
+    const bool whole = line - at >= 128;
+    static_for<G>([&](auto t_c) {
+      constexpr int t = decltype(t_c)::value;
+      u32x4* to = slot + (t < 2 * NB ? my_w + t * kPP : wave * kPP);
+      const uint8_t* from = src[t] + at;
+      if (!whole) from = left - at >= 16 ? from : reinterpret_cast<const uint8_t*>(&kZeroPiece);
+      __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, 0,
+                                       t < 2 * NB ? kStreamAux : 0);
+    });
+    pin_issue();
+  };
+  auto multiply = [&](const u32x4* slot) {
+    u32x4 v[2 * (NB + MB)];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        v[c * (NB + MB) + j] = lds_read_opaque(slot + my_w + 2 * j * kPP + rpos[c]);
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+        v[c * (NB + MB) + NB + b] = lds_read_opaque(slot + 2 * b * kPP + rpos[c]);
+    }
+    lds_wait(v);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+          acc[j * MB + b] =
+              stream_mfma(v[c * (NB + MB) + NB + b], v[c * (NB + MB) + j], acc[j * MB + b]);
+  };
+  u32x4* const end = lds + R * SH::kSlot;
+  u32x4 *fill = lds, *use = lds;
+  auto next = [&](u32x4* s) { return s + SH::kSlot == end ? lds : s + SH::kSlot; };
+  for (int p = 0; p < R - 1 && p < P; ++p) {
+    issue(fill, p);
+    fill = next(fill);
+  }
+  int p = 0;
+  for (; p + R - 1 < P; ++p) {
+    wait_vmcnt<(R - 2) * G>();
+    // Every wavefront's loads of step p have landed, and every wavefront's reads
+    // of step p-1, whose slot is filled next, have completed (lds_wait).  Every
+    // wavefront passes P barriers.
+    barrier_keep_loads();
+    issue(fill, p + R - 1);
+    fill = next(fill);
+    multiply(use);
+    use = next(use);
+  }
+  static_for<R - 1>([&](auto i_c) {
+    constexpr int younger = R - 2 - decltype(i_c)::value;
+    if (P - p == younger + 1) {
+      wait_vmcnt<younger * G>();
+      barrier_keep_loads();
+      multiply(use);
+      use = next(use);
+      ++p;
+    }
+  });
+}
+
+template <int AP, int NB, int R>
+__global__ __launch_bounds__(kPanelWaves* kWave) void gemm_i8_panel_kernel(I8Args a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  using SH = I8Panel<AP, NB, R>;
+  constexpr int MB = SH::MB;
+  __shared__ u32x4 lds[R * SH::kSlot];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int n0 = ((int)blockIdx.x * kPanelWaves + wave) * 16 * NB;
+  const int P = (a.K + 127) / 128;
+  i32x4 acc[NB * MB];
+#pragma unroll
+  for (int i = 0; i < NB * MB; ++i) acc[i] = i32x4{0, 0, 0, 0};
+  if (wave < AP)
+    i8_panel_loop<AP, NB, R, true>(a, lds, n0, P, acc);
+  else
+    i8_panel_loop<AP, NB, R, false>(a, lds, n0, P, acc);
+  stream_settle(acc);
+#pragma unroll
+  for (int q = 0; q < NB * MB; ++q)
+    i8_store(a, acc[q], q % MB, n0 + 16 * (q / MB) + (lane & 15), lane >> 4);
 #endif
 }
 
 namespace {
 
-template <int MB, int NB>
-const void* kernel_of() {
-  constexpr int R = I8Shape<MB, NB, 4>::valid ? 4 : I8Shape<MB, NB, 3>::valid ? 3 : 2;
-  static_assert(I8Shape<MB, NB, R>::valid, "the ring fits");
-  return reinterpret_cast<const void*>(&gemm_i8_kernel<MB, NB, R>);
+// The deepest ring, up to R slots, that LDS and the wait counter allow.
+template <int AP, int NB, int R>
+constexpr int stretch_ring() {
+  if constexpr (I8Shape<AP, NB, R>::valid) return R;
+  else return stretch_ring<AP, NB, R - 1>();
 }
-const void* pick_kernel(int MB, int NB) {
-  static const void* const table[4][4] = {
-      {kernel_of<1, 1>(), kernel_of<1, 2>(), kernel_of<1, 3>(), kernel_of<1, 4>()},
-      {kernel_of<2, 1>(), kernel_of<2, 2>(), kernel_of<2, 3>(), kernel_of<2, 4>()},
-      {kernel_of<3, 1>(), kernel_of<3, 2>(), kernel_of<3, 3>(), kernel_of<3, 4>()},
-      {kernel_of<4, 1>(), kernel_of<4, 2>(), kernel_of<4, 3>(), kernel_of<4, 4>()}};
-  return table[MB - 1][NB - 1];
+template <int AP, int NB>
+const void* stretch_of() {
+  return reinterpret_cast<const void*>(&gemm_i8_stretch_kernel<AP, NB, stretch_ring<AP, NB, 4>()>);
+}
+template <int AP, int NB>
+const void* panel_of() {
+  static_assert(I8Panel<AP, NB, 3>::valid, "the ring fits");
+  return reinterpret_cast<const void*>(&gemm_i8_panel_kernel<AP, NB, 3>);
 }
 
-// The width of 16..64 weight rows whose workgroups load the fewest rows in all:
-// rounds of 256 workgroups (one per CU) times a step's rows.
-int pick_width(int M, int N) {
-  const int act = (M + 15) / 16;
-  int best = 1;
-  long best_cost = 0;
-  for (int nb = 1; nb <= 4; ++nb) {
-    const long tiles = ((long)N + 16 * nb - 1) / (16 * nb);
-    const long cost = (tiles + 255) / 256 * (act + nb);
-    if (nb == 1 || cost < best_cost) {
-      best = nb;
-      best_cost = cost;
-    }
-  }
-  return best;
+struct I8Plan {
+  bool panel;
+  int NB, splits;
+  int width() const { return (panel ? 16 * kPanelWaves : 16) * NB; }
+  int tiles(int N) const { return (int)(((int64_t)N + width() - 1) / width()); }
+};
+
+const void* i8_kernel(int MB, const I8Plan& p) {
+  static const void* const stretch[4][4] = {
+      {stretch_of<2, 1>(), stretch_of<2, 2>(), stretch_of<2, 3>(), stretch_of<2, 4>()},
+      {stretch_of<4, 1>(), stretch_of<4, 2>(), stretch_of<4, 3>(), stretch_of<4, 4>()},
+      {stretch_of<6, 1>(), stretch_of<6, 2>(), stretch_of<6, 3>(), stretch_of<6, 4>()},
+      {stretch_of<8, 1>(), stretch_of<8, 2>(), stretch_of<8, 3>(), stretch_of<8, 4>()}};
+  static const void* const panel[3][2] = {{panel_of<4, 1>(), panel_of<4, 2>()},
+                                          {panel_of<6, 1>(), panel_of<6, 2>()},
+                                          {panel_of<8, 1>(), panel_of<8, 2>()}};
+  return p.panel ? panel[MB - 2][p.NB - 1] : stretch[MB - 1][p.NB - 1];
 }
 
 constexpr int64_t kI8MaxK = 131056;   // 128 * 128 * K stays below 2^31
+// What a split launch may use of the workspace: counter lines, one for each
+// tile, and blocks of 16 x 16 partial sums.
+constexpr int kI8MaxTiles = LOWM_I8_STATUS_N / 16;
+constexpr long kI8MaxBlocks = 8192;
+constexpr size_t kI8LineBytes = 256 * (size_t)kI8MaxTiles;
+constexpr size_t kI8SlotBytes = (size_t)kI8MaxBlocks * kWave * 4 * 4;
+
+// How to cut the product.  Measured on MI355X, W from HBM, us a call:
+//   - above 16 rows and 16384 columns the panel kind: M 64, K 4096, N 24576 /
+//     32768 / 49152 25.7 / 33.8 / 46.4 against 30.6 / 37.9 / 56.2 for the best
+//     stretch tiles (a workgroup then loads 64 rows of A for 128 or 256 of W, not
+//     for 64); M 24, N 49152 38.6 against 41.2.  At 16 rows it loses (43.0
+//     against 37.4), at N 12288 its tiles are too few (23.8 against 16.8).  The
+//     width with the fewest rounds of 256 workgroups times rows loaded.
+//   - otherwise stretch tiles of the width, and the split of K, of least cost:
+//     rounds times bytes loaded by a workgroup, at 67 KB a us, and for a split's
+//     exchange 1 us, 0.25 a split and 0.2 a block of 16 x 16 sums sent.  M 16,
+//     N 6144, K 4096 NB 2 7.5 us (NB 1 8.3, NB 3 8.6); M 64, N 12288, K 8192 NB 3
+//     25.2 (NB 4 29.2); M 64, N 1536, K 8192 NB 1 in two splits 10.9 (whole 13.2);
+//     M 23, N 2304, K 12288 NB 2 in three 11.4 (NB 1 whole 12.5); M 64, N 4096,
+//     K 4096 NB 1 whole 9.2 (two splits 16.3).
+I8Plan i8_plan(int M, int N, int K, bool split) {
+  const int MB = (M + 15) / 16;
+  if (M > 16 && N > 16384) {
+    const I8Plan one{true, 1, 1}, two{true, 2, 1};
+    auto cost = [&](const I8Plan& p) {
+      return (int64_t)(p.tiles(N) + 255) / 256 * (16 * MB + p.width());
+    };
+    return cost(two) < cost(one) ? two : one;
+  }
+  I8Plan best{false, 1, 1};
+  double best_us = 0;
+  for (int nb = 1; nb <= 4; ++nb)
+    for (int s = 1; s <= (split ? kI8MaxSplits : 1); ++s) {
+      const I8Plan p{false, nb, s};
+      const int64_t tiles = p.tiles(N);
+      if (s > 1 && (tiles > kI8MaxTiles || tiles * s * nb * MB > kI8MaxBlocks)) continue;
+      if (s > 1 && K / s < 128 * kWaves) continue;       // a step for every wavefront
+      const double us = (double)((tiles * s + 255) / 256) * (16 * (MB + nb)) * K / s / 67.0e3 +
+                        (s > 1 ? 1.0 + 0.25 * s + 0.2 * (nb * MB) * (s - 1) : 0.0);
+      if ((nb == 1 && s == 1) || us < best_us) {
+        best = p;
+        best_us = us;
+      }
+    }
+  return best;
+}
 
 size_t i8_workspace(int M, int N, int K) {
-  if (M < 1 || M > LOWM_MAX_M || N < 1 || K < 1 || K % 16 || K > LOWM_QUANTIZE_MAX_K) return 0;
-  return ((size_t)M * K + 255) / 256 * 256 + LOWM_MAX_M * sizeof(float);
+  if (M < 1 || M > LOWM_MAX_M || N < 1 || K < 1 || K % 16 || K > kI8MaxK) return 0;
+  return kI8LineBytes + kI8SlotBytes + ((size_t)M * K + 255) / 256 * 256 +
+         LOWM_MAX_M * sizeof(float);
 }
 
 int gemm_i8(const lowm_gemm_i8_args* u, hipStream_t stream) {
@@ -152,10 +420,10 @@ int gemm_i8(const lowm_gemm_i8_args* u, hipStream_t stream) {
     return LOWM_ERR_INVALID_ARG;
   if (u->M > LOWM_MAX_M || u->K % 16 || u->K > (quantised ? kI8MaxK : LOWM_QUANTIZE_MAX_K))
     return LOWM_ERR_UNSUPPORTED;
-  const size_t need = quantised ? 0 : i8_workspace(u->M, u->N, u->K);
-  if (need && (!u->workspace || u->workspace_bytes < need)) return LOWM_ERR_WORKSPACE;
+  const size_t need = i8_workspace(u->M, u->N, u->K);
+  if (u->workspace ? u->workspace_bytes < need : !quantised) return LOWM_ERR_WORKSPACE;
   const int cb = type_bytes(u->c_type), ab = type_bytes(u->a_type);
-  if ((((uintptr_t)u->A | (uintptr_t)u->W | (need ? (uintptr_t)u->workspace : 0)) & 15) ||
+  if ((((uintptr_t)u->A | (uintptr_t)u->W) & 15) || ((uintptr_t)u->workspace & 255) ||
       ((uintptr_t)u->C & (cb - 1)) || ((uintptr_t)u->w_scale & 3) ||
       (quantised && ((uintptr_t)u->a_scale & 3)))
     return LOWM_ERR_UNSUPPORTED;
@@ -164,26 +432,40 @@ int gemm_i8(const lowm_gemm_i8_args* u, hipStream_t stream) {
                      span_of(u->w_scale, 1, N, N, 4),
                      span_of(quantised ? u->a_scale : nullptr, 1, M, M, 4)};
   const Span c = span_of(u->C, M, N, N, cb),
-             ws = span_of(need ? u->workspace : nullptr, 1, (int64_t)need, (int64_t)need, 1);
+             ws = span_of(u->workspace, 1, (int64_t)need, (int64_t)need, 1);
   for (const Span& s : in)
     if (meet(c, s) || meet(ws, s)) return LOWM_ERR_INVALID_ARG;
   if (meet(c, ws)) return LOWM_ERR_INVALID_ARG;
 
-  I8Args a{static_cast<const uint8_t*>(u->A), static_cast<const uint8_t*>(u->W), u->a_scale,
-           u->w_scale, u->C, u->M, u->N, u->K, u->c_type == LOWM_F32};
+  I8Args a{};
+  a.A = static_cast<const uint8_t*>(u->A);
+  a.W = static_cast<const uint8_t*>(u->W);
+  a.a_scale = u->a_scale;
+  a.w_scale = u->w_scale;
+  a.C = u->C;
+  a.M = u->M;
+  a.N = u->N;
+  a.K = u->K;
+  a.f32 = u->c_type == LOWM_F32;
+  uint8_t* w = static_cast<uint8_t*>(u->workspace);
   if (!quantised) {
-    uint8_t* q = static_cast<uint8_t*>(u->workspace);
-    float* s = reinterpret_cast<float*>(q + (need - LOWM_MAX_M * sizeof(float)));
+    uint8_t* q = w + kI8LineBytes + kI8SlotBytes;
+    float* s = reinterpret_cast<float*>(w + need - LOWM_MAX_M * sizeof(float));
     const int rc = quantize_rows(u->A, LOWM_BF16, K, u->M, u->K, q, s, stream);
     if (rc != LOWM_OK) return rc;
     a.A = q;
     a.a_scale = s;
   }
-  const int NB = pick_width(u->M, u->N);
+  const I8Plan p = i8_plan(u->M, u->N, u->K, w != nullptr);
+  a.splits = p.splits;
+  a.lines = reinterpret_cast<uint32_t*>(w);
+  a.slots = reinterpret_cast<uint32_t*>(w + (w ? kI8LineBytes : 0));
+  const size_t tiles = (size_t)p.tiles(u->N);
+  const size_t grid = p.panel ? tiles : (tiles + kXcds - 1) / kXcds * kXcds * p.splits;
   void* args[] = {&a};
-  return launched(hipLaunchKernel(pick_kernel((u->M + 15) / 16, NB),
-                                  dim3((unsigned)((N + 16 * NB - 1) / (16 * NB))), dim3(kThreads),
-                                  args, 0, stream));
+  return launched(hipLaunchKernel(i8_kernel((u->M + 15) / 16, p), dim3((unsigned)grid),
+                                  dim3(p.panel ? kPanelWaves * kWave : kThreads), args, 0,
+                                  stream));
 }
 
 }  // namespace

@@ -4,8 +4,8 @@
 // With few tokens the layer is a stream of weights: every expert that some
 // token chose is read once, 6 D I bytes, against a few rows of activations.
 // Three kernels:
-//   route  l = x router^T by tiles of 16 experts and 16 tokens; the last workgroup
-//          to arrive picks each token's experts and sorts the (token, expert)
+//   route  l = x router^T by tiles of 16 experts and 16 tokens (and, with few of
+//          those, stretches of D); the last workgroup to arrive picks each token's experts and sorts the (token, expert)
 //          pairs by expert into segments of up to 16 rows, the matrix
 //          instructions' height;
 //   up     one workgroup per segment and 16 columns of h: 16 gate and 16 up rows;
@@ -25,6 +25,8 @@ constexpr int kMaxK = LOWM_MOE_MAX_K;
 constexpr int kSegRows = 16;
 constexpr int kCols = 16;                 // columns of h, and of the output, per workgroup
 constexpr int kMaxDownSplits = 8;
+constexpr int kRouteWaves = 16;
+constexpr int kRouteThreads = kRouteWaves * kWave;
 constexpr int kMaxSize = 65536;
 
 struct Segment {
@@ -41,19 +43,27 @@ struct Pair {
 // finds another size's leavings where its zeros have to be.
 constexpr size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 constexpr size_t kCounterBytes = 256 * (1 + (size_t)kMaxSize / kCols);
-constexpr size_t kRouteSlots = (size_t)kMaxT * kMaxE;
+constexpr int kMaxRouteSplits = 4;
+constexpr size_t kRouteSlots = kMaxRouteSplits * (size_t)kMaxT * kMaxE;
 constexpr size_t kDownSlots = 512 * (size_t)kMaxT * kCols;       // most tiles * splits, times the tile
 constexpr size_t kRouteAt = kCounterBytes;
 constexpr size_t kDownAt = kRouteAt + 4 * kRouteSlots;
 constexpr size_t kListsAt = kDownAt + 4 * kDownSlots;
 
 struct Layout {
-  int down_splits, max_segments;
+  int route_splits, down_splits, max_segments;
   size_t pairs, h, bytes;
 };
 
 static Layout layout_of(int T, int D, int I, int E, int K) {
   Layout l{};
+  // Router: a tile's weights come from far and slowly to one CU, so few tiles
+  // are cut along D: up to 32 workgroups, a step at least for each wavefront.
+  const int router_tiles = ((E + 15) / 16) * ((T + 15) / 16), steps = (2 * D + 127) / 128;
+  l.route_splits = 1;
+  while (l.route_splits < kMaxRouteSplits && router_tiles * l.route_splits * 2 <= 32 &&
+         steps >= 2 * l.route_splits * kRouteWaves)
+    l.route_splits *= 2;
   // Down: enough workgroups for 256 CUs (tiles * splits < 512).
   const int tiles = (D + kCols - 1) / kCols;
   l.down_splits = 1;
@@ -77,61 +87,23 @@ struct MoeArgs {
   int* ids;
   float* gates;
   uint32_t* counters;                     // [1 + tiles], 64 words apart; 0 is the router's
-  uint32_t* route_slots;                  // [T][E]
+  uint32_t* route_slots;                  // [route_splits][T][E]
   uint32_t* down_slots;                   // [tiles][down_splits][T][kCols]
   int* lists;                             // number of segments, 3 unused, then the segments
   Pair* pairs;
   uint8_t* h;                             // [T * top_k, I] bf16, in the pairs' order
   int T, D, I, E, top_k, flags;
   float routed_scale;
-  int down_splits;
+  int route_splits, down_splits;
 };
-
-// Exchange between workgroups: a slot holds the complement of an fp32 value's
-// bits, so zero means "not there yet", and each is written once per call; the
-// reader waits for it, whatever order the counter and the slots become visible
-// in.  The wait is bounded: a slot that stays zero sets the line's fault word.
-__device__ __forceinline__ float take_slot(uint32_t* slot, uint32_t w, uint32_t* line) {
-  if (w == 0u) {
-    const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
-    while ((w = load_slot(slot)) == 0u) {
-      if (__builtin_amdgcn_s_memrealtime() - t0 > kFoldPollTicks) {
-        store_slot(line + kFaultWord, 1u);
-        break;
-      }
-      __builtin_amdgcn_s_sleep(4);
-    }
-  }
-  store_slot(slot, 0u);
-  return dec_partial(w);
-}
-
-// Whether this workgroup is the last of `total` to arrive at the line; the
-// last one sets the count back to zero.
-__device__ __forceinline__ bool arrive_last(uint32_t* line, int total, int* lds) {
-  if (threadIdx.x == 0) {
-    const uint32_t before =
-        __hip_atomic_fetch_add(line, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *lds = before == (uint32_t)(total - 1);
-    if (*lds) store_slot(line, 0u);
-  }
-  __syncthreads();
-  return *lds != 0;
-}
 
 // ---------------------------------------------------------------------------
 // route
 // ---------------------------------------------------------------------------
-// 16 wavefronts cut D between them, so that a tile's few weights come in one
-// round trip and no sum has to cross workgroups.
-constexpr int kRouteWaves = 16;
-constexpr int kRouteThreads = kRouteWaves * kWave;
-struct RouteShape {
-  static constexpr int R = 2;
-  using S = StreamShape<1, 1, R>;
-  static constexpr int kRings = kRouteWaves * S::kRing * 16;
-  static_assert(kRings >= 4 * kMaxT * kMaxE, "the logits fit where the rings were");
-};
+// The wavefronts cut D between them and load their operands straight into
+// registers in the matrix layout, kRouteBatch steps at a time: there is little
+// to read and one round trip to wait for, so a ring would only add trips.
+constexpr int kRouteBatch = 4;
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
 
@@ -248,71 +220,71 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, const int (*chosen)
 
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using SH = RouteShape;
-  constexpr int G = SH::S::G;
-  __shared__ u32x4 lds[SH::kRings / 16];
+  __shared__ float logits[kMaxT * kMaxE];
   __shared__ int chosen[kMaxT][kMaxK];
   __shared__ float gates[kMaxT][kMaxK];
   __shared__ uint32_t mask[kMaxE][2];
   __shared__ uint32_t starts[kMaxE];
   __shared__ int last;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int g = lane >> 4, l16 = lane & 15;
   const int tiles = (a.E + 15) / 16;
-  const int e0 = blockIdx.x % tiles * 16, t0 = blockIdx.x / tiles * 16;
+  const int split = blockIdx.x % a.route_splits, place = blockIdx.x / a.route_splits;
+  const int e0 = place % tiles * 16, t0 = place / tiles * 16;
 
-  const int steps = (2 * a.D + 127) / 128;
-  const int s0 = steps * wave / kRouteWaves, P = steps * (wave + 1) / kRouteWaves - s0;
-  const int k0 = s0 * 128 + stream_piece(lane) * 16;
+  const int steps = (2 * a.D + 127) / 128, parts = a.route_splits * kRouteWaves;
+  const int part = split * kRouteWaves + wave;
+  const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
+  const uint8_t* w =
+      a.router + (size_t)(e0 + l16 < a.E ? e0 + l16 : a.E - 1) * a.D * 2;
+  const uint8_t* x = a.x + (size_t)(t0 + l16 < a.T ? t0 + l16 : a.T - 1) * a.D * 2;
   f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-  if (P > 0) {
-    const uint8_t* src[G];
+  for (int s = s0; s < s1; s += kRouteBatch) {
+    u32x4 wv[2 * kRouteBatch], xv[2 * kRouteBatch];
 #pragma unroll
-    for (int t = 0; t < G; ++t) {
-      int r = 8 * (t & 1) + stream_row(lane);
-      if (t < 2) {
-        r = e0 + r < a.E ? e0 + r : a.E - 1;
-        src[t] = a.router + (size_t)r * a.D * 2 + k0;
-      } else {
-        r = t0 + r < a.T ? t0 + r : a.T - 1;
-        src[t] = a.x + (size_t)r * a.D * 2 + k0;
-      }
+    for (int j = 0; j < 2 * kRouteBatch; ++j) {
+      const int k = (2 * s + j) * 64 + 16 * g;           // the lane's 16 bytes
+      const bool in = s + j / 2 < s1 && k < 2 * a.D;
+      wv[j] = xv[j] = u32x4{0u, 0u, 0u, 0u};
+      if (in) wv[j] = *reinterpret_cast<const u32x4*>(w + k);
+      if (in) xv[j] = *reinterpret_cast<const u32x4*>(x + k);
     }
-    stream_tile<1, 1, SH::R>(lds + wave * SH::S::kRing, src, 2 * a.D - k0, P, acc);
+#pragma unroll
+    for (int j = 0; j < 2 * kRouteBatch; ++j) acc[0] = mfma(xv[j], wv[j], acc[0]);
   }
   stream_settle(acc);
-  f32x4* sums = reinterpret_cast<f32x4*>(lds);
-  __syncthreads();
+  f32x4* sums = reinterpret_cast<f32x4*>(logits);
+  static_assert(sizeof(logits) >= kRouteThreads * sizeof(f32x4), "the sums fit");
   sums[wave * kWave + lane] = acc[0];
-  mask[threadIdx.x % kMaxE][threadIdx.x / kMaxE & 1] = 0u;
+  if (threadIdx.x < 2 * kMaxE) (&mask[0][0])[threadIdx.x] = 0u;
   __syncthreads();
   // Wavefront i adds row 4 g + i of lane group g, in 64 bits so that experts next
   // to the border are told apart as well as fp32 can.
   if (wave < 4) {
     double v = 0.0;
 #pragma unroll
-    for (int w = 0; w < kRouteWaves; ++w)
-      v += (double)reinterpret_cast<const float*>(sums + w * kWave + lane)[wave];
-    const int t = t0 + 4 * (lane >> 4) + wave, e = e0 + (lane & 15);
-    if (t < a.T && e < a.E) store_slot(a.route_slots + t * a.E + e, enc_partial((float)v));
+    for (int p = 0; p < kRouteWaves; ++p)
+      v += (double)reinterpret_cast<const float*>(sums + p * kWave + lane)[wave];
+    const int t = t0 + 4 * g + wave, e = e0 + l16;
+    if (t < a.T && e < a.E)
+      store_slot(a.route_slots + ((size_t)split * a.T + t) * a.E + e, enc_partial((float)v));
   }
   if (!arrive_last(a.counters, gridDim.x, &last)) return;
 
   // The last workgroup has every logit before it.
-  float* logits = reinterpret_cast<float*>(lds);
   const int cells = a.T * a.E;
-  constexpr int kAtOnce = 4;
-  for (int c0 = threadIdx.x; c0 < cells; c0 += kAtOnce * kRouteThreads) {
-    uint32_t w[kAtOnce];
+  for (int c = threadIdx.x; c < cells; c += kRouteThreads) {
+    uint32_t v[kMaxRouteSplits];
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
-      const int c = c0 + j * kRouteThreads;
-      w[j] = load_slot(a.route_slots + (c < cells ? c : c0));
-    }
+    for (int s = 0; s < kMaxRouteSplits; ++s)
+      if (s < a.route_splits) v[s] = load_slot(a.route_slots + (size_t)s * cells + c);
+    double sum = 0.0;
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
-      const int c = c0 + j * kRouteThreads;
-      if (c < cells) logits[c] = take_slot(a.route_slots + c, w[j], a.counters);
-    }
+    for (int s = 0; s < kMaxRouteSplits; ++s)
+      if (s < a.route_splits)
+        sum += (double)dec_partial(
+            take_slot(a.route_slots + (size_t)s * cells + c, v[s], a.counters));
+    logits[c] = (float)sum;
   }
   __syncthreads();
   for (int t = wave; t < a.T; t += kRouteWaves) pick_experts(a, t, logits, chosen, gates);
@@ -324,16 +296,18 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
 // ---------------------------------------------------------------------------
 // up
 // ---------------------------------------------------------------------------
+template <int R>
 struct UpShape {
-  static constexpr int R = 3;
-  using S = StreamShape<2, 1, R>;
+  using S = StreamShape<2, 2, R>;
   static constexpr int kRings = kWaves * S::kRing * 16;
 };
 
+template <int R>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int G = UpShape::S::G;
-  __shared__ u32x4 lds[UpShape::kRings / 16];
+  using SH = UpShape<R>;
+  constexpr int G = SH::S::G;
+  __shared__ u32x4 lds[SH::kRings / 16];
   const int tiles = (a.I + kCols - 1) / kCols;
   const int seg = blockIdx.x / tiles, i0 = blockIdx.x % tiles * kCols;
   if (seg >= a.lists[0]) return;
@@ -359,7 +333,7 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
         src[t] = a.x + (size_t)a.pairs[s.first + r].token * a.D * 2 + k0;
       }
     }
-    stream_tile<2, 1, UpShape::R>(lds + wave * UpShape::S::kRing, src, 2 * a.D - k0, P, acc);
+    stream_tile<2, 2, R>(lds + wave * SH::S::kRing, src, 2 * a.D - k0, P, acc);
   }
   stream_settle(acc);
   f32x4* sums = reinterpret_cast<f32x4*>(lds);
@@ -384,9 +358,9 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
 // ---------------------------------------------------------------------------
 // down
 // ---------------------------------------------------------------------------
+template <int R>
 struct DownShape {
-  static constexpr int R = 6;
-  using S = StreamShape<1, 1, R>;
+  using S = StreamShape<1, 2, R>;
   static constexpr int kRings = kWaves * S::kRing * 16;
 };
 
@@ -405,12 +379,13 @@ __device__ __forceinline__ void lds_add_opaque(float* p, float v) {
 }
 
 // The segments' steps as one sequence: step q is step q mod n of segment q / n.
+template <int R>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using S = DownShape::S;
-  constexpr int R = DownShape::R, G = S::G, kPP = S::kPP;
+  using S = typename DownShape<R>::S;
+  constexpr int G = S::G, kPP = S::kPP;
   extern __shared__ u32x4 dyn[];
-  __shared__ u32x4 rings[DownShape::kRings / 16];
+  __shared__ u32x4 rings[DownShape<R>::kRings / 16];
   __shared__ int last;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int g = lane >> 4, l16 = lane & 15;
@@ -593,7 +568,8 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
 #pragma unroll
         for (int r = 0; r < kMaxDownSplits; ++r)
           if (r < a.down_splits) {
-            const float part_sum = take_slot(slots + (size_t)r * cells + c, w[r], line);
+            const float part_sum =
+                dec_partial(take_slot(slots + (size_t)r * cells + c, w[r], line));
             sum = r == 0 ? part_sum : sum + part_sum;
           }
         v[j] = sum;
@@ -666,21 +642,25 @@ int moe(const lowm_moe_args* u, hipStream_t stream) {
   a.top_k = K;
   a.flags = u->flags;
   a.routed_scale = u->routed_scale;
+  a.route_splits = l.route_splits;
   a.down_splits = l.down_splits;
   void* args[] = {&a};
   auto go = [&](const void* fn, size_t grid, size_t lds, int threads = kThreads) {
     return launched(hipLaunchKernel(fn, dim3((unsigned)grid), dim3(threads), args, lds, stream));
   };
   int rc = go(reinterpret_cast<const void*>(&moe_route_kernel),
-              (size_t)((E + 15) / 16) * ((T + 15) / 16), 0, kRouteThreads);
+              (size_t)((E + 15) / 16) * ((T + 15) / 16) * l.route_splits, 0, kRouteThreads);
+  const size_t up_grid = (size_t)l.max_segments * ((I + kCols - 1) / kCols);
   if (rc == LOWM_OK)
-    rc = go(reinterpret_cast<const void*>(&moe_up_kernel),
-            (size_t)l.max_segments * ((I + kCols - 1) / kCols), 0);
+    rc = go(up_grid <= 256 ? reinterpret_cast<const void*>(&moe_up_kernel<6>)
+                           : reinterpret_cast<const void*>(&moe_up_kernel<3>),
+            up_grid, 0);
   const size_t lds = sizeof(Segment) * (size_t)l.max_segments +
                      sizeof(Pair) * (size_t)((T * K + 1) / 2 * 2) +
                      sizeof(float) * kWaves * (size_t)T * kCols;
   if (rc == LOWM_OK)
-    rc = go(reinterpret_cast<const void*>(&moe_down_kernel),
+    rc = go(T <= 16 ? reinterpret_cast<const void*>(&moe_down_kernel<8>)
+                    : reinterpret_cast<const void*>(&moe_down_kernel<6>),
             (size_t)((D + kCols - 1) / kCols) * l.down_splits, lds);
   return rc;
 }

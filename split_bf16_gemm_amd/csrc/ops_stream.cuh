@@ -39,14 +39,17 @@ __device__ __forceinline__ void stream_settle(i32x4 (&acc)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+a"(acc[i]));
 }
 
-// NB blocks of 16 weight rows, MB blocks of 16 activation rows, R ring slots.
-template <int NB, int MB, int R>
+// NB blocks of 16 weight rows, AP pieces of 8 activation rows, R ring slots.
+template <int NB, int AP, int R>
 struct StreamShape {
+  static constexpr int MB = (AP + 1) / 2;        // blocks of 16 activation rows
   static constexpr int kPP = 68;                 // u32x4 per piece of 8 rows (1088 B)
-  static constexpr int G = 2 * (NB + MB);        // pieces, and loads, per step
-  static constexpr int kSlot = G * kPP;          // u32x4 per slot
+  static constexpr int G = 2 * NB + AP;          // pieces, and loads, per step
+  // An odd last piece leaves the upper half of its block unwritten: rows whose
+  // results nobody takes.
+  static constexpr int kSlot = (2 * NB + 2 * MB) * kPP;   // u32x4 per slot
   static constexpr int kRing = R * kSlot;        // u32x4 per wavefront
-  static_assert(R >= 2 && (R - 1) * G <= 63, "the wait counter is 6 bits");
+  static constexpr bool valid = R >= 2 && (R - 1) * G <= 63;   // the wait counter is 6 bits
 };
 
 // Lane's row within a piece of 8 and its 16-byte piece of the row's line.
@@ -58,11 +61,13 @@ __device__ __forceinline__ int stream_piece(int lane) { return ((lane & 7) - (la
 // weight rows, then activation rows); left: bytes from there to the row's end,
 // the same for every t.  Every address up to the row's end must be readable;
 // none past it is read.
-template <int NB, int MB, int R, typename Acc>
-__device__ __forceinline__ void stream_tile(u32x4* ring, const uint8_t* (&src)[2 * (NB + MB)],
-                                            int left, int P, Acc (&acc)[NB * MB]) {
-  using SH = StreamShape<NB, MB, R>;
-  constexpr int G = SH::G, kPP = SH::kPP;
+template <int NB, int AP, int R, typename Acc>
+__device__ __forceinline__ void stream_tile(u32x4* ring, const uint8_t* (&src)[2 * NB + AP],
+                                            int left, int P,
+                                            Acc (&acc)[NB * ((AP + 1) / 2)]) {
+  using SH = StreamShape<NB, AP, R>;
+  static_assert(SH::valid, "a ring the waits can count");
+  constexpr int G = SH::G, kPP = SH::kPP, MB = SH::MB;
   const int lane = threadIdx.x & (kWave - 1);
   const int g = lane >> 4, l16 = lane & 15;
   // Lane 7 of each 8-row piece's row 0 holds the line's last 16 bytes: a step is
@@ -128,6 +133,39 @@ __device__ __forceinline__ void stream_tile(u32x4* ring, const uint8_t* (&src)[2
       ++p;
     }
   });
+}
+
+// Exchange between workgroups.  A slot is a word that is zero until its owner
+// writes it, once in a call, with a word that is not (an fp32 value's complement,
+// a biased integer); the reader waits for it, whatever order the counter and the
+// slots become visible in, and sets it back to zero.  The wait is bounded: a slot
+// that stays zero sets the counter line's fault word.
+__device__ __forceinline__ uint32_t take_slot(uint32_t* slot, uint32_t w, uint32_t* line) {
+  if (w == 0u) {
+    const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
+    while ((w = load_slot(slot)) == 0u) {
+      if (__builtin_amdgcn_s_memrealtime() - t0 > kFoldPollTicks) {
+        store_slot(line + kFaultWord, 1u);
+        break;
+      }
+      __builtin_amdgcn_s_sleep(4);
+    }
+  }
+  store_slot(slot, 0u);
+  return w;
+}
+
+// Whether this workgroup is the last of `total` to arrive at the line; the
+// last one sets the count back to zero.
+__device__ __forceinline__ bool arrive_last(uint32_t* line, int total, int* lds) {
+  if (threadIdx.x == 0) {
+    const uint32_t before =
+        __hip_atomic_fetch_add(line, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *lds = before == (uint32_t)(total - 1);
+    if (*lds) store_slot(line, 0u);
+  }
+  __syncthreads();
+  return *lds != 0;
 }
 
 }  // namespace lowm

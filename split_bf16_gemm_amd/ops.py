@@ -10,6 +10,7 @@ fallback: when the library is not built, or a call fails, this raises.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -24,34 +25,47 @@ MOE_SIGMOID, MOE_NO_RENORM = 1, 2
 _vp, _i, _l, _f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 
+def _layout(fields):
+    """(ctypes.Structure's fields, struct format) of an argument struct of lowm_ops.h; a call
+    packs its values in one go, which costs a fraction of setting a Structure's fields."""
+    codes = {_vp: "P", _i: "i", _l: "q", _f: "f", ctypes.c_size_t: "N"}
+    names = [(n, t) for types, t in fields for n in types.split()]
+    # "0P": the size is rounded up to the struct's alignment, as in C
+    form = struct.Struct("@" + "".join(codes[t] for _, t in names) + "0P")
+    return names, form
+
+
+_size = ctypes.c_size_t
+_NORM_FIELDS, _NORM = _layout((
+    ("y r r_out x x_scale w_post w_pre gate", _vp),
+    ("ld_y ld_r ld_r_out ld_x gate_row gate_col", _l),
+    ("M D y_type r_type w_type gate_type x_type flags", _i),
+    ("residual_scale branch_scale eps", _f)))
+_I8_FIELDS, _I8 = _layout((
+    ("A W a_scale w_scale C workspace", _vp), ("workspace_bytes", _size),
+    ("M N K a_type c_type", _i)))
+_MOE_FIELDS, _MOE = _layout((
+    ("x router bias w13 w2 out ids gates workspace", _vp), ("workspace_bytes", _size),
+    ("T D I E top_k flags", _i), ("routed_scale", _f)))
+_LOGPROBS_FIELDS, _LOGPROBS = _layout((
+    ("logits tokens logprob entropy rank top_logprob top_id workspace", _vp),
+    ("workspace_bytes", _size), ("ld", _l), ("M V top_n logits_type tokens_bytes", _i)))
+
+
 class ResidualNormArgs(ctypes.Structure):
-    _fields_ = [("y", _vp), ("r", _vp), ("r_out", _vp), ("x", _vp), ("x_scale", _vp),
-                ("w_post", _vp), ("w_pre", _vp), ("gate", _vp),
-                ("ld_y", _l), ("ld_r", _l), ("ld_r_out", _l), ("ld_x", _l),
-                ("gate_row", _l), ("gate_col", _l), ("M", _i), ("D", _i),
-                ("y_type", _i), ("r_type", _i), ("w_type", _i), ("gate_type", _i),
-                ("x_type", _i), ("flags", _i),
-                ("residual_scale", _f), ("branch_scale", _f), ("eps", _f)]
+    _fields_ = _NORM_FIELDS
 
 
 class GemmI8Args(ctypes.Structure):
-    _fields_ = [("A", _vp), ("W", _vp), ("a_scale", _vp), ("w_scale", _vp), ("C", _vp),
-                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("M", _i), ("N", _i),
-                ("K", _i), ("a_type", _i), ("c_type", _i)]
+    _fields_ = _I8_FIELDS
 
 
 class MoeArgs(ctypes.Structure):
-    _fields_ = [("x", _vp), ("router", _vp), ("bias", _vp), ("w13", _vp), ("w2", _vp),
-                ("out", _vp), ("ids", _vp), ("gates", _vp), ("workspace", _vp),
-                ("workspace_bytes", ctypes.c_size_t), ("T", _i), ("D", _i), ("I", _i),
-                ("E", _i), ("top_k", _i), ("flags", _i), ("routed_scale", _f)]
+    _fields_ = _MOE_FIELDS
 
 
 class TokenLogprobsArgs(ctypes.Structure):
-    _fields_ = [("logits", _vp), ("tokens", _vp), ("logprob", _vp), ("entropy", _vp),
-                ("rank", _vp), ("top_logprob", _vp), ("top_id", _vp), ("workspace", _vp),
-                ("workspace_bytes", ctypes.c_size_t), ("ld", _l), ("M", _i), ("V", _i),
-                ("top_n", _i), ("logits_type", _i), ("tokens_bytes", _i)]
+    _fields_ = _LOGPROBS_FIELDS
 
 
 _lib = None
@@ -80,7 +94,7 @@ def library() -> binding.Library:
 
 def _stream(stream, device) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream
 
 
@@ -103,35 +117,59 @@ def _need(ok: bool, what: str, error=ValueError):
         raise error(what)
 
 
-def _rows(name: str, t: torch.Tensor, shape, types) -> int:
-    """The row pitch of a GPU tensor [M, D] with contiguous rows."""
-    if t.dtype not in types:
+_REAL = {torch.bfloat16: BF16, torch.float32: F32}
+_ONLY = {t: {t: c} for t, c in _TYPES.items()}
+
+
+def _rows(name: str, t: torch.Tensor, shape, types):
+    """(row pitch, type code) of a GPU tensor [M, D] with contiguous rows."""
+    code = types.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be one of {[str(x) for x in types]}, not {t.dtype}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape and tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
-    m, d = t.shape
+    if t.shape != shape or len(shape) != 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     sm, sd = t.stride()
+    m, d = shape
     if sd != 1 and d > 1:
         raise ValueError(f"{name} must have contiguous rows (stride {sd})")
-    return sm if m > 1 and sm >= d else _pitch(name, m, d, sm)
+    if sm < d:
+        if m > 1:
+            raise ValueError(f"{name}'s rows overlap (row stride {sm} of {d} elements)")
+        sm = d
+    return sm, code
 
 
-def _pitch(name, m, d, sm) -> int:
-    if m > 1 and sm < d:
-        raise ValueError(f"{name}'s rows overlap (row stride {sm} of {d} elements)")
-    return d
-
-
-def _dense(name: str, t: torch.Tensor, shape, dtype, device=None):
+def _dense(name: str, t: torch.Tensor, shape, dtype) -> int:
+    """The address of a contiguous GPU tensor of this shape and type."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+    if t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous GPU tensor of shape {tuple(shape)}")
+    return t.data_ptr()
 
 
-_REAL = (torch.bfloat16, torch.float32)
+def _gate(gate: torch.Tensor, M: int, D: int):
+    """(address, type code, row stride, column stride) of a gate [D], [M, 1] or [M, D]."""
+    code = _REAL.get(gate.dtype)
+    _need(code is not None, "gate must be bf16 or fp32", TypeError)
+    _need(gate.is_cuda, "gate must be on the GPU")
+    shape = gate.shape
+    if len(shape) == 1 and shape[0] == D:
+        row, col = 0, gate.stride(0)
+    elif len(shape) == 2 and shape[0] in (1, M) and shape[1] in (1, D):
+        row, col = gate.stride()
+        if shape[0] == 1:
+            row = 0
+        if shape[1] == 1:
+            col = 0
+    else:
+        raise ValueError(f"gate has shape {tuple(shape)}: not [{D}], [{M}, 1] or [{M}, {D}]")
+    if D == 1:
+        col = 0
+    _need(col in (0, 1) and row >= 0, "gate must have contiguous rows")
+    return gate.data_ptr(), code, row, col
 
 
 def residual_norm(y: torch.Tensor, residual: torch.Tensor, *, post_norm: bool = True,
@@ -153,66 +191,51 @@ def residual_norm(y: torch.Tensor, residual: torch.Tensor, *, post_norm: bool = 
     ``quantize`` int8 rows with fp32 ``scale`` [M] (else None), as gemm_i8 takes
     them.  gate: [D], [M, 1] or [M, D].  norm: root mean square, or with
     ``center`` also the mean taken off."""
-    ld_r = _rows("residual", residual, None, _REAL)
-    shape = residual.shape
-    ld_y = _rows("y", y, shape, _REAL)
+    lib = (_lib or library()).lib
+    shape, dev = residual.shape, residual.device
+    ld_r, r_type = _rows("residual", residual, shape, _REAL)
+    ld_y, y_type = _rows("y", y, shape, _REAL)
     M, D = shape
-    dev = residual.device
     if residual_out is None:
         residual_out = _empty(shape, residual.dtype, dev, stream)
+    ld_r_out, _ = _rows("residual_out", residual_out, shape, _ONLY[residual.dtype])
     flags = (NORM_POST if post_norm else 0) | (NORM_CENTER if center else 0)
-    a = ResidualNormArgs(y=y.data_ptr(), r=residual.data_ptr(), r_out=residual_out.data_ptr(),
-                         ld_y=ld_y, ld_r=ld_r,
-                         ld_r_out=_rows("residual_out", residual_out, shape, (residual.dtype,)),
-                         M=M, D=D, y_type=_TYPES[y.dtype], r_type=_TYPES[residual.dtype],
-                         residual_scale=residual_scale, branch_scale=branch_scale, eps=eps)
-    wtype = None
+    w_post = w_pre = w_type = 0
+    first = None
     if post_norm and post_weight is not None:
-        wtype = post_weight.dtype
-        _need(wtype in _REAL, "post_weight must be bf16 or fp32", TypeError)
-        _dense("post_weight", post_weight, (D,), wtype)
-        a.w_post = post_weight.data_ptr()
+        first = post_weight.dtype
+        _need(first in _REAL, "post_weight must be bf16 or fp32", TypeError)
+        w_post, w_type = _dense("post_weight", post_weight, (D,), first), _REAL[first]
     if pre_norm and pre_weight is not None:
-        _need(wtype in (None, pre_weight.dtype) and pre_weight.dtype in _REAL,
+        kind = pre_weight.dtype
+        _need(kind in _REAL and first in (None, kind),
               "post_weight and pre_weight must both be bf16 or both fp32", TypeError)
-        wtype = pre_weight.dtype
-        _dense("pre_weight", pre_weight, (D,), wtype)
-        a.w_pre = pre_weight.data_ptr()
-    if wtype is not None:
-        a.w_type = _TYPES[wtype]
+        w_pre, w_type = _dense("pre_weight", pre_weight, (D,), kind), _REAL[kind]
+    g = g_type = g_row = g_col = 0
     if gate is not None:
-        _need(gate.dtype in _REAL, "gate must be bf16 or fp32", TypeError)
-        _need(gate.is_cuda, "gate must be on the GPU")
-        if gate.dim() == 1 and gate.shape[0] == D:
-            row, col = 0, gate.stride(0)
-        elif gate.dim() == 2 and gate.shape[0] in (1, M) and gate.shape[1] in (1, D):
-            row = gate.stride(0) if gate.shape[0] == M and M > 1 else 0
-            col = gate.stride(1) if gate.shape[1] == D and D > 1 else 0
-        else:
-            raise ValueError(f"gate has shape {tuple(gate.shape)}: not [{D}], [{M}, 1] or "
-                             f"[{M}, {D}]")
-        if D == 1:
-            col = 0
-        _need(col in (0, 1) and row >= 0, "gate must have contiguous rows")
-        a.gate, a.gate_type, a.gate_row, a.gate_col = (gate.data_ptr(), _TYPES[gate.dtype], row,
-                                                       col)
+        g, g_type, g_row, g_col = _gate(gate, M, D)
+    x = x_scale = ld_x = x_type = 0
     if pre_norm:
         want = torch.int8 if quantize else torch.bfloat16
         if out is None:
             out = _empty(shape, want, dev, stream)
-        a.ld_x = _rows("out", out, shape, (want,))
-        a.x, a.x_type = out.data_ptr(), I8 if quantize else BF16
+        ld_x, x_type = _rows("out", out, shape, _ONLY[want])
+        x = out.data_ptr()
         if quantize:
             if scale_out is None:
                 scale_out = _empty((M,), torch.float32, dev, stream)
-            _dense("scale_out", scale_out, (M,), torch.float32)
-            a.x_scale = scale_out.data_ptr()
+            x_scale = _dense("scale_out", scale_out, (M,), torch.float32)
     else:
         _need(not quantize, "quantize needs pre_norm")
         flags |= NORM_NO_PRE
         out = None
-    a.flags = flags
-    _check((_lib or library()).lib.lowm_residual_norm(ctypes.byref(a), _stream(stream, dev)))
+    rc = lib.lowm_residual_norm(
+        _NORM.pack(y.data_ptr(), residual.data_ptr(), residual_out.data_ptr(), x, x_scale, w_post,
+                   w_pre, g, ld_y, ld_r, ld_r_out, ld_x, g_row, g_col, M, D, y_type, r_type,
+                   w_type, g_type, x_type, flags, residual_scale, branch_scale, eps),
+        _stream(stream, dev))
+    if rc:
+        _check(rc)
     return residual_out, out, scale_out if quantize else None
 
 
@@ -221,24 +244,26 @@ def quantize_rows(x: torch.Tensor, *, out: Optional[torch.Tensor] = None,
     """(q, scale): int8 rows q = rint(x / scale), scale = max|x| / 127 per row
     (fp32), of x [M, K] bf16 or fp32.  A row with an infinity or a NaN gets the
     scale NaN."""
-    ld = _rows("x", x, None, _REAL)
+    ld, kind = _rows("x", x, x.shape, _REAL)
     M, K = x.shape
     if out is None:
         out = _empty((M, K), torch.int8, x.device, stream)
     if scale_out is None:
         scale_out = _empty((M,), torch.float32, x.device, stream)
-    _dense("out", out, (M, K), torch.int8)
-    _dense("scale_out", scale_out, (M,), torch.float32)
-    _check((_lib or library()).lib.lowm_quantize_rows(
-        x.data_ptr(), _TYPES[x.dtype], ld, M, K, out.data_ptr(), scale_out.data_ptr(),
-        _stream(stream, x.device)))
+    q = _dense("out", out, (M, K), torch.int8)
+    scale = _dense("scale_out", scale_out, (M,), torch.float32)
+    rc = (_lib or library()).lib.lowm_quantize_rows(x.data_ptr(), kind, ld, M, K, q, scale,
+                                                    _stream(stream, x.device))
+    if rc:
+        _check(rc)
     return out, scale_out
 
 
 def make_gemm_i8_workspace(M: int, N: int, K: int, device="cuda") -> Optional[torch.Tensor]:
-    """The workspace of gemm_i8 with a bf16 A of these sizes (None for sizes it rejects)."""
+    """A zeroed workspace of gemm_i8 for these sizes (None for sizes it rejects); it also serves
+    any other sizes that need no more bytes, one call at a time."""
     n = library().lib.lowm_gemm_i8_workspace_bytes(M, N, K)
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
 
 def gemm_i8(A: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, *,
@@ -248,39 +273,42 @@ def gemm_i8(A: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, *,
     """(A @ W.T) * a_scale[:, None] * w_scale on the GPU, W [N, K] int8 with w_scale [N].
 
     A [M, K], M <= 64: int8 with a_scale [M] (as quantize_rows or residual_norm give them), or
-    bf16, quantised per row within the call (``workspace``: make_gemm_i8_workspace)."""
-    if A.dim() != 2 or W.dim() != 2 or A.shape[1] != W.shape[1]:
-        raise ValueError(f"shapes {tuple(A.shape)} and {tuple(W.shape)} do not chain")
-    M, K = A.shape
-    N = W.shape[0]
-    dev = A.device
-    given = A.dtype == torch.int8
-    if not given and A.dtype != torch.bfloat16:
-        raise TypeError(f"A must be int8 or bfloat16, not {A.dtype}")
-    _dense("A", A, (M, K), A.dtype)
-    _dense("W", W, (N, K), torch.int8)
-    _dense("w_scale", w_scale, (N,), torch.float32)
+    bf16, quantised per row within the call.  workspace: make_gemm_i8_workspace; an int8 A does
+    without one, but its K is then not split over workgroups."""
+    lib = (_lib or library()).lib
+    a_shape, w_shape = A.shape, W.shape
+    if len(a_shape) != 2 or len(w_shape) != 2 or a_shape[1] != w_shape[1]:
+        raise ValueError(f"shapes {tuple(a_shape)} and {tuple(w_shape)} do not chain")
+    M, K = a_shape
+    N = w_shape[0]
+    dev, kind = A.device, A.dtype
+    given = kind == torch.int8
+    if not given and kind != torch.bfloat16:
+        raise TypeError(f"A must be int8 or bfloat16, not {kind}")
     if out is None:
         out = _empty((M, N), out_dtype, dev, stream)
-    if out.dtype not in _REAL:
+    c_type = _REAL.get(out.dtype)
+    if c_type is None:
         raise TypeError(f"the output must be bf16 or fp32, not {out.dtype}")
-    _dense("out", out, (M, N), out.dtype)
-    lib = (_lib or library()).lib
-    a = GemmI8Args(A.data_ptr(), W.data_ptr(), None, w_scale.data_ptr(), out.data_ptr(), None, 0,
-                   M, N, K, I8 if given else BF16, _TYPES[out.dtype])
+    sa = ws = ws_bytes = 0
     if given:
         _need(a_scale is not None, "an int8 A needs a_scale")
-        _dense("a_scale", a_scale, (M,), torch.float32)
-        a.a_scale = a_scale.data_ptr()
+        sa = _dense("a_scale", a_scale, (M,), torch.float32)
     else:
         _need(a_scale is None, "a bf16 A takes no a_scale")
-        if workspace is None:
-            need = lib.lowm_gemm_i8_workspace_bytes(M, N, K)
-            workspace = _empty((need,), torch.uint8, dev, stream) if need else None
-        if workspace is not None:
-            a.workspace = workspace.data_ptr()
-            a.workspace_bytes = workspace.numel() * workspace.element_size()
-    _check(lib.lowm_gemm_i8(ctypes.byref(a), _stream(stream, dev)))
+    if workspace is not None:
+        _need(workspace.is_cuda and workspace.is_contiguous(),
+              "the workspace must be a contiguous GPU tensor (make_gemm_i8_workspace)")
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    elif not given:
+        raise ValueError("a bf16 A needs a zeroed workspace (make_gemm_i8_workspace)")
+    rc = lib.lowm_gemm_i8(
+        _I8.pack(_dense("A", A, a_shape, kind), _dense("W", W, w_shape, torch.int8), sa,
+                 _dense("w_scale", w_scale, (N,), torch.float32),
+                 _dense("out", out, (M, N), out.dtype), ws, ws_bytes, M, N, K,
+                 I8 if given else BF16, c_type), _stream(stream, dev))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -305,13 +333,11 @@ def moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w2: torch.Tens
     (fp32) the largest score + bias; its gates are their scores ("softmax" over the experts or
     "sigmoid"), divided by their sum with ``renormalize``, times ``routed_scale``; out is the
     gated sum of w2 (silu(w13_gate x) * (w13_up x)).  workspace: make_moe_workspace."""
-    if x.dim() != 2 or router.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
-        raise ValueError("x and router must have two dimensions, w13 and w2 three")
+    lib = (_lib or library()).lib
+    if x.dim() != 2 or w2.dim() != 3:
+        raise ValueError("x must have two dimensions, w2 three")
     T, D = x.shape
     E, _, I = w2.shape
-    for name, t, shape in (("x", x, (T, D)), ("router", router, (E, D)),
-                           ("w13", w13, (E, 2 * I, D)), ("w2", w2, (E, D, I))):
-        _dense(name, t, shape, torch.bfloat16)
     if score not in ("softmax", "sigmoid"):
         raise ValueError(f"score must be 'softmax' or 'sigmoid', not {score!r}")
     dev = x.device
@@ -321,20 +347,22 @@ def moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w2: torch.Tens
         ids_out = _empty((T, top_k), torch.int32, dev, stream)
     if gates_out is None:
         gates_out = _empty((T, top_k), torch.float32, dev, stream)
-    _dense("out", out, (T, D), torch.bfloat16)
-    _dense("ids_out", ids_out, (T, top_k), torch.int32)
-    _dense("gates_out", gates_out, (T, top_k), torch.float32)
-    if bias is not None:
-        _dense("bias", bias, (E,), torch.float32)
     if workspace is None or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("moe needs a zeroed workspace on the GPU (make_moe_workspace)")
-    a = MoeArgs(x.data_ptr(), router.data_ptr(), None if bias is None else bias.data_ptr(),
-                w13.data_ptr(), w2.data_ptr(), out.data_ptr(), ids_out.data_ptr(),
-                gates_out.data_ptr(), workspace.data_ptr(),
-                workspace.numel() * workspace.element_size(), T, D, I, E, top_k,
-                (MOE_SIGMOID if score == "sigmoid" else 0)
-                | (0 if renormalize else MOE_NO_RENORM), routed_scale)
-    _check((_lib or library()).lib.lowm_moe(ctypes.byref(a), _stream(stream, dev)))
+    half = torch.bfloat16
+    rc = lib.lowm_moe(
+        _MOE.pack(_dense("x", x, (T, D), half), _dense("router", router, (E, D), half),
+                  0 if bias is None else _dense("bias", bias, (E,), torch.float32),
+                  _dense("w13", w13, (E, 2 * I, D), half), _dense("w2", w2, (E, D, I), half),
+                  _dense("out", out, (T, D), half),
+                  _dense("ids_out", ids_out, (T, top_k), torch.int32),
+                  _dense("gates_out", gates_out, (T, top_k), torch.float32),
+                  workspace.data_ptr(), workspace.nbytes, T, D, I, E, top_k,
+                  (MOE_SIGMOID if score == "sigmoid" else 0)
+                  | (0 if renormalize else MOE_NO_RENORM), routed_scale),
+        _stream(stream, dev))
+    if rc:
+        _check(rc)
     return out, ids_out, gates_out
 
 
@@ -353,32 +381,30 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int = 0, *
     logprob and entropy are those of softmax(logits); rank counts the logits greater than the
     token's; the alternatives are the top_n most likely tokens, equal ones by id, -1 past the last
     unmasked one.  fp32 and int32 outputs (``outs``: five tensors to write into)."""
-    ld = _rows("logits", logits, None, _REAL)
-    M, V = logits.shape
-    dev = logits.device
-    if tokens.dtype not in (torch.int64, torch.int32):
-        raise TypeError(f"tokens must be int64 or int32, not {tokens.dtype}")
-    _dense("tokens", tokens, (M,), tokens.dtype)
-    if outs is None:
-        outs = tuple(_empty(s, t, dev, stream)
-                     for s, t in (((M,), torch.float32), ((M,), torch.float32),
-                                  ((M,), torch.int32), ((M, top_n), torch.float32),
-                                  ((M, top_n), torch.int32)))
-    else:
-        for name, t, shape, dtype in zip(
-                ("logprob", "entropy", "rank", "top_logprob", "top_id"), outs,
-                ((M,), (M,), (M,), (M, top_n), (M, top_n)),
-                (torch.float32, torch.float32, torch.int32, torch.float32, torch.int32)):
-            _dense(name, t, shape, dtype)
     lib = (_lib or library()).lib
-    if workspace is None:
-        need = lib.lowm_token_logprobs_workspace_bytes(M, V, top_n)
-        workspace = _empty((need,), torch.uint8, dev, stream) if need else None
-    a = TokenLogprobsArgs(
-        logits.data_ptr(), tokens.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(),
-        outs[2].data_ptr(), outs[3].data_ptr(), outs[4].data_ptr(),
-        0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        ld, M, V, top_n, _TYPES[logits.dtype], tokens.element_size())
-    _check(lib.lowm_token_logprobs(ctypes.byref(a), _stream(stream, dev)))
-    return tuple(outs)
+    ld, kind = _rows("logits", logits, logits.shape, _REAL)
+    M, V = logits.shape
+    dev, t_type = logits.device, tokens.dtype
+    if t_type not in (torch.int64, torch.int32):
+        raise TypeError(f"tokens must be int64 or int32, not {t_type}")
+    f32, i32 = torch.float32, torch.int32
+    if outs is None:
+        outs = (_empty((M,), f32, dev, stream), _empty((M,), f32, dev, stream),
+                _empty((M,), i32, dev, stream), _empty((M, top_n), f32, dev, stream),
+                _empty((M, top_n), i32, dev, stream))
+    logprob, entropy, rank, top_logprob, top_id = outs
+    need = lib.lowm_token_logprobs_workspace_bytes(M, V, top_n)
+    if workspace is None and need:
+        workspace = _empty((need,), torch.uint8, dev, stream)
+    ws, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if need else (0, 0)
+    rc = lib.lowm_token_logprobs(
+        _LOGPROBS.pack(logits.data_ptr(), _dense("tokens", tokens, (M,), t_type),
+                       _dense("logprob", logprob, (M,), f32),
+                       _dense("entropy", entropy, (M,), f32), _dense("rank", rank, (M,), i32),
+                       _dense("top_logprob", top_logprob, (M, top_n), f32),
+                       _dense("top_id", top_id, (M, top_n), i32), ws, ws_bytes, ld, M, V, top_n,
+                       kind, 8 if t_type == torch.int64 else 4),
+        _stream(stream, dev))
+    if rc:
+        _check(rc)
+    return logprob, entropy, rank, top_logprob, top_id

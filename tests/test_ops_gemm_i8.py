@@ -20,6 +20,11 @@ def formula(q, sa, W, sw, dtype):
     return (total.to(torch.int32).float() * sa[:, None] * sw).to(dtype)
 
 
+def workspace_is_clean(ws):
+    """What has to be zero between calls: the counters and the partial sums."""
+    assert ws[:256 * 512 + 8192 * 1024].count_nonzero() == 0
+
+
 def operands(g, M, N, K, lo=-128):
     q = torch.randint(lo, 128, (M, K), generator=g, dtype=I8)
     W = torch.randint(lo, 128, (N, K), generator=g, dtype=I8)
@@ -29,7 +34,8 @@ def operands(g, M, N, K, lo=-128):
 SHAPES = [(1, 1, 16), (1, 17, 48), (2, 16, 128), (3, 33, 144), (5, 100, 496), (16, 64, 512),
           (17, 65, 528), (23, 2304, 1040), (32, 31, 2048), (33, 48, 4096), (40, 257, 1616),
           (48, 15, 640), (49, 4099, 1024), (64, 96, 4112), (64, 9000, 256), (7, 13000, 256),
-          (1, 768, 12304), (30, 6151, 400), (64, 6150, 384), (4, 49152, 112)]
+          (1, 768, 12304), (30, 6151, 400), (64, 6150, 384), (4, 49152, 112), (17, 16385, 144), (33, 16400, 272),
+          (64, 20000, 1040), (24, 33000, 400), (50, 49152, 512), (64, 66000, 128)]
 
 
 @pytest.mark.gpu
@@ -38,9 +44,14 @@ SHAPES = [(1, 1, 16), (1, 17, 48), (2, 16, 128), (3, 33, 144), (5, 100, 496), (1
 def test_int8_rows(M, N, K, dtype):
     g = torch.Generator().manual_seed(M + N + K)
     q, sa, W, sw = operands(g, M, N, K)
-    got = sbg.gemm_i8(q.cuda(), W.cuda(), sw.cuda(), a_scale=sa.cuda(), out_dtype=dtype)
+    args = (q.cuda(), W.cuda(), sw.cuda())
+    ws = sbg.make_gemm_i8_workspace(M, N, K)
+    whole = sbg.gemm_i8(*args, a_scale=sa.cuda(), out_dtype=dtype)
+    split = sbg.gemm_i8(*args, a_scale=sa.cuda(), out_dtype=dtype, workspace=ws)
     torch.cuda.synchronize()
-    assert torch.equal(got.cpu(), formula(q, sa, W, sw, dtype))
+    want = formula(q, sa, W, sw, dtype)
+    assert torch.equal(whole.cpu(), want) and torch.equal(split.cpu(), want)
+    workspace_is_clean(ws)
 
 
 @pytest.mark.gpu
@@ -48,8 +59,12 @@ def test_int8_rows(M, N, K, dtype):
 def test_every_row_count(M):
     g = torch.Generator().manual_seed(M)
     q, sa, W, sw = operands(g, M, 50, 1168)
-    got = sbg.gemm_i8(q.cuda(), W.cuda(), sw.cuda(), a_scale=sa.cuda(), out_dtype=F32)
-    assert torch.equal(got.cpu(), formula(q, sa, W, sw, F32))
+    ws = sbg.make_gemm_i8_workspace(M, 50, 1168)
+    for w in (None, ws):
+        got = sbg.gemm_i8(q.cuda(), W.cuda(), sw.cuda(), a_scale=sa.cuda(), out_dtype=F32,
+                          workspace=w)
+        assert torch.equal(got.cpu(), formula(q, sa, W, sw, F32))
+    workspace_is_clean(ws)
 
 
 @pytest.mark.gpu
@@ -59,8 +74,10 @@ def test_the_largest_sums():
     W = torch.full((3, K), -128, dtype=I8)
     W[1] = 127
     one = torch.ones(3)
-    got = sbg.gemm_i8(q.cuda(), W.cuda(), one.cuda(), a_scale=one[:2].cuda(), out_dtype=F32)
-    assert torch.equal(got.cpu(), formula(q, one[:2], W, one, F32))
+    for ws in (None, sbg.make_gemm_i8_workspace(2, 3, K)):
+        got = sbg.gemm_i8(q.cuda(), W.cuda(), one.cuda(), a_scale=one[:2].cuda(), out_dtype=F32,
+                          workspace=ws)
+        assert torch.equal(got.cpu(), formula(q, one[:2], W, one, F32))
 
 
 @pytest.mark.gpu
@@ -74,9 +91,11 @@ def test_bf16_rows_are_quantised_as_quantize_rows_does(M, N, K):
     x[0, K // 2] = 9.0
     sa = x.float().abs().amax(1) / 127
     q = torch.round(x.float() / sa[:, None]).to(I8)
+    ws = sbg.make_gemm_i8_workspace(M, N, K)
     for dtype in (BF16, F32):
-        got = sbg.gemm_i8(x.cuda(), W.cuda(), sw.cuda(), out_dtype=dtype)
+        got = sbg.gemm_i8(x.cuda(), W.cuda(), sw.cuda(), out_dtype=dtype, workspace=ws)
         assert torch.equal(got.cpu(), formula(q, sa, W, sw, dtype))
+    workspace_is_clean(ws)
 
 
 @pytest.mark.gpu
@@ -87,7 +106,8 @@ def test_rows_of_zeros_and_without_a_scale(K):
     x = torch.randn(4, K, generator=g).to(BF16)
     x[0] = 0
     x[1, K - 3], x[2, 0] = float("inf"), float("nan")
-    got = sbg.gemm_i8(x.cuda(), W.cuda(), sw.cuda()).cpu()
+    got = sbg.gemm_i8(x.cuda(), W.cuda(), sw.cuda(),
+                      workspace=sbg.make_gemm_i8_workspace(4, 20, K)).cpu()
     assert (got[0] == 0).all() and got[1:3].isnan().all() and got[3].isfinite().all()
 
 
@@ -107,26 +127,27 @@ def test_on_another_stream_and_in_a_graph():
     _, _, W, sw = operands(g, 1, 1000, 2048)
     W, sw = W.cuda(), sw.cuda()
     x = torch.randn(6, 2048, generator=g).to(BF16).cuda()
-    ws = sbg.make_gemm_i8_workspace(6, 1000, 2048)
+    ws, ws2 = (sbg.make_gemm_i8_workspace(6, 1000, 2048) for _ in range(2))
     out = sbg.gemm_i8(x, W, sw, workspace=ws)
     graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
     with torch.cuda.graph(graph):
         sbg.gemm_i8(x, W, sw, workspace=ws, out=out)
     for i in range(3):
         x.copy_(torch.randn(6, 2048, generator=g))
-        want = sbg.gemm_i8(x, W, sw)
+        want = sbg.gemm_i8(x, W, sw, workspace=ws2)
         torch.cuda.synchronize()
-        other = sbg.gemm_i8(x, W, sw, stream=side)
+        other = sbg.gemm_i8(x, W, sw, workspace=ws2, stream=side)
         side.synchronize()
         out.zero_()
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(other, want)
+    assert sbg.load().workspace_status(ws, 8192) == (0, 0)
 
 
 # -- refusals ------------------------------------------------------------------------------------
 BASE = dict(A=0x10000000, W=0x20000000, a_scale=0x30000000, w_scale=0x31000000, C=0x32000000,
-            workspace=0x33000000, workspace_bytes=1 << 20, M=4, N=64, K=512, a_type=2, c_type=0)
+            workspace=0x33000000, workspace_bytes=1 << 24, M=4, N=64, K=512, a_type=2, c_type=0)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -134,11 +155,13 @@ BASE = dict(A=0x10000000, W=0x20000000, a_scale=0x30000000, w_scale=0x31000000, 
     (dict(C=None), -1), (dict(M=0), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(a_type=1), -1),
     (dict(c_type=2), -1), (dict(C=0x10000400), -1), (dict(C=0x31000010), -1),
     (dict(a_type=0, C=0x33000000), -1), (dict(a_type=0, workspace=0x20000100), -1),
+    (dict(workspace=0x20000100), -1),
     (dict(M=65), -2), (dict(K=520), -2), (dict(K=131072), -2), (dict(a_type=0, K=32784), -2),
     (dict(A=0x10000008), -2), (dict(W=0x20000004), -2), (dict(C=0x32000001), -2),
     (dict(C=0x32000002, c_type=1), -2), (dict(w_scale=0x31000002), -2),
-    (dict(a_scale=0x30000001), -2), (dict(a_type=0, workspace=0x33000008), -2),
-    (dict(a_type=0, workspace=None), -3), (dict(a_type=0, workspace_bytes=4 * 512), -3)])
+    (dict(a_scale=0x30000001), -2), (dict(workspace=0x33000080), -2),
+    (dict(a_type=0, workspace=None), -3), (dict(a_type=0, workspace_bytes=1 << 20), -3),
+    (dict(workspace_bytes=1 << 20), -3)])
 def test_refuses(kw, code):
     a = ops.GemmI8Args(**{**BASE, **kw})
     assert ops.library().lib.lowm_gemm_i8(ctypes.byref(a), None) == code
@@ -146,13 +169,14 @@ def test_refuses(kw, code):
 
 def test_workspace_bytes():
     f = ops.library().lib.lowm_gemm_i8_workspace_bytes
-    assert f(4, 64, 512) == 2048 + 256 and f(1, 64, 16) == 256 + 256
-    assert f(65, 64, 512) == f(4, 64, 520) == f(0, 64, 512) == f(4, 64, 32784) == 0
+    assert f(4, 64, 512) == 256 * 512 + 8192 * 1024 + 2048 + 256
+    assert f(65, 64, 512) == f(4, 64, 520) == f(0, 64, 512) == f(4, 64, 131072) == 0
 
 
 def test_python_checks():
     q = torch.zeros(2, 16, dtype=I8)
-    for bad in (lambda: sbg.gemm_i8(q, q, torch.ones(2)), lambda: sbg.gemm_i8(q.half(), q, q),
+    for bad in (lambda: sbg.gemm_i8(q, q, torch.ones(2)),
+                lambda: sbg.gemm_i8(q.to(BF16), q, torch.ones(2)), lambda: sbg.gemm_i8(q.half(), q, q),
                 lambda: sbg.gemm_i8(q, q[:, :8], q)):
         with pytest.raises((ValueError, TypeError)):
             bad()

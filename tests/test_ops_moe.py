@@ -65,7 +65,7 @@ def draw(g, T, D, I, E, k):
 
 def workspace_is_clean(ws, T, D, I, E, k):
     """What has to be zero between calls: all of the front part."""
-    front = 256 * (1 + 65536 // 16) + 4 * 64 * 256 + 4 * 512 * 64 * 16
+    front = 256 * (1 + 65536 // 16) + 4 * 4 * 64 * 256 + 4 * 512 * 64 * 16
     assert ws[:front].count_nonzero() == 0
 
 
