@@ -211,10 +211,15 @@ int lowm_moe(const lowm_moe_args* args, void* stream);
  * logits bf16 or fp32, rows ld elements apart (>= V); tokens int64 or int32
  * [M]; logprob, entropy fp32 [M]; rank int32 [M]; top_logprob fp32 and top_id
  * int32 [M, top_n] (unused with top_n 0, at most LOWM_LOGPROBS_MAX_TOP).
- * logits must not overlap an output or the workspace.  The workspace needs no
- * clearing, holds nothing between calls, and may be NULL where
- * lowm_token_logprobs_workspace_bytes is 0.
+ * logits must not overlap an output or the workspace.
+ *
+ * The workspace (256-byte aligned; it may be NULL where
+ * lowm_token_logprobs_workspace_bytes is 0, as for many rows) joins the pieces
+ * that few rows are cut into.  It is zeroed once before its first use; every
+ * call that completes leaves it zero, for any sizes.  One workspace per call in
+ * flight.  lowm_workspace_status reads it, with N = LOWM_LOGPROBS_STATUS_N.
  */
+#define LOWM_LOGPROBS_STATUS_N 16384
 #define LOWM_LOGPROBS_MAX_TOP 32
 typedef struct lowm_token_logprobs_args {
     const void* logits;
@@ -238,7 +243,7 @@ size_t lowm_token_logprobs_workspace_bytes(int M, int V, int top_n);
 
 /* Errors: NULL operand, M < 0, V < 1, ld < V, top_n < 0, an unknown type,
  * overlap: LOWM_ERR_INVALID_ARG; top_n > LOWM_LOGPROBS_MAX_TOP, V > 2^30, a
- * pointer not aligned to its element (the workspace: to 16 bytes):
+ * pointer not aligned to its element (the workspace: to 256 bytes):
  * LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
  * LOWM_ERR_WORKSPACE.  M == 0 does nothing. */
 int lowm_token_logprobs(const lowm_token_logprobs_args* args, void* stream);

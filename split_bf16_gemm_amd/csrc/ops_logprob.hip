@@ -1,23 +1,26 @@
 // ops_logprob.hip -- log probabilities of given tokens, with entropy, rank and
 // the most likely alternatives (include/lowm_ops.h), for gfx950.
 //
-// One pass over a row of logits with a running maximum m, S = sum e^(l-m) and
-// T = sum e^(l-m) (l-m), each lane its own and joined at the row's end:
+// One pass over a row of logits with a running maximum m, each lane its own and
+// joined at the row's end.  With L = log2 e and c = m L, rounded,
 //
-//   m' = max(m, l) ;  S' = S e^(m-m') + e^(l-m') ;  T' = (T + S (m-m')) e^(m-m') + ...
-//   log p = l - m - log S ;  entropy = log S - T / S
+//   d = l L - c ;  S = sum 2^d ;  T = sum 2^d d
+//   m' > m:  T' = (T + S (c-c')) 2^(c-c') ;  S' = S 2^(c-c')
+//   log p = l - m - (log S + (c - m L) log 2) ;  entropy = log S - log 2 T / S
 //
+// (d is one fused multiply-add, rounded once; what c's own rounding moves all the
+// terms by is exactly known and put back at the end),
 // so nothing overflows and the logits are read once.  The alternatives cost the
 // pass nothing: each lane's running maximum is its greatest logit, the top_n-th
-// of them bounds the row's top_n-th from below, and only the few lanes whose
+// of those bounds the row's top_n-th from below, and only the few lanes whose
 // maximum passes the bound have their logits read again (from the caches).
 // What passes is sorted by a 64-bit key: the logit's bits in an order that
 // integers compare, then the complement of its id, so equal logits go by id and
 // no two keys are equal.
 // Bound by HBM for many rows (2 or 4 bytes a logit against some 12 vector
-// instructions); few rows are cut into up to kMaxSplits pieces, joined by a
-// second small kernel.
-#include "ops_common.cuh"
+// instructions); few rows are cut into up to kMaxSplits pieces, joined by the
+// last workgroup of a row to arrive.
+#include "ops_stream.cuh"
 
 namespace lowm {
 namespace {
@@ -35,36 +38,78 @@ constexpr float kNone = -__builtin_inff();
 struct LogprobArgs {
   lowm_token_logprobs_args u;
   int splits, per;                       // pieces of a row, logits in each
+  uint32_t* lines;
+  uint64_t* records;
 };
 
-// A piece's part of a row's sums, followed by its top_n keys.
-struct Part {
-  float m, s, t;
-  int32_t above;                         // logits greater than the token's
-};
-__host__ __device__ constexpr size_t part_bytes(int n) { return sizeof(Part) + 8 * (size_t)n; }
+// The workspace: a counter line for each row, then a record for each piece of a
+// row, 64-bit slots that are zero between calls: the maximum and S, T and the
+// count of greater logits, the top_n keys.  Rows are cut only while they are
+// fewer than kSplitBelow, into about that many pieces in all.
+constexpr int kSplitBelow = 1024;
+constexpr size_t kRecord = 2 + kMaxTop;
+constexpr size_t kLineBytes = 256 * (size_t)kSplitBelow;
+constexpr size_t kWorkspace = kLineBytes + 8 * kRecord * 2 * kSplitBelow;
+constexpr uint64_t kNoKey = 1;           // an empty key's slot (no key is that small)
+
+__device__ __forceinline__ void store_slot64(uint64_t* p, uint64_t w) {
+  __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t load_slot64(const uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// See take_slot.
+__device__ __forceinline__ uint64_t take_slot64(uint64_t* slot, uint64_t w, uint32_t* line) {
+  if (w == 0u) {
+    const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
+    while ((w = load_slot64(slot)) == 0u) {
+      if (__builtin_amdgcn_s_memrealtime() - t0 > kFoldPollTicks) {
+        store_slot(line + kFaultWord, 1u);
+        break;
+      }
+      __builtin_amdgcn_s_sleep(4);
+    }
+  }
+  store_slot64(slot, 0u);
+  return w;
+}
+// Two words as the complement of their bits: zero only for two words of all
+// ones, which a maximum and a count never are.
+__device__ __forceinline__ uint64_t pack_words(uint32_t lo, uint32_t hi) {
+  return ~((uint64_t)hi << 32 | lo);
+}
 
 __device__ __forceinline__ uint64_t key_of(float x, int id) {
   return (uint64_t)order(x) << 32 | (uint32_t)~id;
 }
 
-// e^d for d <= 0: the difference is exact to a rounding before the scaling.
-__device__ __forceinline__ float exp_of(float d) {
-  return __builtin_amdgcn_exp2f(d * 1.44269504088896340736f);
-}
-// A difference of logits for a factor that multiplies e^d: below -200 e^d is 0
-// in fp32, and 0 * -infinity would be NaN.
-__device__ __forceinline__ float held(float d) { return fmaxf(d, -200.f); }
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// A difference for a factor that multiplies 2^d: below -300 2^d is 0 in fp32, and
+// 0 * -infinity would be NaN.
+__device__ __forceinline__ float held(float d) { return fmaxf(d, -300.f); }
+
+// A maximum too large to be scaled (a row of the type's lowest value, say): its
+// terms take d = (l - m) L instead.  Another maximum is then either equal to it
+// or further off than any term reaches.
+__device__ __forceinline__ bool huge(float m) { return fabsf(m) > 1e30f; }
 
 struct Sums {
   float m, s, t;
+  // What the terms are relative to; 0 while there is nothing but masked logits.
+  __device__ __forceinline__ float base() const { return m == kNone ? 0.f : m * kLog2e; }
   // Rescales to the maximum m2 >= m.
   __device__ __forceinline__ void to(float m2) {
-    const float d = held(m - m2);        // NaN (both -infinity) becomes -200: s and t are 0
-    const float k = exp_of(d);
+    // (Nothing there yet: s and t are 0 and stay so.  A NaN, of two infinite
+    // bases, is held; of an infinite maximum s is one already.)
+    const float from = m == kNone ? kNone : base();
+    const bool same = m == m2;
+    m = m2;
+    const float d = same ? 0.f : held(from - base());
+    const float k = __builtin_amdgcn_exp2f(d);
     t = (t + s * d) * k;
     s *= k;
-    m = m2;
   }
 };
 
@@ -82,14 +127,21 @@ __device__ __forceinline__ uint32_t below(uint32_t t) {
   return t == 0x80000000u ? 0x7f7fffffu : t - 1;
 }
 
-// An order() that at least n of the wavefront's logits are above: the n-th of
-// its 64 lanes' own greatest logits, to 16 bits.  (n <= 32, so there always are n.)
-__device__ __forceinline__ uint32_t wave_bound(float most, int n) {
-  const uint32_t o = order(most);
+// A bound that at least n of the workgroup's logits pass: the n-th greatest of its
+// lanes' own greatest ones (their order()s), to 16 bits.  Every wavefront finds it
+// for itself.  (n <= 32, so there always are n.)
+__device__ __forceinline__ uint32_t bound_of(const uint32_t* orders, int n) {
+  const int lane = threadIdx.x & (kWave - 1);
+  uint32_t o[kW];
+#pragma unroll
+  for (int w = 0; w < kW; ++w) o[w] = orders[w * kWave + lane];
   uint32_t t = 0;
   for (int bit = 31; bit >= 16; --bit) {
     const uint32_t more = t | 1u << bit;
-    if (__popcll(__ballot(o >= more)) >= n) t = more;
+    int have = 0;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) have += __popcll(__ballot(o[w] >= more));
+    if (have >= n) t = more;
   }
   t = below(t);
   return t > kMasked ? t : kMasked;
@@ -116,18 +168,32 @@ struct Raw<uint16_t> {
   }
 };
 
-// The sums' part of N logits of each lane; the greatest of them is `most`.
+// N logits of each lane; the greatest of them is `most`.  `above` is the
+// wavefront's.
 template <int N>
 __device__ __forceinline__ void add_logits(Sums& sum, int& above, const float (&x)[N], float most,
                                            float token_logit) {
   sum.to(fmaxf(sum.m, most));
-  const float m = sum.m == kNone ? 0.f : sum.m;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float d = x[i] - m, e = exp_of(d);
+  const float c = sum.base();
+  auto term = [&](float d) {
+    const float e = __builtin_amdgcn_exp2f(d);
     sum.s += e;                          // a NaN logit shows here
-    sum.t += e * held(d);
-    above += x[i] > token_logit;
+    sum.t = __builtin_fmaf(e, held(d), sum.t);
+  };
+  const bool far = sum.m != kNone && huge(sum.m);
+  if (__builtin_expect(__ballot(far) != 0, 0)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      term(far ? (x[i] - sum.m) * kLog2e : __builtin_fmaf(x[i], kLog2e, -c));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) term(__builtin_fmaf(x[i], kLog2e, -c));
+  }
+  // Counted by the scalar unit, which has little else to do; and not at all
+  // where no lane has a logit that counts.
+  if (__ballot(most > token_logit)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) above += __popcll(__ballot(x[i] > token_logit));
   }
 }
 
@@ -138,10 +204,12 @@ __device__ __forceinline__ void finish_row(const lowm_token_logprobs_args& u, in
   // An infinity or a NaN among the logits makes S a NaN (inf - inf).
   *bad = !(a.s >= 0.f) || a.m == -kNone;
   const bool empty = a.m == kNone;
-  const float ls = empty ? 0.f : logf(a.s);
+  const float c = a.base();
+  const float shift = huge(a.m) ? 0.f : __builtin_fmaf(-a.m, kLog2e, c) * kLn2;
+  const float ls = empty ? 0.f : logf(a.s) + shift;
   const float nan = __builtin_nanf("");
   u.logprob[row] = *bad || !token_ok ? nan : empty ? kNone : token_logit - a.m - ls;
-  u.entropy[row] = *bad ? nan : empty ? 0.f : ls - a.t / a.s;
+  u.entropy[row] = *bad ? nan : empty ? 0.f : logf(a.s) - kLn2 * (a.t / a.s);
   u.rank[row] = token_ok ? above : -1;
   *log_s = ls;
 }
@@ -164,17 +232,17 @@ __device__ __forceinline__ bool token_of(const lowm_token_logprobs_args& u, int6
 }
 
 template <typename T>
-__global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
+__global__ __launch_bounds__(kTh, 8) void token_logprobs_kernel(LogprobArgs a) {
   using R = Raw<T>;
   constexpr int kRuns = kPerThread / R::kPer;   // of 16 bytes
-  __shared__ uint64_t keys[kCap];
+  __shared__ uint64_t keys[kMaxSplits * kMaxTop];
   __shared__ uint64_t list[kMaxTop];
   __shared__ uint64_t best[kW];
   __shared__ Sums sums[kW];
   __shared__ int totals[kW];
-  __shared__ uint32_t bounds[kW];
+  __shared__ uint32_t orders[kTh];
   __shared__ int lanes[kTh];
-  __shared__ int n_lanes, n_keys;
+  __shared__ int n_lanes, n_keys, last;
   const lowm_token_logprobs_args& u = a.u;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int64_t row = blockIdx.x / a.splits;
@@ -190,18 +258,22 @@ __global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
   const int chunks = (runs + kTh * kRuns - 1) / (kTh * kRuns);
   const ops_u32x4* body = reinterpret_cast<const ops_u32x4*>(src + head);
 
-  auto run_at = [&](int c, int r) { return (c * kRuns + r) * kTh + tid; };
   auto fetch = [&](int c, ops_u32x4 (&w)[kRuns]) {
+    const int j0 = c * kRuns * kTh;
+    if (j0 + kRuns * kTh <= runs) {
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) {
-      w[r] = ops_u32x4{R::kMask, R::kMask, R::kMask, R::kMask};
-      const int j = run_at(c, r);
-      if (j < runs) w[r] = body[j];
+      for (int r = 0; r < kRuns; ++r) w[r] = body[j0 + r * kTh + tid];
+    } else {
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r) {
+        w[r] = ops_u32x4{R::kMask, R::kMask, R::kMask, R::kMask};
+        if (j0 + r * kTh + tid < runs) w[r] = body[j0 + r * kTh + tid];
+      }
     }
   };
 
-  ops_u32x4 w[kRuns], ahead[kRuns];
-  fetch(0, w);
+  ops_u32x4 even[kRuns], odd[kRuns];
+  fetch(0, even);
   float token_logit;
   const bool token_ok = token_of(u, row, &token_logit);
   Sums sum{kNone, 0.f, 0.f};
@@ -210,8 +282,7 @@ __global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
   if (tid == 0) n_lanes = n_keys = 0;
   if (tid < kMaxTop) list[tid] = 0;
 
-  for (int c = 0; c < chunks; ++c) {
-    if (c + 1 < chunks) fetch(c + 1, ahead);
+  auto take = [&](const ops_u32x4 (&w)[kRuns]) {
     float x[kPerThread];
 #pragma unroll
     for (int r = 0; r < kRuns; ++r)
@@ -221,8 +292,14 @@ __global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
 #pragma unroll
     for (int i = 1; i < kPerThread; ++i) most = fmaxf(most, x[i]);
     add_logits(sum, above, x, most, token_logit);
-#pragma unroll
-    for (int r = 0; r < kRuns; ++r) w[r] = ahead[r];
+  };
+  for (int c = 0; c < chunks; c += 2) {
+    if (c + 1 < chunks) fetch(c + 1, odd);
+    take(even);
+    if (c + 1 < chunks) {
+      if (c + 2 < chunks) fetch(c + 2, even);
+      take(odd);
+    }
   }
   const float most = sum.m;              // of the lane's runs
   // The single logits beside the runs, one for each of the first lanes.
@@ -235,22 +312,14 @@ __global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
   }
 
   sum = wave_join(sum);
-#pragma unroll
-  for (int o = kWave / 2; o > 0; o >>= 1) above += __shfl_xor(above, o);
   if (lane == 0) {
     sums[wave] = sum;
     totals[wave] = above;
   }
-  if (n > 0) {
-    const uint32_t own = wave_bound(most, n);
-    if (lane == 0) bounds[wave] = own;
-  }
+  orders[tid] = order(most);
   __syncthreads();
   if (n > 0) {
-    uint32_t thr = bounds[0];
-#pragma unroll
-    for (int v = 1; v < kW; ++v) thr = bounds[v] > thr ? bounds[v] : thr;
-    const float bar = value_of(thr);
+    const float bar = value_of(bound_of(orders, n));
     if (most > bar) lanes[atomicAdd(&n_lanes, 1)] = tid;
     auto add = [&](float v, int e) {
       if (v > bar) {
@@ -313,10 +382,74 @@ __global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
     total += totals[v];
   }
   if (a.splits > 1) {
-    char* part = static_cast<char*>(u.workspace) + (size_t)blockIdx.x * part_bytes(n);
-    if (tid == 0) *reinterpret_cast<Part*>(part) = Part{all.m, all.s, all.t, total};
-    if (tid < n) reinterpret_cast<uint64_t*>(part + sizeof(Part))[tid] = list[tid];
-    return;
+    uint64_t* record = a.records + (size_t)row * a.splits * (2 + n);
+    uint64_t* own = record + (size_t)piece * (2 + n);
+    if (tid == 0) {
+      store_slot64(own, pack_words(__builtin_bit_cast(uint32_t, all.s),
+                                   __builtin_bit_cast(uint32_t, all.m)));
+      store_slot64(own + 1, pack_words(__builtin_bit_cast(uint32_t, all.t), (uint32_t)total));
+    }
+    if (tid < n) store_slot64(own + 2 + tid, list[tid] ? list[tid] : kNoKey);
+    uint32_t* line = a.lines + row * kCtrStride;
+    if (!arrive_last(line, a.splits, &last)) return;
+    // The pieces' sums by the first wavefront, their keys by all.  Each piece's
+    // keys are in order, so the greatest of the pieces' last keys bounds the
+    // row's n-th from below.
+    uint64_t w0 = 0, w1 = 0, w[kMaxSplits * kMaxTop / kTh];
+    if (tid < a.splits) {
+      w0 = load_slot64(record + (size_t)tid * (2 + n));
+      w1 = load_slot64(record + (size_t)tid * (2 + n) + 1);
+    }
+    const int slots = a.splits * n;
+    auto slot = [&](int j) {
+      const int i = tid + j * kTh;
+      return record + (size_t)(i / n) * (2 + n) + 2 + i % n;
+    };
+#pragma unroll
+    for (int j = 0; j < kMaxSplits * kMaxTop / kTh; ++j)
+      if (tid + j * kTh < slots) w[j] = load_slot64(slot(j));
+    if (tid == 0) {
+      best[0] = 0;
+      n_keys = 0;
+    }
+    if (tid < kMaxTop) list[tid] = 0;
+    if (tid < kWave) {
+      all = Sums{kNone, 0.f, 0.f};
+      total = 0;
+      if (tid < a.splits) {
+        w0 = ~take_slot64(record + (size_t)tid * (2 + n), w0, line);
+        w1 = ~take_slot64(record + (size_t)tid * (2 + n) + 1, w1, line);
+        all = Sums{__builtin_bit_cast(float, (uint32_t)(w0 >> 32)),
+                   __builtin_bit_cast(float, (uint32_t)w0),
+                   __builtin_bit_cast(float, (uint32_t)w1)};
+        total = (int)(w1 >> 32);
+      }
+      all = wave_join(all);
+#pragma unroll
+      for (int o = kWave / 2; o > 0; o >>= 1) total += __shfl_xor(total, o);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMaxSplits * kMaxTop / kTh; ++j)
+      if (tid + j * kTh < slots) {
+        w[j] = take_slot64(slot(j), w[j], line);
+        if ((tid + j * kTh) % n == n - 1)
+          atomicMax(reinterpret_cast<unsigned long long*>(&best[0]), (unsigned long long)w[j]);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMaxSplits * kMaxTop / kTh; ++j)
+      if (tid + j * kTh < slots && w[j] >= best[0] && w[j] > kNoKey)
+        keys[atomicAdd(&n_keys, 1)] = w[j];
+    __syncthreads();
+    const int found = n_keys;
+    for (int i = tid; i < found; i += kTh) {
+      const uint64_t key = keys[i];
+      int place = 0;
+      for (int j = 0; j < found; ++j) place += keys[j] > key;
+      if (place < n) list[place] = key;
+    }
+    __syncthreads();
   }
   float log_s = 0.f;
   bool bad = false;
@@ -327,83 +460,18 @@ __global__ __launch_bounds__(kTh) void token_logprobs_kernel(LogprobArgs a) {
     if (tid < n) finish_top(u, row, tid, list[tid], all.m, log_s, bad);
   }
 }
-// Joins a row's pieces.  Each piece's keys are in order, so the greatest of the
-// pieces' last keys bounds the row's n-th from below.
-__global__ __launch_bounds__(kTh) void token_logprobs_join_kernel(LogprobArgs a) {
-  __shared__ uint64_t buf[kMaxSplits * kMaxTop];
-  __shared__ uint64_t list[kMaxTop];
-  __shared__ int count;
-  __shared__ float scale[2];
-  __shared__ int is_bad;
-  const lowm_token_logprobs_args& u = a.u;
-  const int tid = threadIdx.x, n = u.top_n;
-  const int64_t row = blockIdx.x;
-  const char* parts = static_cast<const char*>(u.workspace) + (size_t)row * a.splits * part_bytes(n);
-  if (tid == 0) count = 0;
-  if (tid < kMaxTop) list[tid] = 0;
-  __syncthreads();
-  if (tid < kWave) {
-    float token_logit;
-    const bool token_ok = token_of(u, row, &token_logit);
-    Part p{kNone, 0.f, 0.f, 0};
-    uint64_t last = 0;
-    if (tid < a.splits) {
-      const char* at = parts + (size_t)tid * part_bytes(n);
-      p = *reinterpret_cast<const Part*>(at);
-      if (n > 0) last = reinterpret_cast<const uint64_t*>(at + sizeof(Part))[n - 1];
-    }
-    const Sums all = wave_join(Sums{p.m, p.s, p.t});
-    int above = p.above;
-#pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) {
-      above += __shfl_xor(above, off);
-      const uint64_t o = __shfl_xor(last, off);
-      last = o > last ? o : last;
-    }
-    if (tid == 0) {
-      float log_s;
-      bool bad;
-      finish_row(u, row, all, above, token_logit, token_ok, &log_s, &bad);
-      scale[0] = all.m;
-      scale[1] = log_s;
-      is_bad = bad;
-      list[0] = last;                    // for a moment: the bound
-    }
-  }
-  if (n == 0) return;
-  __syncthreads();
-  const uint64_t bound = list[0];
-  __syncthreads();
-  if (tid == 0) list[0] = 0;
-  for (int i = tid; i < a.splits * n; i += kTh) {
-    const uint64_t key =
-        reinterpret_cast<const uint64_t*>(parts + (size_t)(i / n) * part_bytes(n) + sizeof(Part))[i % n];
-    if (key >= bound && key) buf[atomicAdd(&count, 1)] = key;
-  }
-  __syncthreads();
-  const int found = count;
-  for (int i = tid; i < found; i += kTh) {
-    const uint64_t key = buf[i];
-    int place = 0;
-    for (int j = 0; j < found; ++j) place += buf[j] > key;
-    if (place < n) list[place] = key;
-  }
-  __syncthreads();
-  if (tid < n) finish_top(u, row, tid, list[tid], scale[0], scale[1], is_bad != 0);
-}
 
-// Pieces of a row: enough that the rows' pieces number 1024 (four workgroups
-// per CU), each at least kPiece long.
+// Pieces of a row: enough that the rows' pieces number kSplitBelow (four
+// workgroups per CU), each at least kPiece long.
 int splits_of(int M, int V) {
-  const int want = (1024 + M - 1) / M, most = (V + kPiece - 1) / kPiece;
+  const int want = (kSplitBelow + M - 1) / M, most = (V + kPiece - 1) / kPiece;
   const int s = want < most ? want : most;
   return s < kMaxSplits ? s : kMaxSplits;
 }
 
 size_t logprobs_workspace(int M, int V, int n) {
   if (M < 1 || V < 1 || V > (1 << 30) || n < 0 || n > kMaxTop) return 0;
-  const int s = splits_of(M, V);
-  return s > 1 ? (size_t)M * s * part_bytes(n) : 0;
+  return splits_of(M, V) > 1 ? kWorkspace : 0;
 }
 
 int token_logprobs(const lowm_token_logprobs_args* u, hipStream_t stream) {
@@ -422,7 +490,7 @@ int token_logprobs(const lowm_token_logprobs_args* u, hipStream_t stream) {
   if (((uintptr_t)u->logits & (es - 1)) || ((uintptr_t)u->tokens & (u->tokens_bytes - 1)) ||
       (((uintptr_t)u->logprob | (uintptr_t)u->entropy | (uintptr_t)u->rank) & 3) ||
       (u->top_n > 0 && (((uintptr_t)u->top_logprob | (uintptr_t)u->top_id) & 3)) ||
-      (need > 0 && ((uintptr_t)u->workspace & 15)))
+      (need > 0 && ((uintptr_t)u->workspace & 255)))
     return LOWM_ERR_UNSUPPORTED;
   const int64_t M = u->M, n = u->top_n;
   const Span in[] = {span_of(u->logits, M, u->V, u->ld, es),
@@ -438,7 +506,9 @@ int token_logprobs(const lowm_token_logprobs_args* u, hipStream_t stream) {
     for (int j = 0; j < i; ++j)
       if (meet(out[i], out[j])) return LOWM_ERR_INVALID_ARG;
   }
-  LogprobArgs a{*u, splits_of(u->M, u->V), 0};
+  char* w = static_cast<char*>(u->workspace);
+  LogprobArgs a{*u, splits_of(u->M, u->V), 0, reinterpret_cast<uint32_t*>(w),
+                reinterpret_cast<uint64_t*>(w + (need ? kLineBytes : 0))};
   // Pieces of whole 16-byte runs, so that an aligned row has aligned pieces.
   a.per = ((u->V + a.splits - 1) / a.splits + 7) / 8 * 8;
   a.splits = (u->V + a.per - 1) / a.per;
@@ -447,11 +517,8 @@ int token_logprobs(const lowm_token_logprobs_args* u, hipStream_t stream) {
   const void* fn = u->logits_type == LOWM_F32
                        ? reinterpret_cast<const void*>(&token_logprobs_kernel<float>)
                        : reinterpret_cast<const void*>(&token_logprobs_kernel<uint16_t>);
-  int rc = launched(hipLaunchKernel(fn, dim3((unsigned)(a.splits * M)), dim3(kTh), args, 0, stream));
-  if (rc == LOWM_OK && a.splits > 1)
-    rc = launched(hipLaunchKernel(reinterpret_cast<const void*>(&token_logprobs_join_kernel),
-                                  dim3((unsigned)M), dim3(kTh), args, 0, stream));
-  return rc;
+  return launched(
+      hipLaunchKernel(fn, dim3((unsigned)(a.splits * M)), dim3(kTh), args, 0, stream));
 }
 
 }  // namespace

@@ -3,8 +3,8 @@ C ABI of include/lowm_ops.h.
 
 Argument checks and marshalling only: every step runs in the HIP kernels of
 liblowm.so, on the caller's current stream (or ``stream``), asynchronously and
-without allocating beyond the outputs and workspaces a caller does not pass
-(those belong to the stream the call runs on).  There is no
+without allocating beyond the outputs a caller does not pass (those belong to
+the stream the call runs on).  There is no
 fallback: when the library is not built, or a call fails, this raises.
 """
 from __future__ import annotations
@@ -368,9 +368,10 @@ def moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w2: torch.Tens
 
 def make_token_logprobs_workspace(M: int, V: int, top_n: int = 0,
                                   device="cuda") -> Optional[torch.Tensor]:
-    """The workspace of token_logprobs for these sizes (None where it needs none)."""
+    """A zeroed workspace of token_logprobs for these sizes (None where it needs none); it serves
+    any other sizes too, one call at a time."""
     n = library().lib.lowm_token_logprobs_workspace_bytes(M, V, top_n)
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int = 0, *,
@@ -380,7 +381,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int = 0, *
 
     logprob and entropy are those of softmax(logits); rank counts the logits greater than the
     token's; the alternatives are the top_n most likely tokens, equal ones by id, -1 past the last
-    unmasked one.  fp32 and int32 outputs (``outs``: five tensors to write into)."""
+    unmasked one.  fp32 and int32 outputs (``outs``: five tensors to write into).  workspace:
+    make_token_logprobs_workspace (many rows need none)."""
     lib = (_lib or library()).lib
     ld, kind = _rows("logits", logits, logits.shape, _REAL)
     M, V = logits.shape
@@ -394,9 +396,12 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int = 0, *
                 _empty((M, top_n), i32, dev, stream))
     logprob, entropy, rank, top_logprob, top_id = outs
     need = lib.lowm_token_logprobs_workspace_bytes(M, V, top_n)
-    if workspace is None and need:
-        workspace = _empty((need,), torch.uint8, dev, stream)
-    ws, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if need else (0, 0)
+    ws = ws_bytes = 0
+    if need:
+        if workspace is None or not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError(f"{M} rows of {V} need a zeroed workspace on the GPU "
+                             "(make_token_logprobs_workspace)")
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
     rc = lib.lowm_token_logprobs(
         _LOGPROBS.pack(logits.data_ptr(), _dense("tokens", tokens, (M,), t_type),
                        _dense("logprob", logprob, (M,), f32),

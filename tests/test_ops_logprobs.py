@@ -70,6 +70,15 @@ def judge(x, tok, n, got):
     near(tl, top, lp_err.expand_as(top))
 
 
+def run(x, tok, n):
+    """One call with a workspace of its own, which has to be zero again after it."""
+    ws = sbg.make_token_logprobs_workspace(x.shape[0], x.shape[1], n)
+    got = sbg.token_logprobs(x, tok, n, workspace=ws)
+    torch.cuda.synchronize()
+    assert ws is None or ws.count_nonzero() == 0
+    return got
+
+
 def logits(g, M, V, dtype, std=3.0):
     return (torch.randn(M, V, generator=g) * std).to(dtype)
 
@@ -86,7 +95,7 @@ def test_token_logprobs(M, V, dtype, n):
     if V > 40:
         x[:, torch.randperm(V, generator=g)[:V // 7]] = -INF
     ttype = torch.int32 if n == 1 else torch.int64
-    got = sbg.token_logprobs(x.cuda(), tok.to(ttype).cuda(), n)
+    got = run(x.cuda(), tok.to(ttype).cuda(), n)
     torch.cuda.synchronize()
     judge(x, tok, n, got)
 
@@ -102,7 +111,7 @@ def test_strided_rows_of_any_alignment(dtype, start, M):
     wide[:, start:start + V] = logits(g, M, V, dtype)
     x = wide[:, start:start + V]
     tok = torch.randint(0, V, (M,), generator=g)
-    got = sbg.token_logprobs(wide.cuda()[:, start:start + V], tok.cuda(), 6)
+    got = run(wide.cuda()[:, start:start + V], tok.cuda(), 6)
     torch.cuda.synchronize()
     judge(x, tok, 6, got)
 
@@ -141,7 +150,7 @@ def test_rows_that_fill_the_candidates(M, n, kind):
         y = x.to(dtype)
         if kind == "lowest" and dtype == BF16:
             y = y.clamp(min=torch.finfo(BF16).min)
-        got = sbg.token_logprobs(y.cuda(), tok.cuda(), n)
+        got = run(y.cuda(), tok.cuda(), n)
         torch.cuda.synchronize()
         judge(y, tok, n, got)
 
@@ -159,7 +168,7 @@ def test_rows_without_a_distribution(M):
     tok = torch.randint(0, V, (M,), generator=g)
     tok[5] = V
     tok[0] = -1
-    lp, ent, rank, tl, ti = (t.cpu() for t in sbg.token_logprobs(x.cuda(), tok.cuda(), n))
+    lp, ent, rank, tl, ti = (t.cpu() for t in run(x.cuda(), tok.cuda(), n))
     assert lp[1] == -INF and ent[1] == 0 and rank[1] == 0
     assert (tl[1] == -INF).all() and (ti[1] == -1).all()
     for r in (2, 3, 4):
@@ -174,7 +183,7 @@ def test_rows_without_a_distribution(M):
 def test_same_bits_each_time_and_in_a_graph():
     g = torch.Generator().manual_seed(2)
     x, tok = logits(g, 3, 50001, BF16).cuda(), torch.randint(0, 50001, (3,), generator=g).cuda()
-    ws = sbg.make_token_logprobs_workspace(3, 50001, 20)
+    ws, ws2 = (sbg.make_token_logprobs_workspace(3, 50001, 20) for _ in range(2))
     outs = sbg.token_logprobs(x, tok, 20, workspace=ws)
     outs = tuple(torch.zeros_like(t) for t in outs)
     graph = torch.cuda.CUDAGraph()
@@ -183,14 +192,15 @@ def test_same_bits_each_time_and_in_a_graph():
     side = torch.cuda.Stream()
     for i in range(3):
         x.copy_(logits(g, 3, 50001, BF16))
-        want = sbg.token_logprobs(x, tok, 20)
+        want = sbg.token_logprobs(x, tok, 20, workspace=ws2)
         torch.cuda.synchronize()
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
-        again = sbg.token_logprobs(x, tok, 20, stream=side)
+        again = sbg.token_logprobs(x, tok, 20, workspace=ws2, stream=side)
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(again, want))
+    assert sbg.load().workspace_status(ws, 16384) == (0, 0)
 
 
 # -- refusals ------------------------------------------------------------------------------------
@@ -207,7 +217,7 @@ BASE = dict(logits=0x10000000, tokens=0x20000000, logprob=0x21000000, entropy=0x
     (dict(entropy=0x21000004), -1), (dict(logprob=0x10000000), -1), (dict(top_id=0x26000000), -1),
     (dict(top_n=33), -2), (dict(V=(1 << 30) + 1, ld=1 << 31), -2), (dict(logits=0x10000001), -2),
     (dict(logits=0x10000002, logits_type=1), -2), (dict(tokens=0x20000004), -2),
-    (dict(rank=0x23000002), -2), (dict(workspace=0x26000008), -2),
+    (dict(rank=0x23000002), -2), (dict(workspace=0x26000080), -2),
     (dict(workspace=None), -3), (dict(workspace_bytes=64), -3), (dict(M=0, logits=None), 0)])
 def test_refuses(kw, code):
     a = ops.TokenLogprobsArgs(**{**BASE, **kw})
@@ -217,9 +227,24 @@ def test_refuses(kw, code):
 def test_workspace_bytes():
     f = ops.library().lib.lowm_token_logprobs_workspace_bytes
     assert f(2048, 49152, 5) == 0                    # enough rows: no row is cut
-    assert f(1, 49152, 5) == 12 * (16 + 5 * 8)
-    assert f(1, 4096, 5) == 0 and f(1, 4097, 0) == 2 * 16
+    assert f(1, 49152, 5) == f(1000, 5000, 32) == 1024 * 256 + 2048 * 34 * 8
+    assert f(1, 4096, 5) == 0 and f(1, 4097, 0) > 0 and f(1024, 99999, 1) == 0
     assert f(0, 5, 5) == f(1, 0, 5) == f(1, 5, 33) == f(1, 5, -1) == 0
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_all_sizes_and_none_without_it():
+    g = torch.Generator().manual_seed(12)
+    ws = sbg.make_token_logprobs_workspace(1, 131072, 32)
+    for M, V, n in ((1, 131072, 32), (900, 9000, 3), (64, 8193, 32), (1023, 5000, 0), (7, 99999, 20),
+                    (1, 4097, 1)):
+        x, tok = logits(g, M, V, BF16), torch.randint(0, V, (M,), generator=g)
+        got = sbg.token_logprobs(x.cuda(), tok.cuda(), n, workspace=ws)
+        torch.cuda.synchronize()
+        judge(x, tok, n, got)
+        assert ws.count_nonzero() == 0
+    with pytest.raises(ValueError):
+        sbg.token_logprobs(x.cuda(), tok.cuda(), 1)
 
 
 def test_python_checks():
