@@ -219,7 +219,7 @@ int lowm_moe(const lowm_moe_args* args, void* stream);
  * call that completes leaves it zero, for any sizes.  One workspace per call in
  * flight.  lowm_workspace_status reads it, with N = LOWM_LOGPROBS_STATUS_N.
  */
-#define LOWM_LOGPROBS_STATUS_N 16384
+#define LOWM_LOGPROBS_STATUS_N 8192
 #define LOWM_LOGPROBS_MAX_TOP 32
 typedef struct lowm_token_logprobs_args {
     const void* logits;

@@ -46,7 +46,7 @@ struct LogprobArgs {
 // row, 64-bit slots that are zero between calls: the maximum and S, T and the
 // count of greater logits, the top_n keys.  Rows are cut only while they are
 // fewer than kSplitBelow, into about that many pieces in all.
-constexpr int kSplitBelow = 1024;
+constexpr int kSplitBelow = 512;
 constexpr size_t kRecord = 2 + kMaxTop;
 constexpr size_t kLineBytes = 256 * (size_t)kSplitBelow;
 constexpr size_t kWorkspace = kLineBytes + 8 * kRecord * 2 * kSplitBelow;
@@ -320,7 +320,6 @@ __global__ __launch_bounds__(kTh, 8) void token_logprobs_kernel(LogprobArgs a) {
   __syncthreads();
   if (n > 0) {
     const float bar = value_of(bound_of(orders, n));
-    if (most > bar) lanes[atomicAdd(&n_lanes, 1)] = tid;
     auto add = [&](float v, int e) {
       if (v > bar) {
         const int to = atomicAdd(&n_keys, 1);
@@ -328,14 +327,25 @@ __global__ __launch_bounds__(kTh, 8) void token_logprobs_kernel(LogprobArgs a) {
       }
     };
     if (wave == 0) add(x1[0], single);
-    __syncthreads();
-    const int per_lane = (runs + kTh - 1) / kTh, tasks = n_lanes * per_lane;
-    for (int q = tid; q < tasks; q += kTh) {
-      const int j = q % per_lane * kTh + lanes[q / per_lane];
-      if (j < runs) {
-        const ops_u32x4 again = body[j];
+    if (chunks <= 1) {                   // all there is is still in registers
+      if (most > bar) {
 #pragma unroll
-        for (int i = 0; i < R::kPer; ++i) add(R::get(again, i), head + j * R::kPer + i);
+        for (int r = 0; r < kRuns; ++r)
+#pragma unroll
+          for (int i = 0; i < R::kPer; ++i)
+            add(R::get(even[r], i), head + (r * kTh + tid) * R::kPer + i);
+      }
+    } else {
+      if (most > bar) lanes[atomicAdd(&n_lanes, 1)] = tid;
+      __syncthreads();
+      const int per_lane = (runs + kTh - 1) / kTh, tasks = n_lanes * per_lane;
+      for (int q = tid; q < tasks; q += kTh) {
+        const int j = q % per_lane * kTh + lanes[q / per_lane];
+        if (j < runs) {
+          const ops_u32x4 again = body[j];
+#pragma unroll
+          for (int i = 0; i < R::kPer; ++i) add(R::get(again, i), head + j * R::kPer + i);
+        }
       }
     }
     __syncthreads();
@@ -461,8 +471,10 @@ __global__ __launch_bounds__(kTh, 8) void token_logprobs_kernel(LogprobArgs a) {
   }
 }
 
-// Pieces of a row: enough that the rows' pieces number kSplitBelow (four
-// workgroups per CU), each at least kPiece long.
+// Pieces of a row: enough that the rows' pieces number kSplitBelow (two
+// workgroups per CU), each at least kPiece long.  Measured on MI355X at 256 / 512
+// / 1024: M 64, V 49152 bf16 10.4 / 10.9 / 11.0 us, M 128 12.9 / 11.9 / 13.2,
+// M 512 16.9 / 16.7 / 18.2, M 800 22.5 / 22.4 / 24.6.
 int splits_of(int M, int V) {
   const int want = (kSplitBelow + M - 1) / M, most = (V + kPiece - 1) / kPiece;
   const int s = want < most ? want : most;
