@@ -3,9 +3,12 @@
     python -m split_bf16_gemm_amd.build
 
 produces, under split_bf16_gemm_amd/_lib/:
-  liblowm.so         the GEMM (C ABI of include/lowm.h)
+  liblowm.so         the GEMM and the operators around it (C ABI of include/lowm.h
+                     and include/lowm_ops.h)
   liblowm_stress.so  the same sources with -DLOWM_STRESS (stall injection)
   libbwprobe.so      streaming read/copy kernels for the HBM ceiling
+  ops_binding.so     the operators' Python entry (csrc/ops_binding.cpp, host code),
+                     linked against liblowm.so
 
 and, only when named (python -m split_bf16_gemm_amd.build liblowm_fenced.so):
   liblowm_fenced.so  the same sources with -DLOWM_FENCED (a release arrival
@@ -92,6 +95,29 @@ def _link(lib: str, verbose: bool) -> Path:
     return out
 
 
+def _binding(verbose: bool) -> Path:
+    """Compile and link ops_binding.so.  g++, since it holds no device code; torch's
+    headers and libraries are those of the torch it is imported into."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cxx = shutil.which("g++") or "g++"
+    out = LIBDIR / "ops_binding.so"
+    tmp = LIBDIR / f"ops_binding.so.tmp{os.getpid()}"
+    includes = [f"-I{p}" for p in (*cpp_extension.include_paths(),
+                                   sysconfig.get_paths()["include"], INCLUDE)]
+    libs = [f"-L{p}" for p in cpp_extension.library_paths()]
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *includes,
+          "-o", str(tmp), str(CSRC / "ops_binding.cpp"), *libs, "-ltorch_python", "-ltorch",
+          "-ltorch_cpu", "-lc10", f"-L{LIBDIR}", "-llowm", "-Wl,-rpath,$ORIGIN"],
+         "building ops_binding.so", verbose)
+    os.replace(tmp, out)
+    return out
+
+
 def build(verbose: bool = False, only: list[str] | None = None) -> list[Path]:
     """Compile every library (objects in parallel) and return their paths."""
     LIBDIR.mkdir(exist_ok=True)
@@ -106,7 +132,10 @@ def build(verbose: bool = False, only: list[str] | None = None) -> list[Path]:
     workers = max(1, min(len(jobs), os.cpu_count() or 1, 16))
     with ThreadPoolExecutor(max_workers=workers) as ex:
         list(ex.map(lambda j: _compile(*j, verbose), jobs))
-    return [_link(lib, verbose) for lib in libs]
+    paths = [_link(lib, verbose) for lib in libs]
+    if "liblowm.so" in libs:
+        paths.append(_binding(verbose))
+    return paths
 
 
 if __name__ == "__main__":

@@ -231,6 +231,33 @@ def test_on_another_stream_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(bufs, want))
 
 
+@pytest.mark.gpu
+def test_no_rows_at_all():
+    y = torch.zeros(0, 64, dtype=BF16, device="cuda")
+    r, x, s = sbg.residual_norm(y, y, quantize=True)
+    assert r.shape == x.shape == (0, 64) and s.shape == (0,)
+    assert sbg.quantize_rows(y)[0].shape == (0, 64)
+    lp = sbg.token_logprobs(y, torch.zeros(0, dtype=torch.int64, device="cuda"), 3)
+    assert lp[0].shape == (0,) and lp[3].shape == (0, 3)
+
+
+@pytest.mark.gpu
+def test_tensors_that_do_not_fit_are_refused():
+    y, w = torch.zeros(4, 64, dtype=BF16, device="cuda"), torch.ones(64, device="cuda")
+    for kw, error in ((dict(post_weight=w[:32]), ValueError), (dict(post_weight=w.double()), TypeError),
+                      (dict(post_weight=w, pre_weight=w.to(BF16)), TypeError),
+                      (dict(gate=w[:5]), ValueError), (dict(gate=y.t()[:4]), ValueError),
+                      (dict(out=y.float()), TypeError), (dict(out=y[:2]), ValueError),
+                      (dict(residual_out=y.float()), TypeError), (dict(post_weight=7), TypeError),
+                      (dict(quantize=True, pre_norm=False), ValueError),
+                      (dict(residual_out=y), sbg.LowmError)):     # an output over an input
+        with pytest.raises(error):
+            sbg.residual_norm(y, y.clone(), **kw)
+    for a in ((y.t(), y.t()), (y.expand(2, 4, 64)[0], y[0]), (y.half(), y)):
+        with pytest.raises((ValueError, TypeError)):
+            sbg.residual_norm(*a)
+
+
 # -- refusals: no kernel is launched, no pointer is read -----------------------------------------
 A0, B0, C0, D0 = 0x1000000, 0x2000000, 0x3000000, 0x4000000
 
