@@ -51,23 +51,37 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return (uint32_t)a | ((uint32_t)b << 16);
 }
 
-// Eight consecutive elements from 16-byte aligned memory.
-__device__ __forceinline__ void load8(const void* base, int64_t at, bool f32, float (&v)[8]) {
+// Eight consecutive elements of 16-byte aligned memory as they lie there; their
+// values are taken out later, so that a kernel's loads do not wait for one another
+// in the branches on its operands' types.
+struct Raw8 {
+  ops_u32x4 a, b;
+};
+__device__ __forceinline__ Raw8 load8(const void* base, int64_t at, bool f32) {
+  Raw8 r;
   if (f32) {
-    const ops_f32x4* p = reinterpret_cast<const ops_f32x4*>(static_cast<const float*>(base) + at);
-    const ops_f32x4 a = p[0], b = p[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
-    }
+    const ops_u32x4* p = reinterpret_cast<const ops_u32x4*>(static_cast<const float*>(base) + at);
+    r.a = p[0];
+    r.b = p[1];
   } else {
-    const ops_u32x4 a =
-        *reinterpret_cast<const ops_u32x4*>(static_cast<const uint16_t*>(base) + at);
+    r.a = *reinterpret_cast<const ops_u32x4*>(static_cast<const uint16_t*>(base) + at);
+    r.b = ops_u32x4{0u, 0u, 0u, 0u};
+  }
+  return r;
+}
+__device__ __forceinline__ void values8(const Raw8& r, bool f32, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = r.a[i], b = r.b[i];
+    v[i] = __builtin_bit_cast(float, a);
+    v[4 + i] = __builtin_bit_cast(float, b);
+  }
+  if (!f32) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_lo(a[i]);
-      v[2 * i + 1] = bf16_hi(a[i]);
+      const uint32_t w = r.a[i];
+      v[2 * i] = bf16_lo(w);
+      v[2 * i + 1] = bf16_hi(w);
     }
   }
 }
@@ -132,5 +146,45 @@ __device__ __forceinline__ uint32_t order(float x) {
 __device__ __forceinline__ float value_of(uint32_t o) {
   return __builtin_bit_cast(float, o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
+
+// A row's scale for int8 from the bits of its largest magnitude: a row of zeros
+// has scale 0, one with an infinity or a NaN (whose bits are the greatest) scale
+// NaN; the q of both are 0.
+struct RowScale {
+  float scale, recip;
+  bool some;
+  __device__ __forceinline__ explicit RowScale(uint32_t top) {
+    const bool finite = top < 0x7f800000u;
+    const float s = __builtin_bit_cast(float, top) / 127.0f;
+    scale = finite ? s : __builtin_nanf("");
+    some = finite && s > 0.f;
+    // no reciprocal for a subnormal scale: its values all take the divide
+    recip = s >= 1.17549435e-38f ? 1.0f / s : __builtin_nanf("");
+  }
+  // Four of rint(x / scale), as bytes, the divide correctly rounded so that q is
+  // the same number on any machine.  x recip is within 127 * 2^-22 of the
+  // quotient: away from the halves it rounds to the same integer, and next to one
+  // the divide itself decides.  (Adding 1.5 * 2^23 rounds to an integer and leaves
+  // it in the low bits.  A subnormal scale can be rounded far enough that a
+  // quotient passes 127: such a value is held there.)
+  __device__ __forceinline__ uint32_t quantise4(float x0, float x1, float x2, float x3) const {
+    constexpr float kRound = 12582912.f;
+    const float x[4] = {x0, x1, x2, x3};
+    uint32_t b[4];
+    bool clear = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float y = __builtin_fmaf(x[i], recip, kRound);
+      clear = clear && fabsf(__builtin_fmaf(x[i], recip, kRound - y)) <= 0.4998f;
+      b[i] = __builtin_bit_cast(uint32_t, y);
+    }
+    if (__builtin_expect(!clear, 0)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        b[i] = some ? (uint32_t)(int)fminf(fmaxf(rintf(x[i] / scale), -127.f), 127.f) : 0u;
+    }
+    return (b[0] & 255u) | (b[1] & 255u) << 8 | (b[2] & 255u) << 16 | b[3] << 24;
+  }
+};
 
 }  // namespace lowm

@@ -13,7 +13,9 @@
 //            each, with one panel of A per step for all of them: more rows of W
 //            for each byte of A read.
 // Where they are too few for the CUs, K is split over several workgroups whose
-// int32 sums the last to arrive adds.
+// int32 sums the last to arrive adds.  A few rows of bf16 are quantised by each
+// workgroup for itself while its first rows of W are on their way (few); more
+// rows once, by a kernel of their own.
 #include "ops_stream.cuh"
 
 namespace lowm {
@@ -54,7 +56,8 @@ __device__ __forceinline__ uint32_t i8_encode(int v) { return (uint32_t)v ^ 0x80
 __device__ __forceinline__ int i8_decode(uint32_t w) { return (int)(w ^ 0x80000000u); }
 
 // Row 4 g + i of block b, column n: element i of v.
-__device__ __forceinline__ void i8_store(const I8Args& a, const i32x4& v, int b, int n, int g) {
+__device__ __forceinline__ void i8_store(const I8Args& a, const float* a_scale, const i32x4& v,
+                                         int b, int n, int g) {
   if (n >= a.N) return;
   const float sw = a.w_scale[n];
 #pragma unroll
@@ -63,7 +66,7 @@ __device__ __forceinline__ void i8_store(const I8Args& a, const i32x4& v, int b,
     if (m >= a.M) continue;
     const int sum = v[i];
     // int32 to fp32 rounds a sum past 2^24 by half a step of fp32.
-    const float c = (float)sum * a.a_scale[m] * sw;
+    const float c = (float)sum * a_scale[m] * sw;
     const size_t at = (size_t)m * a.N + n;
     if (a.f32)
       static_cast<float*>(a.C)[at] = c;
@@ -183,7 +186,197 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_stretch_kernel(I8Args a) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int q = wave + j * kWaves;
-    if (q < SH::kBlocks) i8_store(a, v[j], q % MB, n0 + 16 * (q / MB) + l16, g);
+    if (q < SH::kBlocks) i8_store(a, a.a_scale, v[j], q % MB, n0 + 16 * (q / MB) + l16, g);
+  }
+#endif
+}
+
+// Few bf16 rows (M <= 4 * RQ, at most 8), each workgroup quantising them for
+// itself: stretch tiles whose wavefronts hold their stretch of A, PM steps at
+// most, in LDS: first as it is (the row's scale needs all of K, so all
+// wavefronts'), then, through registers, as int8 in the same place.  The ring
+// streams W alone, and its first steps are on their way before A is looked at.
+template <int RQ, int PM, int NB, int R>
+struct I8Few {
+  static constexpr int kPP = 68;
+  static constexpr int G = 2 * NB;                       // loads per step
+  static constexpr int kSlot = G * kPP;
+  static constexpr int kRing = R * kSlot;
+  // Each step's 4 * RQ rows of 256 bytes, then its int8 piece of 8 rows; that
+  // block's other piece holds rows that are not there: whatever follows (one
+  // piece of room after the last).
+  static constexpr int kRaw = RQ * kWave;
+  static constexpr int kRows = PM * (kRaw > kPP ? kRaw : kPP);
+  static constexpr int kElems = kWaves * (kRing + kRows) + kPP;
+  static constexpr int kSums = kWaves * NB * kWave;
+  static constexpr bool valid = R >= 2 && (R - 1) * G <= 63 && kSums <= kWaves * kRing &&
+                                kElems * 16 <= 160 * 1024 - 512;
+};
+
+template <int RQ, int PM, int NB, int R>
+__global__ __launch_bounds__(kThreads) void gemm_i8_few_kernel(I8Args a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  using SH = I8Few<RQ, PM, NB, R>;
+  constexpr int G = SH::G, kPP = SH::kPP;
+  __shared__ u32x4 lds[SH::kElems];
+  __shared__ u32x4 tops[4 * RQ];         // [row][wavefront]
+  __shared__ float scales[4 * RQ];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int g = lane >> 4, l16 = lane & 15;
+  const int n0 = blockIdx.x * 16 * NB;
+  const int steps = (a.K + 127) / 128;
+  const int s0 = steps * wave / kWaves, P = steps * (wave + 1) / kWaves - s0;
+
+  u32x4* ring = lds + wave * SH::kRing;
+  u32x4* rows = lds + kWaves * SH::kRing + wave * SH::kRows;
+  const int k0 = s0 * 128 + stream_piece(lane) * 16, left = a.K - k0;
+  const int line = __builtin_amdgcn_readfirstlane(left);
+  const uint8_t* src[G];
+#pragma unroll
+  for (int t = 0; t < G; ++t) {
+    const int r = n0 + 8 * t + stream_row(lane);
+    src[t] = a.W + (size_t)(r < a.N ? r : a.N - 1) * a.K + k0;
+  }
+  auto issue = [&](u32x4* slot, int p) {
+    const int at = p * 128;
+    const bool whole = line - at >= 128;
+    static_for<G>([&](auto t_c) {
+      constexpr int t = decltype(t_c)::value;
+      const uint8_t* from = src[t] + at;
+      if (!whole) from = left - at >= 16 ? from : reinterpret_cast<const uint8_t*>(&kZeroPiece);
+      __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)(slot + t * kPP),
+                                       16, 0, kStreamAux);
+    });
+    pin_issue();
+  };
+  u32x4* const end = ring + SH::kRing;
+  u32x4 *fill = ring, *use = ring;
+  auto next = [&](u32x4* s) { return s + SH::kSlot == end ? ring : s + SH::kSlot; };
+  // Lane (g, l16) takes elements 8 l16 .. 8 l16 + 7 of a step's 128, of rows g and,
+  // for RQ 2, g + 4; zeros past the end.
+  const uint16_t* A = reinterpret_cast<const uint16_t*>(a.A);
+  static_for<PM * RQ>([&](auto i_c) {
+    constexpr int p = decltype(i_c)::value / RQ, q = decltype(i_c)::value % RQ;
+    const int m = g + 4 * q < a.M ? g + 4 * q : a.M - 1;
+    const int k = (s0 + p) * 128 + 8 * l16;
+    const void* from = p < P && k < a.K ? static_cast<const void*>(A + (size_t)m * a.K + k)
+                                        : static_cast<const void*>(&kZeroPiece);
+    __builtin_amdgcn_global_load_lds(
+        from, (__attribute__((address_space(3))) void*)(rows + (p * RQ + q) * kWave), 16, 0, 0);
+  });
+  // All of the ring's slots, whether there are as many steps or not (past them
+  // there are zeros to read), so that the wait for A below knows how many loads
+  // may stay in flight.
+  static_for<R - 1>([&](auto i_c) {
+    issue(fill, decltype(i_c)::value);
+    fill = next(fill);
+  });
+
+  wait_vmcnt<(R - 1) * G>();
+  u32x4 raw[PM * RQ];                    // step p's rows g + 4 q at p * RQ + q
+#pragma unroll
+  for (int i = 0; i < PM * RQ; ++i) raw[i] = lds_read_opaque(rows + i * kWave + lane);
+  lds_wait(raw);
+  // The rows' largest magnitudes, as bit patterns: over the 16 lanes that share
+  // a row, then over the wavefronts.
+#pragma unroll
+  for (int q = 0; q < RQ; ++q) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int p = 0; p < PM; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = raw[p * RQ + q][i], hi = w & 0x7fff0000u, lo = (w & 0x7fffu) << 16;
+        top = hi > top ? hi : top;
+        top = lo > top ? lo : top;
+      }
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) {
+      const uint32_t o = __shfl_xor(top, off);
+      top = o > top ? o : top;
+    }
+    if (l16 == 0) reinterpret_cast<uint32_t*>(&tops[g + 4 * q])[wave] = top;
+  }
+  // (the ring's loads stay in flight)
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+  for (int q = 0; q < RQ; ++q) {
+    u32x4 all[1] = {lds_read_opaque(&tops[g + 4 * q])};
+    lds_wait(all);
+    uint32_t top = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const uint32_t o = all[0][w];
+      top = o > top ? o : top;
+    }
+    const RowScale rs(top);
+    if (wave == 0 && l16 == 0) scales[g + 4 * q] = rs.scale;
+    // Row m's 16-byte piece j of a line lies at place (j + m / 2) mod 8 of the row,
+    // as the loads into the ring place it.
+    const int m = g + 4 * q, at = (m * 8 + (((l16 >> 1) + (m >> 1)) & 7)) * 16 + (l16 & 1) * 8;
+#pragma unroll
+    for (int p = 0; p < PM; ++p) {
+      ops_u32x2 q8;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = raw[p * RQ + q][2 * h], hi = raw[p * RQ + q][2 * h + 1];
+        q8[h] = rs.quantise4(bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi));
+      }
+      if (p < P) lds_write8_opaque(reinterpret_cast<char*>(rows + p * kPP) + at, q8);
+    }
+  }
+  wait_lgkmcnt0();                       // (a wavefront reads only its own rows)
+
+  int rpos[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    rpos[c] = (l16 >> 3) * kPP + (l16 & 7) * 8 + ((4 * c + g + ((l16 & 7) >> 1)) & 7);
+  i32x4 acc[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) acc[j] = i32x4{0, 0, 0, 0};
+  auto multiply = [&](const u32x4* slot, const u32x4* row) {
+    u32x4 v[2 * (NB + 1)];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) v[c * (NB + 1) + j] = lds_read_opaque(slot + 2 * j * kPP + rpos[c]);
+      v[c * (NB + 1) + NB] = lds_read_opaque(row + rpos[c]);
+    }
+    lds_wait(v);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        acc[j] = stream_mfma(v[c * (NB + 1) + NB], v[c * (NB + 1) + j], acc[j]);
+  };
+  int p = 0;
+  for (; p + R - 1 < P; ++p) {
+    wait_vmcnt<(R - 2) * G>();
+    issue(fill, p + R - 1);
+    fill = next(fill);
+    multiply(use, rows + p * kPP);
+    use = next(use);
+  }
+  static_for<R - 1>([&](auto i_c) {
+    constexpr int younger = R - 2 - decltype(i_c)::value;
+    if (P - p == younger + 1) {
+      wait_vmcnt<younger * G>();
+      multiply(use, rows + p * kPP);
+      use = next(use);
+      ++p;
+    }
+  });
+  stream_settle(acc);
+  i32x4* sums = reinterpret_cast<i32x4*>(lds);
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < NB; ++q) sums[(wave * NB + q) * kWave + lane] = acc[q];
+  __syncthreads();
+  if (wave < NB) {
+    i32x4 v = sums[wave * kWave + lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += sums[(w * NB + wave) * kWave + lane];
+    i8_store(a, scales, v, 0, n0 + 16 * wave + l16, g);
   }
 #endif
 }
@@ -315,7 +508,7 @@ __global__ __launch_bounds__(kPanelWaves* kWave) void gemm_i8_panel_kernel(I8Arg
   stream_settle(acc);
 #pragma unroll
   for (int q = 0; q < NB * MB; ++q)
-    i8_store(a, acc[q], q % MB, n0 + 16 * (q / MB) + (lane & 15), lane >> 4);
+    i8_store(a, a.a_scale, acc[q], q % MB, n0 + 16 * (q / MB) + (lane & 15), lane >> 4);
 #endif
 }
 
@@ -343,6 +536,29 @@ struct I8Plan {
   int width() const { return (panel ? 16 * kPanelWaves : 16) * NB; }
   int tiles(int N) const { return (int)(((int64_t)N + width() - 1) / width()); }
 };
+
+template <int RQ, int PM, int NB, int R>
+constexpr int few_ring() {
+  if constexpr (I8Few<RQ, PM, NB, R>::valid) return R;
+  else return few_ring<RQ, PM, NB, R - 1>();
+}
+template <int RQ, int PM, int NB>
+const void* few_of() {
+  return reinterpret_cast<const void*>(
+      &gemm_i8_few_kernel<RQ, PM, NB, few_ring<RQ, PM, NB, 8>()>);
+}
+// The kernel that quantises M bf16 rows itself, if there is one: M <= 8 rows whose
+// stretches fit a wavefront's registers, in one round of workgroups.
+const void* few_kernel(int M, int K, const I8Plan& p, int tiles) {
+  static const void* const table[3][4] = {
+      {few_of<1, 8, 1>(), few_of<1, 8, 2>(), few_of<1, 8, 3>(), few_of<1, 8, 4>()},
+      {few_of<1, 16, 1>(), few_of<1, 16, 2>(), few_of<1, 16, 3>(), few_of<1, 16, 4>()},
+      {few_of<2, 8, 1>(), few_of<2, 8, 2>(), few_of<2, 8, 3>(), few_of<2, 8, 4>()}};
+  if (M > 8 || p.panel || tiles > 256) return nullptr;
+  const int steps = ((K + 127) / 128 + kWaves - 1) / kWaves;
+  const int row = steps <= 8 ? (M <= 4 ? 0 : 2) : steps <= 16 && M <= 4 ? 1 : -1;
+  return row < 0 ? nullptr : table[row][p.NB - 1];
+}
 
 const void* i8_kernel(int MB, const I8Plan& p) {
   static const void* const stretch[4][4] = {
@@ -448,7 +664,12 @@ int gemm_i8(const lowm_gemm_i8_args* u, hipStream_t stream) {
   a.K = u->K;
   a.f32 = u->c_type == LOWM_F32;
   uint8_t* w = static_cast<uint8_t*>(u->workspace);
+  void* args[] = {&a};
   if (!quantised) {
+    const I8Plan p = i8_plan(u->M, u->N, u->K, false);
+    const int tiles = p.tiles(u->N);
+    if (const void* fn = few_kernel(u->M, u->K, p, tiles))
+      return launched(hipLaunchKernel(fn, dim3((unsigned)tiles), dim3(kThreads), args, 0, stream));
     uint8_t* q = w + kI8LineBytes + kI8SlotBytes;
     float* s = reinterpret_cast<float*>(w + need - LOWM_MAX_M * sizeof(float));
     const int rc = quantize_rows(u->A, LOWM_BF16, K, u->M, u->K, q, s, stream);
@@ -462,7 +683,6 @@ int gemm_i8(const lowm_gemm_i8_args* u, hipStream_t stream) {
   a.slots = reinterpret_cast<uint32_t*>(w + (w ? kI8LineBytes : 0));
   const size_t tiles = (size_t)p.tiles(u->N);
   const size_t grid = p.panel ? tiles : (tiles + kXcds - 1) / kXcds * kXcds * p.splits;
-  void* args[] = {&a};
   return launched(hipLaunchKernel(i8_kernel((u->M + 15) / 16, p), dim3((unsigned)grid),
                                   dim3(p.panel ? kPanelWaves * kWave : kThreads), args, 0,
                                   stream));

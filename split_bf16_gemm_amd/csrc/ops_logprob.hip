@@ -266,14 +266,17 @@ __global__ __launch_bounds__(kTh, 8) void token_logprobs_kernel(LogprobArgs a) {
     } else {
 #pragma unroll
       for (int r = 0; r < kRuns; ++r) {
-        w[r] = ops_u32x4{R::kMask, R::kMask, R::kMask, R::kMask};
-        if (j0 + r * kTh + tid < runs) w[r] = body[j0 + r * kTh + tid];
+        // (read something and drop it: loads under a branch wait for one another)
+        const int j = j0 + r * kTh + tid;
+        w[r] = body[j < runs ? j : runs - 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[r][i] = j < runs ? w[r][i] : R::kMask;
       }
     }
   };
 
   ops_u32x4 even[kRuns], odd[kRuns];
-  fetch(0, even);
+  if (chunks > 0) fetch(0, even);
   float token_logit;
   const bool token_ok = token_of(u, row, &token_logit);
   Sums sum{kNone, 0.f, 0.f};

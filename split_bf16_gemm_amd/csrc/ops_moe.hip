@@ -103,7 +103,7 @@ struct MoeArgs {
 // The wavefronts cut D between them and load their operands straight into
 // registers in the matrix layout, kRouteBatch steps at a time: there is little
 // to read and one round trip to wait for, so a ring would only add trips.
-constexpr int kRouteBatch = 4;
+[[maybe_unused]] constexpr int kRouteBatch = 4;
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
 
@@ -239,19 +239,32 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
       a.router + (size_t)(e0 + l16 < a.E ? e0 + l16 : a.E - 1) * a.D * 2;
   const uint8_t* x = a.x + (size_t)(t0 + l16 < a.T ? t0 + l16 : a.T - 1) * a.D * 2;
   f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-  for (int s = s0; s < s1; s += kRouteBatch) {
-    u32x4 wv[2 * kRouteBatch], xv[2 * kRouteBatch];
+  auto batch = [&](auto n_c, int s) {
+    constexpr int N = 2 * decltype(n_c)::value;
+    u32x4 wv[N], xv[N];
 #pragma unroll
-    for (int j = 0; j < 2 * kRouteBatch; ++j) {
+    for (int j = 0; j < N; ++j) {
       const int k = (2 * s + j) * 64 + 16 * g;           // the lane's 16 bytes
-      const bool in = s + j / 2 < s1 && k < 2 * a.D;
-      wv[j] = xv[j] = u32x4{0u, 0u, 0u, 0u};
-      if (in) wv[j] = *reinterpret_cast<const u32x4*>(w + k);
-      if (in) xv[j] = *reinterpret_cast<const u32x4*>(x + k);
+      // (past the end something is read and dropped: loads under a branch wait
+      // for one another)
+      wv[j] = *reinterpret_cast<const u32x4*>(w + (k < 2 * a.D ? k : 0));
+      xv[j] = *reinterpret_cast<const u32x4*>(x + (k < 2 * a.D ? k : 0));
     }
 #pragma unroll
-    for (int j = 0; j < 2 * kRouteBatch; ++j) acc[0] = mfma(xv[j], wv[j], acc[0]);
-  }
+    for (int j = 0; j < N; ++j) {
+      const bool in = (2 * s + j) * 64 + 16 * g < 2 * a.D;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        wv[j][i] = in ? wv[j][i] : 0u;
+        xv[j][i] = in ? xv[j][i] : 0u;
+      }
+      acc[0] = mfma(xv[j], wv[j], acc[0]);
+    }
+  };
+  int s = s0;
+  for (; s + kRouteBatch <= s1; s += kRouteBatch)
+    batch(std::integral_constant<int, kRouteBatch>{}, s);
+  for (; s < s1; ++s) batch(std::integral_constant<int, 1>{}, s);
   stream_settle(acc);
   f32x4* sums = reinterpret_cast<f32x4*>(logits);
   static_assert(sizeof(logits) >= kRouteThreads * sizeof(f32x4), "the sums fit");
@@ -363,20 +376,6 @@ struct DownShape {
   using S = StreamShape<1, 2, R>;
   static constexpr int kRings = kWaves * S::kRing * 16;
 };
-
-// LDS accesses the compiler does not see, for tables read while loads into LDS
-// are in flight (it would wait for all of those first).
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
-}
-__device__ __forceinline__ ops_u32x2 lds_read8_opaque(const void* p) {
-  ops_u32x2 v;
-  asm volatile("ds_read_b64 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(v) : "v"(lds_address(p)) : "memory");
-  return v;
-}
-__device__ __forceinline__ void lds_add_opaque(float* p, float v) {
-  asm volatile("ds_add_f32 %0, %1" : : "v"(lds_address(p)), "v"(v) : "memory");
-}
 
 // The segments' steps as one sequence: step q is step q mod n of segment q / n.
 template <int R>

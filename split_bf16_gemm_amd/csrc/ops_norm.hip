@@ -66,19 +66,33 @@ struct Row {
   }
   __device__ __forceinline__ bool has(int v, int i) const { return at(v, i) < D; }
 
-  __device__ __forceinline__ void load(const void* p, int64_t base, bool f32, float fill,
-                                       float (&x)[V][8]) const {
+  // What a lane reads of a row, and later its values.  Past the row's end the
+  // row's first elements are read and dropped: loads under a branch wait for one
+  // another.
+  struct Held {
+    Raw8 v[VEC ? V : 1];
+    float s[VEC ? 1 : V][8];
+  };
+  __device__ __forceinline__ Held load(const void* p, int64_t base, bool f32) const {
+    Held h;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if constexpr (VEC) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[v][i] = fill;
-        if (has(v, 0)) load8(p, base + at(v, 0), f32, x[v]);
+        h.v[v] = load8(p, base + (has(v, 0) ? at(v, 0) : 0), f32);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[v][i] = has(v, i) ? load1(p, base + at(v, i), f32) : fill;
+        for (int i = 0; i < 8; ++i) h.s[v][i] = load1(p, base + (has(v, i) ? at(v, i) : 0), f32);
       }
+    }
+    return h;
+  }
+  __device__ __forceinline__ void values(const Held& h, bool f32, float (&x)[V][8]) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (VEC) values8(h.v[v], f32, x[v]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[v][i] = has(v, i) ? (VEC ? x[v][i] : h.s[VEC ? 0 : v][i]) : 0.f;
     }
   }
   __device__ __forceinline__ void store(void* p, int64_t base, bool f32,
@@ -126,10 +140,8 @@ __device__ __forceinline__ void normalise(const Row<G, V, VEC>& row, Group<G>& g
     for (int i = 0; i < 8; ++i) x[v][i] *= k;
 }
 
-// Row to int8: s = max|x| / 127 and q = rint(x / s), both with the correctly
-// rounded divide, so that q is the same number on any machine.  The magnitudes
-// are compared as bit patterns: a NaN or an infinity then comes out on top
-// instead of being passed over, and gives the row the scale NaN.
+// Row to int8 (RowScale).  The magnitudes are compared as bit patterns, so that a
+// NaN or an infinity comes out on top instead of being passed over.
 template <int G, int V, bool VEC>
 __device__ __forceinline__ void quantise(const Row<G, V, VEC>& row, Group<G>& grp,
                                          const float (&x)[V][8], int8_t* q, int64_t base,
@@ -143,31 +155,18 @@ __device__ __forceinline__ void quantise(const Row<G, V, VEC>& row, Group<G>& gr
       if (row.has(v, i)) top = b > top ? b : top;
     }
   top = grp.umax(top);
-  const bool finite = top < 0x7f800000u;
-  const float s = __builtin_bit_cast(float, top) / 127.0f;
-  if (row.lane == 0) *scale = finite ? s : __builtin_nanf("");
-  const bool some = finite && s > 0.f;
+  const RowScale rs(top);
+  if (row.lane == 0) *scale = rs.scale;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    int n[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // A scale in the subnormals can be rounded far enough that a quotient
-      // passes 127: such a value is held at 127.
-      const float t = some ? rintf(x[v][i] / s) : 0.f;
-      n[i] = (int)fminf(fmaxf(t, -127.f), 127.f);
-    }
+    const ops_u32x2 w = {rs.quantise4(x[v][0], x[v][1], x[v][2], x[v][3]),
+                         rs.quantise4(x[v][4], x[v][5], x[v][6], x[v][7])};
     if constexpr (VEC) {
-      ops_u32x2 w;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[h] = (uint32_t)(n[4 * h] & 255) | (uint32_t)(n[4 * h + 1] & 255) << 8 |
-               (uint32_t)(n[4 * h + 2] & 255) << 16 | (uint32_t)n[4 * h + 3] << 24;
       if (row.has(v, 0)) *reinterpret_cast<ops_u32x2*>(q + base + row.at(v, 0)) = w;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (row.has(v, i)) q[base + row.at(v, i)] = (int8_t)n[i];
+        if (row.has(v, i)) q[base + row.at(v, i)] = (int8_t)(w[i / 4] >> 8 * (i % 4));
     }
   }
 }
@@ -185,36 +184,36 @@ __global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(NormArg
   const Row<G, V, VEC> row{(int)threadIdx.x % G, u.D};
   Group<G> grp{lds};
 
-  float p[V][8], r[V][8], w[V][8], g[V][8];
-  row.load(u.y, m * u.ld_y, u.y_type == LOWM_F32, 0.f, p);
-  row.load(u.r, m * u.ld_r, u.r_type == LOWM_F32, 0.f, r);
+  // Every load, then every value.  An operand that is not there reads y again.
   const bool post = u.flags & LOWM_NORM_POST, center = u.flags & LOWM_NORM_CENTER;
-  // what multiplies the branch: b * gate * w_post
+  const bool pre = !(u.flags & LOWM_NORM_NO_PRE);
+  const bool weigh_post = post && u.w_post, weigh_pre = pre && u.w_pre;
+  const bool y32 = u.y_type == LOWM_F32, r32 = u.r_type == LOWM_F32, w32 = u.w_type == LOWM_F32,
+             g32 = u.gate_type == LOWM_F32, gate_row = u.gate && u.gate_col;
+  const int64_t at_y = m * u.ld_y;
+  const auto held_y = row.load(u.y, at_y, y32);
+  const auto held_r = row.load(u.r, m * u.ld_r, r32);
+  const auto held_post =
+      row.load(weigh_post ? u.w_post : u.y, weigh_post ? 0 : at_y, weigh_post ? w32 : y32);
+  const auto held_gate =
+      row.load(gate_row ? u.gate : u.y, gate_row ? m * u.gate_row : at_y, gate_row ? g32 : y32);
+  const auto held_pre =
+      row.load(weigh_pre ? u.w_pre : u.y, weigh_pre ? 0 : at_y, weigh_pre ? w32 : y32);
+  const float gate_one = u.gate && !u.gate_col ? load1(u.gate, m * u.gate_row, g32) : 1.f;
+
+  float p[V][8], r[V][8], w[V][8], g[V][8];
+  row.values(held_y, y32, p);
+  // what multiplies the branch: gate * w_post
+  row.values(held_post, w32, w);
+  row.values(held_gate, g32, g);
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[v][i] = 1.f;
-  if (post && u.w_post) row.load(u.w_post, 0, u.w_type == LOWM_F32, 0.f, g);
-  if (u.gate) {
-    if (u.gate_col) {
-      row.load(u.gate, m * u.gate_row, u.gate_type == LOWM_F32, 0.f, w);
-    } else {
-      const float one = load1(u.gate, m * u.gate_row, u.gate_type == LOWM_F32);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[v][i] = one;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[v][i] *= w[v][i];
-  }
-  const bool pre = !(u.flags & LOWM_NORM_NO_PRE);
-  const bool weigh = pre && u.w_pre;
-  if (weigh) row.load(u.w_pre, 0, u.w_type == LOWM_F32, 0.f, w);
+    for (int i = 0; i < 8; ++i)
+      g[v][i] = (gate_row ? g[v][i] : gate_one) * (weigh_post ? w[v][i] : 1.f);
 
   if (post) normalise(row, grp, center, u.eps, p);
+  row.values(held_r, r32, r);
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -222,10 +221,11 @@ __global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(NormArg
       const float t = u.residual_scale * r[v][i] + u.branch_scale * (g[v][i] * p[v][i]);
       r[v][i] = row.has(v, i) ? t : 0.f;
     }
-  row.store(u.r_out, m * u.ld_r_out, u.r_type == LOWM_F32, r);
+  row.store(u.r_out, m * u.ld_r_out, r32, r);
   if (!pre) return;
   normalise(row, grp, center, u.eps, r);
-  if (weigh) {
+  if (weigh_pre) {
+    row.values(held_pre, w32, w);
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(group_threads(G)) void quantize_rows_kernel(QuantAr
   const Row<G, V, VEC> row{(int)threadIdx.x % G, a.D};
   Group<G> grp{lds};
   float x[V][8];
-  row.load(a.x, m * a.ld, a.f32 != 0, 0.f, x);
+  row.values(row.load(a.x, m * a.ld, a.f32 != 0), a.f32 != 0, x);
   quantise(row, grp, x, a.q, m * (int64_t)a.D, a.scale + m);
 }
 

@@ -39,6 +39,24 @@ __device__ __forceinline__ void stream_settle(i32x4 (&acc)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+a"(acc[i]));
 }
 
+// LDS accesses the compiler does not see, for use while loads into LDS are in
+// flight (it would wait for all of those first).  A wavefront's own complete in
+// order; the read waits for itself.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+__device__ __forceinline__ ops_u32x2 lds_read8_opaque(const void* p) {
+  ops_u32x2 v;
+  asm volatile("ds_read_b64 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(v) : "v"(lds_address(p)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void lds_write8_opaque(void* p, ops_u32x2 v) {
+  asm volatile("ds_write_b64 %0, %1" : : "v"(lds_address(p)), "v"(v) : "memory");
+}
+__device__ __forceinline__ void lds_add_opaque(float* p, float v) {
+  asm volatile("ds_add_f32 %0, %1" : : "v"(lds_address(p)), "v"(v) : "memory");
+}
+
 // NB blocks of 16 weight rows, AP pieces of 8 activation rows, R ring slots.
 template <int NB, int AP, int R>
 struct StreamShape {

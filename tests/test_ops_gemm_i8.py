@@ -83,7 +83,10 @@ def test_the_largest_sums():
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(1, 6144, 4096), (1, 40, 16), (4, 300, 8192), (13, 70, 4112),
                                    (16, 512, 4096), (17, 128, 1536), (64, 1000, 4096),
-                                   (2, 48, 32768), (64, 64, 32768), (1, 33, 32752)])
+                                   (2, 48, 32768), (64, 64, 32768), (1, 33, 32752),
+                                   (3, 100, 48), (4, 16384, 512), (5, 700, 4096), (8, 6144, 4080),
+                                   (8, 16400, 640), (2, 12000, 8192), (4, 90, 8176), (6, 50, 1040),
+                                   (7, 2304, 144), (8, 9000, 4096), (1, 20, 4112)])
 def test_bf16_rows_are_quantised_as_quantize_rows_does(M, N, K):
     g = torch.Generator().manual_seed(K + M)
     _, _, W, sw = operands(g, 1, N, K)
