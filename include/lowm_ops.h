@@ -156,7 +156,7 @@ int lowm_gemm_i8(const lowm_gemm_i8_args* args, void* stream);
  * The workspace (lowm_moe_workspace_bytes, 256-byte aligned) is zeroed once
  * before its first use; every call that completes leaves what must be zero so,
  * for any sizes.  One workspace per call in flight.  lowm_workspace_status of
- * the GEMM reads it too, with N = D + 16.
+ * the GEMM reads it too, with N = D + 80.
  */
 #define LOWM_MOE_MAX_T 64
 #define LOWM_MOE_MAX_E 256

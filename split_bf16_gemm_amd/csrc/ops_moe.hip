@@ -5,9 +5,9 @@
 // token chose is read once, 6 D I bytes, against a few rows of activations.
 // Three kernels:
 //   route  l = x router^T by tiles of 16 experts and 16 tokens (and, with few of
-//          those, stretches of D); the last workgroup to arrive picks each token's experts and sorts the (token, expert)
-//          pairs by expert into segments of up to 16 rows, the matrix
-//          instructions' height;
+//          those, stretches of D); the last workgroup of a block of tokens picks
+//          their experts, and the last block's sorts the (token, expert) pairs by
+//          expert into segments of up to 16 rows, the matrix instructions' height;
 //   up     one workgroup per segment and 16 columns of h: 16 gate and 16 up rows;
 //   down   one workgroup per 16 output columns walks the segments as one long
 //          inner dimension, cut evenly over its wavefronts (and, for a narrow D,
@@ -42,13 +42,16 @@ struct Pair {
 // The first part has one place and size for all calls, so that a call never
 // finds another size's leavings where its zeros have to be.
 constexpr size_t up256(size_t b) { return (b + 255) / 256 * 256; }
-constexpr size_t kCounterBytes = 256 * (1 + (size_t)kMaxSize / kCols);
+constexpr int kFirstTileLine = 1 + kMaxT / 16;   // after the router's
+constexpr size_t kCounterBytes = 256 * (kFirstTileLine + (size_t)kMaxSize / kCols);
+constexpr size_t kPairSlots = 2 * (size_t)kMaxT * kMaxK;
 constexpr int kMaxRouteSplits = 4;
 constexpr size_t kRouteSlots = kMaxRouteSplits * (size_t)kMaxT * kMaxE;
 constexpr size_t kDownSlots = 512 * (size_t)kMaxT * kCols;       // most tiles * splits, times the tile
 constexpr size_t kRouteAt = kCounterBytes;
 constexpr size_t kDownAt = kRouteAt + 4 * kRouteSlots;
-constexpr size_t kListsAt = kDownAt + 4 * kDownSlots;
+constexpr size_t kPairsAt = kDownAt + 4 * kDownSlots;
+constexpr size_t kListsAt = kPairsAt + 4 * kPairSlots;
 
 struct Layout {
   int route_splits, down_splits, max_segments;
@@ -58,10 +61,10 @@ struct Layout {
 static Layout layout_of(int T, int D, int I, int E, int K) {
   Layout l{};
   // Router: a tile's weights come from far and slowly to one CU, so few tiles
-  // are cut along D: up to 32 workgroups, a step at least for each wavefront.
+  // are cut along D: up to 64 workgroups, a step at least for each wavefront.
   const int router_tiles = ((E + 15) / 16) * ((T + 15) / 16), steps = (2 * D + 127) / 128;
   l.route_splits = 1;
-  while (l.route_splits < kMaxRouteSplits && router_tiles * l.route_splits * 2 <= 32 &&
+  while (l.route_splits < kMaxRouteSplits && router_tiles * l.route_splits * 2 <= 64 &&
          steps >= 2 * l.route_splits * kRouteWaves)
     l.route_splits *= 2;
   // Down: enough workgroups for 256 CUs (tiles * splits < 512).
@@ -86,8 +89,9 @@ struct MoeArgs {
   __bf16* out;
   int* ids;
   float* gates;
-  uint32_t* counters;                     // [1 + tiles], 64 words apart; 0 is the router's
+  uint32_t* counters;                     // lines: the router's, its blocks', the down tiles'
   uint32_t* route_slots;                  // [route_splits][T][E]
+  uint32_t* pair_slots;                   // [T][top_k][2]: id + 1, gate
   uint32_t* down_slots;                   // [tiles][down_splits][T][kCols]
   int* lists;                             // number of segments, 3 unused, then the segments
   Pair* pairs;
@@ -107,82 +111,100 @@ struct MoeArgs {
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
 
-// One token's experts, by one wavefront: lane l holds experts l, l + 64, ...
-__device__ __forceinline__ void pick_experts(const MoeArgs& a, int t, const float* logits,
-                                             int (*chosen)[kMaxK], float (*gates)[kMaxK]) {
+constexpr int kBlock = 16;                // tokens of a router tile
+
+struct RouteLds {
+  float logits[kBlock * kMaxE];           // of one block of tokens
+  int chosen[kMaxT][kMaxK];
+  float gates[kMaxT][kMaxK];
+  uint32_t mask[kMaxE][2];
+  uint32_t starts[kMaxE];
+  uint32_t ends[kMaxE / kWave];
+  int last;
+};
+
+// One token's experts in order and their gates, by one wavefront: lane l holds
+// experts l, l + 64, ... (NJ of them), and in the end the l-th choice.
+template <int NJ>
+__device__ __forceinline__ void pick_experts(const MoeArgs& a, const float* logits, int& my_id,
+                                             float& my_gate) {
   const int lane = threadIdx.x & (kWave - 1);
-  constexpr int kPer = kMaxE / kWave;
-  float l[kPer];
-  float m = -__builtin_inff();
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = lane + kWave * j;
-    l[j] = e < a.E ? logits[t * a.E + e] : -__builtin_inff();
-    m = fmaxf(m, l[j]);
-  }
-  m = value_of(wave_umax(order(m)));
   const bool sig = a.flags & LOWM_MOE_SIGMOID, renorm = !(a.flags & LOWM_MOE_NO_RENORM);
-  float all = 1.f;
-  if (!sig) {
+  float l[NJ];
+  uint32_t o[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int e = lane + kWave * j;
+    l[j] = logits[e < a.E ? e : 0];
+    o[j] = e < a.E ? order(l[j]) : 0u;
+  }
+  // Softmax over all experts only where it shows: in a choice by score + bias, or
+  // in gates that are not divided by the chosen ones' sum.  Otherwise any
+  // multiple of the scores does, such as e^(l - the chosen ones' largest l).
+  const bool whole = !sig && (!renorm || a.bias);
+  float most = 0.f, total = 1.f;
+  if (whole) {
+    uint32_t top = o[0];
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) top = o[j] > top ? o[j] : top;
+    most = value_of(wave_umax(top));
     float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (lane + kWave * j < a.E) s += expf(l[j] - m);
-    all = wave_sum(s);
+    for (int j = 0; j < NJ; ++j) s += lane + kWave * j < a.E ? expf(l[j] - most) : 0.f;
+    total = wave_sum(s);
   }
-  auto score = [&](float v) { return sig ? sigmoid(v) : expf(v - m) / all; };
-  uint32_t o[kPer];
+  if (a.bias) {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = lane + kWave * j;
-    o[j] = e < a.E ? order(a.bias ? score(l[j]) + a.bias[e] : l[j]) : 0u;
+    for (int j = 0; j < NJ; ++j) {
+      const int e = lane + kWave * j;
+      const float score = sig ? sigmoid(l[j]) : expf(l[j] - most) / total;
+      o[j] = e < a.E ? order(score + a.bias[e < a.E ? e : 0]) : 0u;
+    }
   }
-  int my_id = 0;
+  my_id = 0;
   for (int i = 0; i < a.top_k; ++i) {
     uint32_t top = o[0];
 #pragma unroll
-    for (int j = 1; j < kPer; ++j) top = o[j] > top ? o[j] : top;
+    for (int j = 1; j < NJ; ++j) top = o[j] > top ? o[j] : top;
     top = wave_umax(top);
     // the lowest id among equals: the first j, then the first lane
-    int e = -1;
+    uint64_t at = __ballot(o[0] == top);
+    int first = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const uint64_t at = __ballot(o[j] == top);
-      if (e < 0 && at) e = kWave * j + __builtin_ctzll(at);
-    }
+    for (int j = 1; j < NJ; ++j)
+      if (!at) {
+        at = __ballot(o[j] == top);
+        first = kWave * j;
+      }
+    const int e = first + __builtin_ctzll(at);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (lane + kWave * j == e) o[j] = 0u;
-    if (lane == i) my_id = e;
+    for (int j = 0; j < NJ; ++j) o[j] = lane + kWave * j == e ? 0u : o[j];
+    my_id = lane == i ? e : my_id;
   }
-  const float mine = lane < a.top_k ? score(logits[t * a.E + my_id]) : 0.f;
-  const float sum = wave_sum(mine);
-  if (lane < a.top_k) {
-    const float gate = (renorm ? mine / sum : mine) * a.routed_scale;
-    chosen[t][lane] = my_id;
-    gates[t][lane] = gate;
-    if (a.ids) a.ids[t * a.top_k + lane] = my_id;
-    if (a.gates) a.gates[t * a.top_k + lane] = gate;
-  }
+  const bool mine = lane < a.top_k;
+  const float v = logits[my_id];
+  // (without a bias the first choice has the largest logit)
+  if (!whole) most = __builtin_bit_cast(
+      float, (uint32_t)__builtin_amdgcn_readfirstlane((int)__builtin_bit_cast(uint32_t, v)));
+  const float score = !mine ? 0.f : sig ? sigmoid(v) : expf(v - most) / total;
+  const float sum = wave_sum(score);
+  my_gate = (renorm ? score / sum : score) * a.routed_scale;
 }
 
 // The pairs in order of expert, then token, and their segments.  Each expert's
 // tokens are the bits of a mask, so a pair's place is a count of bits below.
-__device__ __forceinline__ void sort_pairs(const MoeArgs& a, const int (*chosen)[kMaxK],
-                                           const float (*gates)[kMaxK], uint32_t (*mask)[2],
-                                           uint32_t* starts) {
+__device__ __forceinline__ void sort_pairs(const MoeArgs& a, RouteLds& r) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int pairs = a.T * a.top_k;
   for (int p = tid; p < pairs; p += kRouteThreads) {
     const int t = p / a.top_k;
-    atomicOr(&mask[chosen[t][p % a.top_k]][t >> 5], 1u << (t & 31));
+    atomicOr(&r.mask[r.chosen[t][p - t * a.top_k]][t >> 5], 1u << (t & 31));
   }
-  __shared__ uint32_t ends[kMaxE / kWave];
   __syncthreads();
   // thread e: expert e's pairs (low half) and segments (high half), summed over
   // the experts before it
   const bool one = tid < kMaxE;
-  const int rows = one ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
+  const int rows = one ? __popc(r.mask[tid][0]) + __popc(r.mask[tid][1]) : 0;
   const uint32_t own = (uint32_t)rows | (uint32_t)((rows + kSegRows - 1) / kSegRows) << 16;
   uint32_t before = own;
 #pragma unroll
@@ -190,17 +212,17 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, const int (*chosen)
     const uint32_t v = __shfl_up(before, off);
     if (lane >= off) before += v;
   }
-  if (one && lane == kWave - 1) ends[wave] = before;
+  if (one && lane == kWave - 1) r.ends[wave] = before;
   __syncthreads();
   if (one) {
     uint32_t total = 0;
 #pragma unroll
     for (int w = 0; w < kMaxE / kWave; ++w) {
-      if (w < wave) before += ends[w];
-      total += ends[w];
+      if (w < wave) before += r.ends[w];
+      total += r.ends[w];
     }
     before -= own;
-    starts[tid] = before & 0xffffu;
+    r.starts[tid] = before & 0xffffu;
     Segment* segments = reinterpret_cast<Segment*>(a.lists + 4);
     for (int s = 0; s * kSegRows < rows; ++s)
       segments[(before >> 16) + s] =
@@ -210,27 +232,22 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, const int (*chosen)
   }
   __syncthreads();
   for (int p = tid; p < pairs; p += kRouteThreads) {
-    const int t = p / a.top_k, e = chosen[t][p % a.top_k];
-    const uint32_t lo = mask[e][0], hi = mask[e][1];
+    const int t = p / a.top_k, e = r.chosen[t][p - t * a.top_k];
+    const uint32_t lo = r.mask[e][0], hi = r.mask[e][1];
     const int below = t < 32 ? __popc(lo & ((1u << t) - 1u))
                              : __popc(lo) + __popc(hi & ((1u << (t - 32)) - 1u));
-    a.pairs[starts[e] + below] = Pair{t, gates[t][p % a.top_k]};
+    a.pairs[r.starts[e] + below] = Pair{t, r.gates[t][p - t * a.top_k]};
   }
 }
 
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ float logits[kMaxT * kMaxE];
-  __shared__ int chosen[kMaxT][kMaxK];
-  __shared__ float gates[kMaxT][kMaxK];
-  __shared__ uint32_t mask[kMaxE][2];
-  __shared__ uint32_t starts[kMaxE];
-  __shared__ int last;
+  __shared__ RouteLds r;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int g = lane >> 4, l16 = lane & 15;
   const int tiles = (a.E + 15) / 16;
   const int split = blockIdx.x % a.route_splits, place = blockIdx.x / a.route_splits;
-  const int e0 = place % tiles * 16, t0 = place / tiles * 16;
+  const int e0 = place % tiles * 16, block = place / tiles, t0 = block * kBlock;
 
   const int steps = (2 * a.D + 127) / 128, parts = a.route_splits * kRouteWaves;
   const int part = split * kRouteWaves + wave;
@@ -266,10 +283,10 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
     batch(std::integral_constant<int, kRouteBatch>{}, s);
   for (; s < s1; ++s) batch(std::integral_constant<int, 1>{}, s);
   stream_settle(acc);
-  f32x4* sums = reinterpret_cast<f32x4*>(logits);
-  static_assert(sizeof(logits) >= kRouteThreads * sizeof(f32x4), "the sums fit");
+  f32x4* sums = reinterpret_cast<f32x4*>(r.logits);
+  static_assert(sizeof(r.logits) >= kRouteThreads * sizeof(f32x4), "the sums fit");
   sums[wave * kWave + lane] = acc[0];
-  if (threadIdx.x < 2 * kMaxE) (&mask[0][0])[threadIdx.x] = 0u;
+  if (threadIdx.x < 2 * kMaxE) (&r.mask[0][0])[threadIdx.x] = 0u;
   __syncthreads();
   // Wavefront i adds row 4 g + i of lane group g, in 64 bits so that experts next
   // to the border are told apart as well as fp32 can.
@@ -282,27 +299,70 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
     if (t < a.T && e < a.E)
       store_slot(a.route_slots + ((size_t)split * a.T + t) * a.E + e, enc_partial((float)v));
   }
-  if (!arrive_last(a.counters, gridDim.x, &last)) return;
+  uint32_t* line = a.counters + (size_t)(1 + block) * kCtrStride;
+  if (!arrive_last(line, tiles * a.route_splits, &r.last)) return;
 
-  // The last workgroup has every logit before it.
-  const int cells = a.T * a.E;
-  for (int c = threadIdx.x; c < cells; c += kRouteThreads) {
-    uint32_t v[kMaxRouteSplits];
+  // The last workgroup of a block of tokens has all its logits before it.
+  const int rows = a.T - t0 < kBlock ? a.T - t0 : kBlock, cells = rows * a.E;
+  constexpr int kAtOnce = 4;              // cells a thread asks for in one trip
+  auto slot = [&](int c, int s) {
+    return a.route_slots + ((size_t)s * a.T + t0) * a.E + c;
+  };
+  for (int c0 = threadIdx.x; c0 < cells; c0 += kAtOnce * kRouteThreads) {
+    uint32_t v[kAtOnce][kMaxRouteSplits];
 #pragma unroll
-    for (int s = 0; s < kMaxRouteSplits; ++s)
-      if (s < a.route_splits) v[s] = load_slot(a.route_slots + (size_t)s * cells + c);
-    double sum = 0.0;
+    for (int j = 0; j < kAtOnce; ++j)
 #pragma unroll
-    for (int s = 0; s < kMaxRouteSplits; ++s)
-      if (s < a.route_splits)
-        sum += (double)dec_partial(
-            take_slot(a.route_slots + (size_t)s * cells + c, v[s], a.counters));
-    logits[c] = (float)sum;
+      for (int s = 0; s < kMaxRouteSplits; ++s) {
+        const int c = c0 + j * kRouteThreads;
+        v[j][s] = load_slot(slot(c < cells ? c : c0, s < a.route_splits ? s : 0));
+      }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int c = c0 + j * kRouteThreads;
+      if (c >= cells) break;
+      double sum = 0.0;
+#pragma unroll
+      for (int s = 0; s < kMaxRouteSplits; ++s)
+        if (s < a.route_splits) sum += (double)dec_partial(take_slot(slot(c, s), v[j][s], line));
+      r.logits[c] = (float)sum;
+    }
   }
   __syncthreads();
-  for (int t = wave; t < a.T; t += kRouteWaves) pick_experts(a, t, logits, chosen, gates);
+  const int blocks = (a.T + kBlock - 1) / kBlock;
+  if (wave < rows) {
+    int id;
+    float gate;
+    const float* l = r.logits + wave * a.E;
+    if (a.E <= kWave) pick_experts<1>(a, l, id, gate);
+    else if (a.E <= 2 * kWave) pick_experts<2>(a, l, id, gate);
+    else pick_experts<kMaxE / kWave>(a, l, id, gate);
+    const int t = t0 + wave;
+    if (lane < a.top_k) {
+      const int p = t * a.top_k + lane;
+      if (a.ids) a.ids[p] = id;
+      if (a.gates) a.gates[p] = gate;
+      if (blocks == 1) {
+        r.chosen[t][lane] = id;
+        r.gates[t][lane] = gate;
+      } else {
+        store_slot(a.pair_slots + 2 * p, (uint32_t)id + 1u);
+        store_slot(a.pair_slots + 2 * p + 1, enc_partial(gate));
+      }
+    }
+  }
+  if (blocks > 1) {
+    // The last block's workgroup has every token's choice before it.
+    if (!arrive_last(a.counters, blocks, &r.last)) return;
+    for (int p = threadIdx.x; p < a.T * a.top_k; p += kRouteThreads) {
+      const int t = p / a.top_k, i = p - t * a.top_k;
+      const uint32_t w0 = load_slot(a.pair_slots + 2 * p), w1 = load_slot(a.pair_slots + 2 * p + 1);
+      r.chosen[t][i] = (int)take_slot(a.pair_slots + 2 * p, w0, a.counters) - 1;
+      r.gates[t][i] = dec_partial(take_slot(a.pair_slots + 2 * p + 1, w1, a.counters));
+    }
+  }
   __syncthreads();
-  sort_pairs(a, chosen, gates, mask, starts);
+  sort_pairs(a, r);
 #endif
 }
 
@@ -553,7 +613,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
       const int c = threadIdx.x + j * kThreads;
       if (c < cells) store_slot(slots + (size_t)split * cells + c, enc_partial(v[j]));
     }
-    uint32_t* line = a.counters + (size_t)(1 + tile) * kCtrStride;
+    uint32_t* line = a.counters + (size_t)(kFirstTileLine + tile) * kCtrStride;
     if (!arrive_last(line, a.down_splits, &last)) return;
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
@@ -631,6 +691,7 @@ int moe(const lowm_moe_args* u, hipStream_t stream) {
   a.counters = reinterpret_cast<uint32_t*>(ws);
   a.route_slots = reinterpret_cast<uint32_t*>(ws + kRouteAt);
   a.down_slots = reinterpret_cast<uint32_t*>(ws + kDownAt);
+  a.pair_slots = reinterpret_cast<uint32_t*>(ws + kPairsAt);
   a.lists = reinterpret_cast<int*>(ws + kListsAt);
   a.pairs = reinterpret_cast<Pair*>(ws + l.pairs);
   a.h = reinterpret_cast<uint8_t*>(ws + l.h);

@@ -65,7 +65,7 @@ def draw(g, T, D, I, E, k):
 
 def workspace_is_clean(ws, T, D, I, E, k):
     """What has to be zero between calls: all of the front part."""
-    front = 256 * (1 + 65536 // 16) + 4 * 4 * 64 * 256 + 4 * 512 * 64 * 16
+    front = 256 * (5 + 65536 // 16) + 4 * (4 * 64 * 256 + 512 * 64 * 16 + 2 * 64 * 16)
     assert ws[:front].count_nonzero() == 0
 
 
@@ -201,7 +201,7 @@ def test_same_bits_each_time_in_a_graph_and_on_another_stream():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
         assert all(torch.equal(a, b) for a, b in zip(other, want))
-    assert sbg.load().workspace_status(ws, 1032 + 16) == (0, 0)
+    assert sbg.load().workspace_status(ws, 1032 + 80) == (0, 0)
 
 
 @pytest.mark.gpu
