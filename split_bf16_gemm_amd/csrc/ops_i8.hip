@@ -9,9 +9,9 @@
 // caches.  Two kinds of workgroup:
 //   stretch  16*NB rows of W, its four wavefronts a stretch of K each
 //            (ops_stream.cuh), their sums added through LDS;
-//   panel    128*NB rows of W, 16*NB to each of eight wavefronts, all of K for
-//            each, with one panel of A per step for all of them: more rows of W
-//            for each byte of A read.
+//   panel    16 rows of W to each of 4 to 16 wavefronts, all of K for each, with
+//            one panel of A per step for all of them: more rows of W for each
+//            byte of A read.
 // Where they are too few for the CUs, K is split over several workgroups whose
 // int32 sums the last to arrive adds.  A few rows of bf16 are quantised by each
 // workgroup for itself while its first rows of W are on their way (few); more
@@ -381,41 +381,40 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_few_kernel(I8Args a) {
 #endif
 }
 
-// A step's slot of the panel kernel: the panel's pieces, one to a wavefront, then
-// each wavefront's 2*NB pieces of W.
-constexpr int kPanelWaves = 8;
-template <int AP, int NB, int R>
+// A step's slot of the panel kernel: the panel's pieces, then each of the PW
+// wavefronts' two pieces of W.
+template <int AP, int PW, int R>
 struct I8Panel {
   static constexpr int MB = (AP + 1) / 2;
   static constexpr int kPP = 68;
-  static constexpr int kSlot = (2 * MB + 2 * NB * kPanelWaves) * kPP;
+  static constexpr int kEach = AP / PW, kRest = AP % PW;   // panel pieces a wavefront loads
+  static constexpr int kSlot = (2 * MB + 2 * PW) * kPP;
   static constexpr int lds_bytes = R * kSlot * 16;
   static constexpr bool valid =
-      R >= 2 && (R - 1) * (1 + 2 * NB) <= 63 && lds_bytes <= 160 * 1024 - 64;
-  static_assert(AP <= kPanelWaves, "a piece to a wavefront");
+      R >= 2 && (R - 1) * (kEach + 1 + 2) <= 63 && lds_bytes <= 160 * 1024 - 64;
   
 };
 
-// The loop of one wavefront; MINE: whether it loads a piece of the panel (its
-// waits count that load too).
-template <int AP, int NB, int R, bool MINE>
+// The loop of one wavefront; MINE: how many pieces of the panel it loads (its
+// waits count those loads too).
+template <int AP, int PW, int R, int MINE>
 __device__ __forceinline__ void i8_panel_loop(const I8Args& a, u32x4* lds, int n0, int P,
-                                              i32x4 (&acc)[NB * ((AP + 1) / 2)]) {
-  using SH = I8Panel<AP, NB, R>;
-  constexpr int G = 2 * NB + (MINE ? 1 : 0), kPP = SH::kPP, MB = SH::MB;
+                                              i32x4 (&acc)[(AP + 1) / 2]) {
+  using SH = I8Panel<AP, PW, R>;
+  constexpr int G = 2 + MINE, kPP = SH::kPP, MB = SH::MB;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int g = lane >> 4, l16 = lane & 15;
   const int k0 = stream_piece(lane) * 16, left = a.K - k0;
   const int line = __builtin_amdgcn_readfirstlane(left);
-  const int my_w = (2 * MB + wave * 2 * NB) * kPP;       // within a slot
+  const int my_w = (2 * MB + wave * 2) * kPP;       // within a slot
   const uint8_t* src[G];
 #pragma unroll
   for (int t = 0; t < G; ++t) {
-    if (t < 2 * NB) {
+    if (t < 2) {
       const int r = n0 + 8 * t + stream_row(lane);
       src[t] = a.W + (size_t)(r < a.N ? r : a.N - 1) * a.K + k0;
     } else {
-      const int r = 8 * wave + stream_row(lane);
+      const int r = 8 * (wave + (t - 2) * PW) + stream_row(lane);
       src[t] = a.A + (size_t)(r < a.M ? r : a.M - 1) * a.K + k0;
     }
   }
@@ -429,34 +428,29 @@ __device__ __forceinline__ void i8_panel_loop(const I8Args& a, u32x4* lds, int n
     const bool whole = line - at >= 128;
     static_for<G>([&](auto t_c) {
       constexpr int t = decltype(t_c)::value;
-      u32x4* to = slot + (t < 2 * NB ? my_w + t * kPP : wave * kPP);
+      u32x4* to = slot + (t < 2 ? my_w + t * kPP : (wave + (t - 2) * PW) * kPP);
       const uint8_t* from = src[t] + at;
       if (!whole) from = left - at >= 16 ? from : reinterpret_cast<const uint8_t*>(&kZeroPiece);
       __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, 0,
-                                       t < 2 * NB ? kStreamAux : 0);
+                                       t < 2 ? kStreamAux : 0);
     });
     pin_issue();
   };
   auto multiply = [&](const u32x4* slot) {
-    u32x4 v[2 * (NB + MB)];
+    u32x4 v[2 * (1 + MB)];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        v[c * (NB + MB) + j] = lds_read_opaque(slot + my_w + 2 * j * kPP + rpos[c]);
+      v[c * (1 + MB)] = lds_read_opaque(slot + my_w + rpos[c]);
 #pragma unroll
       for (int b = 0; b < MB; ++b)
-        v[c * (NB + MB) + NB + b] = lds_read_opaque(slot + 2 * b * kPP + rpos[c]);
+        v[c * (1 + MB) + 1 + b] = lds_read_opaque(slot + 2 * b * kPP + rpos[c]);
     }
     lds_wait(v);
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-          acc[j * MB + b] =
-              stream_mfma(v[c * (NB + MB) + NB + b], v[c * (NB + MB) + j], acc[j * MB + b]);
+      for (int b = 0; b < MB; ++b)
+        acc[b] = stream_mfma(v[c * (1 + MB) + 1 + b], v[c * (1 + MB)], acc[b]);
   };
   u32x4* const end = lds + R * SH::kSlot;
   u32x4 *fill = lds, *use = lds;
@@ -489,26 +483,25 @@ __device__ __forceinline__ void i8_panel_loop(const I8Args& a, u32x4* lds, int n
   });
 }
 
-template <int AP, int NB, int R>
-__global__ __launch_bounds__(kPanelWaves* kWave) void gemm_i8_panel_kernel(I8Args a) {
+template <int AP, int PW, int R>
+__global__ __launch_bounds__(PW* kWave) void gemm_i8_panel_kernel(I8Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using SH = I8Panel<AP, NB, R>;
+  using SH = I8Panel<AP, PW, R>;
   constexpr int MB = SH::MB;
   __shared__ u32x4 lds[R * SH::kSlot];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int n0 = ((int)blockIdx.x * kPanelWaves + wave) * 16 * NB;
+  const int n0 = ((int)blockIdx.x * PW + wave) * 16;
   const int P = (a.K + 127) / 128;
-  i32x4 acc[NB * MB];
+  i32x4 acc[MB];
 #pragma unroll
-  for (int i = 0; i < NB * MB; ++i) acc[i] = i32x4{0, 0, 0, 0};
-  if (wave < AP)
-    i8_panel_loop<AP, NB, R, true>(a, lds, n0, P, acc);
+  for (int i = 0; i < MB; ++i) acc[i] = i32x4{0, 0, 0, 0};
+  if (wave < SH::kRest)
+    i8_panel_loop<AP, PW, R, SH::kEach + 1>(a, lds, n0, P, acc);
   else
-    i8_panel_loop<AP, NB, R, false>(a, lds, n0, P, acc);
+    i8_panel_loop<AP, PW, R, SH::kEach>(a, lds, n0, P, acc);
   stream_settle(acc);
 #pragma unroll
-  for (int q = 0; q < NB * MB; ++q)
-    i8_store(a, a.a_scale, acc[q], q % MB, n0 + 16 * (q / MB) + (lane & 15), lane >> 4);
+  for (int b = 0; b < MB; ++b) i8_store(a, a.a_scale, acc[b], b, n0 + (lane & 15), lane >> 4);
 #endif
 }
 
@@ -524,16 +517,25 @@ template <int AP, int NB>
 const void* stretch_of() {
   return reinterpret_cast<const void*>(&gemm_i8_stretch_kernel<AP, NB, stretch_ring<AP, NB, 4>()>);
 }
-template <int AP, int NB>
+template <int AP, int PW>
 const void* panel_of() {
-  static_assert(I8Panel<AP, NB, 3>::valid, "the ring fits");
-  return reinterpret_cast<const void*>(&gemm_i8_panel_kernel<AP, NB, 3>);
+  static_assert(I8Panel<AP, PW, 3>::valid, "the ring fits");
+  return reinterpret_cast<const void*>(&gemm_i8_panel_kernel<AP, PW, 3>);
+}
+constexpr int kPanelWaves[] = {4, 6, 8, 12, 16};
+template <int AP>
+const void* panel_by_waves(int waves) {
+  return waves == 4    ? panel_of<AP, 4>()
+         : waves == 6  ? panel_of<AP, 6>()
+         : waves == 8  ? panel_of<AP, 8>()
+         : waves == 12 ? panel_of<AP, 12>()
+                       : panel_of<AP, 16>();
 }
 
 struct I8Plan {
-  bool panel;
+  int panel;                              // the panel kind's wavefronts, 0 for the stretch kind
   int NB, splits;
-  int width() const { return (panel ? 16 * kPanelWaves : 16) * NB; }
+  int width() const { return 16 * (panel ? panel : 1) * NB; }
   int tiles(int N) const { return (int)(((int64_t)N + width() - 1) / width()); }
 };
 
@@ -566,10 +568,10 @@ const void* i8_kernel(int MB, const I8Plan& p) {
       {stretch_of<4, 1>(), stretch_of<4, 2>(), stretch_of<4, 3>(), stretch_of<4, 4>()},
       {stretch_of<6, 1>(), stretch_of<6, 2>(), stretch_of<6, 3>(), stretch_of<6, 4>()},
       {stretch_of<8, 1>(), stretch_of<8, 2>(), stretch_of<8, 3>(), stretch_of<8, 4>()}};
-  static const void* const panel[3][2] = {{panel_of<4, 1>(), panel_of<4, 2>()},
-                                          {panel_of<6, 1>(), panel_of<6, 2>()},
-                                          {panel_of<8, 1>(), panel_of<8, 2>()}};
-  return p.panel ? panel[MB - 2][p.NB - 1] : stretch[MB - 1][p.NB - 1];
+  if (!p.panel) return stretch[MB - 1][p.NB - 1];
+  return MB == 2   ? panel_by_waves<4>(p.panel)
+         : MB == 3 ? panel_by_waves<6>(p.panel)
+                   : panel_by_waves<8>(p.panel);
 }
 
 constexpr int64_t kI8MaxK = 131056;   // 128 * 128 * K stays below 2^31
@@ -581,12 +583,13 @@ constexpr size_t kI8LineBytes = 256 * (size_t)kI8MaxTiles;
 constexpr size_t kI8SlotBytes = (size_t)kI8MaxBlocks * kWave * 4 * 4;
 
 // How to cut the product.  Measured on MI355X, W from HBM, us a call:
-//   - above 16 rows and 16384 columns the panel kind: M 64, K 4096, N 24576 /
-//     32768 / 49152 25.7 / 33.8 / 46.4 against 30.6 / 37.9 / 56.2 for the best
-//     stretch tiles (a workgroup then loads 64 rows of A for 128 or 256 of W, not
-//     for 64); M 24, N 49152 38.6 against 41.2.  At 16 rows it loses (43.0
-//     against 37.4), at N 12288 its tiles are too few (23.8 against 16.8).  The
-//     width with the fewest rounds of 256 workgroups times rows loaded.
+//   - above 16 rows and 16384 columns the panel kind (a workgroup then loads 64
+//     rows of A for up to 256 of W, not for 64), of the width with the fewest
+//     rounds of 256 workgroups times rows loaded.  M 64, K 4096: N 24576 with 6
+//     wavefronts 25.3 (4: 28.3, 8: 26.9, stretch 30.5), N 49152 with 12 37.5 (4:
+//     42.1, 16: 39.6, stretch 56.2), N 32768 with 8 34.1 (4: 31.8, 16: 37.3, stretch
+//     37.9).  M 24, N 49152 38.1 against 41.7.  At 16 rows it loses (43.0 against
+//     37.4), at N 12288 its tiles are too few (19.1 against 16.8).
 //   - otherwise stretch tiles of the width, and the split of K, of least cost:
 //     rounds times bytes loaded by a workgroup, at 67 KB a us, and for a split's
 //     exchange 1 us, 0.25 a split and 0.2 a block of 16 x 16 sums sent.  M 16,
@@ -597,17 +600,23 @@ constexpr size_t kI8SlotBytes = (size_t)kI8MaxBlocks * kWave * 4 * 4;
 I8Plan i8_plan(int M, int N, int K, bool split) {
   const int MB = (M + 15) / 16;
   if (M > 16 && N > 16384) {
-    const I8Plan one{true, 1, 1}, two{true, 2, 1};
-    auto cost = [&](const I8Plan& p) {
-      return (int64_t)(p.tiles(N) + 255) / 256 * (16 * MB + p.width());
-    };
-    return cost(two) < cost(one) ? two : one;
+    I8Plan best{0, 1, 1};
+    int64_t best_cost = 0;
+    for (int waves : kPanelWaves) {
+      const I8Plan p{waves, 1, 1};
+      const int64_t cost = (int64_t)(p.tiles(N) + 255) / 256 * (16 * MB + p.width());
+      if (best.panel == 0 || cost < best_cost) {
+        best = p;
+        best_cost = cost;
+      }
+    }
+    return best;
   }
-  I8Plan best{false, 1, 1};
+  I8Plan best{0, 1, 1};
   double best_us = 0;
   for (int nb = 1; nb <= 4; ++nb)
     for (int s = 1; s <= (split ? kI8MaxSplits : 1); ++s) {
-      const I8Plan p{false, nb, s};
+      const I8Plan p{0, nb, s};
       const int64_t tiles = p.tiles(N);
       if (s > 1 && (tiles > kI8MaxTiles || tiles * s * nb * MB > kI8MaxBlocks)) continue;
       if (s > 1 && K / s < 128 * kWaves) continue;       // a step for every wavefront
@@ -684,7 +693,7 @@ int gemm_i8(const lowm_gemm_i8_args* u, hipStream_t stream) {
   const size_t tiles = (size_t)p.tiles(u->N);
   const size_t grid = p.panel ? tiles : (tiles + kXcds - 1) / kXcds * kXcds * p.splits;
   return launched(hipLaunchKernel(i8_kernel((u->M + 15) / 16, p), dim3((unsigned)grid),
-                                  dim3(p.panel ? kPanelWaves * kWave : kThreads), args, 0,
+                                  dim3(p.panel ? p.panel * kWave : kThreads), args, 0,
                                   stream));
 }
 
