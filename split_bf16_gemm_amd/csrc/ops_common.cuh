@@ -38,7 +38,6 @@ inline int type_bytes(int type) { return type == LOWM_F32 ? 4 : type == LOWM_BF1
 
 typedef uint32_t ops_u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t ops_u32x2 __attribute__((ext_vector_type(2)));
-typedef float ops_f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) {
@@ -51,20 +50,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return (uint32_t)a | ((uint32_t)b << 16);
 }
 
-// Eight consecutive elements of 16-byte aligned memory as they lie there; their
-// values are taken out later, so that a kernel's loads do not wait for one another
-// in the branches on its operands' types.
+// Vectors at any address (the GPU's unaligned access): rows of an odd length or
+// pitch start anywhere.
+struct __attribute__((packed, aligned(1))) AnyU32x4 {
+  ops_u32x4 v;
+};
+struct __attribute__((packed, aligned(1))) AnyU32x2 {
+  ops_u32x2 v;
+};
+
+// Eight consecutive elements as they lie in memory; their values are taken out
+// later, so that a kernel's loads do not wait for one another in the branches on
+// its operands' types.
 struct Raw8 {
   ops_u32x4 a, b;
 };
 __device__ __forceinline__ Raw8 load8(const void* base, int64_t at, bool f32) {
   Raw8 r;
   if (f32) {
-    const ops_u32x4* p = reinterpret_cast<const ops_u32x4*>(static_cast<const float*>(base) + at);
-    r.a = p[0];
-    r.b = p[1];
+    const AnyU32x4* p = reinterpret_cast<const AnyU32x4*>(static_cast<const float*>(base) + at);
+    r.a = p[0].v;
+    r.b = p[1].v;
   } else {
-    r.a = *reinterpret_cast<const ops_u32x4*>(static_cast<const uint16_t*>(base) + at);
+    r.a = reinterpret_cast<const AnyU32x4*>(static_cast<const uint16_t*>(base) + at)->v;
     r.b = ops_u32x4{0u, 0u, 0u, 0u};
   }
   return r;
@@ -91,14 +99,19 @@ __device__ __forceinline__ float load1(const void* base, int64_t at, bool f32) {
 }
 __device__ __forceinline__ void store8(void* base, int64_t at, bool f32, const float (&v)[8]) {
   if (f32) {
-    ops_f32x4* p = reinterpret_cast<ops_f32x4*>(static_cast<float*>(base) + at);
-    p[0] = ops_f32x4{v[0], v[1], v[2], v[3]};
-    p[1] = ops_f32x4{v[4], v[5], v[6], v[7]};
+    AnyU32x4* p = reinterpret_cast<AnyU32x4*>(static_cast<float*>(base) + at);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      ops_u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(uint32_t, v[4 * h + i]);
+      p[h].v = w;
+    }
   } else {
     ops_u32x4 w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<ops_u32x4*>(static_cast<uint16_t*>(base) + at) = w;
+    reinterpret_cast<AnyU32x4*>(static_cast<uint16_t*>(base) + at)->v = w;
   }
 }
 __device__ __forceinline__ void store1(void* base, int64_t at, bool f32, float v) {

@@ -56,32 +56,46 @@ struct Group {
   }
 };
 
-// The elements of a row that a lane owns: with VEC, V runs of 8 consecutive
-// ones, G lanes apart; otherwise 8 V single ones, G apart.
-template <int G, int V, bool VEC>
+// The elements of a row that a lane owns: V runs of 8 consecutive ones, G lanes
+// apart.  kRagged: the row ends inside a run; that run's lane reads the row's last
+// 8 elements instead and owns those past the run before.  kTiny (fewer than 8
+// elements): 8 V single ones, G apart.  Rows may start anywhere.
+enum RowKind { kWhole, kRagged, kTiny };
+
+template <int G, int V, RowKind KIND>
 struct Row {
   int lane, D;
-  __device__ __forceinline__ int at(int v, int i) const {
-    return VEC ? (v * G + lane) * 8 + i : (v * 8 + i) * G + lane;
+  __device__ __forceinline__ int start(int v) const { return (v * G + lane) * 8; }
+  // Where run v is read; past the row's end the row's first elements are, and
+  // dropped (loads under a branch wait for one another).
+  __device__ __forceinline__ int base(int v) const {
+    const int s = start(v);
+    if (KIND == kRagged && s < D) return s + 8 <= D ? s : D - 8;
+    return s < D ? s : 0;
   }
-  __device__ __forceinline__ bool has(int v, int i) const { return at(v, i) < D; }
+  __device__ __forceinline__ int at(int v, int i) const {
+    return KIND == kTiny ? (v * 8 + i) * G + lane : base(v) + i;
+  }
+  __device__ __forceinline__ bool has(int v, int i) const {
+    if (KIND == kTiny) return at(v, i) < D;
+    return start(v) < D && (KIND == kWhole || base(v) + i >= start(v));
+  }
+  __device__ __forceinline__ bool whole(int v) const { return start(v) + 8 <= D; }
 
-  // What a lane reads of a row, and later its values.  Past the row's end the
-  // row's first elements are read and dropped: loads under a branch wait for one
-  // another.
+  // What a lane reads of a row, and later its values.
   struct Held {
-    Raw8 v[VEC ? V : 1];
-    float s[VEC ? 1 : V][8];
+    Raw8 v[KIND == kTiny ? 1 : V];
+    float s[KIND == kTiny ? V : 1][8];
   };
-  __device__ __forceinline__ Held load(const void* p, int64_t base, bool f32) const {
+  __device__ __forceinline__ Held load(const void* p, int64_t row, bool f32) const {
     Held h;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if constexpr (VEC) {
-        h.v[v] = load8(p, base + (has(v, 0) ? at(v, 0) : 0), f32);
+      if constexpr (KIND != kTiny) {
+        h.v[v] = load8(p, row + base(v), f32);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h.s[v][i] = load1(p, base + (has(v, i) ? at(v, i) : 0), f32);
+        for (int i = 0; i < 8; ++i) h.s[v][i] = load1(p, row + (has(v, i) ? at(v, i) : 0), f32);
       }
     }
     return h;
@@ -89,31 +103,41 @@ struct Row {
   __device__ __forceinline__ void values(const Held& h, bool f32, float (&x)[V][8]) const {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if constexpr (VEC) values8(h.v[v], f32, x[v]);
+      if constexpr (KIND != kTiny) values8(h.v[v], f32, x[v]);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        x[v][i] = has(v, i) ? (VEC ? x[v][i] : h.s[VEC ? 0 : v][i]) : 0.f;
+        x[v][i] = has(v, i) ? (KIND == kTiny ? h.s[KIND == kTiny ? v : 0][i] : x[v][i]) : 0.f;
     }
   }
-  __device__ __forceinline__ void store(void* p, int64_t base, bool f32,
+  __device__ __forceinline__ void store(void* p, int64_t row, bool f32,
                                         const float (&x)[V][8]) const {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if constexpr (VEC) {
-        if (has(v, 0)) store8(p, base + at(v, 0), f32, x[v]);
-      } else {
+      if (KIND != kTiny && whole(v)) {
+        store8(p, row + base(v), f32, x[v]);
+      } else if (KIND != kWhole) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (has(v, i)) store1(p, base + at(v, i), f32, x[v][i]);
+          if (has(v, i)) store1(p, row + at(v, i), f32, x[v][i]);
       }
+    }
+  }
+  __device__ __forceinline__ void store_i8(int8_t* p, int64_t row, int v, uint32_t lo,
+                                           uint32_t hi) const {
+    if (KIND != kTiny && whole(v)) {
+      reinterpret_cast<AnyU32x2*>(p + row + base(v))->v = ops_u32x2{lo, hi};
+    } else if (KIND != kWhole) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (has(v, i)) p[row + at(v, i)] = (int8_t)((i < 4 ? lo : hi) >> 8 * (i % 4));
     }
   }
 };
 
 // x -> N(x), without weights.  Elements past the row's end are zero on entry
 // and are left out of the centred sum; their values on exit are not used.
-template <int G, int V, bool VEC>
-__device__ __forceinline__ void normalise(const Row<G, V, VEC>& row, Group<G>& grp, bool center,
+template <int G, int V, RowKind KIND>
+__device__ __forceinline__ void normalise(const Row<G, V, KIND>& row, Group<G>& grp, bool center,
                                           float eps, float (&x)[V][8]) {
   const float inv_d = 1.0f / (float)row.D;
   if (center) {
@@ -142,8 +166,8 @@ __device__ __forceinline__ void normalise(const Row<G, V, VEC>& row, Group<G>& g
 
 // Row to int8 (RowScale).  The magnitudes are compared as bit patterns, so that a
 // NaN or an infinity comes out on top instead of being passed over.
-template <int G, int V, bool VEC>
-__device__ __forceinline__ void quantise(const Row<G, V, VEC>& row, Group<G>& grp,
+template <int G, int V, RowKind KIND>
+__device__ __forceinline__ void quantise(const Row<G, V, KIND>& row, Group<G>& grp,
                                          const float (&x)[V][8], int8_t* q, int64_t base,
                                          float* scale) {
   uint32_t top = 0;
@@ -159,29 +183,22 @@ __device__ __forceinline__ void quantise(const Row<G, V, VEC>& row, Group<G>& gr
   if (row.lane == 0) *scale = rs.scale;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const ops_u32x2 w = {rs.quantise4(x[v][0], x[v][1], x[v][2], x[v][3]),
-                         rs.quantise4(x[v][4], x[v][5], x[v][6], x[v][7])};
-    if constexpr (VEC) {
-      if (row.has(v, 0)) *reinterpret_cast<ops_u32x2*>(q + base + row.at(v, 0)) = w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (row.has(v, i)) q[base + row.at(v, i)] = (int8_t)(w[i / 4] >> 8 * (i % 4));
-    }
+    row.store_i8(q, base, v, rs.quantise4(x[v][0], x[v][1], x[v][2], x[v][3]),
+                 rs.quantise4(x[v][4], x[v][5], x[v][6], x[v][7]));
   }
 }
 
 // Threads of a workgroup whose rows belong to groups of G lanes.
 constexpr int group_threads(int G) { return G < 256 ? 256 : G; }
 
-template <int G, int V, bool VEC>
+template <int G, int V, RowKind KIND>
 __global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(NormArgs a) {
   const lowm_residual_norm_args& u = a.u;
   __shared__ float lds[kMaxReductions * (G / kWave)];
   const int64_t m = (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
   // Whole wavefronts leave here, and only where no group spans two of them.
   if (m >= u.M) return;
-  const Row<G, V, VEC> row{(int)threadIdx.x % G, u.D};
+  const Row<G, V, KIND> row{(int)threadIdx.x % G, u.D};
   Group<G> grp{lds};
 
   // Every load, then every value.  An operand that is not there reads y again.
@@ -245,12 +262,12 @@ struct QuantArgs {
   int M, D, f32;
 };
 
-template <int G, int V, bool VEC>
+template <int G, int V, RowKind KIND>
 __global__ __launch_bounds__(group_threads(G)) void quantize_rows_kernel(QuantArgs a) {
   __shared__ float lds[kMaxReductions * (G / kWave)];
   const int64_t m = (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
   if (m >= a.M) return;
-  const Row<G, V, VEC> row{(int)threadIdx.x % G, a.D};
+  const Row<G, V, KIND> row{(int)threadIdx.x % G, a.D};
   Group<G> grp{lds};
   float x[V][8];
   row.values(row.load(a.x, m * a.ld, a.f32 != 0), a.f32 != 0, x);
@@ -263,8 +280,8 @@ __global__ __launch_bounds__(group_threads(G)) void quantize_rows_kernel(QuantAr
 // stay in registers).  Measured on MI355X, residual_norm, us a call: 4096 rows of
 // 6144 44.6 with 512 lanes and two runs, 64.7 with 1024 lanes and one (a workgroup
 // of 16 wavefronts leaves the CU idle between rows); one row 4.4 against 4.2.
-template <template <int, int, bool> class K, bool VEC, int VMAX, typename A>
-int launch_rows(const A& a, int M, int D, hipStream_t stream) {
+template <template <int, int, RowKind> class K, RowKind KIND, int VMAX, typename A>
+int launch_kind(const A& a, int M, int D, hipStream_t stream) {
   auto go = [&](auto fn, int G) {
     const int per = group_threads(G) / G;
     void* args[] = {const_cast<A*>(&a)};
@@ -272,22 +289,32 @@ int launch_rows(const A& a, int M, int D, hipStream_t stream) {
                                     dim3((unsigned)((M + per - 1) / per)),
                                     dim3(group_threads(G)), args, 0, stream));
   };
-  if (D <= 512) return go(K<64, 1, VEC>::fn(), 64);
-  if (D <= 2048) return go(K<256, 1, VEC>::fn(), 256);
-  if (D <= 4096) return go(K<256, 2, VEC>::fn(), 256);
-  if (D <= 8192) return go(K<512, 2, VEC>::fn(), 512);
-  if constexpr (VMAX > 2) {
-    if (D > 16384) return go(K<1024, 4, VEC>::fn(), 1024);
+  if constexpr (KIND == kTiny) {
+    return go(K<64, 1, KIND>::fn(), 64);
+  } else {
+    if (D <= 512) return go(K<64, 1, KIND>::fn(), 64);
+    if (D <= 2048) return go(K<256, 1, KIND>::fn(), 256);
+    if (D <= 4096) return go(K<256, 2, KIND>::fn(), 256);
+    if (D <= 8192) return go(K<512, 2, KIND>::fn(), 512);
+    if constexpr (VMAX > 2) {
+      if (D > 16384) return go(K<1024, 4, KIND>::fn(), 1024);
+    }
+    return go(K<1024, 2, KIND>::fn(), 1024);
   }
-  return go(K<1024, 2, VEC>::fn(), 1024);
 }
-template <int G, int V, bool VEC>
+template <template <int, int, RowKind> class K, int VMAX, typename A>
+int launch_rows(const A& a, int M, int D, hipStream_t stream) {
+  return D < 8        ? launch_kind<K, kTiny, VMAX>(a, M, D, stream)
+         : D % 8 == 0 ? launch_kind<K, kWhole, VMAX>(a, M, D, stream)
+                      : launch_kind<K, kRagged, VMAX>(a, M, D, stream);
+}
+template <int G, int V, RowKind KIND>
 struct NormK {
-  static auto fn() { return &residual_norm_kernel<G, V, VEC>; }
+  static auto fn() { return &residual_norm_kernel<G, V, KIND>; }
 };
-template <int G, int V, bool VEC>
+template <int G, int V, RowKind KIND>
 struct QuantK {
-  static auto fn() { return &quantize_rows_kernel<G, V, VEC>; }
+  static auto fn() { return &quantize_rows_kernel<G, V, KIND>; }
 };
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
@@ -332,16 +359,8 @@ int residual_norm(const lowm_residual_norm_args* u, hipStream_t stream) {
   if ((!inplace && meet(ro, r)) || meet(x, r) || meet(xs, r) || meet(ro, x) || meet(ro, xs) ||
       meet(x, xs))
     return LOWM_ERR_INVALID_ARG;
-  // Whole 16-byte vectors (8-byte ones of int8) need every row to start on
-  // one and D to be a whole number of runs of 8.
-  bool vec = D % 8 == 0 && u->ld_y % 8 == 0 && u->ld_r % 8 == 0 && u->ld_r_out % 8 == 0 &&
-             aligned(u->y, 16) && aligned(u->r, 16) && aligned(u->r_out, 16) &&
-             aligned(u->w_post, 16) && aligned(u->w_pre, 16);
-  if (pre) vec = vec && u->ld_x % 8 == 0 && aligned(u->x, i8 ? 8 : 16);
-  if (u->gate && u->gate_col) vec = vec && u->gate_row % 8 == 0 && aligned(u->gate, 16);
   const NormArgs a{*u};
-  return vec ? launch_rows<NormK, true, 2>(a, u->M, u->D, stream)
-             : launch_rows<NormK, false, 2>(a, u->M, u->D, stream);
+  return launch_rows<NormK, 2>(a, u->M, u->D, stream);
 }
 
 }  // namespace
@@ -359,9 +378,7 @@ int quantize_rows(const void* x, int x_type, int64_t ld, int M, int K, void* q, 
              ss = span_of(scale, 1, M, M, 4);
   if (meet(xs, qs) || meet(xs, ss) || meet(qs, ss)) return LOWM_ERR_INVALID_ARG;
   const QuantArgs a{x, static_cast<int8_t*>(q), scale, ld, M, K, x_type == LOWM_F32};
-  const bool vec = K % 8 == 0 && ld % 8 == 0 && aligned(x, 16) && aligned(q, 8);
-  return vec ? launch_rows<QuantK, true, 4>(a, M, K, stream)
-             : launch_rows<QuantK, false, 4>(a, M, K, stream);
+  return launch_rows<QuantK, 4>(a, M, K, stream);
 }
 
 }  // namespace lowm

@@ -92,6 +92,12 @@ CASES = [
     (2, 8192, BF16, BF16, BF16, "channel", BF16, False, True, False, False),
     (3, 16384, BF16, F32, BF16, "element", BF16, True, True, True, False),
     (2, 16383, BF16, BF16, BF16, "token", F32, False, True, False, True),
+    (6, 9, F32, BF16, F32, "element", BF16, True, True, True, False),
+    (7, 8, BF16, F32, BF16, "channel", BF16, False, True, True, True),
+    (5, 511, BF16, BF16, BF16, "element", F32, True, True, True, False),
+    (3, 4095, F32, F32, F32, "element", F32, False, True, False, True),
+    (3, 4097, BF16, BF16, BF16, "channel", BF16, True, True, True, False),
+    (2, 8193, BF16, F32, BF16, "element", BF16, False, True, True, True),
 ]
 
 
@@ -179,7 +185,8 @@ def test_rows_of_zeros_infinities_and_nans(i8):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,K", [(1, 1), (3, 17), (64, 4096), (5, 8200), (2, 32768), (7, 30001)])
+@pytest.mark.parametrize("M,K", [(1, 1), (3, 17), (64, 4096), (5, 8200), (2, 32768), (7, 30001),
+                                 (4, 8), (4, 7), (5, 9), (3, 513), (2, 16391)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_quantize_rows_is_the_formula_exactly(M, K, dtype):
     """fp32 divides are correctly rounded on both sides: the same bits."""
