@@ -67,10 +67,12 @@ static Layout layout_of(int T, int D, int I, int E, int K) {
   while (l.route_splits < kMaxRouteSplits && router_tiles * l.route_splits * 2 <= 64 &&
          steps >= 2 * l.route_splits * kRouteWaves)
     l.route_splits *= 2;
-  // Down: enough workgroups for 256 CUs (tiles * splits < 512).
+  // Down: enough workgroups for 256 CUs.  Nearly enough will do: a split costs its
+  // join (T 27, D 3632, 227 tiles: 91 us whole, 96 us in two; T 52, D 3008, 188
+  // tiles: 162 us whole, 154 us in two).
   const int tiles = (D + kCols - 1) / kCols;
   l.down_splits = 1;
-  while (l.down_splits < kMaxDownSplits && tiles * l.down_splits < 256) l.down_splits *= 2;
+  while (l.down_splits < kMaxDownSplits && tiles * l.down_splits < 200) l.down_splits *= 2;
   const int pairs = T * K, active = pairs < E ? pairs : E;
   // sum of ceil(n / 16) over the active experts, each with 1 <= n <= T pairs
   l.max_segments = T <= kSegRows ? active : (pairs + (kSegRows - 1) * active) / kSegRows;
@@ -357,7 +359,10 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
     for (int p = threadIdx.x; p < a.T * a.top_k; p += kRouteThreads) {
       const int t = p / a.top_k, i = p - t * a.top_k;
       const uint32_t w0 = load_slot(a.pair_slots + 2 * p), w1 = load_slot(a.pair_slots + 2 * p + 1);
-      r.chosen[t][i] = (int)take_slot(a.pair_slots + 2 * p, w0, a.counters) - 1;
+      // (held in range whatever a workspace that was not zero makes of it: an
+      // expert taken twice then only leaves a pair that no segment counts)
+      const int id = (int)take_slot(a.pair_slots + 2 * p, w0, a.counters) - 1;
+      r.chosen[t][i] = id < 0 ? 0 : id < a.E ? id : a.E - 1;
       r.gates[t][i] = dec_partial(take_slot(a.pair_slots + 2 * p + 1, w1, a.counters));
     }
   }
@@ -375,7 +380,7 @@ struct UpShape {
   static constexpr int kRings = kWaves * S::kRing * 16;
 };
 
-template <int R>
+template <int R, bool SHIFTED>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using SH = UpShape<R>;
@@ -406,7 +411,11 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
         src[t] = a.x + (size_t)a.pairs[s.first + r].token * a.D * 2 + k0;
       }
     }
-    stream_tile<2, 2, R>(lds + wave * SH::S::kRing, src, 2 * a.D - k0, P, acc);
+    u32x4* ring = lds + wave * SH::S::kRing;
+    if constexpr (SHIFTED)
+      stream_tile_shifted<2, 2, R>(ring, src, k0, 2 * a.D - k0, P, acc);
+    else
+      stream_tile<2, 2, R>(ring, src, 2 * a.D - k0, P, acc);
   }
   stream_settle(acc);
   f32x4* sums = reinterpret_cast<f32x4*>(lds);
@@ -438,7 +447,12 @@ struct DownShape {
 };
 
 // The segments' steps as one sequence: step q is step q mod n of segment q / n.
-template <int R>
+// WHOLE: rows are whole lines, which are read once and need no place in the
+// caches.  Otherwise two requests share a line, and the second finds it in the L2
+// if it was read without the streaming hint (T 52, D 3032, I 776, E 64: 85 us
+// against 95; with whole lines through the ring as in stream_tile_shifted, whose
+// extra line every run pays, 125).
+template <int R, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using S = typename DownShape<R>::S;
@@ -521,7 +535,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
       if (!whole)
         from = 2 * a.I - piece - at >= 16 ? from : reinterpret_cast<const uint8_t*>(&kZeroPiece);
       __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)(slot + t * kPP),
-                                       16, 0, t < 2 ? kStreamAux : 0);
+                                       16, 0, WHOLE && t < 2 ? kStreamAux : 0);
     });
     pin_issue();
     ++loaded;
@@ -708,20 +722,32 @@ int moe(const lowm_moe_args* u, hipStream_t stream) {
   auto go = [&](const void* fn, size_t grid, size_t lds, int threads = kThreads) {
     return launched(hipLaunchKernel(fn, dim3((unsigned)grid), dim3(threads), args, lds, stream));
   };
+  // Rows of weights that are not whole lines of memory.
+  using Kernel = void (*)(MoeArgs);
+  auto in_lines = [](int cols, const void* w, Kernel shifted, Kernel whole) {
+    const bool any = ((uintptr_t)w | (uintptr_t)cols * 2) & 127;
+    return reinterpret_cast<const void*>(any ? shifted : whole);
+  };
   int rc = go(reinterpret_cast<const void*>(&moe_route_kernel),
               (size_t)((E + 15) / 16) * ((T + 15) / 16) * l.route_splits, 0, kRouteThreads);
   const size_t up_grid = (size_t)l.max_segments * ((I + kCols - 1) / kCols);
   if (rc == LOWM_OK)
-    rc = go(up_grid <= 256 ? reinterpret_cast<const void*>(&moe_up_kernel<6>)
-                           : reinterpret_cast<const void*>(&moe_up_kernel<3>),
+    rc = go(up_grid <= 256 ? in_lines(D, u->w13, &moe_up_kernel<6, true>, &moe_up_kernel<6, false>)
+                           : in_lines(D, u->w13, &moe_up_kernel<3, true>, &moe_up_kernel<3, false>),
             up_grid, 0);
   const size_t lds = sizeof(Segment) * (size_t)l.max_segments +
                      sizeof(Pair) * (size_t)((T * K + 1) / 2 * 2) +
                      sizeof(float) * kWaves * (size_t)T * kCols;
+  const size_t down_grid = (size_t)((D + kCols - 1) / kCols) * l.down_splits;
   if (rc == LOWM_OK)
-    rc = go(T <= 16 ? reinterpret_cast<const void*>(&moe_down_kernel<8>)
-                    : reinterpret_cast<const void*>(&moe_down_kernel<6>),
-            (size_t)((D + kCols - 1) / kCols) * l.down_splits, lds);
+    // Up to one workgroup to a CU the ring is as deep as half its LDS allows; more
+    // share a CU in pairs, rather than leave the last ones a round of their own
+    // (T 16, D 2488, I 272, E 128, 312 workgroups: 66 us with 3 slots, 76 with 6;
+    // T 64, D 4096, I 1024, E 64, 256 workgroups: 289 and 261).
+    rc = go(down_grid <= 256
+                ? in_lines(I, u->w2, &moe_down_kernel<6, false>, &moe_down_kernel<6, true>)
+                : in_lines(I, u->w2, &moe_down_kernel<3, false>, &moe_down_kernel<3, true>),
+            down_grid, lds);
   return rc;
 }
 

@@ -153,6 +153,151 @@ __device__ __forceinline__ void stream_tile(u32x4* ring, const uint8_t* (&src)[2
   });
 }
 
+// Waits until at most `young` steps' loads of G each are in flight, 0 <= young <= MOST.
+template <int MOST, int G>
+__device__ __forceinline__ void stream_wait(int young) {
+  if (young >= MOST) {
+    wait_vmcnt<MOST * G>();
+    return;
+  }
+  static_for<MOST>([&](auto i_c) {
+    constexpr int i = decltype(i_c)::value;
+    if (young == i) wait_vmcnt<i * G>();
+  });
+}
+
+// Weight rows that start anywhere in a line (a multiple of 16 bytes).  A request
+// for bytes 0 .. 127 of such a row touches two lines, and with the streaming hint
+// both are fetched again for the row's next request.  So the ring takes whole
+// lines of memory, `shift` 16-byte pieces of which lie before the step's own, and
+// the reads find piece z of the step at piece z + shift: in the step's slot or in
+// the one after it, which therefore has to have landed too.  Only the lines at a
+// stretch's ends, which a neighbour reads as well, go without the hint.  (The
+// experts' up kernel, 64 experts of 1552 rows of 6064 bytes, 593 MB: 94 us against
+// 139 us through stream_tile, which fetched 1.5 times as much, and 119 us through
+// stream_tile without the hint.)
+//
+// Where lane (g, l16) finds the 16 bytes of row l16 of a block of 16 weight rows
+// whose pieces' shifts this lane's loads have (lo, hi): the place in the slots,
+// and in `past` whether that is the next slot.
+__device__ __forceinline__ int shifted_place(uint32_t lo, uint32_t hi, int c, int slot, int pp,
+                                             bool& past) {
+  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, l16 = lane & 15;
+  const uint32_t a = __shfl(lo, 8 * (l16 & 7)), b = __shfl(hi, 8 * (l16 & 7));
+  const int z = 4 * c + g + (int)(l16 < 8 ? a : b);
+  past = z > 7;
+  return (past ? slot : 0) + (l16 >> 3) * pp + (l16 & 7) * 8 + ((z + ((l16 & 7) >> 1)) & 7);
+}
+// The shift of the row that `at`, a pointer to this lane's piece of it, lies in.
+__device__ __forceinline__ uint32_t shift_of(const uint8_t* at, int piece) {
+  return ((uint32_t)((uintptr_t)at >> 4) - (uint32_t)piece) & 7u;
+}
+
+// stream_tile for such rows; k0: bytes from the row's start to this lane's first.
+template <int NB, int AP, int R, typename Acc>
+__device__ __forceinline__ void stream_tile_shifted(u32x4* ring,
+                                                    const uint8_t* (&src)[2 * NB + AP], int k0,
+                                                    int left, int P,
+                                                    Acc (&acc)[NB * ((AP + 1) / 2)]) {
+  using SH = StreamShape<NB, AP, R>;
+  static_assert(SH::valid && R >= 3, "a ring the waits can count, and two slots to read from");
+  constexpr int G = SH::G, kPP = SH::kPP, MB = SH::MB;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int g = lane >> 4, l16 = lane & 15;
+  const int line = __builtin_amdgcn_readfirstlane(left);
+  int back[2 * NB];                      // bytes from the step's start back to the line's
+  uint32_t most = 0;
+#pragma unroll
+  for (int t = 0; t < 2 * NB; ++t) {
+    const uint32_t s = shift_of(src[t], stream_piece(lane));
+    most = s > most ? s : most;
+    back[t] = 16 * (int)s;
+    src[t] -= back[t];
+  }
+  most = wave_umax(most);
+  int place[2][NB], turn[2][NB];         // turn: what the last slot's next is away
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      bool past;
+      place[c][j] = 2 * j * kPP + shifted_place((uint32_t)back[2 * j] / 16,
+                                                (uint32_t)back[2 * j + 1] / 16, c, SH::kSlot, kPP,
+                                                past);
+      turn[c][j] = past ? SH::kRing : 0;
+    }
+  int rpos[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    rpos[c] = (l16 >> 3) * kPP + (l16 & 7) * 8 + ((4 * c + g + ((l16 & 7) >> 1)) & 7);
+  // Whether the rows reach into the line after the last step's.
+  const int lines = P + (128 * P < line + 16 * (int)most ? 1 : 0);
+
+  auto issue = [&](u32x4* slot, int p) {
+    const int at = p * 128;
+    if (p > 0 && p + 1 < lines && line - at >= 128) {
+      static_for<G>([&](auto t_c) {
+        constexpr int t = decltype(t_c)::value;
+        __builtin_amdgcn_global_load_lds(
+            src[t] + at, (__attribute__((address_space(3))) void*)(slot + t * kPP), 16, 0,
+            t < 2 * NB ? kStreamAux : 0);
+      });
+    } else {
+      static_for<G>([&](auto t_c) {
+        constexpr int t = decltype(t_c)::value;
+        int to = at;                     // bytes from the lane's first to this
+        if constexpr (t < 2 * NB) to -= back[t];
+        const bool in = left - to >= 16 && k0 + to >= 0;
+        const uint8_t* from = in ? src[t] + at : reinterpret_cast<const uint8_t*>(&kZeroPiece);
+        __builtin_amdgcn_global_load_lds(
+            from, (__attribute__((address_space(3))) void*)(slot + t * kPP), 16, 0, 0);
+      });
+    }
+    pin_issue();
+  };
+  u32x4* const end = ring + SH::kRing;
+  u32x4 *fill = ring, *use = ring;
+  auto next = [&](u32x4* s) { return s + SH::kSlot == end ? ring : s + SH::kSlot; };
+  for (int p = 0; p < R - 1 && p < lines; ++p) {
+    issue(fill, p);
+    fill = next(fill);
+  }
+  for (int p = 0; p < P; ++p) {
+    if (p + R - 1 < lines) {
+      issue(fill, p + R - 1);            // into the slot step p-1 was read from
+      fill = next(fill);
+    }
+    stream_wait<R - 2, G>((p + R < lines ? p + R : lines) - (p + 2 < lines ? p + 2 : lines));
+    u32x4 v[2 * (NB + MB)];
+    const bool turned = next(use) == ring;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int t = 0; t < NB + MB; ++t)
+        v[c * (NB + MB) + t] =
+            t < NB ? lds_read_opaque(use + place[c][t < NB ? t : 0] -
+                                     (turned ? turn[c][t < NB ? t : 0] : 0))
+                   : lds_read_opaque(use + 2 * t * kPP + rpos[c]);
+    lds_wait(v);
+    if (p + 1 == lines) {                // nothing there: the row has ended
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          if (turn[c][j]) v[c * (NB + MB) + j] = u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+          acc[j * MB + b] =
+              stream_mfma(v[c * (NB + MB) + NB + b], v[c * (NB + MB) + j], acc[j * MB + b]);
+    use = next(use);
+  }
+}
+
 // Exchange between workgroups.  A slot is a word that is zero until its owner
 // writes it, once in a call, with a word that is not (an fp32 value's complement,
 // a biased integer); the reader waits for it, whatever order the counter and the

@@ -151,6 +151,39 @@ def test_integers_are_exact(size):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 6, 40])
+@pytest.mark.parametrize("D,I", [(72, 16), (520, 200), (648, 24), (1240, 328), (1312, 408),
+                                 (1960, 88), (2104, 120), (264, 1048), (512, 64)])
+@pytest.mark.parametrize("offset", [0, 8, 56])
+def test_rows_anywhere_in_a_line_of_memory(T, D, I, offset):
+    """Weights that start `offset` elements into their storage, among NaN, which also fills
+    every expert that no token chose: exact integers, so a byte too many or too few shows."""
+    E = 7
+    g = torch.Generator().manual_seed(T + D + I + offset)
+    x, router, w13, w2 = exact_operands(g, T, D, I, E)
+    logits = x.double() @ router.double().t()
+    want = torch.sort(logits, dim=1, descending=True, stable=True).indices[:, 0]
+    idle = [e for e in range(E) if not (want == e).any()]
+
+    def placed(w):
+        w = w.to(BF16)
+        w[idle] = float("nan")
+        room = torch.full((w.numel() + offset + 512,), float("nan"), dtype=BF16, device="cuda")
+        view = room[offset:offset + w.numel()].view(w.shape)
+        view.copy_(w)
+        return view
+
+    out, ids, _ = sbg.moe(x.to(BF16).cuda(), router.to(BF16).cuda(), placed(w13), placed(w2), 1,
+                          workspace=sbg.make_moe_workspace(T, D, I, E, 1))
+    assert torch.equal(ids[:, 0].cpu().long(), want)
+    for t in range(T):
+        e = int(want[t])
+        h = 32 * (w13[e, I:].double() @ x[t].double())
+        y = (w2[e].double() @ h.to(BF16).double()).to(torch.float32).to(BF16)
+        assert torch.equal(out[t].cpu(), y)
+
+
+@pytest.mark.gpu
 def test_every_token_count_and_one_workspace_for_all():
     D, I, E, k = 256, 64, 7, 3
     g = torch.Generator().manual_seed(5)
