@@ -126,7 +126,8 @@ struct I8Shape {
   static constexpr bool valid = S::valid && lds_bytes <= 160 * 1024 - 64;
 };
 
-template <int AP, int NB, int R>
+// WHOLE, here and below: W's rows are whole lines of memory.
+template <int AP, int NB, int R, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void gemm_i8_stretch_kernel(I8Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using SH = I8Shape<AP, NB, R>;
@@ -160,7 +161,11 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_stretch_kernel(I8Args a) {
         src[t] = a.A + (size_t)r * a.K + k0;
       }
     }
-    stream_tile<NB, AP, R>(lds + wave * SH::S::kRing, src, a.K - k0, P, acc);
+    u32x4* ring = lds + wave * SH::S::kRing;
+    if constexpr (WHOLE)
+      stream_tile<NB, AP, R>(ring, src, a.K - k0, P, acc);
+    else
+      stream_tile_shifted<NB, AP, R>(ring, src, k0, a.K - k0, P, acc);
   }
   stream_settle(acc);
 
@@ -213,7 +218,7 @@ struct I8Few {
                                 kElems * 16 <= 160 * 1024 - 512;
 };
 
-template <int RQ, int PM, int NB, int R>
+template <int RQ, int PM, int NB, int R, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void gemm_i8_few_kernel(I8Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using SH = I8Few<RQ, PM, NB, R>;
@@ -237,16 +242,25 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_few_kernel(I8Args a) {
     const int r = n0 + 8 * t + stream_row(lane);
     src[t] = a.W + (size_t)(r < a.N ? r : a.N - 1) * a.K + k0;
   }
+  const StreamRows<WHOLE, NB, SH::kSlot, SH::kRing, kPP> w_rows(src);
+  const int lines = w_rows.lines(P, line);
   auto issue = [&](u32x4* slot, int p) {
     const int at = p * 128;
-    const bool whole = line - at >= 128;
-    static_for<G>([&](auto t_c) {
-      constexpr int t = decltype(t_c)::value;
-      const uint8_t* from = src[t] + at;
-      if (!whole) from = left - at >= 16 ? from : reinterpret_cast<const uint8_t*>(&kZeroPiece);
-      __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)(slot + t * kPP),
-                                       16, 0, kStreamAux);
-    });
+    if (line - at >= 128 && (WHOLE || (p > 0 && p + 1 < lines))) {
+      static_for<G>([&](auto t_c) {
+        constexpr int t = decltype(t_c)::value;
+        __builtin_amdgcn_global_load_lds(
+            src[t] + at, (__attribute__((address_space(3))) void*)(slot + t * kPP), 16, 0,
+            kStreamAux);
+      });
+    } else {
+      static_for<G>([&](auto t_c) {
+        constexpr int t = decltype(t_c)::value;
+        __builtin_amdgcn_global_load_lds(
+            w_rows.from(src[t], t, at, k0, left),
+            (__attribute__((address_space(3))) void*)(slot + t * kPP), 16, 0, 0);
+      });
+    }
     pin_issue();
   };
   u32x4* const end = ring + SH::kRing;
@@ -334,38 +348,57 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_few_kernel(I8Args a) {
   i32x4 acc[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) acc[j] = i32x4{0, 0, 0, 0};
-  auto multiply = [&](const u32x4* slot, const u32x4* row) {
+  auto multiply = [&](int p) {
     u32x4 v[2 * (NB + 1)];
+    const bool turned = next(use) == ring;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) v[c * (NB + 1) + j] = lds_read_opaque(slot + 2 * j * kPP + rpos[c]);
-      v[c * (NB + 1) + NB] = lds_read_opaque(row + rpos[c]);
+      for (int j = 0; j < NB; ++j) v[c * (NB + 1) + j] = w_rows.read(use, turned, c, j);
+      v[c * (NB + 1) + NB] = lds_read_opaque(rows + p * kPP + rpos[c]);
     }
     lds_wait(v);
+    if (!WHOLE && p + 1 == lines) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) w_rows.cut(v[c * (NB + 1) + j], c, j);
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int j = 0; j < NB; ++j)
         acc[j] = stream_mfma(v[c * (NB + 1) + NB], v[c * (NB + 1) + j], acc[j]);
+    use = next(use);
   };
   int p = 0;
-  for (; p + R - 1 < P; ++p) {
-    wait_vmcnt<(R - 2) * G>();
-    issue(fill, p + R - 1);
-    fill = next(fill);
-    multiply(use, rows + p * kPP);
-    use = next(use);
-  }
-  static_for<R - 1>([&](auto i_c) {
-    constexpr int younger = R - 2 - decltype(i_c)::value;
-    if (P - p == younger + 1) {
-      wait_vmcnt<younger * G>();
-      multiply(use, rows + p * kPP);
-      use = next(use);
-      ++p;
+  if constexpr (WHOLE) {
+    for (; p + R - 1 < P; ++p) {
+      wait_vmcnt<(R - 2) * G>();
+      issue(fill, p + R - 1);
+      fill = next(fill);
+      multiply(p);
     }
-  });
+    static_for<R - 1>([&](auto i_c) {
+      constexpr int younger = R - 2 - decltype(i_c)::value;
+      if (P - p == younger + 1) {
+        wait_vmcnt<younger * G>();
+        multiply(p);
+        ++p;
+      }
+    });
+  } else {
+    static_assert(R >= 3, "two slots to read from");
+    for (; p < P; ++p) {
+      if (p + R - 1 < lines) {
+        issue(fill, p + R - 1);
+        fill = next(fill);
+      }
+      const int issued = lines < R - 1 ? R - 1 : p + R < lines ? p + R : lines;
+      stream_wait<R - 2, G>(issued - (p + 2 < lines ? p + 2 : lines));
+      multiply(p);
+    }
+  }
   stream_settle(acc);
   i32x4* sums = reinterpret_cast<i32x4*>(lds);
   __syncthreads();
@@ -392,12 +425,11 @@ struct I8Panel {
   static constexpr int lds_bytes = R * kSlot * 16;
   static constexpr bool valid =
       R >= 2 && (R - 1) * (kEach + 1 + 2) <= 63 && lds_bytes <= 160 * 1024 - 64;
-  
 };
 
 // The loop of one wavefront; MINE: how many pieces of the panel it loads (its
 // waits count those loads too).
-template <int AP, int PW, int R, int MINE>
+template <int AP, int PW, int R, int MINE, bool WHOLE>
 __device__ __forceinline__ void i8_panel_loop(const I8Args& a, u32x4* lds, int n0, int P,
                                               i32x4 (&acc)[(AP + 1) / 2]) {
   using SH = I8Panel<AP, PW, R>;
@@ -423,67 +455,102 @@ __device__ __forceinline__ void i8_panel_loop(const I8Args& a, u32x4* lds, int n
   for (int c = 0; c < 2; ++c)
     rpos[c] = (l16 >> 3) * kPP + (l16 & 7) * 8 + ((4 * c + g + ((l16 & 7) >> 1)) & 7);
 
+  const StreamRows<WHOLE, 1, SH::kSlot, R * SH::kSlot, kPP> w_rows(src);
+  const int lines = w_rows.lines(P, line);
   auto issue = [&](u32x4* slot, int p) {
     const int at = p * 128;
-    const bool whole = line - at >= 128;
-    static_for<G>([&](auto t_c) {
+    auto load = [&](auto t_c, const uint8_t* from, auto aux_c) {
       constexpr int t = decltype(t_c)::value;
       u32x4* to = slot + (t < 2 ? my_w + t * kPP : (wave + (t - 2) * PW) * kPP);
-      const uint8_t* from = src[t] + at;
-      if (!whole) from = left - at >= 16 ? from : reinterpret_cast<const uint8_t*>(&kZeroPiece);
       __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, 0,
-                                       t < 2 ? kStreamAux : 0);
-    });
+                                       decltype(aux_c)::value);
+    };
+    if (line - at >= 128 && (WHOLE || (p > 0 && p + 1 < lines)))
+      static_for<G>([&](auto t_c) {
+        constexpr int t = decltype(t_c)::value;
+        load(t_c, src[t] + at, std::integral_constant<int, t < 2 ? kStreamAux : 0>{});
+      });
+    else
+      static_for<G>([&](auto t_c) {
+        constexpr int t = decltype(t_c)::value;
+        const uint8_t* from = src[t] + at;
+        if constexpr (t < 2)
+          from = w_rows.from(src[t], t, at, k0, left);
+        else
+          from = left - at >= 16 ? from : reinterpret_cast<const uint8_t*>(&kZeroPiece);
+        load(t_c, from, std::integral_constant<int, 0>{});
+      });
     pin_issue();
   };
-  auto multiply = [&](const u32x4* slot) {
+  u32x4* const end = lds + R * SH::kSlot;
+  u32x4 *fill = lds, *use = lds;
+  auto next = [&](u32x4* s) { return s + SH::kSlot == end ? lds : s + SH::kSlot; };
+  auto multiply = [&](int p) {
     u32x4 v[2 * (1 + MB)];
+    const bool turned = next(use) == lds;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      v[c * (1 + MB)] = lds_read_opaque(slot + my_w + rpos[c]);
+      v[c * (1 + MB)] = w_rows.read(use + my_w, turned, c, 0);
 #pragma unroll
       for (int b = 0; b < MB; ++b)
-        v[c * (1 + MB) + 1 + b] = lds_read_opaque(slot + 2 * b * kPP + rpos[c]);
+        v[c * (1 + MB) + 1 + b] = lds_read_opaque(use + 2 * b * kPP + rpos[c]);
     }
     lds_wait(v);
+    if (!WHOLE && p + 1 == lines) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) w_rows.cut(v[c * (1 + MB)], c, 0);
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int b = 0; b < MB; ++b)
         acc[b] = stream_mfma(v[c * (1 + MB) + 1 + b], v[c * (1 + MB)], acc[b]);
+    use = next(use);
   };
-  u32x4* const end = lds + R * SH::kSlot;
-  u32x4 *fill = lds, *use = lds;
-  auto next = [&](u32x4* s) { return s + SH::kSlot == end ? lds : s + SH::kSlot; };
-  for (int p = 0; p < R - 1 && p < P; ++p) {
+  for (int p = 0; p < R - 1 && p < lines; ++p) {
     issue(fill, p);
     fill = next(fill);
   }
   int p = 0;
-  for (; p + R - 1 < P; ++p) {
-    wait_vmcnt<(R - 2) * G>();
-    // Every wavefront's loads of step p have landed, and every wavefront's reads
-    // of step p-1, whose slot is filled next, have completed (lds_wait).  Every
-    // wavefront passes P barriers.
-    barrier_keep_loads();
-    issue(fill, p + R - 1);
-    fill = next(fill);
-    multiply(use);
-    use = next(use);
-  }
-  static_for<R - 1>([&](auto i_c) {
-    constexpr int younger = R - 2 - decltype(i_c)::value;
-    if (P - p == younger + 1) {
-      wait_vmcnt<younger * G>();
+  if constexpr (WHOLE) {
+    for (; p + R - 1 < P; ++p) {
+      wait_vmcnt<(R - 2) * G>();
+      // Every wavefront's loads of step p have landed, and every wavefront's reads
+      // of step p-1, whose slot is filled next, have completed (lds_wait).  Every
+      // wavefront passes P barriers.
       barrier_keep_loads();
-      multiply(use);
-      use = next(use);
-      ++p;
+      issue(fill, p + R - 1);
+      fill = next(fill);
+      multiply(p);
     }
-  });
+    static_for<R - 1>([&](auto i_c) {
+      constexpr int younger = R - 2 - decltype(i_c)::value;
+      if (P - p == younger + 1) {
+        wait_vmcnt<younger * G>();
+        barrier_keep_loads();
+        multiply(p);
+        ++p;
+      }
+    });
+  } else {
+    static_assert(R >= 3, "two slots to read from");
+    for (; p < P; ++p) {
+      // As above; then the wavefront's own rows' next line, after which the slot
+      // freed by the barrier is being filled again.
+      const int before = p + R - 1 < lines ? p + R - 1 : lines;
+      stream_wait<R - 2, G>(before - (p + 1));
+      barrier_keep_loads();
+      if (p + R - 1 < lines) {
+        issue(fill, p + R - 1);
+        fill = next(fill);
+      }
+      stream_wait<R - 2, G>((p + R < lines ? p + R : lines) - (p + 2 < lines ? p + 2 : lines));
+      multiply(p);
+    }
+  }
 }
 
-template <int AP, int PW, int R>
+template <int AP, int PW, int R, bool WHOLE>
 __global__ __launch_bounds__(PW* kWave) void gemm_i8_panel_kernel(I8Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using SH = I8Panel<AP, PW, R>;
@@ -496,9 +563,9 @@ __global__ __launch_bounds__(PW* kWave) void gemm_i8_panel_kernel(I8Args a) {
 #pragma unroll
   for (int i = 0; i < MB; ++i) acc[i] = i32x4{0, 0, 0, 0};
   if (wave < SH::kRest)
-    i8_panel_loop<AP, PW, R, SH::kEach + 1>(a, lds, n0, P, acc);
+    i8_panel_loop<AP, PW, R, SH::kEach + 1, WHOLE>(a, lds, n0, P, acc);
   else
-    i8_panel_loop<AP, PW, R, SH::kEach>(a, lds, n0, P, acc);
+    i8_panel_loop<AP, PW, R, SH::kEach, WHOLE>(a, lds, n0, P, acc);
   stream_settle(acc);
 #pragma unroll
   for (int b = 0; b < MB; ++b) i8_store(a, a.a_scale, acc[b], b, n0 + (lane & 15), lane >> 4);
@@ -507,24 +574,43 @@ __global__ __launch_bounds__(PW* kWave) void gemm_i8_panel_kernel(I8Args a) {
 
 namespace {
 
+// From this many bytes of W on, rows that are not whole lines are read line by line
+// (ShiftedRows); below, what it costs to find one's place in the lines is more than
+// the bytes read twice (16 rows: N 2048, K 4112 6.9 against 7.5 us, N 8192, K 1040
+// 6.0 against 5.8; 1 row: N 2048, K 8208 8.2 against 7.8, N 8192, K 2064 6.6 against
+// 7.1, N 16000, K 8208 25.3 against 38.8).
+constexpr int64_t kI8ShiftFrom = 1 << 24;
+
 // The deepest ring, up to R slots, that LDS and the wait counter allow.
 template <int AP, int NB, int R>
 constexpr int stretch_ring() {
   if constexpr (I8Shape<AP, NB, R>::valid) return R;
   else return stretch_ring<AP, NB, R - 1>();
 }
+// A kernel for W of whole lines, and the one for other rows, which there is for
+// rings of three slots and more.
+struct Pair {
+  const void *whole, *shifted;
+};
+constexpr bool three_slots(int MB, int NB) { return MB + NB <= 6; }
 template <int AP, int NB>
-const void* stretch_of() {
-  return reinterpret_cast<const void*>(&gemm_i8_stretch_kernel<AP, NB, stretch_ring<AP, NB, 4>()>);
+Pair stretch_of() {
+  constexpr int R = stretch_ring<AP, NB, 4>();
+  static_assert(three_slots(AP / 2, NB) == (R >= 3), "what the plan takes it for");
+  Pair k{reinterpret_cast<const void*>(&gemm_i8_stretch_kernel<AP, NB, R, true>), nullptr};
+  if constexpr (R >= 3)
+    k.shifted = reinterpret_cast<const void*>(&gemm_i8_stretch_kernel<AP, NB, R, false>);
+  return k;
 }
 template <int AP, int PW>
-const void* panel_of() {
+Pair panel_of() {
   static_assert(I8Panel<AP, PW, 3>::valid, "the ring fits");
-  return reinterpret_cast<const void*>(&gemm_i8_panel_kernel<AP, PW, 3>);
+  return {reinterpret_cast<const void*>(&gemm_i8_panel_kernel<AP, PW, 3, true>),
+          reinterpret_cast<const void*>(&gemm_i8_panel_kernel<AP, PW, 3, false>)};
 }
 constexpr int kPanelWaves[] = {4, 6, 8, 12, 16};
 template <int AP>
-const void* panel_by_waves(int waves) {
+Pair panel_by_waves(int waves) {
   return waves == 4    ? panel_of<AP, 4>()
          : waves == 6  ? panel_of<AP, 6>()
          : waves == 8  ? panel_of<AP, 8>()
@@ -545,25 +631,28 @@ constexpr int few_ring() {
   else return few_ring<RQ, PM, NB, R - 1>();
 }
 template <int RQ, int PM, int NB>
-const void* few_of() {
-  return reinterpret_cast<const void*>(
-      &gemm_i8_few_kernel<RQ, PM, NB, few_ring<RQ, PM, NB, 8>()>);
+Pair few_of() {
+  constexpr int R = few_ring<RQ, PM, NB, 8>();
+  Pair k{reinterpret_cast<const void*>(&gemm_i8_few_kernel<RQ, PM, NB, R, true>), nullptr};
+  if constexpr (R >= 3)
+    k.shifted = reinterpret_cast<const void*>(&gemm_i8_few_kernel<RQ, PM, NB, R, false>);
+  return k;
 }
 // The kernel that quantises M bf16 rows itself, if there is one: M <= 8 rows whose
 // stretches fit a wavefront's registers, in one round of workgroups.
-const void* few_kernel(int M, int K, const I8Plan& p, int tiles) {
-  static const void* const table[3][4] = {
+Pair few_kernel(int M, int K, const I8Plan& p, int tiles) {
+  static const Pair table[3][4] = {
       {few_of<1, 8, 1>(), few_of<1, 8, 2>(), few_of<1, 8, 3>(), few_of<1, 8, 4>()},
       {few_of<1, 16, 1>(), few_of<1, 16, 2>(), few_of<1, 16, 3>(), few_of<1, 16, 4>()},
       {few_of<2, 8, 1>(), few_of<2, 8, 2>(), few_of<2, 8, 3>(), few_of<2, 8, 4>()}};
-  if (M > 8 || p.panel || tiles > 256) return nullptr;
+  if (M > 8 || p.panel || tiles > 256) return {};
   const int steps = ((K + 127) / 128 + kWaves - 1) / kWaves;
   const int row = steps <= 8 ? (M <= 4 ? 0 : 2) : steps <= 16 && M <= 4 ? 1 : -1;
-  return row < 0 ? nullptr : table[row][p.NB - 1];
+  return row < 0 ? Pair{} : table[row][p.NB - 1];
 }
 
-const void* i8_kernel(int MB, const I8Plan& p) {
-  static const void* const stretch[4][4] = {
+Pair i8_kernel(int MB, const I8Plan& p) {
+  static const Pair stretch[4][4] = {
       {stretch_of<2, 1>(), stretch_of<2, 2>(), stretch_of<2, 3>(), stretch_of<2, 4>()},
       {stretch_of<4, 1>(), stretch_of<4, 2>(), stretch_of<4, 3>(), stretch_of<4, 4>()},
       {stretch_of<6, 1>(), stretch_of<6, 2>(), stretch_of<6, 3>(), stretch_of<6, 4>()},
@@ -597,7 +686,12 @@ constexpr size_t kI8SlotBytes = (size_t)kI8MaxBlocks * kWave * 4 * 4;
 //     25.2 (NB 4 29.2); M 64, N 1536, K 8192 NB 1 in two splits 10.9 (whole 13.2);
 //     M 23, N 2304, K 12288 NB 2 in three 11.4 (NB 1 whole 12.5); M 64, N 4096,
 //     K 4096 NB 1 whole 9.2 (two splits 16.3).
-I8Plan i8_plan(int M, int N, int K, bool split) {
+//   - the panel kind of 4 wavefronts competes by the same cost where K is short (no
+//     sums to add up at the end: N 16384, K 512, M 64 7.3 against 9.0, M 32 5.5
+//     against 6.6; K 4096 22.4 against 21.6, 19.3 against 16.4), and for rows of W
+//     that are not whole lines where the wide tiles' rings are too short for those
+//     (M 64, N 16384, K 4112 25.8 against 29.7; K 12272 64.5 against 72.6).
+I8Plan i8_plan(int M, int N, int K, bool split, bool whole) {
   const int MB = (M + 15) / 16;
   if (M > 16 && N > 16384) {
     I8Plan best{0, 1, 1};
@@ -614,7 +708,11 @@ I8Plan i8_plan(int M, int N, int K, bool split) {
   }
   I8Plan best{0, 1, 1};
   double best_us = 0;
-  for (int nb = 1; nb <= 4; ++nb)
+  if (MB >= 2 && (K <= 1536 || (!whole && MB >= 3))) {
+    best = I8Plan{4, 1, 1};
+    best_us = (double)((best.tiles(N) + 255) / 256) * (16 * MB + best.width()) * K / 67.0e3;
+  }
+  for (int nb = 1; nb <= 4 && (whole || three_slots(MB, nb)); ++nb)
     for (int s = 1; s <= (split ? kI8MaxSplits : 1); ++s) {
       const I8Plan p{0, nb, s};
       const int64_t tiles = p.tiles(N);
@@ -622,7 +720,7 @@ I8Plan i8_plan(int M, int N, int K, bool split) {
       if (s > 1 && K / s < 128 * kWaves) continue;       // a step for every wavefront
       const double us = (double)((tiles * s + 255) / 256) * (16 * (MB + nb)) * K / s / 67.0e3 +
                         (s > 1 ? 1.0 + 0.25 * s + 0.2 * (nb * MB) * (s - 1) : 0.0);
-      if ((nb == 1 && s == 1) || us < best_us) {
+      if (best_us == 0 || us < best_us) {
         best = p;
         best_us = us;
       }
@@ -674,10 +772,12 @@ int gemm_i8(const lowm_gemm_i8_args* u, hipStream_t stream) {
   a.f32 = u->c_type == LOWM_F32;
   uint8_t* w = static_cast<uint8_t*>(u->workspace);
   void* args[] = {&a};
+  const bool whole = !(((uintptr_t)a.W | (uintptr_t)u->K) & 127) || N * K < kI8ShiftFrom;
+  auto in_lines = [whole](const Pair& k) { return whole ? k.whole : k.shifted; };
   if (!quantised) {
-    const I8Plan p = i8_plan(u->M, u->N, u->K, false);
+    const I8Plan p = i8_plan(u->M, u->N, u->K, false, whole);
     const int tiles = p.tiles(u->N);
-    if (const void* fn = few_kernel(u->M, u->K, p, tiles))
+    if (const void* fn = in_lines(few_kernel(u->M, u->K, p, tiles)))
       return launched(hipLaunchKernel(fn, dim3((unsigned)tiles), dim3(kThreads), args, 0, stream));
     uint8_t* q = w + kI8LineBytes + kI8SlotBytes;
     float* s = reinterpret_cast<float*>(w + need - LOWM_MAX_M * sizeof(float));
@@ -686,13 +786,13 @@ int gemm_i8(const lowm_gemm_i8_args* u, hipStream_t stream) {
     a.A = q;
     a.a_scale = s;
   }
-  const I8Plan p = i8_plan(u->M, u->N, u->K, w != nullptr);
+  const I8Plan p = i8_plan(u->M, u->N, u->K, w != nullptr, whole);
   a.splits = p.splits;
   a.lines = reinterpret_cast<uint32_t*>(w);
   a.slots = reinterpret_cast<uint32_t*>(w + (w ? kI8LineBytes : 0));
   const size_t tiles = (size_t)p.tiles(u->N);
   const size_t grid = p.panel ? tiles : (tiles + kXcds - 1) / kXcds * kXcds * p.splits;
-  return launched(hipLaunchKernel(i8_kernel((u->M + 15) / 16, p), dim3((unsigned)grid),
+  return launched(hipLaunchKernel(in_lines(i8_kernel((u->M + 15) / 16, p)), dim3((unsigned)grid),
                                   dim3(p.panel ? p.panel * kWave : kThreads), args, 0,
                                   stream));
 }

@@ -177,21 +177,88 @@ __device__ __forceinline__ void stream_wait(int young) {
 // 139 us through stream_tile, which fetched 1.5 times as much, and 119 us through
 // stream_tile without the hint.)
 //
-// Where lane (g, l16) finds the 16 bytes of row l16 of a block of 16 weight rows
-// whose pieces' shifts this lane's loads have (lo, hi): the place in the slots,
-// and in `past` whether that is the next slot.
-__device__ __forceinline__ int shifted_place(uint32_t lo, uint32_t hi, int c, int slot, int pp,
-                                             bool& past) {
-  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, l16 = lane & 15;
-  const uint32_t a = __shfl(lo, 8 * (l16 & 7)), b = __shfl(hi, 8 * (l16 & 7));
-  const int z = 4 * c + g + (int)(l16 < 8 ? a : b);
-  past = z > 7;
-  return (past ? slot : 0) + (l16 >> 3) * pp + (l16 & 7) * 8 + ((z + ((l16 & 7) >> 1)) & 7);
-}
-// The shift of the row that `at`, a pointer to this lane's piece of it, lies in.
-__device__ __forceinline__ uint32_t shift_of(const uint8_t* at, int piece) {
-  return ((uint32_t)((uintptr_t)at >> 4) - (uint32_t)piece) & 7u;
-}
+// NB blocks of 16 rows, read by a lane whose loads are pieces 0 .. 2NB-1 of 8 rows;
+// KSLOT, KRING: u32x4 in a slot and in the ring, PP in a piece.
+template <int NB, int KSLOT, int KRING, int PP>
+struct ShiftedRows {
+  int back[2 * NB];                      // bytes from the lane's first back to its line's
+  int place[2][NB];                      // of the lane's 16 bytes of each block, in the slot
+  int turn[2][NB];                       // if in the next slot: what that is away after the last
+  int most;                              // the largest of back, over the lanes
+
+  // src[t]: this lane's 16 bytes of piece t in the first step; moved back to the
+  // line's.  Before any load into LDS.
+  template <int G>
+  __device__ __forceinline__ explicit ShiftedRows(const uint8_t* (&src)[G]) {
+    const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, l16 = lane & 15;
+    uint32_t top = 0;
+#pragma unroll
+    for (int t = 0; t < 2 * NB; ++t) {
+      const uint32_t s = ((uint32_t)((uintptr_t)src[t] >> 4) - (uint32_t)stream_piece(lane)) & 7u;
+      top = s > top ? s : top;
+      back[t] = 16 * (int)s;
+      src[t] -= back[t];
+    }
+    most = 16 * (int)wave_umax(top);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      // row l16's shift is with the lanes that load it
+      const int lo = __shfl(back[2 * j], 8 * (l16 & 7)), hi = __shfl(back[2 * j + 1], 8 * (l16 & 7));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int z = 4 * c + g + (l16 < 8 ? lo : hi) / 16;
+        place[c][j] = (2 * j + (l16 >> 3)) * PP + (l16 & 7) * 8 + ((z + ((l16 & 7) >> 1)) & 7) +
+                      (z > 7 ? KSLOT : 0);
+        turn[c][j] = z > 7 ? KRING : 0;
+      }
+    }
+  }
+  // How many lines hold P steps of rows with `line` bytes left.
+  __device__ __forceinline__ int lines(int P, int line) const {
+    return P + (128 * P < line + most ? 1 : 0);
+  }
+  // Where load t finds its 16 bytes of the line `at` bytes on, in a row with k0
+  // bytes before the lane's first and `left` after: the rows' ends read zeros.
+  __device__ __forceinline__ const uint8_t* from(const uint8_t* src, int t, int at, int k0,
+                                                 int left) const {
+    const int to = at - back[t];
+    return left - to >= 16 && k0 + to >= 0 ? src + at
+                                           : reinterpret_cast<const uint8_t*>(&kZeroPiece);
+  }
+  // The reads of block j's half c; `turned`: from the ring's last slot.
+  __device__ __forceinline__ u32x4 read(const u32x4* slot, bool turned, int c, int j) const {
+    return lds_read_opaque(slot + place[c][j] - (turned ? turn[c][j] : 0));
+  }
+  // After the wait, in a last step that has no line after it: nothing is there.
+  __device__ __forceinline__ void cut(u32x4& v, int c, int j) const {
+    if (turn[c][j]) v = u32x4{0u, 0u, 0u, 0u};
+  }
+};
+
+// The same for rows of whole lines, for code that serves both.
+template <int NB, int KSLOT, int KRING, int PP>
+struct WholeRows {
+  int place[2];
+  template <int G>
+  __device__ __forceinline__ explicit WholeRows(const uint8_t* (&)[G]) {
+    const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, l16 = lane & 15;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      place[c] = (l16 >> 3) * PP + (l16 & 7) * 8 + ((4 * c + g + ((l16 & 7) >> 1)) & 7);
+  }
+  __device__ __forceinline__ int lines(int P, int) const { return P; }
+  __device__ __forceinline__ const uint8_t* from(const uint8_t* src, int, int at, int,
+                                                 int left) const {
+    return left - at >= 16 ? src + at : reinterpret_cast<const uint8_t*>(&kZeroPiece);
+  }
+  __device__ __forceinline__ u32x4 read(const u32x4* slot, bool, int c, int j) const {
+    return lds_read_opaque(slot + 2 * j * PP + place[c]);
+  }
+  __device__ __forceinline__ void cut(u32x4&, int, int) const {}
+};
+template <bool WHOLE, int NB, int KSLOT, int KRING, int PP>
+using StreamRows = std::conditional_t<WHOLE, WholeRows<NB, KSLOT, KRING, PP>,
+                                      ShiftedRows<NB, KSLOT, KRING, PP>>;
 
 // stream_tile for such rows; k0: bytes from the row's start to this lane's first.
 template <int NB, int AP, int R, typename Acc>
@@ -205,33 +272,12 @@ __device__ __forceinline__ void stream_tile_shifted(u32x4* ring,
   const int lane = threadIdx.x & (kWave - 1);
   const int g = lane >> 4, l16 = lane & 15;
   const int line = __builtin_amdgcn_readfirstlane(left);
-  int back[2 * NB];                      // bytes from the step's start back to the line's
-  uint32_t most = 0;
-#pragma unroll
-  for (int t = 0; t < 2 * NB; ++t) {
-    const uint32_t s = shift_of(src[t], stream_piece(lane));
-    most = s > most ? s : most;
-    back[t] = 16 * (int)s;
-    src[t] -= back[t];
-  }
-  most = wave_umax(most);
-  int place[2][NB], turn[2][NB];         // turn: what the last slot's next is away
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      bool past;
-      place[c][j] = 2 * j * kPP + shifted_place((uint32_t)back[2 * j] / 16,
-                                                (uint32_t)back[2 * j + 1] / 16, c, SH::kSlot, kPP,
-                                                past);
-      turn[c][j] = past ? SH::kRing : 0;
-    }
+  const ShiftedRows<NB, SH::kSlot, SH::kRing, kPP> rows(src);
+  const int lines = rows.lines(P, line);
   int rpos[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c)
     rpos[c] = (l16 >> 3) * kPP + (l16 & 7) * 8 + ((4 * c + g + ((l16 & 7) >> 1)) & 7);
-  // Whether the rows reach into the line after the last step's.
-  const int lines = P + (128 * P < line + 16 * (int)most ? 1 : 0);
 
   auto issue = [&](u32x4* slot, int p) {
     const int at = p * 128;
@@ -245,10 +291,11 @@ __device__ __forceinline__ void stream_tile_shifted(u32x4* ring,
     } else {
       static_for<G>([&](auto t_c) {
         constexpr int t = decltype(t_c)::value;
-        int to = at;                     // bytes from the lane's first to this
-        if constexpr (t < 2 * NB) to -= back[t];
-        const bool in = left - to >= 16 && k0 + to >= 0;
-        const uint8_t* from = in ? src[t] + at : reinterpret_cast<const uint8_t*>(&kZeroPiece);
+        const uint8_t* from = src[t] + at;
+        if constexpr (t < 2 * NB)
+          from = rows.from(src[t], t, at, k0, left);
+        else
+          from = left - at >= 16 ? from : reinterpret_cast<const uint8_t*>(&kZeroPiece);
         __builtin_amdgcn_global_load_lds(
             from, (__attribute__((address_space(3))) void*)(slot + t * kPP), 16, 0, 0);
       });
@@ -275,16 +322,14 @@ __device__ __forceinline__ void stream_tile_shifted(u32x4* ring,
 #pragma unroll
       for (int t = 0; t < NB + MB; ++t)
         v[c * (NB + MB) + t] =
-            t < NB ? lds_read_opaque(use + place[c][t < NB ? t : 0] -
-                                     (turned ? turn[c][t < NB ? t : 0] : 0))
+            t < NB ? rows.read(use, turned, c, t < NB ? t : 0)
                    : lds_read_opaque(use + 2 * t * kPP + rpos[c]);
     lds_wait(v);
-    if (p + 1 == lines) {                // nothing there: the row has ended
+    if (p + 1 == lines) {
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
-          if (turn[c][j]) v[c * (NB + MB) + j] = u32x4{0u, 0u, 0u, 0u};
+        for (int j = 0; j < NB; ++j) rows.cut(v[c * (NB + MB) + j], c, j);
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c)

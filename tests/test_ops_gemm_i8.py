@@ -102,6 +102,38 @@ def test_bf16_rows_are_quantised_as_quantize_rows_does(M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 40, 16), (3, 500, 112), (16, 700, 400), (64, 4100, 144),
+                                   (64, 16000, 1040), (40, 24700, 528),
+                                   # 2^24 bytes of W and more
+                                   (1, 2056, 8208), (1, 16400, 1072), (3, 5000, 3376),
+                                   (8, 9100, 1872), (6, 13000, 1296), (4, 1100, 15904),
+                                   (8, 70000, 240), (16, 1400, 12016), (16, 40000, 432),
+                                   (31, 9000, 1904), (32, 65600, 256), (20, 16500, 1040),
+                                   (40, 24700, 688), (64, 4100, 4112), (64, 12500, 1360),
+                                   (33, 16000, 2064), (64, 50000, 400), (50, 150000, 112)])
+@pytest.mark.parametrize("offset", [0, 16, 112])
+def test_rows_anywhere_in_a_line_of_memory(M, N, K, offset):
+    """W starts `offset` bytes into its storage, among bytes of 127."""
+    g = torch.Generator().manual_seed(M + N + K + offset)
+    q, sa, W, sw = operands(g, M, N, K)
+    room = torch.full((offset + N * K + 512,), 127, dtype=I8, device="cuda")
+    placed = room[offset:offset + N * K].view(N, K)
+    placed.copy_(W)
+    ws = sbg.make_gemm_i8_workspace(M, N, K)
+    want = formula(q, sa, W, sw, F32)
+    for w in (None, ws):
+        got = sbg.gemm_i8(q.cuda(), placed, sw.cuda(), a_scale=sa.cuda(), out_dtype=F32, workspace=w)
+        assert torch.equal(got.cpu(), want)
+    if M <= 8:
+        x = q.to(BF16)
+        x[:, 0] = -127.0                                # so that the scales are ones
+        x.clamp_(min=-127.0)
+        got = sbg.gemm_i8(x.cuda(), placed, sw.cuda(), out_dtype=F32, workspace=ws)
+        assert torch.equal(got.cpu(), formula(x.to(I8), torch.ones(M), W, sw, F32))
+    workspace_is_clean(ws)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("K", [512, 4096, 32768])
 def test_rows_of_zeros_and_without_a_scale(K):
     g = torch.Generator().manual_seed(6)
