@@ -7,7 +7,8 @@
 //   route  l = x router^T by tiles of 16 experts and 16 tokens (and, with few of
 //          those, stretches of D); the last workgroup of a block of tokens picks
 //          their experts, and the last block's sorts the (token, expert) pairs by
-//          expert into segments of up to 16 rows, the matrix instructions' height;
+//          expert into segments of up to 16 rows, the matrix instructions' height
+//          (32 or 64 where experts get many);
 //   up     one workgroup per segment and 16 columns of h: 16 gate and 16 up rows;
 //   down   one workgroup per 16 output columns walks the segments as one long
 //          inner dimension, cut evenly over its wavefronts (and, for a narrow D,
@@ -22,7 +23,6 @@ namespace lowm {
 constexpr int kMaxT = LOWM_MOE_MAX_T;
 constexpr int kMaxE = LOWM_MOE_MAX_E;
 constexpr int kMaxK = LOWM_MOE_MAX_K;
-constexpr int kSegRows = 16;
 constexpr int kCols = 16;                 // columns of h, and of the output, per workgroup
 constexpr int kMaxDownSplits = 8;
 constexpr int kRouteWaves = 16;
@@ -54,9 +54,19 @@ constexpr size_t kPairsAt = kDownAt + 4 * kDownSlots;
 constexpr size_t kListsAt = kPairsAt + 4 * kPairSlots;
 
 struct Layout {
-  int route_splits, down_splits, max_segments;
+  int seg_rows, route_splits, down_splits, max_segments;
   size_t pairs, h, bytes;
 };
+
+// Rows of a segment, by the rows that an expert gets on average.  A further segment
+// reads the expert's weights again, from the caches at best, while a larger one
+// keeps the LDS of more rows.  us at 16, 32 and 64 rows: T 48, D 4096, I 1024, E 20,
+// top_k 5 (12 rows on average) 101, 108, 134; T 64, D 4096, I 1024, E 8, top_k 2 (16)
+// 60.8, 55.2, 64.8; T 47, D 4000, I 488, E 20, top_k 8 (19) 97, 82, 92; T 64,
+// D 4096, I 1024, E 16, top_k 8 (32) 153, 131, 119.
+static int seg_rows_of(int T, int E, int K) {
+  return T * K >= 28 * E ? 64 : T * K >= 14 * E ? 32 : 16;
+}
 
 static Layout layout_of(int T, int D, int I, int E, int K) {
   Layout l{};
@@ -74,8 +84,9 @@ static Layout layout_of(int T, int D, int I, int E, int K) {
   l.down_splits = 1;
   while (l.down_splits < kMaxDownSplits && tiles * l.down_splits < 200) l.down_splits *= 2;
   const int pairs = T * K, active = pairs < E ? pairs : E;
-  // sum of ceil(n / 16) over the active experts, each with 1 <= n <= T pairs
-  l.max_segments = T <= kSegRows ? active : (pairs + (kSegRows - 1) * active) / kSegRows;
+  l.seg_rows = seg_rows_of(T, E, K);
+  // sum of ceil(n / seg_rows) over the active experts, each with 1 <= n <= T pairs
+  l.max_segments = T <= l.seg_rows ? active : (pairs + (l.seg_rows - 1) * active) / l.seg_rows;
   l.pairs = kListsAt + up256(16 + sizeof(Segment) * (size_t)l.max_segments);
   l.h = l.pairs + up256(sizeof(Pair) * (size_t)pairs);
   l.bytes = l.h + up256((size_t)2 * pairs * I);
@@ -100,7 +111,7 @@ struct MoeArgs {
   uint8_t* h;                             // [T * top_k, I] bf16, in the pairs' order
   int T, D, I, E, top_k, flags;
   float routed_scale;
-  int route_splits, down_splits;
+  int seg_rows, route_splits, down_splits;
 };
 
 // ---------------------------------------------------------------------------
@@ -207,7 +218,8 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, RouteLds& r) {
   // the experts before it
   const bool one = tid < kMaxE;
   const int rows = one ? __popc(r.mask[tid][0]) + __popc(r.mask[tid][1]) : 0;
-  const uint32_t own = (uint32_t)rows | (uint32_t)((rows + kSegRows - 1) / kSegRows) << 16;
+  const int most = a.seg_rows;            // a power of 2
+  const uint32_t own = (uint32_t)rows | (uint32_t)((rows + most - 1) >> __builtin_ctz(most)) << 16;
   uint32_t before = own;
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
@@ -226,10 +238,10 @@ __device__ __forceinline__ void sort_pairs(const MoeArgs& a, RouteLds& r) {
     before -= own;
     r.starts[tid] = before & 0xffffu;
     Segment* segments = reinterpret_cast<Segment*>(a.lists + 4);
-    for (int s = 0; s * kSegRows < rows; ++s)
+    for (int s = 0; s * most < rows; ++s)
       segments[(before >> 16) + s] =
-          Segment{tid, (int)(before & 0xffffu) + s * kSegRows,
-                  rows - s * kSegRows < kSegRows ? rows - s * kSegRows : kSegRows, 0};
+          Segment{tid, (int)(before & 0xffffu) + s * most,
+                  rows - s * most < most ? rows - s * most : most, 0};
     if (tid == 0) a.lists[0] = (int)(total >> 16);
   }
   __syncthreads();
@@ -374,17 +386,18 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
 // ---------------------------------------------------------------------------
 // up
 // ---------------------------------------------------------------------------
-template <int R>
+// AP pieces of 8 rows to a segment.
+template <int AP, int R>
 struct UpShape {
-  using S = StreamShape<2, 2, R>;
+  using S = StreamShape<2, AP, R>;
   static constexpr int kRings = kWaves * S::kRing * 16;
 };
 
-template <int R, bool SHIFTED>
+template <int AP, int R, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using SH = UpShape<R>;
-  constexpr int G = SH::S::G;
+  using SH = UpShape<AP, R>;
+  constexpr int G = SH::S::G, MB = SH::S::MB;
   __shared__ u32x4 lds[SH::kRings / 16];
   const int tiles = (a.I + kCols - 1) / kCols;
   const int seg = blockIdx.x / tiles, i0 = blockIdx.x % tiles * kCols;
@@ -395,14 +408,16 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
   const int steps = (2 * a.D + 127) / 128;
   const int s0 = steps * wave / kWaves, P = steps * (wave + 1) / kWaves - s0;
   const int k0 = s0 * 128 + stream_piece(lane) * 16;
-  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  f32x4 acc[2 * MB];                      // gate's blocks of 16 rows, then up's
+#pragma unroll
+  for (int q = 0; q < 2 * MB; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (P > 0) {
     const uint8_t* w = a.w13 + (size_t)s.expert * 4 * a.I * a.D + k0;
     const uint8_t* src[G];
 #pragma unroll
     for (int t = 0; t < G; ++t) {
       // 16 gate rows, the 16 up rows of the same columns, then the segment's tokens
-      int r = 8 * (t & 1) + stream_row(lane);
+      int r = 8 * (t < 4 ? t & 1 : t - 4) + stream_row(lane);
       if (t < 4) {
         r = i0 + r < a.I ? i0 + r : a.I - 1;
         src[t] = w + (size_t)(t < 2 ? r : a.I + r) * a.D * 2;
@@ -412,37 +427,40 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
       }
     }
     u32x4* ring = lds + wave * SH::S::kRing;
-    if constexpr (SHIFTED)
-      stream_tile_shifted<2, 2, R>(ring, src, k0, 2 * a.D - k0, P, acc);
+    if constexpr (WHOLE)
+      stream_tile<2, AP, R>(ring, src, 2 * a.D - k0, P, acc);
     else
-      stream_tile<2, 2, R>(ring, src, 2 * a.D - k0, P, acc);
+      stream_tile_shifted<2, AP, R>(ring, src, k0, 2 * a.D - k0, P, acc);
   }
   stream_settle(acc);
   f32x4* sums = reinterpret_cast<f32x4*>(lds);
   __syncthreads();
-  sums[(wave * 2) * kWave + lane] = acc[0];
-  sums[(wave * 2 + 1) * kWave + lane] = acc[1];
-  __syncthreads();
-  // wavefront i takes row 4 g + i of lane group g
-  float gate = 0.f, up = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    gate += reinterpret_cast<const float*>(sums + (w * 2) * kWave + lane)[wave];
-    up += reinterpret_cast<const float*>(sums + (w * 2 + 1) * kWave + lane)[wave];
+  for (int q = 0; q < 2 * MB; ++q) sums[(wave * 2 * MB + q) * kWave + lane] = acc[q];
+  __syncthreads();
+  // wavefront i takes rows 4 g + i of lane group g
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    float gate = 0.f, up = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      gate += reinterpret_cast<const float*>(sums + (w * 2 * MB + b) * kWave + lane)[wave];
+      up += reinterpret_cast<const float*>(sums + (w * 2 * MB + MB + b) * kWave + lane)[wave];
+    }
+    const int row = 16 * b + 4 * (lane >> 4) + wave, i = i0 + (lane & 15);
+    if (row < s.rows && i < a.I)
+      reinterpret_cast<__bf16*>(a.h)[(size_t)(s.first + row) * a.I + i] =
+          static_cast<__bf16>(gate * sigmoid(gate) * up);
   }
-  const int row = 4 * (lane >> 4) + wave, i = i0 + (lane & 15);
-  if (row < s.rows && i < a.I)
-    reinterpret_cast<__bf16*>(a.h)[(size_t)(s.first + row) * a.I + i] =
-        static_cast<__bf16>(gate * sigmoid(gate) * up);
 #endif
 }
 
 // ---------------------------------------------------------------------------
 // down
 // ---------------------------------------------------------------------------
-template <int R>
+template <int AP, int R>
 struct DownShape {
-  using S = StreamShape<1, 2, R>;
+  using S = StreamShape<1, AP, R>;
   static constexpr int kRings = kWaves * S::kRing * 16;
 };
 
@@ -452,13 +470,13 @@ struct DownShape {
 // if it was read without the streaming hint (T 52, D 3032, I 776, E 64: 85 us
 // against 95; with whole lines through the ring as in stream_tile_shifted, whose
 // extra line every run pays, 125).
-template <int R, bool WHOLE>
+template <int AP, int R, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using S = typename DownShape<R>::S;
-  constexpr int G = S::G, kPP = S::kPP;
+  using S = typename DownShape<AP, R>::S;
+  constexpr int G = S::G, kPP = S::kPP, MB = S::MB;
   extern __shared__ u32x4 dyn[];
-  __shared__ u32x4 rings[DownShape<R>::kRings / 16];
+  __shared__ u32x4 rings[DownShape<AP, R>::kRings / 16];
   __shared__ int last;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int g = lane >> 4, l16 = lane & 15;
@@ -519,7 +537,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) src[t] = w + wrow[t];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < AP; ++t) {
       int r = 8 * t + qr;
       r = r < s.rows ? r : s.rows - 1;
       src[2 + t] = a.h + (size_t)(s.first + r) * a.I * 2 + piece;
@@ -545,31 +563,42 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
       if (loaded < P) point();
     }
   };
-  f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+  f32x4 acc[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
   int us = ls, uk = lk, used = 0;                        // the next step to use
   auto flush = [&]() {
     stream_settle(acc);
     const Segment s = segment_at(us);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 4 * g + i;
-      const ops_u32x2 p = lds_read8_opaque(pairs + s.first + (row < s.rows ? row : 0));
-      const uint32_t token = p[0], gate_bits = p[1];
-      const float gate = __builtin_bit_cast(float, gate_bits);
-      const float v = acc[0][i];
-      if (row < s.rows) lds_add_opaque(mine + token * kCols + l16, gate * v);
+    for (int b = 0; b < MB; ++b) {
+      if (b > 0 && 16 * b >= s.rows) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 16 * b + 4 * g + i;
+        const ops_u32x2 p = lds_read8_opaque(pairs + s.first + (row < s.rows ? row : 0));
+        const uint32_t token = p[0], gate_bits = p[1];
+        const float gate = __builtin_bit_cast(float, gate_bits);
+        const float v = acc[b][i];
+        if (row < s.rows) lds_add_opaque(mine + token * kCols + l16, gate * v);
+      }
     }
-    acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
   };
   auto multiply = [&](const u32x4* slot) {
-    u32x4 v[4];
+    u32x4 v[2 * (1 + MB)];
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) v[2 * c + t] = lds_read_opaque(slot + 2 * t * kPP + rpos[c]);
+      for (int t = 0; t < 1 + MB; ++t)
+        v[c * (1 + MB) + t] = lds_read_opaque(slot + 2 * t * kPP + rpos[c]);
     lds_wait(v);
-    acc[0] = mfma(v[1], v[0], acc[0]);
-    acc[0] = mfma(v[3], v[2], acc[0]);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+        acc[b] = mfma(v[c * (1 + MB) + 1 + b], v[c * (1 + MB)], acc[b]);
     ++used;
     if (++uk == per || used == P) {
       flush();
@@ -716,6 +745,7 @@ int moe(const lowm_moe_args* u, hipStream_t stream) {
   a.top_k = K;
   a.flags = u->flags;
   a.routed_scale = u->routed_scale;
+  a.seg_rows = l.seg_rows;
   a.route_splits = l.route_splits;
   a.down_splits = l.down_splits;
   void* args[] = {&a};
@@ -732,8 +762,13 @@ int moe(const lowm_moe_args* u, hipStream_t stream) {
               (size_t)((E + 15) / 16) * ((T + 15) / 16) * l.route_splits, 0, kRouteThreads);
   const size_t up_grid = (size_t)l.max_segments * ((I + kCols - 1) / kCols);
   if (rc == LOWM_OK)
-    rc = go(up_grid <= 256 ? in_lines(D, u->w13, &moe_up_kernel<6, true>, &moe_up_kernel<6, false>)
-                           : in_lines(D, u->w13, &moe_up_kernel<3, true>, &moe_up_kernel<3, false>),
+    rc = go(l.seg_rows == 64
+                ? in_lines(D, u->w13, &moe_up_kernel<8, 3, false>, &moe_up_kernel<8, 3, true>)
+            : l.seg_rows == 32
+                ? in_lines(D, u->w13, &moe_up_kernel<4, 4, false>, &moe_up_kernel<4, 4, true>)
+            : up_grid <= 256
+                ? in_lines(D, u->w13, &moe_up_kernel<2, 6, false>, &moe_up_kernel<2, 6, true>)
+                : in_lines(D, u->w13, &moe_up_kernel<2, 3, false>, &moe_up_kernel<2, 3, true>),
             up_grid, 0);
   const size_t lds = sizeof(Segment) * (size_t)l.max_segments +
                      sizeof(Pair) * (size_t)((T * K + 1) / 2 * 2) +
@@ -744,9 +779,13 @@ int moe(const lowm_moe_args* u, hipStream_t stream) {
     // share a CU in pairs, rather than leave the last ones a round of their own
     // (T 16, D 2488, I 272, E 128, 312 workgroups: 66 us with 3 slots, 76 with 6;
     // T 64, D 4096, I 1024, E 64, 256 workgroups: 289 and 261).
-    rc = go(down_grid <= 256
-                ? in_lines(I, u->w2, &moe_down_kernel<6, false>, &moe_down_kernel<6, true>)
-                : in_lines(I, u->w2, &moe_down_kernel<3, false>, &moe_down_kernel<3, true>),
+    rc = go(l.seg_rows == 64
+                ? in_lines(I, u->w2, &moe_down_kernel<8, 3, false>, &moe_down_kernel<8, 3, true>)
+            : l.seg_rows == 32
+                ? in_lines(I, u->w2, &moe_down_kernel<4, 5, false>, &moe_down_kernel<4, 5, true>)
+            : down_grid <= 256
+                ? in_lines(I, u->w2, &moe_down_kernel<2, 6, false>, &moe_down_kernel<2, 6, true>)
+                : in_lines(I, u->w2, &moe_down_kernel<2, 3, false>, &moe_down_kernel<2, 3, true>),
             down_grid, lds);
   return rc;
 }

@@ -151,14 +151,13 @@ def test_integers_are_exact(size):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [1, 6, 40])
+@pytest.mark.parametrize("T,E", [(1, 7), (6, 7), (40, 7), (50, 3), (64, 2)])
 @pytest.mark.parametrize("D,I", [(72, 16), (520, 200), (648, 24), (1240, 328), (1312, 408),
                                  (1960, 88), (2104, 120), (264, 1048), (512, 64)])
 @pytest.mark.parametrize("offset", [0, 8, 56])
-def test_rows_anywhere_in_a_line_of_memory(T, D, I, offset):
+def test_rows_anywhere_in_a_line_of_memory(T, E, D, I, offset):
     """Weights that start `offset` elements into their storage, among NaN, which also fills
     every expert that no token chose: exact integers, so a byte too many or too few shows."""
-    E = 7
     g = torch.Generator().manual_seed(T + D + I + offset)
     x, router, w13, w2 = exact_operands(g, T, D, I, E)
     logits = x.double() @ router.double().t()
@@ -181,6 +180,22 @@ def test_rows_anywhere_in_a_line_of_memory(T, D, I, offset):
         h = 32 * (w13[e, I:].double() @ x[t].double())
         y = (w2[e].double() @ h.to(BF16).double()).to(torch.float32).to(BF16)
         assert torch.equal(out[t].cpu(), y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,I,E,k", [(64, 264, 120, 4, 3), (64, 256, 128, 6, 2), (61, 512, 64, 2, 2),
+                                       (33, 136, 200, 3, 2), (64, 128, 64, 16, 8), (40, 64, 264, 1, 1)])
+def test_many_rows_to_an_expert(T, D, I, E, k):
+    """Every token's first choices the same experts, so that some get all rows, others none."""
+    g = torch.Generator().manual_seed(T + D + I)
+    x, router, w13, w2 = draw(g, T, D, I, E, k)
+    bias = torch.arange(E, 0, -1).float() * 4
+    out, ids, gates = sbg.moe(x.cuda(), router.cuda(), w13.cuda(), w2.cuda(), k, score="sigmoid",
+                              bias=bias.cuda(), workspace=sbg.make_moe_workspace(T, D, I, E, k))
+    assert (ids.cpu() == torch.arange(k, dtype=torch.int32)).all()
+    want, err = reference(x, w13, w2, ids.cpu().long(), gates.cpu().double())
+    diff = (out.cpu().double() - want).abs()
+    assert (diff <= err + 2.0 ** -8 * (want.abs() + err)).all()
 
 
 @pytest.mark.gpu
