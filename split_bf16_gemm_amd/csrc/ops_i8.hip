@@ -457,8 +457,14 @@ __device__ __forceinline__ void i8_panel_loop(const I8Args& a, u32x4* lds, int n
 
   const StreamRows<WHOLE, 1, SH::kSlot, R * SH::kSlot, kPP> w_rows(src);
   const int lines = w_rows.lines(P, line);
+  // Neighbours start at different steps and go round: else all ask at one time for
+  // one column of rows a power of two of bytes apart, that is, of a few memory
+  // channels (K 4096: M 40, N 32768 34.5 against 28 us, M 64, N 49152 38.9 against 37;
+  // M 24, N 33000, K 8192 61.5 against 48; K 4224 the same; whole-K panels only: the
+  // stretch kind's wavefronts start K / 4 apart and gain nothing).
+  const int start = WHOLE ? (int)(blockIdx.x % (unsigned)P) : 0;
   auto issue = [&](u32x4* slot, int p) {
-    const int at = p * 128;
+    const int at = (WHOLE && p + start >= P ? p + start - P : p + start) * 128;
     auto load = [&](auto t_c, const uint8_t* from, auto aux_c) {
       constexpr int t = decltype(t_c)::value;
       u32x4* to = slot + (t < 2 ? my_w + t * kPP : (wave + (t - 2) * PW) * kPP);
@@ -658,7 +664,8 @@ Pair i8_kernel(int MB, const I8Plan& p) {
       {stretch_of<6, 1>(), stretch_of<6, 2>(), stretch_of<6, 3>(), stretch_of<6, 4>()},
       {stretch_of<8, 1>(), stretch_of<8, 2>(), stretch_of<8, 3>(), stretch_of<8, 4>()}};
   if (!p.panel) return stretch[MB - 1][p.NB - 1];
-  return MB == 2   ? panel_by_waves<4>(p.panel)
+  return MB == 1   ? panel_by_waves<2>(p.panel)
+         : MB == 2 ? panel_by_waves<4>(p.panel)
          : MB == 3 ? panel_by_waves<6>(p.panel)
                    : panel_by_waves<8>(p.panel);
 }
@@ -672,13 +679,14 @@ constexpr size_t kI8LineBytes = 256 * (size_t)kI8MaxTiles;
 constexpr size_t kI8SlotBytes = (size_t)kI8MaxBlocks * kWave * 4 * 4;
 
 // How to cut the product.  Measured on MI355X, W from HBM, us a call:
-//   - above 16 rows and 16384 columns the panel kind (a workgroup then loads 64
-//     rows of A for up to 256 of W, not for 64), of the width with the fewest
-//     rounds of 256 workgroups times rows loaded.  M 64, K 4096: N 24576 with 6
-//     wavefronts 25.3 (4: 28.3, 8: 26.9, stretch 30.5), N 49152 with 12 37.5 (4:
-//     42.1, 16: 39.6, stretch 56.2), N 32768 with 8 34.1 (4: 31.8, 16: 37.3, stretch
-//     37.9).  M 24, N 49152 38.1 against 41.7.  At 16 rows it loses (43.0 against
-//     37.4), at N 12288 its tiles are too few (19.1 against 16.8).
+//   - from 16385 columns on the panel kind (a workgroup then loads 64 rows of A for
+//     up to 256 of W, not for 64), of the width with the fewest rounds of 256
+//     workgroups times rows loaded.  M 64, K 4096: N 20000 with 6 wavefronts 24.4 (4:
+//     28.9, 8: 27.1), N 32768 with 8 31.3 (4: 34.4, 16: 39.5), N 49152 with 12 39.9
+//     (4: 48.4, 16: 41.4; stretch 56.2).  Up to 16 rows, where A is little to save,
+//     from 32768 columns on: M 16, K 4096 N 20000 19.2 against 19.8, but K 8192 37.0
+//     against 34.2; N 49152 35.6 against 40.2, N 32768, K 8192 44.9 against 49.1.  At
+//     N 16384 its tiles are too few (M 64, K 8192 38.6 against 33.8).
 //   - otherwise stretch tiles of the width, and the split of K, of least cost:
 //     rounds times bytes loaded by a workgroup, at 67 KB a us, and for a split's
 //     exchange 1 us, 0.25 a split and 0.2 a block of 16 x 16 sums sent.  M 16,
@@ -693,7 +701,7 @@ constexpr size_t kI8SlotBytes = (size_t)kI8MaxBlocks * kWave * 4 * 4;
 //     (M 64, N 16384, K 4112 25.8 against 29.7; K 12272 64.5 against 72.6).
 I8Plan i8_plan(int M, int N, int K, bool split, bool whole) {
   const int MB = (M + 15) / 16;
-  if (M > 16 && N > 16384) {
+  if (N >= (M > 16 ? 16385 : 32768)) {
     I8Plan best{0, 1, 1};
     int64_t best_cost = 0;
     for (int waves : kPanelWaves) {

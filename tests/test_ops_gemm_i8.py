@@ -110,7 +110,9 @@ def test_bf16_rows_are_quantised_as_quantize_rows_does(M, N, K):
                                    (8, 70000, 240), (16, 1400, 12016), (16, 40000, 432),
                                    (31, 9000, 1904), (32, 65600, 256), (20, 16500, 1040),
                                    (40, 24700, 688), (64, 4100, 4112), (64, 12500, 1360),
-                                   (33, 16000, 2064), (64, 50000, 400), (50, 150000, 112)])
+                                   (33, 16000, 2064), (64, 50000, 400), (50, 150000, 112),
+                                   (9, 33000, 512), (16, 49152, 640), (1, 40000, 528),
+                                   (12, 66000, 272), (2, 100000, 256)])
 @pytest.mark.parametrize("offset", [0, 16, 112])
 def test_rows_anywhere_in_a_line_of_memory(M, N, K, offset):
     """W starts `offset` bytes into its storage, among bytes of 127."""
