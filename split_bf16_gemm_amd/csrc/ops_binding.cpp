@@ -27,10 +27,18 @@ std::string shape_text(const int64_t* s, int n) {
   return t + "]";
 }
 
+// The device of the call's first tensor, which the others have to share.
+thread_local int call_device = -1;
+
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse(PyExc_TypeError, std::string(name) + " must be a tensor");
   const at::Tensor& t = THPVariable_Unpack(o);
   if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(name) + " must be on the GPU");
+  const int device = t.get_device();
+  if (call_device < 0) call_device = device;
+  if (device != call_device)
+    refuse(PyExc_ValueError, std::string(name) + " is on GPU " + std::to_string(device) +
+                                 ", not on GPU " + std::to_string(call_device));
   return t;
 }
 
@@ -286,6 +294,7 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyErr_Format(PyExc_TypeError, "%d arguments needed, %zd given", N, n);
     return nullptr;
   }
+  call_device = -1;
   try {
     return PyLong_FromLong(F(a));
   } catch (const Refusal& r) {

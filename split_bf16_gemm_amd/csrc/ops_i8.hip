@@ -16,6 +16,11 @@
 // int32 sums the last to arrive adds.  A few rows of bf16 are quantised by each
 // workgroup for itself while its first rows of W are on their way (few); more
 // rows once, by a kernel of their own.
+//
+// Measured on MI355X, us a call, W from HBM, beside a plain read of W's bytes: M 1,
+// N 6144, K 4096 from bf16 7.6 (3.8); M 23, N 2304, K 12288 10.9 (4.3); M 64,
+// N 49152, K 4096 37 (31), with 4.6 to quantise its rows before; M 16, N 16384,
+// K 12288 36 (30).
 #include "ops_stream.cuh"
 
 namespace lowm {

@@ -17,9 +17,12 @@
 // What passes is sorted by a 64-bit key: the logit's bits in an order that
 // integers compare, then the complement of its id, so equal logits go by id and
 // no two keys are equal.
-// Bound by HBM for many rows (2 or 4 bytes a logit against some 12 vector
-// instructions); few rows are cut into up to kMaxSplits pieces, joined by the
-// last workgroup of a row to arrive.
+// Bound by HBM and the vector unit alike for many rows (2 or 4 bytes a logit
+// against some 12 vector instructions, the exponential a quarter-rate one): 2048
+// rows of 49152 bf16, 201 MB, 45 us (4.5 TB/s), where a plain read takes 30.  Few
+// rows are cut into up to kMaxSplits pieces, joined by the last workgroup of a row
+// to arrive, and are bound by the chain of latencies: read, reduce, pick, hand on,
+// join (one row of 49152 8.7 us; 61 rows of 50001 fp32 with 20 alternatives 13.3).
 #include "ops_stream.cuh"
 
 namespace lowm {

@@ -16,6 +16,15 @@
 // A segment's weights are all that its workgroups read from HBM; a further
 // segment of the same expert finds them in the caches.  No atomic adds, no
 // order that changes: equal inputs give equal bits.
+//
+// Bound by HBM.  Measured on MI355X, us a call, beside the time of a plain read of
+// the chosen experts: T 1, D 4096, I 1024, E 64, top_k 4 27 (15); T 64, E 128,
+// top_k 8 487 (473).  What is left is the three launches and the routing, which
+// one kernel has to finish before the next can know what to read.
+//
+// Roundings: h = silu(gate) up is rounded to bf16, the matrix instructions' type,
+// from fp32 sums; that is the one rounding besides the result's own, and makes the
+// error against 64 bits 1.4 times that of a layer that keeps h in fp32.
 #include "ops_stream.cuh"
 
 namespace lowm {
@@ -117,6 +126,8 @@ struct MoeArgs {
 // ---------------------------------------------------------------------------
 // route
 // ---------------------------------------------------------------------------
+// 64 tokens, D 4096, 128 experts 11.8 us; one token, 64 experts 6.2 (whole D in one
+// workgroup to a tile instead of four: 10).
 // The wavefronts cut D between them and load their operands straight into
 // registers in the matrix layout, kRouteBatch steps at a time: there is little
 // to read and one round trip to wait for, so a ring would only add trips.
@@ -386,6 +397,11 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
 // ---------------------------------------------------------------------------
 // up
 // ---------------------------------------------------------------------------
+// 16 gate rows and the 16 up rows of the same columns, so that h is there where both
+// sums are; the four wavefronts a stretch of D each (a workgroup's 32 weight rows
+// are few, and this way it waits for a quarter of them).  64 tokens, D 4096,
+// I 1024, 126 active experts, 2.1 GB: 306 us (6.9 TB/s).
+//
 // AP pieces of 8 rows to a segment.
 template <int AP, int R>
 struct UpShape {
@@ -458,6 +474,10 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
 // ---------------------------------------------------------------------------
 // down
 // ---------------------------------------------------------------------------
+// One workgroup has all of an output tile's inner dimension, or a fixed part of it,
+// so the experts' results are added where they are, gate by gate, with no exchange
+// but the splits'.  64 tokens, D 4096, I 1024, 126 active experts, 1.06 GB: 152 us
+// (7.0 TB/s).
 template <int AP, int R>
 struct DownShape {
   using S = StreamShape<1, AP, R>;
@@ -760,6 +780,8 @@ int moe(const lowm_moe_args* u, hipStream_t stream) {
   };
   int rc = go(reinterpret_cast<const void*>(&moe_route_kernel),
               (size_t)((E + 15) / 16) * ((T + 15) / 16) * l.route_splits, 0, kRouteThreads);
+  // Up to one workgroup to a CU the ring is as deep as a CU's LDS (T 2, D 4096, I 512,
+  // two experts each: 22.8 us a call with 6 slots, 24.1 with 3); more share a CU.
   const size_t up_grid = (size_t)l.max_segments * ((I + kCols - 1) / kCols);
   if (rc == LOWM_OK)
     rc = go(l.seg_rows == 64
