@@ -94,9 +94,13 @@ static Layout layout_of(int T, int D, int I, int E, int K) {
   while (l.down_splits < kMaxDownSplits && tiles * l.down_splits < 200) l.down_splits *= 2;
   const int pairs = T * K, active = pairs < E ? pairs : E;
   l.seg_rows = seg_rows_of(T, E, K);
-  // sum of ceil(n / seg_rows) over the active experts, each with 1 <= n <= T pairs
-  l.max_segments = T <= l.seg_rows ? active : (pairs + (l.seg_rows - 1) * active) / l.seg_rows;
-  l.pairs = kListsAt + up256(16 + sizeof(Segment) * (size_t)l.max_segments);
+  // sum of ceil(n / rows) over the active experts, each with 1 <= n <= T pairs
+  auto segments = [&](int rows) {
+    return T <= rows ? active : (pairs + (rows - 1) * active) / rows;
+  };
+  l.max_segments = segments(l.seg_rows);
+  // (room for segments of 16, so that fewer tokens never need more bytes)
+  l.pairs = kListsAt + up256(16 + sizeof(Segment) * (size_t)segments(16));
   l.h = l.pairs + up256(sizeof(Pair) * (size_t)pairs);
   l.bytes = l.h + up256((size_t)2 * pairs * I);
   return l;

@@ -289,6 +289,15 @@ BASE = dict(x=0x10000000, router=0x20000000, w13=0x30000000, w2=0x40000000, out=
             workspace_bytes=1 << 24, T=4, D=64, I=32, E=8, top_k=2, routed_scale=1.0)
 
 
+def test_fewer_tokens_need_no_more_workspace():
+    size = ops.library().lib.lowm_moe_workspace_bytes
+    for D, I in ((64, 8), (4096, 1024)):
+        for E in (1, 2, 7, 8, 20, 64, 66, 128, 256):
+            for k in range(1, min(E, 16) + 1):
+                need = [size(T, D, I, E, k) for T in range(1, 65)]
+                assert need == sorted(need) and need[0] > 0
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), -1), (dict(router=None), -1), (dict(w13=None), -1), (dict(w2=None), -1),
     (dict(out=None), -1), (dict(T=-1), -1), (dict(D=0), -1), (dict(I=0), -1), (dict(E=0), -1),
