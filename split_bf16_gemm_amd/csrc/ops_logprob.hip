@@ -9,8 +9,10 @@
 //   log p = l - m - (log S + (c - m L) log 2) ;  entropy = log S - log 2 T / S
 //
 // (d is one fused multiply-add, rounded once; what c's own rounding moves all the
-// terms by is exactly known and put back at the end),
-// so nothing overflows and the logits are read once.  The alternatives cost the
+// terms by is known and put back where sums join and at the end).  That is under
+// 1/16 up to a maximum of 2^20; past it the terms take d = (l - m) L, which needs
+// nothing put back.  So no term is above 2^(1/16), whatever the finite logits are,
+// and the logits are read once.  The alternatives cost the
 // pass nothing: each lane's running maximum is its greatest logit, the top_n-th
 // of those bounds the row's top_n-th from below, and only the few lanes whose
 // maximum passes the bound have their logits read again (from the caches).
@@ -22,7 +24,7 @@
 // rows of 49152 bf16, 201 MB, 45 us (4.5 TB/s), where a plain read takes 30.  Few
 // rows are cut into up to kMaxSplits pieces, joined by the last workgroup of a row
 // to arrive, and are bound by the chain of latencies: read, reduce, pick, hand on,
-// join (one row of 49152 8.7 us; 61 rows of 50001 fp32 with 20 alternatives 13.3).
+// join (one row of 49152 8.7 us; 61 rows of 50001 fp32 with 20 alternatives 13.5).
 #include "ops_stream.cuh"
 
 namespace lowm {
@@ -93,23 +95,40 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // 0 * -infinity would be NaN.
 __device__ __forceinline__ float held(float d) { return fmaxf(d, -300.f); }
 
-// A maximum too large to be scaled (a row of the type's lowest value, say): its
-// terms take d = (l - m) L instead.  Another maximum is then either equal to it
-// or further off than any term reaches.
-__device__ __forceinline__ bool huge(float m) { return fabsf(m) > 1e30f; }
+// A maximum m past which c = round(m L) is off by too much: half a step of c is
+// 1/16 at 2^20, but 128 and more, a factor 2^d past fp32's range, from 2^31 on.
+// Its terms take d = (l - m) L, two roundings instead of one.  (Any bound from some
+// 2^10 to 2^25 would do: below it the offset is small against 1, and ordinary
+// logits stay below it.)  Infinities are far.
+constexpr float kFar = 0x1p20f;
+__device__ __forceinline__ bool far(float m) { return fabsf(m) > kFar; }
+
+// c, rounded: the product is not to be fused into the sums it is used in.
+__device__ __forceinline__ float scaled(float m) {
+#pragma clang fp contract(off)
+  return m * kLog2e;
+}
+// By how much the terms' exponents are too large: m L - c, in one rounding.
+__device__ __forceinline__ float offset(float m) {
+  return far(m) ? 0.f : __builtin_fmaf(m, kLog2e, -scaled(m));
+}
 
 struct Sums {
   float m, s, t;
-  // What the terms are relative to; 0 while there is nothing but masked logits.
-  __device__ __forceinline__ float base() const { return m == kNone ? 0.f : m * kLog2e; }
+  // What the terms are relative to, where m is not far; 0 while there is nothing
+  // but masked logits.
+  __device__ __forceinline__ float base() const { return m == kNone ? 0.f : scaled(m); }
   // Rescales to the maximum m2 >= m.
   __device__ __forceinline__ void to(float m2) {
-    // (Nothing there yet: s and t are 0 and stay so.  A NaN, of two infinite
-    // bases, is held; of an infinite maximum s is one already.)
-    const float from = m == kNone ? kNone : base();
-    const bool same = m == m2;
+    // (Nothing there yet: s and t are 0 and stay so.  Of an infinite maximum s is a
+    // NaN already.)
+    const float m1 = m, from = m1 == kNone ? kNone : base();
     m = m2;
-    const float d = same ? 0.f : held(from - base());
+    float d = held(from - base());
+    // (where m1 is far above, so is m2)
+    const bool apart = (m2 != kNone && far(m2)) || (m1 != kNone && m1 < -kFar);
+    if (__builtin_expect(__ballot(apart) != 0, 0) && apart)
+      d = m1 == m2 ? 0.f : held((m1 - m2) * kLog2e - (offset(m1) - offset(m2)));
     const float k = __builtin_amdgcn_exp2f(d);
     t = (t + s * d) * k;
     s *= k;
@@ -183,11 +202,11 @@ __device__ __forceinline__ void add_logits(Sums& sum, int& above, const float (&
     sum.s += e;                          // a NaN logit shows here
     sum.t = __builtin_fmaf(e, held(d), sum.t);
   };
-  const bool far = sum.m != kNone && huge(sum.m);
-  if (__builtin_expect(__ballot(far) != 0, 0)) {
+  const bool apart = sum.m != kNone && far(sum.m);
+  if (__builtin_expect(__ballot(apart) != 0, 0)) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      term(far ? (x[i] - sum.m) * kLog2e : __builtin_fmaf(x[i], kLog2e, -c));
+      term(apart ? (x[i] - sum.m) * kLog2e : __builtin_fmaf(x[i], kLog2e, -c));
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) term(__builtin_fmaf(x[i], kLog2e, -c));
@@ -207,9 +226,7 @@ __device__ __forceinline__ void finish_row(const lowm_token_logprobs_args& u, in
   // An infinity or a NaN among the logits makes S a NaN (inf - inf).
   *bad = !(a.s >= 0.f) || a.m == -kNone;
   const bool empty = a.m == kNone;
-  const float c = a.base();
-  const float shift = huge(a.m) ? 0.f : __builtin_fmaf(-a.m, kLog2e, c) * kLn2;
-  const float ls = empty ? 0.f : logf(a.s) + shift;
+  const float ls = empty ? 0.f : logf(a.s) - offset(a.m) * kLn2;
   const float nan = __builtin_nanf("");
   u.logprob[row] = *bad || !token_ok ? nan : empty ? kNone : token_logit - a.m - ls;
   u.entropy[row] = *bad ? nan : empty ? 0.f : logf(a.s) - kLn2 * (a.t / a.s);

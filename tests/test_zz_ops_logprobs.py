@@ -179,6 +179,66 @@ def test_rows_without_a_distribution(M):
         assert torch.equal(ti[r].long(), torch.sort(x[r], descending=True, stable=True).indices[:n])
 
 
+def masked_rows(g, M, V, kind, v):
+    x = torch.randn(M, V, generator=g) * 3
+    if kind == "islands":            # ordinary logits at the end of the row only
+        x[:, :V - 17] = v
+    elif kind == "front":            # whole pieces masked, the rest ordinary
+        x[:, :V * 3 // 4] = v
+    elif kind == "back":
+        x[:, V // 4:] = v
+    elif kind == "scattered":
+        x.masked_fill_(torch.rand(M, V, generator=g) < 0.9, v)
+    elif kind == "wholly":
+        x[:] = v
+    elif kind == "top":              # a few equal ones of the magnitude are the most likely
+        x[:, torch.randperm(V, generator=g)[:9]] = -v
+    elif kind == "top_alone":        # and far below them the rest
+        x[:] = v
+        x[:, V // 3] = -v
+    else:                            # masks of several sizes, one on top of another
+        pick = torch.rand(M, V, generator=g)
+        x.masked_fill_(pick < 0.9, v)
+        x.masked_fill_(pick < 0.6, v * 4)
+        x.masked_fill_(pick < 0.3, -INF)
+        x[:, :V // 2] = v * 2
+    return x
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 3, 1200])
+@pytest.mark.parametrize("kind", ["islands", "front", "back", "scattered", "wholly", "top",
+                                  "top_alone", "several"])
+@pytest.mark.parametrize("v", [-1e4, -1e6, -1e9, -1e10, -1e11, -1e12, -1e20, -1e30, -8e37])
+def test_finite_masks_of_any_size(M, kind, v):
+    V = 9001 if M > 100 else 20011
+    g = torch.Generator().manual_seed(M)
+    x = masked_rows(g, M, V, kind, v)
+    tok = torch.randint(0, V, (M,), generator=g)
+    tok[0] = V - 1
+    for dtype in (BF16, F32):
+        y = x.to(dtype)
+        judge(y, tok, 5, run(y.cuda(), tok.cuda(), 5))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [2, 1200])
+@pytest.mark.parametrize("centre", [2.0 ** e * s for e in (18, 19, 20, 21, 22) for s in (-1, 1)])
+@pytest.mark.parametrize("kind", ["around", "rising", "ordinary_above"])
+def test_maxima_on_both_sides_of_a_power_of_two(M, centre, kind):
+    """Logits a few units around +-2^18 .. 2^22 (fp32 holds them to 1/64 .. 1/2), so that the
+    lanes' maxima lie on either side of any bound there and join."""
+    V = 9001
+    g = torch.Generator().manual_seed(int(abs(centre)) + M)
+    x = torch.randn(M, V, generator=g) * 3 + centre
+    if kind == "rising":
+        x = torch.linspace(-40, 40, V).repeat(M, 1) + centre
+    elif kind == "ordinary_above" and centre < 0:
+        x[:, torch.randperm(V, generator=g)[:3]] = 1.5
+    tok = torch.randint(0, V, (M,), generator=g)
+    judge(x, tok, 5, run(x.cuda(), tok.cuda(), 5))
+
+
 @pytest.mark.gpu
 def test_same_bits_each_time_and_in_a_graph():
     g = torch.Generator().manual_seed(2)
