@@ -167,8 +167,7 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, const float* logi
     o[j] = e < a.E ? order(l[j]) : 0u;
   }
   // Softmax over all experts only where it shows: in a choice by score + bias, or
-  // in gates that are not divided by the chosen ones' sum.  Otherwise any
-  // multiple of the scores does, such as e^(l - the chosen ones' largest l).
+  // in gates that are not divided by the chosen ones' sum.
   const bool whole = !sig && (!renorm || a.bias);
   float most = 0.f, total = 1.f;
   if (whole) {
@@ -211,10 +210,21 @@ __device__ __forceinline__ void pick_experts(const MoeArgs& a, const float* logi
   }
   const bool mine = lane < a.top_k;
   const float v = logits[my_id];
-  // (without a bias the first choice has the largest logit)
-  if (!whole) most = __builtin_bit_cast(
-      float, (uint32_t)__builtin_amdgcn_readfirstlane((int)__builtin_bit_cast(uint32_t, v)));
-  const float score = !mine ? 0.f : sig ? sigmoid(v) : expf(v - most) / total;
+  float score;
+  if (renorm) {
+    // Scores as multiples of one that no chosen expert's is far above, so that their
+    // ratios stay where the scores themselves are below fp32's smallest number: e^l
+    // by the chosen ones' largest l, which is the first choice's without a bias, and
+    // a sigmoid too where that l is negative.
+    const uint32_t bits = __builtin_bit_cast(uint32_t, v);
+    const float top = a.bias ? value_of(wave_umax(mine ? order(v) : 0u))
+                             : __builtin_bit_cast(
+                                   float, (uint32_t)__builtin_amdgcn_readfirstlane((int)bits));
+    score = sig && top >= 0.f ? sigmoid(v) : expf(v - top) / (sig ? 1.0f + expf(v) : 1.0f);
+  } else {
+    score = sig ? sigmoid(v) : expf(v - most) / total;
+  }
+  score = mine ? score : 0.f;
   const float sum = wave_sum(score);
   my_gate = (renorm ? score / sum : score) * a.routed_scale;
 }

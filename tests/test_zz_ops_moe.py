@@ -270,6 +270,38 @@ def test_a_token_of_nan_stays_its_own():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("lift", [0, 2, 16])
+def test_gates_of_scores_below_the_smallest_number(score, biased, lift):
+    """Chosen experts whose scores are 0 in fp32 (logits of -120 to -500, or that far below the
+    largest) still share the gate by the ratios of their scores.  The logits are exact."""
+    T, D, I, E, k = 5, 64, 32, 12, 4
+    g = torch.Generator().manual_seed(21)
+    x, router, w13, w2 = draw(g, T, D, I, E, k)
+    x[:, 0] = torch.tensor([1, 2, 4, 1, 2])
+    router[:] = 0
+    router[:, 0] = -(120 + torch.arange(E) / 2)
+    bias = None
+    if biased:
+        bias = torch.arange(E).float() * 4         # the choice goes by the bias
+    if lift:
+        router[0, 0] = lift / 4                     # one expert far above the others
+    want_ids, want, _ = route(x, router, k, score, bias, True, 1.0)
+    assert want.isfinite().all()
+    out, ids, gates = sbg.moe(x.cuda(), router.cuda(), w13.cuda(), w2.cuda(), k, score=score,
+                              bias=None if bias is None else bias.cuda(),
+                              workspace=sbg.make_moe_workspace(T, D, I, E, k))
+    assert torch.equal(ids.cpu().long(), want_ids)
+    gates = gates.cpu().double()
+    # gates below the smallest normal fp32 may be 0
+    assert ((gates - want).abs() <= 200 * U * want + 2.0 ** -126).all()
+    want_out, err = reference(x, w13, w2, want_ids, gates)
+    diff = (out.cpu().double() - want_out).abs()
+    assert (diff <= err + 2.0 ** -8 * (want_out.abs() + err)).all()
+
+
+@pytest.mark.gpu
 def test_nothing_beside_the_outputs_is_written():
     size = (5, 72, 40, 6, 2)
     g = torch.Generator().manual_seed(11)
