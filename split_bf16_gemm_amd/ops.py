@@ -204,17 +204,17 @@ def gemm_i8(A: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, *,
 
 def make_moe_workspace(T: int, D: int, I: int, E: int, top_k: int,
                        device="cuda") -> Optional[torch.Tensor]:
-    """A zeroed workspace of moe for these sizes (None for sizes it rejects); it also serves
-    any other sizes that need no more bytes, one call at a time."""
+    """A zeroed workspace of moe for these sizes (None for T 0 and for sizes it rejects); it also
+    serves any other sizes that need no more bytes, one call at a time."""
     n = library().lib.lowm_moe_workspace_bytes(T, D, I, E, top_k)
     return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
 
 def moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, top_k: int, *,
         score: str = "softmax", bias: Optional[torch.Tensor] = None, renormalize: bool = True,
-        routed_scale: float = 1.0, workspace: torch.Tensor, out: Optional[torch.Tensor] = None,
-        ids_out: Optional[torch.Tensor] = None, gates_out: Optional[torch.Tensor] = None,
-        stream=None):
+        routed_scale: float = 1.0, workspace: Optional[torch.Tensor],
+        out: Optional[torch.Tensor] = None, ids_out: Optional[torch.Tensor] = None,
+        gates_out: Optional[torch.Tensor] = None, stream=None):
     """(out [T, D], ids [T, top_k], gates [T, top_k]) of a mixture-of-experts layer for T <= 64
     tokens x [T, D]: router [E, D], w13 [E, 2I, D] (gate rows, then up rows), w2 [E, D, I], all
     contiguous bf16.
@@ -222,7 +222,8 @@ def moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w2: torch.Tens
     Each token takes the top_k experts with the largest router logits, or with a ``bias`` [E]
     (fp32) the largest score + bias; its gates are their scores ("softmax" over the experts or
     "sigmoid"), divided by their sum with ``renormalize``, times ``routed_scale``; out is the
-    gated sum of w2 (silu(w13_gate x) * (w13_up x)).  workspace: make_moe_workspace."""
+    gated sum of w2 (silu(w13_gate x) * (w13_up x)).  workspace: make_moe_workspace (None will do
+    where there are no tokens)."""
     if score not in ("softmax", "sigmoid"):
         raise ValueError(f"score must be 'softmax' or 'sigmoid', not {score!r}")
     dev = x.device

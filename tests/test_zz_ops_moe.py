@@ -302,6 +302,19 @@ def test_gates_of_scores_below_the_smallest_number(score, biased, lift):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("given", [False, True])
+def test_no_tokens_at_all(given):
+    size = (0, 64, 32, 6, 2)
+    _, router, w13, w2 = (t.cuda() for t in draw(torch.Generator().manual_seed(1), 1, *size[1:]))
+    x = torch.zeros(0, 64, dtype=BF16, device="cuda")
+    ws = sbg.make_moe_workspace(4, *size[1:]) if given else sbg.make_moe_workspace(*size)
+    out, ids, gates = sbg.moe(x, router, w13, w2, 2, workspace=ws)
+    assert out.shape == (0, 64) and ids.shape == gates.shape == (0, 2)
+    with pytest.raises(ValueError):                # one token needs a workspace
+        sbg.moe(torch.zeros(1, 64, dtype=BF16, device="cuda"), router, w13, w2, 2, workspace=None)
+
+
+@pytest.mark.gpu
 def test_nothing_beside_the_outputs_is_written():
     size = (5, 72, 40, 6, 2)
     g = torch.Generator().manual_seed(11)
