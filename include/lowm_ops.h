@@ -57,7 +57,7 @@ extern "C" {
  * (strides in elements, gate_col 0 or 1): (0, 1) is a gate per channel, (1, 0) one per row,
  * (D, 1) one per element.  NULL: w_post, w_pre, gate are ones.  r_out may be
  * r itself (same ld_r); otherwise no output may overlap an input or another
- * output.  y and x may not overlap.
+ * output.  Column ranges of one buffer do not overlap if their ld are equal bytes.
  */
 #define LOWM_NORM_POST 1
 #define LOWM_NORM_NO_PRE 2

@@ -24,15 +24,25 @@ inline int launched(hipError_t err) {
   return LOWM_ERR_LAUNCH;
 }
 
-// Bytes [lo, hi) of a [rows, cols] array whose rows start `ld` elements apart.
+// Bytes [lo, hi) of a [rows, cols] array whose rows, `width` bytes each, start
+// `ld` elements, `pitch` bytes, apart.
 struct Span {
-  uintptr_t lo, hi;
+  uintptr_t lo, hi, pitch, width;
 };
 inline Span span_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
   const uintptr_t lo = (uintptr_t)p;
-  return {lo, p ? lo + (uintptr_t)(((rows - 1) * ld + cols) * elem) : lo};
+  return {lo, p ? lo + (uintptr_t)(((rows - 1) * ld + cols) * elem) : lo, (uintptr_t)(ld * elem),
+          (uintptr_t)(cols * elem)};
 }
-inline bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+// Whether two arrays share a byte.  Rows of one pitch may lie between one another,
+// as column ranges of one buffer do; of two pitches the whole spans are compared.
+inline bool meet(const Span& a, const Span& b) {
+  if (a.lo >= b.hi || b.lo >= a.hi) return false;
+  if (a.pitch != b.pitch || a.pitch == 0) return true;
+  const Span &first = a.lo <= b.lo ? a : b, &other = a.lo <= b.lo ? b : a;
+  const uintptr_t off = (other.lo - first.lo) % a.pitch;
+  return off < first.width || off + other.width > a.pitch;
+}
 
 inline int type_bytes(int type) { return type == LOWM_F32 ? 4 : type == LOWM_BF16 ? 2 : 1; }
 

@@ -239,6 +239,28 @@ def test_on_another_stream_and_in_a_graph():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 100])
+def test_operands_that_are_columns_of_one_tensor(D):
+    """Column ranges of one tensor share no element though their spans of memory meet."""
+    g = torch.Generator().manual_seed(D)
+    y, r = rand(g, 6, D, dev="cuda"), rand(g, 6, D, dev="cuda")
+    want_r, want_x, _ = sbg.residual_norm(y, r)
+    for order in ((0, 1, 2, 3), (3, 2, 1, 0), (1, 3, 0, 2)):
+        wide = torch.full((6, 4 * D), 5.0, dtype=BF16, device="cuda")
+        at = [wide[:, i * D:(i + 1) * D] for i in order]
+        at[0].copy_(y)
+        at[1].copy_(r)
+        sbg.residual_norm(at[0], at[1], residual_out=at[2], out=at[3])
+        assert torch.equal(at[2], want_r) and torch.equal(at[3], want_x)
+        assert torch.equal(at[0], y) and torch.equal(at[1], r)
+    wide = torch.zeros(6, 4 * D, dtype=BF16, device="cuda")
+    a, b, c = wide[:, :D], wide[:, D:2 * D], wide[:, 2 * D:3 * D]
+    for o in (wide[:, 3 * D - 1:4 * D - 1], wide[:, D - 1:2 * D - 1], wide[:, 1:D + 1]):
+        with pytest.raises(sbg.LowmError):         # one shared column is an overlap
+            sbg.residual_norm(a, b, residual_out=c, out=o)
+
+
+@pytest.mark.gpu
 def test_no_rows_at_all():
     y = torch.zeros(0, 64, dtype=BF16, device="cuda")
     r, x, s = sbg.residual_norm(y, y, quantize=True)
@@ -296,6 +318,14 @@ def test_residual_norm_refuses(kw):
     dict(r=B0 + 2, r_type=1), dict(w_post=0x5000002, w_type=1), dict(x_type=2, x_scale=0x5000002)])
 def test_residual_norm_does_not_support(kw):
     assert call(**kw) == sbg.binding.LOWM_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=A0 + 2 * 63), dict(x=A0 + 2 * (128 - 63)), dict(x=A0 + 2 * 64, ld_x=129),
+    dict(x=A0 + 2 * (128 + 63)), dict(r_out=B0 + 2), dict(r_out=B0 - 2), dict(r_out=C0, x=C0 - 126)])
+def test_columns_that_overlap_are_refused(kw):
+    base = dict(ld_y=128, ld_r=128, ld_r_out=128, ld_x=128)
+    assert call(**{**base, **kw}) == sbg.binding.LOWM_ERR_INVALID_ARG
 
 
 def test_no_rows_is_no_work():
