@@ -24,6 +24,10 @@ inline int launched(hipError_t err) {
   return LOWM_ERR_LAUNCH;
 }
 
+// A launch has fewer than 2^32 threads; more rows than fit go in several, each of
+// at most this many.
+constexpr int64_t kMaxThreads = 1ll << 31;
+
 // Bytes [lo, hi) of a [rows, cols] array whose rows, `width` bytes each, start
 // `ld` elements, `pitch` bytes, apart.
 struct Span {

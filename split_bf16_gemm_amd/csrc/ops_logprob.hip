@@ -43,6 +43,7 @@ constexpr float kNone = -__builtin_inff();
 struct LogprobArgs {
   lowm_token_logprobs_args u;
   int splits, per;                       // pieces of a row, logits in each
+  int64_t first;                         // row of this launch
   uint32_t* lines;
   uint64_t* records;
 };
@@ -265,7 +266,7 @@ __global__ __launch_bounds__(kTh, 8) void token_logprobs_kernel(LogprobArgs a) {
   __shared__ int n_lanes, n_keys, last;
   const lowm_token_logprobs_args& u = a.u;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int64_t row = blockIdx.x / a.splits;
+  const int64_t row = a.first + blockIdx.x / a.splits;
   const int piece = blockIdx.x % a.splits;
   const int first = piece * a.per;                       // this piece: [first, first + len)
   const int len = first + a.per < u.V ? a.per : u.V - first;
@@ -542,18 +543,21 @@ int token_logprobs(const lowm_token_logprobs_args* u, hipStream_t stream) {
       if (meet(out[i], out[j])) return LOWM_ERR_INVALID_ARG;
   }
   char* w = static_cast<char*>(u->workspace);
-  LogprobArgs a{*u, splits_of(u->M, u->V), 0, reinterpret_cast<uint32_t*>(w),
+  LogprobArgs a{*u, splits_of(u->M, u->V), 0, 0, reinterpret_cast<uint32_t*>(w),
                 reinterpret_cast<uint64_t*>(w + (need ? kLineBytes : 0))};
   // Pieces of whole 16-byte runs, so that an aligned row has aligned pieces.
   a.per = ((u->V + a.splits - 1) / a.splits + 7) / 8 * 8;
   a.splits = (u->V + a.per - 1) / a.per;
-  if ((int64_t)a.splits * M > 0x7fffffff) return LOWM_ERR_UNSUPPORTED;
   void* args[] = {&a};
   const void* fn = u->logits_type == LOWM_F32
                        ? reinterpret_cast<const void*>(&token_logprobs_kernel<float>)
                        : reinterpret_cast<const void*>(&token_logprobs_kernel<uint16_t>);
-  return launched(
-      hipLaunchKernel(fn, dim3((unsigned)(a.splits * M)), dim3(kTh), args, 0, stream));
+  constexpr int64_t most = kMaxThreads / kTh;            // (rows in pieces are far fewer)
+  int rc = LOWM_OK;
+  for (int64_t& row = a.first; row < M && rc == LOWM_OK; row += most)
+    rc = launched(hipLaunchKernel(fn, dim3((unsigned)(a.splits * (M - row < most ? M - row : most))),
+                                  dim3(kTh), args, 0, stream));
+  return rc;
 }
 
 }  // namespace

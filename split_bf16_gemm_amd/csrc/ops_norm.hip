@@ -25,6 +25,7 @@ constexpr int kMaxReductions = 5;
 
 struct NormArgs {
   lowm_residual_norm_args u;
+  int64_t first;                         // row of this launch
 };
 
 // Sums over the group of G lanes that shares a row.  A group larger than a
@@ -201,7 +202,7 @@ template <int G, int V, RowKind KIND>
 __global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(NormArgs a) {
   const lowm_residual_norm_args& u = a.u;
   __shared__ float lds[kMaxReductions * (G / kWave)];
-  const int64_t m = (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
+  const int64_t m = a.first + (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
   // Whole wavefronts leave here, and only where no group spans two of them.
   if (m >= u.M) return;
   const Row<G, V, KIND> row{(int)threadIdx.x % G, u.D};
@@ -264,14 +265,14 @@ struct QuantArgs {
   const void* x;
   int8_t* q;
   float* scale;
-  int64_t ld;
+  int64_t ld, first;
   int M, D, f32;
 };
 
 template <int G, int V, RowKind KIND>
 __global__ __launch_bounds__(group_threads(G)) void quantize_rows_kernel(QuantArgs a) {
   __shared__ float lds[kMaxReductions * (G / kWave)];
-  const int64_t m = (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
+  const int64_t m = a.first + (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
   if (m >= a.M) return;
   const Row<G, V, KIND> row{(int)threadIdx.x % G, a.D};
   Group<G> grp{lds};
@@ -287,13 +288,19 @@ __global__ __launch_bounds__(group_threads(G)) void quantize_rows_kernel(QuantAr
 // 6144 44.6 with 512 lanes and two runs, 64.7 with 1024 lanes and one (a workgroup
 // of 16 wavefronts leaves the CU idle between rows); one row 4.4 against 4.2.
 template <template <int, int, RowKind> class K, RowKind KIND, int VMAX, typename A>
-int launch_kind(const A& a, int M, int D, hipStream_t stream) {
+int launch_kind(A a, int M, int D, hipStream_t stream) {
   auto go = [&](auto fn, int G) {
-    const int per = group_threads(G) / G;
-    void* args[] = {const_cast<A*>(&a)};
-    return launched(hipLaunchKernel(reinterpret_cast<const void*>(fn),
-                                    dim3((unsigned)((M + per - 1) / per)),
+    const int64_t per = group_threads(G) / G, most = kMaxThreads / group_threads(G);
+    const int64_t blocks = (M + per - 1) / per;
+    void* args[] = {&a};
+    int rc = LOWM_OK;
+    for (int64_t b = 0; b < blocks && rc == LOWM_OK; b += most) {
+      a.first = b * per;
+      rc = launched(hipLaunchKernel(reinterpret_cast<const void*>(fn),
+                                    dim3((unsigned)(blocks - b < most ? blocks - b : most)),
                                     dim3(group_threads(G)), args, 0, stream));
+    }
+    return rc;
   };
   if constexpr (KIND == kTiny) {
     return go(K<64, 1, KIND>::fn(), 64);
@@ -365,7 +372,7 @@ int residual_norm(const lowm_residual_norm_args* u, hipStream_t stream) {
   if ((!inplace && meet(ro, r)) || meet(x, r) || meet(xs, r) || meet(ro, x) || meet(ro, xs) ||
       meet(x, xs))
     return LOWM_ERR_INVALID_ARG;
-  const NormArgs a{*u};
+  const NormArgs a{*u, 0};
   return launch_rows<NormK, 2>(a, u->M, u->D, stream);
 }
 
@@ -383,7 +390,7 @@ int quantize_rows(const void* x, int x_type, int64_t ld, int M, int K, void* q, 
   const Span xs = span_of(x, M, K, ld, xb), qs = span_of(q, M, K, K, 1),
              ss = span_of(scale, 1, M, M, 4);
   if (meet(xs, qs) || meet(xs, ss) || meet(qs, ss)) return LOWM_ERR_INVALID_ARG;
-  const QuantArgs a{x, static_cast<int8_t*>(q), scale, ld, M, K, x_type == LOWM_F32};
+  const QuantArgs a{x, static_cast<int8_t*>(q), scale, ld, 0, M, K, x_type == LOWM_F32};
   return launch_rows<QuantK, 4>(a, M, K, stream);
 }
 

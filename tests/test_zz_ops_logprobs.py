@@ -240,6 +240,26 @@ def test_maxima_on_both_sides_of_a_power_of_two(M, centre, kind):
 
 
 @pytest.mark.gpu
+def test_more_rows_than_one_launch_holds():
+    """2^24 rows of a workgroup each: every row has the values of its period's row.  (Copies and
+    comparisons by slices, as for the norm.)"""
+    periods, period, V = 2 ** 13, 2 ** 11 + 3, 7
+    g = torch.Generator().manual_seed(13)
+    base, tok = logits(g, period, V, BF16).cuda(), torch.randint(0, V, (period,), generator=g).cuda()
+    x = base.expand(periods, period, V).reshape(-1, V)
+    toks = tok.expand(periods, period).reshape(-1)
+    assert len(x) > 2 ** 24
+
+    def same(many, few):
+        many = many.view(periods, *few.shape)
+        return all((many[i:i + 1024] == few).all() for i in range(0, periods, 1024))
+
+    assert same(x, base) and same(toks, tok)
+    for a, b in zip(sbg.token_logprobs(x, toks, 2), sbg.token_logprobs(base, tok, 2)):
+        assert same(a, b)
+
+
+@pytest.mark.gpu
 def test_same_bits_each_time_and_in_a_graph():
     g = torch.Generator().manual_seed(2)
     x, tok = logits(g, 3, 50001, BF16).cuda(), torch.randint(0, 50001, (3,), generator=g).cuda()

@@ -261,6 +261,26 @@ def test_operands_that_are_columns_of_one_tensor(D):
 
 
 @pytest.mark.gpu
+def test_more_rows_than_one_launch_holds():
+    """2^26 rows of 64 lanes each: every row has the values of its period's row.  (Copies and
+    comparisons by slices: torch's gather of as many rows leaves most of them zero.)"""
+    periods, period, D = 2 ** 15, 2 ** 11 + 3, 8
+    g = torch.Generator().manual_seed(12)
+    base = [rand(g, period, D, dev="cuda") for _ in range(2)]
+    y, r = (b.expand(periods, period, D).reshape(-1, D) for b in base)
+    assert len(y) > 2 ** 26
+
+    def same(many, few):
+        many = many.view(periods, *few.shape)
+        return all((many[i:i + 1024] == few).all() for i in range(0, periods, 1024))
+
+    assert same(y, base[0]) and same(r, base[1])
+    for got, few in ((sbg.quantize_rows(y), sbg.quantize_rows(base[0])),
+                     (sbg.residual_norm(y, r)[:2], sbg.residual_norm(*base)[:2])):
+        assert all(same(*p) for p in zip(got, few))
+
+
+@pytest.mark.gpu
 def test_no_rows_at_all():
     y = torch.zeros(0, 64, dtype=BF16, device="cuda")
     r, x, s = sbg.residual_norm(y, y, quantize=True)
