@@ -98,9 +98,8 @@ __device__ __forceinline__ float held(float d) { return fmaxf(d, -300.f); }
 
 // A maximum m past which c = round(m L) is off by too much: half a step of c is
 // 1/16 at 2^20, but 128 and more, a factor 2^d past fp32's range, from 2^31 on.
-// Its terms take d = (l - m) L, two roundings instead of one.  (Any bound from some
-// 2^10 to 2^25 would do: below it the offset is small against 1, and ordinary
-// logits stay below it.)  Infinities are far.
+// Its terms take d = (l - m) L, two roundings instead of one; ordinary logits stay
+// below.  Infinities are far.
 constexpr float kFar = 0x1p20f;
 __device__ __forceinline__ bool far(float m) { return fabsf(m) > kFar; }
 
