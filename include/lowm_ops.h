@@ -111,6 +111,7 @@ int lowm_quantize_rows(const void* x, int x_type, int64_t ld_x, int M, int K, vo
  * lowm_workspace_status reads it, with N = LOWM_I8_STATUS_N.
  */
 #define LOWM_I8_STATUS_N 8192
+#define LOWM_I8_MAX_N 1073741568   /* 2^30 - 256 */
 typedef struct lowm_gemm_i8_args {
     const void* A;
     const void* W;
@@ -128,10 +129,10 @@ typedef struct lowm_gemm_i8_args {
 size_t lowm_gemm_i8_workspace_bytes(int M, int N, int K);
 
 /* Errors: NULL operand, a size < 1, an unknown type, an output or workspace
- * that overlaps another operand: LOWM_ERR_INVALID_ARG; M > LOWM_MAX_M, K not a
- * multiple of 16, K > 131056 (> LOWM_QUANTIZE_MAX_K for a bf16 A), A or W not
- * 16-byte, the workspace not 256-byte aligned, another pointer not aligned to
- * its element: LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
+ * that overlaps another operand: LOWM_ERR_INVALID_ARG; M > LOWM_MAX_M, N >
+ * LOWM_I8_MAX_N, K not a multiple of 16, K > 131056 (> LOWM_QUANTIZE_MAX_K for a
+ * bf16 A), A or W not 16-byte, the workspace not 256-byte aligned, another pointer
+ * not aligned to its element: LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
  * LOWM_ERR_WORKSPACE. */
 int lowm_gemm_i8(const lowm_gemm_i8_args* args, void* stream);
 

@@ -676,6 +676,9 @@ Pair i8_kernel(int MB, const I8Plan& p) {
 }
 
 constexpr int64_t kI8MaxK = 131056;   // 128 * 128 * K stays below 2^31
+// The panel kind's four threads to a column, in tiles of up to 256 columns, are
+// fewer than 2^32, what a launch takes.
+static_assert(4ll * (LOWM_I8_MAX_N + 255) < 1ll << 32, "one launch");
 // What a split launch may use of the workspace: counter lines, one for each
 // tile, and blocks of 16 x 16 partial sums.
 constexpr int kI8MaxTiles = LOWM_I8_STATUS_N / 16;
@@ -742,7 +745,7 @@ I8Plan i8_plan(int M, int N, int K, bool split, bool whole) {
 }
 
 size_t i8_workspace(int M, int N, int K) {
-  if (M < 1 || M > LOWM_MAX_M || N < 1 || K < 1 || K % 16 || K > kI8MaxK) return 0;
+  if (M < 1 || M > LOWM_MAX_M || N < 1 || N > LOWM_I8_MAX_N || K < 1 || K % 16 || K > kI8MaxK) return 0;
   return kI8LineBytes + kI8SlotBytes + ((size_t)M * K + 255) / 256 * 256 +
          LOWM_MAX_M * sizeof(float);
 }
@@ -754,7 +757,7 @@ int gemm_i8(const lowm_gemm_i8_args* u, hipStream_t stream) {
   if ((!quantised && u->a_type != LOWM_BF16) || (quantised && !u->a_scale) ||
       (u->c_type != LOWM_BF16 && u->c_type != LOWM_F32))
     return LOWM_ERR_INVALID_ARG;
-  if (u->M > LOWM_MAX_M || u->K % 16 || u->K > (quantised ? kI8MaxK : LOWM_QUANTIZE_MAX_K))
+  if (u->M > LOWM_MAX_M || u->N > LOWM_I8_MAX_N || u->K % 16 || u->K > (quantised ? kI8MaxK : LOWM_QUANTIZE_MAX_K))
     return LOWM_ERR_UNSUPPORTED;
   const size_t need = i8_workspace(u->M, u->N, u->K);
   if (u->workspace ? u->workspace_bytes < need : !quantised) return LOWM_ERR_WORKSPACE;

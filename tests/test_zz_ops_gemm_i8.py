@@ -210,6 +210,16 @@ def test_workspace_bytes():
     assert f(65, 64, 512) == f(4, 64, 520) == f(0, 64, 512) == f(4, 64, 131072) == 0
 
 
+def test_more_columns_than_one_launch_holds_are_refused():
+    f = ops.library().lib.lowm_gemm_i8_workspace_bytes
+    most = 2 ** 30 - 256
+    assert f(1, most, 16) > 0
+    for N in (most + 1, 2 ** 30, 2 ** 31 - 1):
+        a = ops.GemmI8Args(**{**BASE, "N": N, "K": 16})
+        assert ops.library().lib.lowm_gemm_i8(ctypes.byref(a), None) == -2
+        assert f(1, N, 16) == 0
+
+
 def test_python_checks():
     q = torch.zeros(2, 16, dtype=I8)
     for bad in (lambda: sbg.gemm_i8(q, q, torch.ones(2)),
