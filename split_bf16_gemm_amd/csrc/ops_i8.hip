@@ -405,6 +405,9 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_few_kernel(I8Args a) {
     }
   }
   stream_settle(acc);
+  // Where there were fewer steps than slots, the others' loads may still be on their
+  // way into LDS, which the sums take next.
+  wait_vmcnt<0>();
   i32x4* sums = reinterpret_cast<i32x4*>(lds);
   __syncthreads();
 #pragma unroll

@@ -136,6 +136,25 @@ def test_rows_anywhere_in_a_line_of_memory(M, N, K, offset):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 4, 8])
+@pytest.mark.parametrize("N,K", [(40, 16), (4096, 112), (8192, 256), (12000, 384), (4000, 640),
+                                 # rows that are not whole lines, 2^24 bytes of W
+                                 (8150, 2064), (6000, 2800), (5000, 3376)])
+def test_bf16_rows_shorter_than_the_ring(M, N, K):
+    """Wavefronts with fewer steps than their ring has slots, or with none: the slots' loads end
+    before the sums take their place."""
+    g = torch.Generator().manual_seed(M + N + K)
+    _, _, W, sw = operands(g, 1, N, K)
+    x = torch.randint(-126, 127, (M, K), generator=g).to(BF16)
+    x[:, K // 3] = 127.0                                # so that the scales are ones
+    ws = sbg.make_gemm_i8_workspace(M, N, K)
+    want = formula(x.to(I8), torch.ones(M), W, sw, F32)
+    x, W, sw = x.cuda(), W.cuda(), sw.cuda()
+    for _ in range(4):
+        assert torch.equal(sbg.gemm_i8(x, W, sw, out_dtype=F32, workspace=ws).cpu(), want)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("K", [512, 4096, 32768])
 def test_rows_of_zeros_and_without_a_scale(K):
     g = torch.Generator().manual_seed(6)
