@@ -17,7 +17,8 @@
  * (a hipStream_t; NULL is the null stream) and returns.  Return values are
  * the LOWM_* codes of lowm.h; lowm_last_hip_error() gives the cause of
  * LOWM_ERR_LAUNCH.  Every struct below is read during the call only.  All
- * calls can be captured into a HIP graph.
+ * calls can be captured into a HIP graph.  The current device has to be that of
+ * the buffers and of the stream.
  */
 #ifndef LOWM_OPS_H
 #define LOWM_OPS_H

@@ -6,6 +6,7 @@
 // Every function takes its arguments by position (split_bf16_gemm_amd/ops.py has
 // the signatures) and returns the C ABI's code; a tensor that does not fit raises
 // ValueError or TypeError.  No C++ exception leaves a function.
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -121,6 +122,12 @@ void workspace(PyObject* o, void** p, size_t* bytes) {
   *bytes = t.nbytes();
 }
 
+// Makes the call's GPU the current one while it launches: a launch goes to the
+// current device, whatever memory its pointers are in and whose stream it is given.
+c10::DeviceGuard on_call_device() {
+  return c10::DeviceGuard(c10::Device(c10::kCUDA, (c10::DeviceIndex)call_device));
+}
+
 int residual_norm(PyObject* const* a) {
   lowm_residual_norm_args u{};
   const at::Tensor& r = tensor(a[1], "residual");
@@ -187,6 +194,7 @@ int residual_norm(PyObject* const* a) {
   u.residual_scale = real(a[9]);
   u.branch_scale = real(a[10]);
   u.eps = real(a[11]);
+  const c10::DeviceGuard guard = on_call_device();
   return lowm_residual_norm(&u, stream_of(a[12]));
 }
 
@@ -197,6 +205,7 @@ int quantize_rows(PyObject* const* a) {
   const int64_t M = x.size(0), K = x.size(1);
   void* q = dense(a[1], "out", at::kChar, {M, K});
   void* s = dense(a[2], "scale_out", at::kFloat, {M});
+  const c10::DeviceGuard guard = on_call_device();
   return lowm_quantize_rows(x.data_ptr(), type, pitch(x, "x"), to_int(M, "M"), to_int(K, "K"), q,
                             static_cast<float*>(s), stream_of(a[3]));
 }
@@ -230,6 +239,7 @@ int gemm_i8(PyObject* const* a) {
   u.M = to_int(M, "M");
   u.N = to_int(N, "N");
   u.K = to_int(K, "K");
+  const c10::DeviceGuard guard = on_call_device();
   return lowm_gemm_i8(&u, stream_of(a[6]));
 }
 
@@ -259,6 +269,7 @@ int moe(PyObject* const* a) {
   u.top_k = to_int(K, "top_k");
   u.flags = (int)integer(a[10]);
   u.routed_scale = real(a[11]);
+  const c10::DeviceGuard guard = on_call_device();
   return lowm_moe(&u, stream_of(a[12]));
 }
 
@@ -286,6 +297,7 @@ int token_logprobs(PyObject* const* a) {
   workspace(a[8], &u.workspace, &u.workspace_bytes);
   if (!u.workspace && lowm_token_logprobs_workspace_bytes(u.M, u.V, u.top_n) > 0)
     refuse(PyExc_ValueError, "these rows need a zeroed workspace (make_token_logprobs_workspace)");
+  const c10::DeviceGuard guard = on_call_device();
   return lowm_token_logprobs(&u, stream_of(a[9]));
 }
 

@@ -105,6 +105,8 @@ def _stream(stream, device) -> int:
     if stream is None:
         # a tensor that is not on a GPU is refused by the call itself
         return torch._C._cuda_getCurrentRawStream(device.index) if device.index is not None else 0
+    if device.index is not None and stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
     return stream.cuda_stream
 
 

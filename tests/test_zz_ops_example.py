@@ -71,6 +71,38 @@ def test_decode_block(tokens, hidden, inner, experts, top_k, vocab):
                        torch.sort(d["logits"], dim=1, descending=True, stable=True).indices[:, :5])
 
 
+def test_a_stream_of_another_gpu_is_refused():
+    class Stream:
+        cuda_stream, device = 0x1230, torch.device("cuda", 1)
+
+    assert ops._stream(Stream(), torch.device("cuda", 1)) == 0x1230
+    with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
+        ops._stream(Stream(), torch.device("cuda", 0))
+
+
+@pytest.mark.gpu
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second GPU")
+def test_tensors_on_a_gpu_that_is_not_the_current_one():
+    """The calls run where the tensors are, and leave the current device as it was."""
+    assert torch.cuda.current_device() == 0
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(3, 4096, generator=g).to(torch.bfloat16).cuda(1)
+    W = torch.randint(-127, 128, (64, 4096), generator=g, dtype=torch.int8).cuda(1)
+    w_scale, tokens = torch.ones(64, device="cuda:1"), torch.zeros(3, dtype=torch.int64, device="cuda:1")
+
+    def calls():
+        return (*sbg.residual_norm(x, x)[:2], *sbg.quantize_rows(x),
+                sbg.gemm_i8(x, W, w_scale, workspace=sbg.make_gemm_i8_workspace(3, 64, 4096, "cuda:1")),
+                *sbg.token_logprobs(x, tokens))
+
+    got = calls()
+    assert torch.cuda.current_device() == 0 and all(t.device.index == 1 for t in got)
+    with torch.cuda.device(1):
+        want = calls()
+    torch.cuda.synchronize(1)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def header():
     return re.sub(r"/\*.*?\*/", "", (ROOT / "include" / "lowm_ops.h").read_text(), flags=re.S)
 
