@@ -348,7 +348,11 @@ int lowm_gemm_splitk_push(const void* A, const void* W, void* C, int M, int N, i
  * after it.  `flags` must hold at least n_flags words (the library cannot
  * check this: a shorter buffer is read past its end); n_flags 1 .. 4096,
  * timeout_us <= 10,000,000, flag_value non-zero; the wait is bounded whether
- * or not any producer runs.
+ * or not any producer runs.  A process has few hardware queues (4 by default),
+ * which its streams are given in turn, and a queue runs its kernels in order: a
+ * wait that is enqueued before its producer needs the two streams to be on
+ * different queues, or it holds the producer up until its own limit and reports
+ * the flags missing.  Enqueued after the producer it passes on any stream.
  */
 int lowm_push_wait(const uint32_t* flags, int n_flags, uint32_t flag_value,
                    uint32_t timeout_us, int* missing, void* stream);

@@ -107,8 +107,9 @@ int lowm_quantize_rows(const void* x, int x_type, int64_t ld_x, int M, int K, vo
  * The workspace (lowm_gemm_i8_workspace_bytes, 256-byte aligned) holds the
  * quantised rows of a bf16 A and the partial sums where K is split over
  * workgroups.  It is zeroed once before its first use; every call that completes
- * leaves what must be zero so, for any sizes.  One workspace per call in flight.
- * An int8 A may come without one (NULL): K is then not split.
+ * leaves what must be zero so, for any sizes.  The rest is not zero after a call:
+ * a workspace serves this operator alone until it is zeroed again.  One workspace
+ * per call in flight.  An int8 A may come without one (NULL): K is then not split.
  * lowm_workspace_status reads it, with N = LOWM_I8_STATUS_N.
  */
 #define LOWM_I8_STATUS_N 8192
@@ -157,8 +158,9 @@ int lowm_gemm_i8(const lowm_gemm_i8_args* args, void* stream);
  *
  * The workspace (lowm_moe_workspace_bytes, 256-byte aligned) is zeroed once
  * before its first use; every call that completes leaves what must be zero so,
- * for any sizes.  One workspace per call in flight.  lowm_workspace_status of
- * the GEMM reads it too, with N = D + 80.
+ * for any sizes.  The rest is not zero after a call: a workspace serves this
+ * operator alone until it is zeroed again.  One workspace per call in flight.
+ * lowm_workspace_status of the GEMM reads it too, with N = D + 80.
  */
 #define LOWM_MOE_MAX_T 64
 #define LOWM_MOE_MAX_E 256

@@ -266,7 +266,9 @@ class Library:
     def push_wait(self, flags, n_flags: int, flag_value: int, timeout_us: int, missing,
                   stream=None):
         """Enqueue the bounded wait for flags[0:n_flags] == flag_value; the count
-        of flags not seen set lands in missing[0] (an int32 GPU tensor)."""
+        of flags not seen set lands in missing[0] (an int32 GPU tensor).  Enqueued before
+        its producer, it needs a stream on another hardware queue than the producer's (a
+        process has few, which its streams are given in turn); after it, any stream will do."""
         if missing.dtype != torch.int32 or not missing.is_cuda or flags.dtype != torch.int32:
             raise ValueError("flags and missing must be int32 GPU tensors")
         if not flags.is_cuda or not flags.is_contiguous() or not 1 <= n_flags <= flags.numel():

@@ -19,8 +19,10 @@
 //
 // Bound by HBM.  Measured on MI355X, us a call, beside the time of a plain read of
 // the chosen experts: T 1, D 4096, I 1024, E 64, top_k 4 27 (15); T 64, E 128,
-// top_k 8 487 (473).  What is left is the three launches and the routing, which
-// one kernel has to finish before the next can know what to read.
+// top_k 8 483 (473).  What is left at T 1 is 6 us of routing, which one kernel has to
+// finish before the next can know what to read, and 5 us in up and down, which take
+// 12.4 and 7.8 us for 67 and 34 MB and load 16 rows of activations a step where one
+// is there.
 //
 // Roundings: h = silu(gate) up is rounded to bf16, the matrix instructions' type,
 // from fp32 sums; that is the one rounding besides the result's own, and makes the
@@ -811,8 +813,9 @@ int moe(const lowm_moe_args* u, hipStream_t stream) {
                      sizeof(float) * kWaves * (size_t)T * kCols;
   const size_t down_grid = (size_t)((D + kCols - 1) / kCols) * l.down_splits;
   if (rc == LOWM_OK)
-    // Up to one workgroup to a CU the ring is as deep as half its LDS allows; more
-    // share a CU in pairs, rather than leave the last ones a round of their own
+    // Up to one workgroup to a CU each has a CU to itself: a ring of 6 slots, 102 KB,
+    // beside up to 29 KB of lists and sums (8 slots are no faster).  More share a CU
+    // in pairs, with 3 slots, rather than leave the last ones a round of their own
     // (T 16, D 2488, I 272, E 128, 312 workgroups: 66 us with 3 slots, 76 with 6;
     // T 64, D 4096, I 1024, E 64, 256 workgroups: 289 and 261).
     rc = go(l.seg_rows == 64

@@ -180,7 +180,7 @@ def quantize_rows(x: torch.Tensor, *, out: Optional[torch.Tensor] = None,
 
 def make_gemm_i8_workspace(M: int, N: int, K: int, device="cuda") -> Optional[torch.Tensor]:
     """A zeroed workspace of gemm_i8 for these sizes (None for sizes it rejects); it also serves
-    any other sizes that need no more bytes, one call at a time."""
+    any other sizes that need no more bytes, one call at a time, but no other operator."""
     n = library().lib.lowm_gemm_i8_workspace_bytes(M, N, K)
     return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
@@ -207,7 +207,7 @@ def gemm_i8(A: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, *,
 def make_moe_workspace(T: int, D: int, I: int, E: int, top_k: int,
                        device="cuda") -> Optional[torch.Tensor]:
     """A zeroed workspace of moe for these sizes (None for T 0 and for sizes it rejects); it also
-    serves any other sizes that need no more bytes, one call at a time."""
+    serves any other sizes that need no more bytes, one call at a time, but no other operator."""
     n = library().lib.lowm_moe_workspace_bytes(T, D, I, E, top_k)
     return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
