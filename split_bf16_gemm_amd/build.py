@@ -3,8 +3,8 @@
     python -m split_bf16_gemm_amd.build
 
 produces, under split_bf16_gemm_amd/_lib/:
-  liblowm.so         the GEMM and the operators around it (C ABI of include/lowm.h
-                     and include/lowm_ops.h)
+  liblowm.so         the GEMM and the operators around it (C ABI of include/lowm.h,
+                     include/lowm_ops.h and include/lowm_cache.h)
   liblowm_stress.so  the same sources with -DLOWM_STRESS (stall injection)
   libbwprobe.so      streaming read/copy kernels for the HBM ceiling
   ops_binding.so     the operators' Python entry (csrc/ops_binding.cpp, host code),
@@ -41,8 +41,9 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 
 GEMM_SOURCES = ["lowm_host.hip", "lowm_inst_bf16.hip", "lowm_inst_f32.hip",
                 "lowm_inst_push.hip"]
-# the operators of include/lowm_ops.h
-OPS_SOURCES = ["ops_norm.hip", "ops_logprob.hip", "ops_i8.hip", "ops_moe.hip"]
+# the operators of include/lowm_ops.h and include/lowm_cache.h
+OPS_SOURCES = ["ops_norm.hip", "ops_logprob.hip", "ops_i8.hip", "ops_moe.hip",
+               "ops_rotary.hip", "ops_cache.hip", "ops_attention.hip", "ops_pages.hip"]
 TARGETS = {
     "liblowm.so": (GEMM_SOURCES + OPS_SOURCES, []),
     "liblowm_stress.so": (GEMM_SOURCES, ["-DLOWM_STRESS"]),

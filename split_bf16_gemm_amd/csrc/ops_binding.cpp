@@ -1,9 +1,10 @@
-// ops_binding.cpp -- Python entry of the operators of include/lowm_ops.h: checks
+// ops_binding.cpp -- Python entry of the operators of include/lowm_ops.h and
+// include/lowm_cache.h: checks
 // a call's tensors, fills the argument struct and calls the C ABI.  Built as a
 // Python extension because these calls are short: the same checks in Python take
 // longer than the smallest kernels (5 us against 1).
 //
-// Every function takes its arguments by position (split_bf16_gemm_amd/ops.py has
+// Every function takes its arguments by position (split_bf16_gemm_amd/ops.py and cache.py have
 // the signatures) and returns the C ABI's code; a tensor that does not fit raises
 // ValueError or TypeError.  No C++ exception leaves a function.
 #include <c10/core/DeviceGuard.h>
@@ -12,7 +13,7 @@
 #include <exception>
 #include <string>
 
-#include "lowm_ops.h"
+#include "lowm_cache.h"
 
 namespace {
 
@@ -301,6 +302,231 @@ int token_logprobs(PyObject* const* a) {
   return lowm_token_logprobs(&u, stream_of(a[9]));
 }
 
+// [T, H, D] of `type` (or any of bf16 and fp32: at::ScalarType::Undefined) with contiguous
+// rows of D; its strides.
+struct HeadsOf {
+  void* p;
+  int64_t T, H, D, row, head;
+  at::ScalarType type;
+};
+HeadsOf heads_of(PyObject* o, const char* name, at::ScalarType type) {
+  const at::Tensor& t = tensor(o, name);
+  if (type == at::ScalarType::Undefined)
+    real_type_of(t, name);
+  else if (t.scalar_type() != type)
+    refuse(PyExc_TypeError, std::string(name) + " must be " + c10::toString(type));
+  if (t.dim() != 3) refuse(PyExc_ValueError, std::string(name) + " must have three dimensions");
+  if (t.size(2) > 1 && t.stride(2) != 1)
+    refuse(PyExc_ValueError, std::string(name) + " must have contiguous rows");
+  HeadsOf h{t.data_ptr(), t.size(0), t.size(1), t.size(2), t.stride(0), t.stride(1),
+            t.scalar_type()};
+  // a stride of a dimension of one element steps nowhere
+  if (h.H == 1) h.head = h.D;
+  if (h.T <= 1) h.row = h.H * (h.head > h.D ? h.head : h.D);
+  return h;
+}
+void same_heads(const HeadsOf& x, const char* name, int64_t T, int64_t H, int64_t D) {
+  if (x.T != T || x.H != H || x.D != D) {
+    const int64_t got[] = {x.T, x.H, x.D}, want[] = {T, H, D};
+    refuse(PyExc_ValueError, std::string(name) + " has shape " + shape_text(got, 3) + ", not " +
+                                 shape_text(want, 3));
+  }
+}
+
+// The cache's four tensors a[0..3]: one layer [P, H, ...] or, where `layers`, also
+// several [L, P, H, ...].
+lowm_kv_cache cache_of(PyObject* const* a, bool layers) {
+  const at::Tensor& k = tensor(a[0], "cache.k");
+  lowm_kv_cache c{};
+  const bool many = k.dim() == 6;
+  if (!(k.dim() == 5 || (many && layers)))
+    refuse(PyExc_ValueError, layers ? "cache.k must have five dimensions, or six with layers"
+                                    : "cache.k must have five dimensions (one layer)");
+  const int64_t L = many ? k.size(0) : 1, P = k.size(many), H = k.size(many + 1),
+                D = k.size(many + 2) * 16;
+  if (k.scalar_type() == at::kChar)
+    c.type = LOWM_I8;
+  else if (k.scalar_type() == at::kFloat8_e4m3fn)
+    c.type = LOWM_E4M3;
+  else
+    refuse(PyExc_TypeError, "cache.k must be int8 or float8_e4m3fn");
+  const at::ScalarType type = k.scalar_type();
+  if (many) {
+    c.k = dense(a[0], "cache.k", type, {L, P, H, D / 16, 64, 16});
+    c.v = dense(a[1], "cache.v", type, {L, P, H, 4, D, 16});
+    c.k_scale = static_cast<float*>(dense(a[2], "cache.k_scale", at::kFloat, {L, P, H}));
+    c.v_scale = static_cast<float*>(dense(a[3], "cache.v_scale", at::kFloat, {L, P, H}));
+  } else {
+    c.k = dense(a[0], "cache.k", type, {P, H, D / 16, 64, 16});
+    c.v = dense(a[1], "cache.v", type, {P, H, 4, D, 16});
+    c.k_scale = static_cast<float*>(dense(a[2], "cache.k_scale", at::kFloat, {P, H}));
+    c.v_scale = static_cast<float*>(dense(a[3], "cache.v_scale", at::kFloat, {P, H}));
+  }
+  c.P = to_int(P, "pages");
+  c.H = to_int(H, "heads");
+  c.D = to_int(D, "head_dim");
+  c.layers = to_int(L, "layers");
+  return c;
+}
+
+// table a[0] [B, W], lens a[1] [B], row_starts a[2] [B + 1] or None, for T rows.
+lowm_sequences sequences_of(PyObject* const* a, int64_t T) {
+  lowm_sequences s{};
+  const at::Tensor& t = tensor(a[0], "table");
+  if (t.scalar_type() != at::kInt) refuse(PyExc_TypeError, "table must be int32");
+  if (t.dim() != 2) refuse(PyExc_ValueError, "table must have two dimensions");
+  const int64_t B = t.size(0), W = t.size(1);
+  s.table_ld = pitch(t, "table");
+  s.table = static_cast<const int32_t*>(t.data_ptr());
+  s.lens = static_cast<const int32_t*>(dense(a[1], "lens", at::kInt, {B}));
+  if (a[2] != Py_None)
+    s.row_starts = static_cast<const int32_t*>(dense(a[2], "row_starts", at::kInt, {B + 1}));
+  else if (B > 0 && T % B)
+    refuse(PyExc_ValueError, std::to_string(T) + " rows are no multiple of " + std::to_string(B) +
+                                 " sequences: row_starts is needed");
+  s.B = to_int(B, "B");
+  s.W = to_int(W, "W");
+  s.T = to_int(T, "T");
+  return s;
+}
+
+int rotary(PyObject* const* a) {
+  lowm_rotary_args u{};
+  const HeadsOf q = heads_of(a[0], "q", at::ScalarType::Undefined);
+  const HeadsOf qo = heads_of(a[1], "q_out", q.type);
+  same_heads(qo, "q_out", q.T, q.H, q.D);
+  u.q = q.p;
+  u.q_out = qo.p;
+  u.q_row = q.row, u.q_head = q.head, u.q_out_row = qo.row, u.q_out_head = qo.head;
+  if (a[2] != Py_None) {
+    const HeadsOf k = heads_of(a[2], "k", q.type);
+    const HeadsOf ko = heads_of(a[3], "k_out", q.type);
+    same_heads(k, "k", q.T, k.H, q.D);
+    same_heads(ko, "k_out", q.T, k.H, q.D);
+    u.k = k.p;
+    u.k_out = ko.p;
+    u.k_row = k.row, u.k_head = k.head, u.k_out_row = ko.row, u.k_out_head = ko.head;
+    u.Hk = to_int(k.H, "heads");
+  }
+  const at::Tensor& pos = tensor(a[4], "positions");
+  if (pos.scalar_type() != at::kLong && pos.scalar_type() != at::kInt)
+    refuse(PyExc_TypeError, "positions must be int64 or int32");
+  u.positions = dense(a[4], "positions", pos.scalar_type(), {q.T});
+  u.positions_bytes = (int)pos.element_size();
+  const at::Tensor& f = tensor(a[5], "freqs");
+  if (f.dim() != 1) refuse(PyExc_ValueError, "freqs must have one dimension");
+  u.freqs = static_cast<const double*>(dense(a[5], "freqs", at::kDouble, {f.size(0)}));
+  u.R = to_int(2 * f.size(0), "freqs");
+  u.T = to_int(q.T, "T");
+  u.Hq = to_int(q.H, "heads");
+  u.D = to_int(q.D, "head_dim");
+  u.type = q.type == at::kFloat ? LOWM_F32 : LOWM_BF16;
+  u.first = to_int(integer(a[6]), "first");
+  u.flags = (int)integer(a[7]);
+  u.scale = real(a[8]);
+  const c10::DeviceGuard guard = on_call_device();
+  return lowm_rotary(&u, stream_of(a[9]));
+}
+
+int cache_append(PyObject* const* a) {
+  lowm_cache_append_args u{};
+  const HeadsOf k = heads_of(a[0], "k", at::ScalarType::Undefined);
+  const HeadsOf v = heads_of(a[1], "v", k.type);
+  u.cache = cache_of(a + 2, false);
+  same_heads(k, "k", k.T, u.cache.H, u.cache.D);
+  same_heads(v, "v", k.T, u.cache.H, u.cache.D);
+  u.seq = sequences_of(a + 6, k.T);
+  u.k = k.p;
+  u.v = v.p;
+  u.k_row = k.row, u.k_head = k.head, u.v_row = v.row, u.v_head = v.head;
+  u.type = k.type == at::kFloat ? LOWM_F32 : LOWM_BF16;
+  const c10::DeviceGuard guard = on_call_device();
+  return lowm_cache_append(&u, stream_of(a[9]));
+}
+
+int cache_read(PyObject* const* a) {
+  lowm_cache_read_args u{};
+  u.cache = cache_of(a + 2, false);
+  const at::Tensor& k = tensor(a[0], "k_out");
+  const int64_t T = k.dim() == 3 ? k.size(0) : 0;
+  u.k_out = dense(a[0], "k_out", at::kBFloat16, {T, u.cache.H, u.cache.D});
+  u.v_out = dense(a[1], "v_out", at::kBFloat16, {T, u.cache.H, u.cache.D});
+  u.seq = sequences_of(a + 6, T);
+  const c10::DeviceGuard guard = on_call_device();
+  return lowm_cache_read(&u, stream_of(a[9]));
+}
+
+int cache_attention(PyObject* const* a) {
+  lowm_cache_attention_args u{};
+  const HeadsOf q = heads_of(a[0], "q", at::kBFloat16);
+  u.cache = cache_of(a + 1, false);
+  same_heads(q, "q", q.T, q.H, u.cache.D);
+  u.seq = sequences_of(a + 5, q.T);
+  u.q = q.p;
+  u.q_row = q.row, u.q_head = q.head;
+  u.Hq = to_int(q.H, "heads");
+  u.out = dense(a[8], "out", at::kBFloat16, {q.T, q.H, q.D});
+  if (a[9] != Py_None) u.lse = static_cast<float*>(dense(a[9], "lse_out", at::kFloat, {q.T, q.H}));
+  workspace(a[10], &u.workspace, &u.workspace_bytes);
+  if (!u.workspace && q.T > 0)
+    refuse(PyExc_ValueError,
+           "cache_attention needs a workspace (make_cache_attention_workspace)");
+  u.window = to_int(integer(a[11]), "window");
+  u.scale = real(a[12]);
+  const c10::DeviceGuard guard = on_call_device();
+  return lowm_cache_attention(&u, stream_of(a[13]));
+}
+
+// A page table and what goes with it, for the calls on pages.
+const int32_t* page_table(PyObject* o, const char* name, int64_t R, int64_t W) {
+  return static_cast<const int32_t*>(dense(o, name, at::kInt, {R, W}));
+}
+
+int fork_pages(PyObject* const* a) {
+  lowm_fork_pages_args u{};
+  u.cache = cache_of(a, true);
+  const at::Tensor& t = tensor(a[4], "table");
+  if (t.dim() != 2) refuse(PyExc_ValueError, "table must have two dimensions");
+  const int64_t R = t.size(0), W = t.size(1), P = u.cache.P;
+  u.table = page_table(a[4], "table", R, W);
+  u.lens = static_cast<const int32_t*>(dense(a[5], "lens", at::kInt, {R}));
+  if (a[6] != Py_None)
+    u.parents = static_cast<const int32_t*>(dense(a[6], "parents", at::kInt, {R}));
+  if (a[7] != Py_None) u.held = static_cast<const int32_t*>(dense(a[7], "held", at::kInt, {P}));
+  u.table_out = const_cast<int32_t*>(page_table(a[8], "table_out", R, W));
+  u.lens_out = static_cast<int32_t*>(dense(a[9], "lens_out", at::kInt, {R}));
+  u.refs_out = static_cast<int32_t*>(dense(a[10], "refs_out", at::kInt, {P}));
+  u.missing_out = static_cast<int32_t*>(dense(a[11], "missing_out", at::kInt, {1}));
+  workspace(a[12], &u.workspace, &u.workspace_bytes);
+  if (!u.workspace)
+    refuse(PyExc_ValueError, "fork_pages needs a workspace (make_pages_workspace)");
+  u.R = to_int(R, "rows");
+  u.W = to_int(W, "W");
+  u.reserve = to_int(integer(a[13]), "reserve");
+  const c10::DeviceGuard guard = on_call_device();
+  return lowm_fork_pages(&u, stream_of(a[14]));
+}
+
+int compact_pages(PyObject* const* a) {
+  lowm_compact_pages_args u{};
+  u.cache = cache_of(a, true);
+  const at::Tensor& t = tensor(a[4], "table");
+  if (t.dim() != 2) refuse(PyExc_ValueError, "table must have two dimensions");
+  const int64_t R = t.size(0), W = t.size(1), P = u.cache.P;
+  u.table = page_table(a[4], "table", R, W);
+  if (a[5] != Py_None) u.held = static_cast<const int32_t*>(dense(a[5], "held", at::kInt, {P}));
+  u.table_out = const_cast<int32_t*>(page_table(a[6], "table_out", R, W));
+  u.refs_out = static_cast<int32_t*>(dense(a[7], "refs_out", at::kInt, {P}));
+  u.counts_out = static_cast<int32_t*>(dense(a[8], "counts_out", at::kInt, {2}));
+  workspace(a[9], &u.workspace, &u.workspace_bytes);
+  if (!u.workspace)
+    refuse(PyExc_ValueError, "compact_pages needs a workspace (make_pages_workspace)");
+  u.R = to_int(R, "rows");
+  u.W = to_int(W, "W");
+  const c10::DeviceGuard guard = on_call_device();
+  return lowm_compact_pages(&u, stream_of(a[10]));
+}
+
 template <int (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != N) {
@@ -331,6 +557,12 @@ PyMethodDef methods[] = {
     {"gemm_i8", fast<gemm_i8, 7>(), METH_FASTCALL, nullptr},
     {"moe", fast<moe, 13>(), METH_FASTCALL, nullptr},
     {"token_logprobs", fast<token_logprobs, 10>(), METH_FASTCALL, nullptr},
+    {"rotary", fast<rotary, 10>(), METH_FASTCALL, nullptr},
+    {"cache_append", fast<cache_append, 10>(), METH_FASTCALL, nullptr},
+    {"cache_read", fast<cache_read, 10>(), METH_FASTCALL, nullptr},
+    {"cache_attention", fast<cache_attention, 14>(), METH_FASTCALL, nullptr},
+    {"fork_pages", fast<fork_pages, 15>(), METH_FASTCALL, nullptr},
+    {"compact_pages", fast<compact_pages, 11>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ops_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -180,11 +180,13 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 struct RowScale {
   float scale, recip;
   bool some;
-  __device__ __forceinline__ explicit RowScale(uint32_t top) {
-    const bool finite = top < 0x7f800000u;
-    const float s = __builtin_bit_cast(float, top) / 127.0f;
-    scale = finite ? s : __builtin_nanf("");
-    some = finite && s > 0.f;
+  __device__ __forceinline__ explicit RowScale(uint32_t top)
+      : RowScale(top < 0x7f800000u ? __builtin_bit_cast(float, top) / 127.0f
+                                   : __builtin_nanf("")) {}
+  // From the scale itself; NaN for a row that has none.
+  __device__ __forceinline__ explicit RowScale(float s) {
+    scale = s;
+    some = s > 0.f;
     // no reciprocal for a subnormal scale: its values all take the divide
     recip = s >= 1.17549435e-38f ? 1.0f / s : __builtin_nanf("");
   }

@@ -1,0 +1,210 @@
+// ops_rotary.hip -- rotary positions for queries and keys (include/lowm_cache.h)
+// for gfx950.
+//
+//   a = pos freq ;  (x, y) -> scale (x cos a - y sin a, x sin a + y cos a)
+//
+// Elementwise but for the angles, which all heads of a token share: a thread owns
+// eight pairs of a token, forms their sines and cosines once and goes through
+// heads with them, so few heads to a thread cost arithmetic and many leave lanes
+// idle (launch_rotary).  The angle is taken modulo a turn in fp64, where position
+// and frequency are exact to 2^-53, and goes to the fp32 sine in half turns.
+#include "ops_cache.cuh"
+
+namespace lowm {
+namespace {
+
+struct RotaryArgs {
+  lowm_rotary_args u;
+  int64_t first_token, tokens;   // of this launch
+  int head_lanes;                // threads that share a token's heads
+  int pair_groups, groups;       // of eight pairs; with those of eight copied elements
+  bool copy_q, copy_k;           // whether what is not turned has to be copied
+};
+
+// Eight (or, at the end of a stretch, n) elements.
+template <bool F32>
+__device__ __forceinline__ void take(const void* p, int64_t at, int n, float (&v)[8]) {
+  if (n >= 8) {
+    values8(load8(p, at, F32), F32, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? load1(p, at + i, F32) : 0.f;
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void put(void* p, int64_t at, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    store8(p, at, F32, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) store1(p, at + i, F32, v[i]);
+  }
+}
+
+template <bool F32, bool HALF>
+__global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
+  const lowm_rotary_args& u = a.u;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int g = (int)(at % a.groups);
+  const int64_t th = at / a.groups;
+  const int lane = (int)(th % a.head_lanes);
+  const int64_t local = th / a.head_lanes;
+  if (local >= a.tokens) return;
+  const int64_t t = a.first_token + local;
+  const int heads = u.Hq + u.Hk, pairs = u.R / 2;
+  auto row_of = [&](int h, const void** x, void** y, int64_t* from, int64_t* to) {
+    const bool q = h < u.Hq;
+    const int i = q ? h : h - u.Hq;
+    *x = q ? u.q : u.k;
+    *y = q ? u.q_out : u.k_out;
+    *from = t * (q ? u.q_row : u.k_row) + i * (q ? u.q_head : u.k_head);
+    *to = t * (q ? u.q_out_row : u.k_out_row) + i * (q ? u.q_out_head : u.k_out_head);
+  };
+
+  if (g >= a.pair_groups) {
+    // eight of the elements that are copied: those before the turned ones, then
+    // those behind them, groups of each apart
+    const int before = (u.first + 7) / 8, c = g - a.pair_groups;
+    const int d = c < before ? 8 * c : u.first + u.R + 8 * (c - before);
+    const int end = c < before ? u.first : u.D;
+    const int n = end - d < 8 ? end - d : 8;
+    for (int h = lane; h < heads; h += a.head_lanes) {
+      if (!(h < u.Hq ? a.copy_q : a.copy_k)) continue;
+      const void* x;
+      void* y;
+      int64_t from, to;
+      row_of(h, &x, &y, &from, &to);
+      float v[8];
+      take<F32>(x, from + d, n, v);
+      put<F32>(y, to + d, n, v);
+    }
+    return;
+  }
+
+  const int p0 = 8 * g, n = pairs - p0 < 8 ? pairs - p0 : 8;
+  const double pos = u.positions_bytes == 8
+                         ? (double)static_cast<const int64_t*>(u.positions)[t]
+                         : (double)static_cast<const int32_t*>(u.positions)[t];
+  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const double half_turns = pos * u.freqs[p0 + (i < n ? i : 0)] * 0.31830988618379067154;
+    const float part = (float)(half_turns - 2.0 * rint(0.5 * half_turns));
+    float si, co;
+    sincospif(part, &si, &co);
+    c[i] = u.scale * co;
+    s[i] = u.scale * (u.flags & LOWM_ROTARY_INVERSE ? -si : si);
+  }
+  const int d0 = u.first + (HALF ? p0 : 2 * p0);
+  const int d1 = HALF ? d0 + pairs : d0 + 8;
+  const int n0 = HALF ? n : 2 * n, n1 = HALF ? n : 2 * n - 8;
+#pragma unroll 2
+  for (int h = lane; h < heads; h += a.head_lanes) {
+    const void* x;
+    void* y;
+    int64_t from, to;
+    row_of(h, &x, &y, &from, &to);
+    float v[8], w[8], v2[8], w2[8];
+    take<F32>(x, from + d0, n0, v);
+    take<F32>(x, from + d1, n1, w);
+    if (HALF) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v2[i] = v[i] * c[i] - w[i] * s[i];
+        w2[i] = v[i] * s[i] + w[i] * c[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v2[2 * i] = v[2 * i] * c[i] - v[2 * i + 1] * s[i];
+        v2[2 * i + 1] = v[2 * i] * s[i] + v[2 * i + 1] * c[i];
+        w2[2 * i] = w[2 * i] * c[4 + i] - w[2 * i + 1] * s[4 + i];
+        w2[2 * i + 1] = w[2 * i] * s[4 + i] + w[2 * i + 1] * c[4 + i];
+      }
+    }
+    put<F32>(y, to + d0, n0, v2);
+    put<F32>(y, to + d1, n1, w2);
+  }
+}
+
+int launch_rotary(RotaryArgs a, hipStream_t stream) {
+  const lowm_rotary_args& u = a.u;
+  const int pairs = u.R / 2, heads = u.Hq + u.Hk;
+  a.pair_groups = (pairs + 7) / 8;
+  a.groups = a.pair_groups + ((a.copy_q || a.copy_k)
+                                  ? (u.first + 7) / 8 + (u.D - u.first - u.R + 7) / 8
+                                  : 0);
+  // As many threads to a token's heads as fill the GPU with 8 wavefronts to a CU.
+  const int64_t per = (int64_t)u.T * a.groups;
+  const int64_t lanes = (256 * 8 * kWave + per - 1) / per;
+  a.head_lanes = (int)(lanes < heads ? lanes : heads);
+  const bool f32 = u.type == LOWM_F32, half = !(u.flags & LOWM_ROTARY_INTERLEAVED);
+  const void* fn = f32 ? (half ? (const void*)&rotary_kernel<true, true>
+                               : (const void*)&rotary_kernel<true, false>)
+                       : (half ? (const void*)&rotary_kernel<false, true>
+                               : (const void*)&rotary_kernel<false, false>);
+  const int64_t threads = (int64_t)a.groups * a.head_lanes, most = kMaxThreads / threads;
+  void* args[] = {&a};
+  int rc = LOWM_OK;
+  for (int64_t t = 0; t < u.T && rc == LOWM_OK; t += most) {
+    a.first_token = t;
+    a.tokens = u.T - t < most ? u.T - t : most;
+    rc = launched(hipLaunchKernel(fn, dim3((unsigned)((a.tokens * threads + 255) / 256)),
+                                  dim3(256), args, 0, stream));
+  }
+  return rc;
+}
+
+int rotary(const lowm_rotary_args* u, hipStream_t stream) {
+  if (!u || u->T < 0 || u->Hq < 1 || u->D < 1 || u->R < 2 || u->R % 2 || u->first < 0 ||
+      u->first > u->D - u->R || (u->k && u->Hk < 1))
+    return LOWM_ERR_INVALID_ARG;
+  if (u->type != LOWM_BF16 && u->type != LOWM_F32) return LOWM_ERR_INVALID_ARG;
+  if (u->positions_bytes != 8 && u->positions_bytes != 4) return LOWM_ERR_INVALID_ARG;
+  if (u->flags & ~(LOWM_ROTARY_INTERLEAVED | LOWM_ROTARY_INVERSE)) return LOWM_ERR_INVALID_ARG;
+  if (u->D > LOWM_ROTARY_MAX_D || u->Hq > LOWM_CACHE_MAX_HEADS || u->Hk > LOWM_CACHE_MAX_HEADS)
+    return LOWM_ERR_UNSUPPORTED;
+  if (u->T == 0) return LOWM_OK;
+  if (!u->q || !u->q_out || !u->positions || !u->freqs || (u->k && !u->k_out))
+    return LOWM_ERR_INVALID_ARG;
+  lowm_rotary_args v = *u;
+  if (!v.k) {
+    v.Hk = 0;
+    v.k_out = nullptr;
+    v.k_row = v.k_head = v.k_out_row = v.k_out_head = 0;
+  }
+  const int b = type_bytes(v.type);
+  if (!aligned_to(v.q, b) || !aligned_to(v.k, b) || !aligned_to(v.q_out, b) ||
+      !aligned_to(v.k_out, b) || !aligned_to(v.positions, v.positions_bytes) ||
+      !aligned_to(v.freqs, 8))
+    return LOWM_ERR_UNSUPPORTED;
+  if (!heads_apart(v.T, v.Hq, v.D, v.q_row, v.q_head) ||
+      !heads_apart(v.T, v.Hq, v.D, v.q_out_row, v.q_out_head) ||
+      (v.k && (!heads_apart(v.T, v.Hk, v.D, v.k_row, v.k_head) ||
+               !heads_apart(v.T, v.Hk, v.D, v.k_out_row, v.k_out_head))))
+    return LOWM_ERR_INVALID_ARG;
+  const bool q_in = v.q == v.q_out && v.q_row == v.q_out_row && v.q_head == v.q_out_head;
+  const bool k_in = v.k && v.k == v.k_out && v.k_row == v.k_out_row && v.k_head == v.k_out_head;
+  const Heads q{v.q, v.T, v.Hq, v.D, v.q_row, v.q_head, b},
+      qo{v.q_out, v.T, v.Hq, v.D, v.q_out_row, v.q_out_head, b},
+      k{v.k, v.T, v.Hk, v.D, v.k_row, v.k_head, b},
+      ko{v.k_out, v.T, v.Hk, v.D, v.k_out_row, v.k_out_head, b};
+  const Span pos = span_of(v.positions, 1, v.T, v.T, v.positions_bytes),
+             fr = span_of(v.freqs, 1, v.R / 2, v.R / 2, 8);
+  if ((!q_in && meet(qo, q)) || (!k_in && meet(ko, k)) || meet(qo, k) || meet(ko, q) ||
+      meet(qo, ko) || meet(qo, pos) || meet(qo, fr) || meet(ko, pos) || meet(ko, fr))
+    return LOWM_ERR_INVALID_ARG;
+  RotaryArgs a{};
+  a.u = v;
+  a.copy_q = !q_in;
+  a.copy_k = v.k && !k_in;
+  return launch_rotary(a, stream);
+}
+
+}  // namespace
+}  // namespace lowm
+
+extern "C" int lowm_rotary(const lowm_rotary_args* args, void* stream) {
+  return lowm::rotary(args, static_cast<hipStream_t>(stream));
+}
