@@ -14,9 +14,8 @@
  * allocates nothing and keeps no state between calls; a call validates its
  * arguments on the host before any HIP call, enqueues its kernels on `stream` and
  * returns.  Every struct is read during the call only.  All calls can be captured
- * into a HIP graph: lengths, tables and positions are read on the device.  The
- * workspaces here need no clearing, hold nothing between calls, and serve one call
- * at a time.
+ * into a HIP graph: lengths, tables and positions are read on the device.  A
+ * workspace serves one call at a time.
  *
  * The cache.  A page holds LOWM_PAGE = 64 tokens of every head of one layer, keys
  * and values apart, a byte an element, with one fp32 scale for each page and head:
@@ -183,7 +182,12 @@ int lowm_cache_read(const lowm_cache_read_args* args, void* stream);
  * Sums and softmax statistics are fp32.  The matrix products take fp16: a row of
  * q scaled by a power of two, the bytes as they are (both exact but for elements
  * below 2^-29 of their row's largest), and e^(x - max), rounded to 11 bits.
- * The same inputs give the same bits.  lens are read on the device.
+ * The same inputs give the same bits.
+ *
+ * The workspace (lowm_cache_attention_workspace_bytes, 256-byte aligned) is zeroed once
+ * before its first use; every call that completes leaves what must be zero so, for any
+ * sizes.  The rest is not zero after a call: a workspace serves this operator alone
+ * until it is zeroed again.
  */
 typedef struct lowm_cache_attention_args {
     lowm_kv_cache cache;
@@ -245,7 +249,7 @@ typedef struct lowm_fork_pages_args {
     int32_t R, W, reserve;
 } lowm_fork_pages_args;
 
-/* Bytes of workspace of this call and the next.  Host-only. */
+/* Bytes of workspace of this call and the next; it needs no clearing.  Host-only. */
 size_t lowm_pages_workspace_bytes(int R, int W, int P);
 
 /* Errors: NULL operand, a size < 1, reserve < 0, overlap: LOWM_ERR_INVALID_ARG; R

@@ -179,10 +179,10 @@ def cache_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, *,
 
 def make_cache_attention_workspace(T: int, q_heads: int, heads: int, head_dim: int,
                                    device="cuda") -> Optional[torch.Tensor]:
-    """A workspace of cache_attention for T rows (None for sizes it rejects); it serves any
-    sizes that need no more bytes, one call at a time, and needs no clearing."""
+    """A zeroed workspace of cache_attention for T rows (None for sizes it rejects); it serves
+    any sizes that need no more bytes, one call at a time, but no other operator."""
     n = _library().lib.lowm_cache_attention_workspace_bytes(T, q_heads, heads, head_dim)
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
 
 def cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor, *,

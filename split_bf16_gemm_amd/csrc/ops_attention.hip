@@ -3,8 +3,7 @@
 //
 //   x_t = scale q . k_t ;  out = sum_t e^(x_t - lse) v_t ;  lse = log sum_t e^x_t
 //
-// One pass over the pages with a running maximum and sum (attend_kernel), and the
-// joining of sequences that several workgroups shared (join_kernel).  Bound by HBM
+// One pass over the pages with a running maximum and sum, in one launch.  Bound by HBM
 // for few rows: a byte of the cache is read once for up to 32 rows of a key head.
 //
 // Layout.  Up to 16 RT rows of one key head (a token's query heads that share it,
@@ -27,8 +26,17 @@
 //
 // Work.  The pages of all sequences, heads and tiles are one list that is cut into
 // equal runs, one to a workgroup, whatever the lengths are; they are read on the
-// device.  A workgroup has at most two tiles that others share, its first and its
-// last, and leaves their unfinished sums in two places of its own in the workspace.
+// device.  A tile counts as kTileCost pages more than it has, so that many short
+// sequences are spread like one long one.  A run has at most two tiles that others
+// share, its first and its last, and leaves its sums of them in two places of its own
+// in the workspace; the last of a tile's runs to arrive at its counter joins them, in the
+// order of the pages, so that the bits do not depend on who that is.
+//
+// The exchange.  Sums go to the workspace with device-scope stores, which pass the
+// XCDs' own caches; a workgroup waits until its stores are acknowledged there and then
+// adds to the counter, and who finds the others' additions reads with device-scope
+// loads.  No cache is written back or invalidated, and nobody waits for another
+// workgroup.  Counters are zero between calls: who joins clears them.
 #include "ops_cache.cuh"
 
 namespace lowm {
@@ -42,7 +50,10 @@ constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kGroupsLog = 9;                // workgroups: two to a CU
 constexpr int kGroups = 1 << kGroupsLog;
-constexpr float kLift = 14.f;                // log2 of what e^(x - max) is scaled by
+constexpr int kJoin = 32;                    // places joined at once
+constexpr int kTileCost = 8;                 // what a tile costs beside its pages, in pages
+constexpr float kLift = 7.f;                 // log2 of what weights are scaled by, and how
+constexpr float kSlack = 8.f;                // far the largest may pass its reference
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct AttendArgs {
@@ -51,6 +62,7 @@ struct AttendArgs {
   const uint16_t* q;
   uint16_t* out;
   float* lse;
+  int* counts;       // [2][2 kGroups]: arrivals in a group of places, and of groups
   float* sums;       // [2 kGroups][rows of a tile][D]
   float* stats;      // [2 kGroups][rows of a tile][2]: maximum, sum
   int64_t q_row, q_head;
@@ -58,7 +70,8 @@ struct AttendArgs {
   float scale;               // times log2 e
 };
 
-// A sequence's share of the list: its tiles' pages, tile after tile.
+// A sequence's share of the list: its tiles, each kTileCost units that stand for no page,
+// then its pages.
 struct Share {
   Rows rows;
   int tiles;          // of a key head
@@ -73,7 +86,7 @@ struct Share {
     first = a.window > 0 && from > 0 ? (int)(from / LOWM_PAGE) : 0;
     pages = (tokens + LOWM_PAGE - 1) / LOWM_PAGE - first;
     if (pages < 0) pages = 0;
-    units = (int64_t)a.cache.H * tiles * pages;
+    units = (int64_t)a.cache.H * tiles * (pages + kTileCost);
   }
 };
 
@@ -137,11 +150,9 @@ struct List {
   }
 };
 
-// Where workgroup w's unfinished sums of a tile are: of the tile that its run begins
-// with, or of the one that it ends with.
-__device__ __forceinline__ int place_of(int64_t w, bool begins) {
-  return 2 * (int)w + (begins ? 0 : 1);
-}
+// Where the unfinished sums of a tile that run w has a part of are: of the one tile that
+// an earlier run began, or of the one that this run begins and a later one ends.
+__device__ __forceinline__ int place_of(int64_t w, bool begun) { return 2 * (int)w + !begun; }
 
 __device__ __forceinline__ float bits_float(uint32_t b) { return __builtin_bit_cast(float, b); }
 __device__ __forceinline__ uint32_t float_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
@@ -197,13 +208,109 @@ __device__ __forceinline__ f16x8 widen(uint32_t a, uint32_t b) {
 __device__ __forceinline__ f32x4 product(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
+// Device-scope accesses, eight bytes at a time.
+__device__ __forceinline__ void put2(float* p, float a, float b) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)float_bits(b) << 32 | float_bits(a),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+struct Two {
+  float a, b;
+};
+__device__ __forceinline__ Two get2(const float* p) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+  return {bits_float((uint32_t)v), bits_float((uint32_t)(v >> 32))};
+}
+
+// One more arrival at a counter, after all stores of the workgroup; whether it was the
+// last of n, which clears the counter.  Every thread gets the answer.
+__device__ __forceinline__ bool arrive(int* count, int n, int* lds) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int before =
+        __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (before == n - 1)
+      __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *lds = before == n - 1;
+  }
+  __syncthreads();
+  const bool last = *lds != 0;
+  __syncthreads();
+  return last;
+}
+
+// Where a tile's rows go.
+struct TileRows {
+  int row0, last_row, head, first;   // first row of the tile, last of the sequence's
+  __device__ __forceinline__ int64_t at(const AttendArgs& a, int r) const {
+    const int j = (row0 + r) / a.G;
+    return (int64_t)(first + j) * a.Hq + head * a.G + (row0 + r - j * a.G);
+  }
+};
+__device__ __forceinline__ void finish(const AttendArgs& a, const TileRows& rows, int r, int d,
+                                       float most, float sum, const f32x4& y) {
+  const int64_t row = rows.at(a, r);
+  const float k = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<ops_u32x2*>(a.out + row * a.cache.D + d) =
+      ops_u32x2{pack_bf16(y[0] * k, y[1] * k), pack_bf16(y[2] * k, y[3] * k)};
+  if (a.lse && d == 0) a.lse[row] = (most + __builtin_amdgcn_logf(sum) - kLift) * kLn2;
+}
+
+// m places' sums joined: place i is of run w + i * step, of the tile that it begins
+// (w + i * step == w0) or of the one it continues.  To the rows, or to place 0.
+__device__ void join(const AttendArgs& a, const TileRows& rows, int64_t w0, int64_t w, int step,
+                     int m, bool last, float* lds) {
+  const int n = rows.last_row - rows.row0 + 1 < a.rows ? rows.last_row - rows.row0 + 1 : a.rows;
+  const int D = a.cache.D;
+  float *most = lds, *sum = lds + kJoin * a.rows;
+  auto at = [&](int i, int r) {
+    const int64_t run = w + (int64_t)i * step;
+    return (int64_t)place_of(run, run > w0) * a.rows + r;
+  };
+  for (int i = threadIdx.x; i < m * n; i += kThreads) {
+    const Two v = get2(a.stats + 2 * at(i / n, i % n));
+    most[i] = v.a;
+    sum[i] = v.b;
+  }
+  __syncthreads();
+  for (int item = threadIdx.x; item < n * (D / 4); item += kThreads) {
+    const int r = item / (D / 4), d = item % (D / 4) * 4;
+    float top = -__builtin_inff();
+    for (int i = 0; i < m; ++i) top = fmaxf(top, most[i * n + r]);
+    const float base = top == -__builtin_inff() ? 0.f : top;
+    float all = 0.f;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int i = 0; i < m; ++i) {
+      const float* p = a.sums + at(i, r) * D + d;
+      const Two lo = get2(p), hi = get2(p + 2);
+      const float f = __builtin_amdgcn_exp2f(most[i * n + r] - base);
+      all += f * sum[i * n + r];
+      y[0] += f * lo.a;
+      y[1] += f * lo.b;
+      y[2] += f * hi.a;
+      y[3] += f * hi.b;
+    }
+    if (last) {
+      finish(a, rows, r, d, top, all, y);
+    } else {
+      float* p = a.sums + at(0, r) * D + d;
+      put2(p, y[0], y[1]);
+      put2(p + 2, y[2], y[3]);
+      if (d == 0) put2(a.stats + 2 * at(0, r), top, all);
+    }
+  }
+  __syncthreads();
+}
+
 // Keeps the loads above it above what follows.
 __device__ __forceinline__ void pin_loads() { asm volatile("" ::: "memory"); }
 
 // DP blocks of 64 elements of a head, all of them there (FULL) or not, RT blocks of 16
 // rows to a tile.
 template <int DP, bool FULL, int RT, bool E4M3>
-__global__ __launch_bounds__(kThreads, DP * RT <= 2 ? 2 : 1) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, DP * RT <= 4 ? 2 : 1) void attend_kernel(AttendArgs a) {
   constexpr int NT = 4 * DP;                // blocks of 16 elements
   constexpr int kRows = 16 * RT;
   constexpr int kPart = DP == 1 ? 4 : DP == 3 ? 6 : 8;   // joined through LDS at a time
@@ -211,6 +318,8 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 2 ? 2 : 1) void attend_kernel(
   constexpr int kPitch = 16 * kPart + 4;    // lanes' rows in distinct banks
   __shared__ __align__(16) float joint[kWaves][kRows][kPitch];
   __shared__ float joint_max[kWaves][kRows], joint_sum[kWaves][kRows];
+  __shared__ int arrived;
+  static_assert(sizeof(joint) >= 2 * kJoin * kRows * sizeof(float), "room to join");
 
   const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
@@ -219,9 +328,13 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 2 ? 2 : 1) void attend_kernel(
 
   const List list(a);
   const int64_t run = list.run();
-  int64_t u = (int64_t)blockIdx.x * run;
-  const int64_t begin = u, end = u + run < list.total ? u + run : list.total;
-  if (u >= end) return;
+  // runs that have units, an eighth of them to each XCD: neighbours, which may share a
+  // head's pages, share an L2
+  const int64_t runs = (list.total + run - 1) / (run > 0 ? run : 1);
+  const int64_t w = (blockIdx.x % 8) * ((runs + 7) / 8) + blockIdx.x / 8;
+  if ((int64_t)blockIdx.x / 8 >= (runs + 7) / 8 || w >= runs) return;
+  int64_t u = w * run;
+  const int64_t end = u + run < list.total ? u + run : list.total;
   int64_t start;
   int b = list.find(a, u, &start);
 
@@ -232,12 +345,74 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 2 ? 2 : 1) void attend_kernel(
       ++b;
       continue;
     }
-    const int64_t tile_at = (u - start) / s.pages;
-    const int page_at = (int)(u - start - tile_at * s.pages);
+    // a tile's units: kTileCost that stand for no page, then its pages
+    const int64_t tile_at = (u - start) / (s.pages + kTileCost);
+    const int from = (int)(u - start - tile_at * (s.pages + kTileCost));
     const int64_t room = end - u;
-    const int pages = s.pages - page_at < room ? s.pages - page_at : (int)room;
+    const int units = s.pages + kTileCost - from < room ? s.pages + kTileCost - from : (int)room;
+    u += units;
+    const int page_at = from > kTileCost ? from - kTileCost : 0,
+              pages = from + units - kTileCost - page_at;
     const int head = (int)(tile_at / s.tiles), tile = (int)(tile_at - (int64_t)head * s.tiles);
     const int row0 = tile * kRows, last_row = s.rows.n * a.G - 1;
+    const TileRows rows{row0, last_row, head, s.rows.first};
+    if (pages <= 0) {
+      // whoever has the first unit of a tile without pages writes its rows
+      if (s.pages == 0 && from == 0)
+        for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads)
+          if (row0 + i / (D / 4) <= last_row)
+            finish(a, rows, i / (D / 4), i % (D / 4) * 4, -__builtin_inff(), 0.f,
+                   f32x4{0.f, 0.f, 0.f, 0.f});
+      continue;
+    }
+    // positions of the tile's first and last row: pages past the last are not seen
+    const int low = s.rows.position(row0 / a.G);
+    const int high = s.rows.position((row0 + kRows - 1 < last_row ? row0 + kRows - 1 : last_row) / a.G);
+    const int high_lo = a.window > 0 && high >= a.window ? high - a.window + 1 : 0;
+    const int seen = high < 0 ? 0 : high / LOWM_PAGE + 1 - s.first;
+    const int stop = page_at + pages < seen ? page_at + pages : seen;
+    const int* table = a.seq.table + b * a.seq.table_ld + s.first;
+
+    ops_u32x4 keys[4][DP], vals[NT];
+    float k_scale = 0.f, v_scale = 0.f;
+    int page = -1, next_page = -1;
+    // The token of row r of score block i is 16 (r / 4) + 4 i + r % 4: then lane group
+    // g has tokens 16 g .. 16 g + 15, in the order of the values' bytes.
+    auto load_keys = [&]() {
+      page = next_page >= 0 && next_page < c.P ? next_page : -1;
+      const int64_t at = (int64_t)(page < 0 ? 0 : page) * c.H + head;
+      const uint8_t* p = static_cast<const uint8_t*>(c.k) + at * (LOWM_PAGE * D);
+      k_scale = c.k_scale[at];
+      v_scale = c.v_scale[at];
+#pragma unroll
+      for (int m = 0; m < DP; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int piece = 4 * m + g;
+          const uint8_t* x = p + (piece * LOWM_PAGE + 16 * (col >> 2) + 4 * i + (col & 3)) * 16;
+          keys[i][m] = ops_u32x4{0u, 0u, 0u, 0u};
+          if (FULL || m < DP - 1 || piece * 16 < D)
+            keys[i][m] = *reinterpret_cast<const ops_u32x4*>(x);
+        }
+      pin_loads();
+    };
+    auto load_vals = [&]() {
+      const uint8_t* p = static_cast<const uint8_t*>(c.v) +
+                         ((int64_t)(page < 0 ? 0 : page) * c.H + head) * (LOWM_PAGE * D);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (FULL || n < NT - 4 || n < nt)
+          vals[n] = __builtin_nontemporal_load(
+              reinterpret_cast<const ops_u32x4*>(p + (g * D + 16 * n + col) * 16));
+      pin_loads();
+    };
+    // the number of a page is read a turn before its keys
+    int at = page_at + wave;
+    if (at < stop) {
+      next_page = table[at];
+      load_keys();
+      next_page = table[at + kWaves < stop ? at + kWaves : at];
+    }
 
     // rows: what they see, and their queries as the matrix operand
     int see_lo[RT], see_hi[RT];
@@ -267,79 +442,42 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 2 ? 2 : 1) void attend_kernel(
           top = top > hi ? top : hi;
         }
       top = row_umax(top);
-      // 2^(14 - exponent of the largest), within what fp32 has
+      // 2^(14 - exponent of the largest), within what fp32 has; with the sign of the
+      // scale, so that larger products are larger scores
       const int e = (int)(top >> 23), up = 127 + 14 - (e - 127);
       const float lift = bits_float((uint32_t)(up < 1 ? 1 : up > 254 ? 254 : up) << 23);
-      unit[t] = top < 0x7f800000u ? a.scale / lift : __builtin_nanf("");
+      const float signed_lift = a.scale < 0.f ? -lift : lift;
+      unit[t] = top < 0x7f800000u ? a.scale / signed_lift : __builtin_nanf("");
 #pragma unroll
       for (int m = 0; m < 2 * DP; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t w = raw[m][i];
-          q[t][m][2 * i] = (_Float16)(bf16_lo(w) * lift);
-          q[t][m][2 * i + 1] = (_Float16)(bf16_hi(w) * lift);
+          q[t][m][2 * i] = (_Float16)(bf16_lo(w) * signed_lift);
+          q[t][m][2 * i + 1] = (_Float16)(bf16_hi(w) * signed_lift);
         }
     }
-    // positions of the tile's first and last row: pages past the last are not seen
-    const int low = s.rows.position(row0 / a.G);
-    const int high = s.rows.position((row0 + kRows - 1 < last_row ? row0 + kRows - 1 : last_row) / a.G);
-    const int high_lo = a.window > 0 && high >= a.window ? high - a.window + 1 : 0;
-    const int seen = high < 0 ? 0 : high / LOWM_PAGE + 1 - s.first;
-    const int stop = page_at + pages < seen ? page_at + pages : seen;
-    const int* table = a.seq.table + b * a.seq.table_ld + s.first;
 
-    float most[RT], sum[RT];
+    // Weights are e^(x + log vs - ref) 2^kLift with vs the page's scale of the values in
+    // units of the first page's, v0: they multiply the bytes as they are, and go into the
+    // sums o without another factor.  ref is the largest x + log vs so far, or up to
+    // kSlack less: the sums are scaled anew only when a page passes that.
+    float ref[RT], sum[RT], v0 = 0.f;
     f32x4 o[RT][NT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      most[t] = -__builtin_inff();
+      ref[t] = -__builtin_inff();
       sum[t] = 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    ops_u32x4 keys[4][DP], vals[NT];
-    float k_scale = 0.f, v_scale = 0.f;
-    int page = -1;
-    // The token of row r of score block i is 16 (r / 4) + 4 i + r % 4: then lane group
-    // g has tokens 16 g .. 16 g + 15, in the order of the values' bytes.
-    auto load_keys = [&](int at) {
-      page = table[at];
-      const bool some = page >= 0 && page < c.P;
-      const int64_t from = (int64_t)(some ? page : 0) * c.H + head;
-      const uint8_t* p = static_cast<const uint8_t*>(c.k) + from * (LOWM_PAGE * D);
-      k_scale = some ? c.k_scale[from] : 0.f;
-      v_scale = some ? c.v_scale[from] : 0.f;
-      if (!some) page = -1;
-#pragma unroll
-      for (int m = 0; m < DP; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int piece = 4 * m + g;
-          const uint8_t* x = p + (piece * LOWM_PAGE + 16 * (col >> 2) + 4 * i + (col & 3)) * 16;
-          keys[i][m] = ops_u32x4{0u, 0u, 0u, 0u};
-          if (FULL || m < DP - 1 || piece * 16 < D) keys[i][m] = *reinterpret_cast<const ops_u32x4*>(x);
-        }
-      pin_loads();
-    };
-    auto load_vals = [&]() {
-      const uint8_t* p = static_cast<const uint8_t*>(c.v) +
-                         ((int64_t)(page < 0 ? 0 : page) * c.H + head) * (LOWM_PAGE * D);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (FULL || n < NT - 4 || n < nt)
-          vals[n] = *reinterpret_cast<const ops_u32x4*>(p + (g * D + 16 * n + col) * 16);
-      pin_loads();
-    };
-
-    int at = page_at + wave;
-    if (at < stop) load_keys(at);
     for (; at < stop; at += kWaves) {
       const int token0 = (s.first + at) * LOWM_PAGE;
       // tokens of the page that are there at all
       int live = s.rows.len - token0;
       live = page < 0 ? 0 : live < LOWM_PAGE ? live : LOWM_PAGE;
-      const float ks = k_scale, vs = v_scale;
+      const float ks = live > 0 ? k_scale : 0.f, vs = live > 0 ? v_scale : 0.f;
       load_vals();
 
       f32x4 x[RT][4];
@@ -359,11 +497,16 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 2 ? 2 : 1) void attend_kernel(
             x[t][i] = product(k1, q[t][2 * m + 1], x[t][i]);
           }
         }
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[t][i] *= unit[t] * ks;
-      if (at + kWaves < stop) load_keys(at + kWaves);
+      if (at + kWaves < stop) {
+        load_keys();
+        next_page = table[at + 2 * kWaves < stop ? at + 2 * kWaves : at];
+      }
+
+      // a scale of 0 (or one too small to be a number with a logarithm) leaves no value
+      const bool some = !(fabsf(vs) < 1.17549435e-38f);
+      if (v0 == 0.f && some && vs > 0.f && vs < __builtin_inff()) v0 = vs;
+      const float vs_here = some ? vs / (v0 == 0.f ? 1.f : v0) : 1.f,
+                  log_vs = __builtin_amdgcn_logf(vs_here), per_vs = 1.f / vs_here;
 
       if (live < LOWM_PAGE || token0 + LOWM_PAGE - 1 > low || token0 < high_lo) {
 #pragma unroll
@@ -379,32 +522,45 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 2 ? 2 : 1) void attend_kernel(
       }
 
       f16x8 p[RT][2];
-      float keep[RT], take[RT];
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
+        // never 0, which would make NaN of the masked ones
+        float per = unit[t] * ks;
+        per = per == 0.f ? 1e-38f : per;
         float here = x[t][0][0];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) here = fmaxf(here, x[t][i][e]);
         here = row_max(here);
+        // a row that sees none of the page is not touched by its scales
         const bool none = here == -__builtin_inff();
-        const float from = none ? 0.f : here - kLift;
-        const float now = fmaxf(most[t], here), base = now == -__builtin_inff() ? 0.f : now;
-        const float rise = __builtin_amdgcn_exp2f(here - base);
-        keep[t] = __builtin_amdgcn_exp2f(most[t] - base);
-        take[t] = none ? 0.f : rise * vs;
-        most[t] = now;
+        here = here * per + log_vs;
+        per = none ? 1.f : per;
+        if (__any(here > ref[t] + kSlack)) {
+          const float now = here > ref[t] + kSlack ? here : ref[t];
+          const float keep = now == ref[t] ? 1.f : __builtin_amdgcn_exp2f(ref[t] - now);
+          ref[t] = now;
+          sum[t] *= keep;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) o[t][n] *= keep;
+        }
+        const float lift =
+            none ? 0.f : log_vs + kLift - (ref[t] == -__builtin_inff() ? 0.f : ref[t]);
         float add = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float w = __builtin_amdgcn_exp2f(x[t][i][e] - from);
+            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][i][e], per, lift));
             add += w;
             p[t][i / 2][4 * (i % 2) + e] = (_Float16)w;
           }
-        sum[t] = sum[t] * keep[t] + add * rise;
+        sum[t] += add * (none ? 1.f : per_vs);
+      }
+      if (!some) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) p[t][0] = p[t][1] = f16x8{};
       }
       if (E4M3 && live < LOWM_PAGE) {
         // what lies behind the sequence may be any byte, a NaN among them
@@ -420,15 +576,12 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 2 ? 2 : 1) void attend_kernel(
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         if (!FULL && n >= NT - 4 && n >= nt) continue;
-        const f16x8 v0 = widen<E4M3>(vals[n][0], vals[n][1]),
-                    v1 = widen<E4M3>(vals[n][2], vals[n][3]);
+        const f16x8 y0 = widen<E4M3>(vals[n][0], vals[n][1]),
+                    y1 = widen<E4M3>(vals[n][2], vals[n][3]);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          f32x4 y = {0.f, 0.f, 0.f, 0.f};
-          y = product(v0, p[t][0], y);
-          y = product(v1, p[t][1], y);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[t][n][e] = o[t][n][e] * keep[t] + y[e] * take[t];
+          o[t][n] = product(y0, p[t][0], o[t][n]);
+          o[t][n] = product(y1, p[t][1], o[t][n]);
         }
       }
     }
@@ -438,19 +591,20 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 2 ? 2 : 1) void attend_kernel(
     for (int t = 0; t < RT; ++t) {
       const float all = row_sum(sum[t]);
       if (g == 0) {
-        joint_max[wave][16 * t + col] = most[t];
+        joint_max[wave][16 * t + col] = ref[t];
         joint_sum[wave][16 * t + col] = all;
       }
     }
     const bool whole = page_at == 0 && pages == s.pages;
-    const int place = place_of(blockIdx.x, u == begin);
+    const int place = place_of(w, page_at > 0);
 #pragma unroll
     for (int n0 = 0; n0 < NT; n0 += kPart) {
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int n = 0; n < kPart; ++n)
-          *reinterpret_cast<f32x4*>(&joint[wave][16 * t + col][16 * n + 4 * g]) = o[t][n0 + n];
+          *reinterpret_cast<f32x4*>(&joint[wave][16 * t + col][16 * n + 4 * g]) =
+              o[t][n0 + n] * v0;
       __syncthreads();
       for (int i = threadIdx.x; i < kRows * 4 * kPart; i += kThreads) {
         const int r = i / (4 * kPart), d4 = i % (4 * kPart), d = 16 * n0 + 4 * d4;
@@ -470,141 +624,32 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 2 ? 2 : 1) void attend_kernel(
           for (int e = 0; e < 4; ++e) y[e] += f * z[e];
         }
         if (whole) {
-          const int j = (row0 + r) / a.G, h = head * a.G + (row0 + r - j * a.G);
-          const int64_t row = (int64_t)(s.rows.first + j) * a.Hq + h;
-          const float k = all == 0.f ? 0.f : 1.f / all;
-          *reinterpret_cast<ops_u32x2*>(a.out + row * D + d) =
-              ops_u32x2{pack_bf16(y[0] * k, y[1] * k), pack_bf16(y[2] * k, y[3] * k)};
-          if (a.lse && d == 0)
-            a.lse[row] = (top + __builtin_amdgcn_logf(all) - kLift) * kLn2;
+          finish(a, rows, r, d, top, all, y);
         } else {
           const int64_t row = (int64_t)place * kRows + r;
-          *reinterpret_cast<f32x4*>(a.sums + row * D + d) = y;
-          if (d == 0) {
-            a.stats[2 * row] = top;
-            a.stats[2 * row + 1] = all;
-          }
+          put2(a.sums + row * D + d, y[0], y[1]);
+          put2(a.sums + row * D + d + 2, y[2], y[3]);
+          if (d == 0) put2(a.stats + 2 * row, top, all);
         }
       }
       __syncthreads();
     }
-    u += pages;
-  }
-}
+    if (whole) continue;
 
-// A workgroup to a row: nothing to do for tiles that one workgroup had whole; zeros
-// for rows of sequences without pages; the sums of the others joined in the order of
-// their pages, 64 at a time.
-__global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
-  constexpr int kStep = 64;
-  __shared__ float factor[kStep];
-  __shared__ float total[2];
-  __shared__ __align__(16) f32x4 part[kThreads];
-  const int lane = threadIdx.x & (kWave - 1);
-  const int D = a.cache.D;
-  const int64_t row = blockIdx.x;
-  const int token = (int)(row / a.Hq), h = (int)(row % a.Hq), head = h / a.G;
-
-  // the sequence that the row belongs to, and the units before its own
-  int b = -1;
-  int64_t start = 0;
-  const List list(a);
-  if (!a.seq.row_starts) {
-    b = token / (a.seq.T / a.seq.B);
-  } else {
-    for (int at = 0; at < a.seq.B && b < 0; at += kWave) {
-      bool mine = false;
-      if (at + lane < a.seq.B) {
-        const Rows r = rows_of(a.seq, at + lane);
-        mine = token >= r.first && token < r.first + r.n;
-      }
-      const uint64_t who = __ballot(mine);
-      if (who) b = at + __builtin_ctzll(who);
-    }
-    if (b < 0) return;
+    // the runs that share the tile, in groups of kJoin, and then the groups
+    const int64_t first_page = start + tile_at * (s.pages + kTileCost) + kTileCost;
+    const int64_t w0 = first_page / run;
+    const int n = (int)((first_page + s.pages - 1) / run - w0) + 1;
+    const int group = (int)(w - w0) / kJoin, groups = (n + kJoin - 1) / kJoin;
+    const int64_t leader = w0 + group * kJoin;
+    const int members = n - group * kJoin < kJoin ? n - group * kJoin : kJoin;
+    if (!arrive(a.counts + place_of(leader, group > 0), members, &arrived)) continue;
+    float* lds = &joint[0][0][0];
+    join(a, rows, w0, leader, 1, members, groups == 1, lds);
+    if (groups == 1) continue;
+    if (arrive(a.counts + 2 * kGroups + place_of(w0, false), groups, &arrived))
+      join(a, rows, w0, w0, kJoin, groups, true, lds);
   }
-  if (a.seq.B <= kWave) {
-    start = lane_value(list.upto - list.own, b);
-  } else {
-    for (int at = 0; at <= b; at += kWave) {
-      const int64_t own = at + lane < b ? Share(a, at + lane).units : 0;
-      start += lane_value(wave_scan64(own), kWave - 1);
-    }
-  }
-  const Share s(a, b);
-  if (s.pages == 0) {
-    for (int d = threadIdx.x; d < D; d += kThreads) a.out[row * D + d] = 0;
-    if (a.lse && threadIdx.x == 0) a.lse[row] = -__builtin_inff();
-    return;
-  }
-  const int r = (token - s.rows.first) * a.G + (h - head * a.G), tile = r / a.rows,
-            in = r - tile * a.rows;
-  const int64_t run = list.run();
-  const int64_t first = start + ((int64_t)head * s.tiles + tile) * s.pages,
-                last = first + s.pages - 1;
-  const int64_t w0 = first / run, w1 = last / run;
-  if (w0 == w1) return;
-  const int n = (int)(w1 - w0) + 1;
-  const bool begins = first == w0 * run;
-  auto at = [&](int i) {
-    return (int64_t)place_of(w0 + i, i > 0 || begins) * a.rows + in;
-  };
-
-  // 16, 32 or 64 lanes to a place's row, four elements to a lane
-  const int lanes = D <= 64 ? 16 : D <= 128 ? 32 : 64;
-  const int sets = kThreads / lanes, set = threadIdx.x / lanes, d = (int)threadIdx.x % lanes * 4;
-  float most = -__builtin_inff(), sum = 0.f;
-  f32x4 y = {0.f, 0.f, 0.f, 0.f};
-  for (int i0 = 0; i0 < n; i0 += kStep) {
-    const int m = n - i0 < kStep ? n - i0 : kStep;
-    float keep = 1.f;
-    if (i0 > 0) __syncthreads();
-    if (threadIdx.x < kWave) {
-      float x = -__builtin_inff(), z = 0.f;
-      if (lane < m) {
-        const float* p = a.stats + 2 * at(i0 + lane);
-        x = p[0];
-        z = p[1];
-      }
-      float now = x;
-#pragma unroll
-      for (int k = 1; k < kWave; k *= 2) now = fmaxf(now, __shfl_xor(now, k));
-      now = fmaxf(now, most);
-      const float base = now == -__builtin_inff() ? 0.f : now;
-      const float f = __builtin_amdgcn_exp2f(x - base);
-      keep = __builtin_amdgcn_exp2f(most - base);
-      sum = sum * keep + wave_sum(lane < m ? f * z : 0.f);
-      most = now;
-      factor[lane] = f;
-      if (lane == 0) total[0] = keep;
-    }
-    __syncthreads();
-    keep = total[0];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] *= keep;
-    if (d < D) {
-#pragma unroll 8
-      for (int i = set; i < m; i += sets) {
-        const f32x4 z = *reinterpret_cast<const f32x4*>(a.sums + at(i0 + i) * D + d);
-        const float f = factor[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] += f * z[e];
-      }
-    }
-  }
-  part[threadIdx.x] = y;
-  if (threadIdx.x == 0) {
-    total[1] = sum;
-    if (a.lse) a.lse[row] = (most + __builtin_amdgcn_logf(sum) - kLift) * kLn2;
-  }
-  __syncthreads();
-  if (set > 0 || d >= D) return;
-  for (int i = 1; i < sets; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] += part[i * lanes + threadIdx.x][e];
-  const float k = total[1] == 0.f ? 0.f : 1.f / total[1];
-  *reinterpret_cast<ops_u32x2*>(a.out + row * D + d) =
-      ops_u32x2{pack_bf16(y[0] * k, y[1] * k), pack_bf16(y[2] * k, y[3] * k)};
 }
 
 template <int DP, bool FULL>
@@ -627,7 +672,7 @@ const void* kernel_for(int D, int rt, bool e4m3) {
 // Rows of a tile that a workspace has room for.
 int64_t room_rows(int T, int G) { return (int64_t)T * G <= 16 ? 16 : 32; }
 size_t workspace_bytes(int T, int G, int D) {
-  return (size_t)(2 * kGroups * room_rows(T, G) * (D + 2) * 4);
+  return (size_t)(2 * kGroups * (2 * 4 + room_rows(T, G) * (D + 2) * 4));
 }
 
 int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
@@ -669,7 +714,8 @@ int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
   a.out = static_cast<uint16_t*>(u->out);
   a.lse = u->lse;
   a.rows = 16 * rt;
-  a.stats = static_cast<float*>(u->workspace);
+  a.counts = static_cast<int*>(u->workspace);
+  a.stats = static_cast<float*>(u->workspace) + 4 * kGroups;
   a.sums = a.stats + 2 * kGroups * a.rows * 2;
   a.q_row = u->q_row;
   a.q_head = u->q_head;
@@ -678,11 +724,8 @@ int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
   a.window = u->window;
   a.scale = u->scale * kLog2e;
   void* args[] = {&a};
-  rc = launched(hipLaunchKernel(kernel_for(c.D, rt, c.type == LOWM_E4M3), dim3(kGroups),
-                                dim3(kThreads), args, 0, stream));
-  if (rc != LOWM_OK) return rc;
-  return launched(hipLaunchKernel((const void*)&join_kernel, dim3((unsigned)rows), dim3(kThreads),
-                                  args, 0, stream));
+  return launched(hipLaunchKernel(kernel_for(c.D, rt, c.type == LOWM_E4M3), dim3(kGroups),
+                                  dim3(kThreads), args, 0, stream));
 }
 
 }  // namespace

@@ -35,6 +35,7 @@ U = 2.0 ** -24
 BF16, F32, I32, F64 = torch.bfloat16, torch.float32, torch.int32, torch.float64
 FP8 = torch.float8_e4m3fn
 HALF = {BF16: 2.0 ** -8, F32: U}
+COUNTERS = 2 * 2 * 512 * 4     # bytes of cache_attention's workspace that are zero between calls
 gpu = pytest.mark.gpu
 
 
@@ -412,11 +413,12 @@ def check_attention(q, cache, table, lens, starts, *, window=0, scale=None, rs="
     scale = D ** -0.5 if scale is None else scale
     if ws is None:
         ws = sbg.make_cache_attention_workspace(T, Hq, cache.k.shape[1], D)
-        ws.fill_(0xff)     # nothing in it is read before it is written
+        ws[COUNTERS:].fill_(0xff)     # nothing there is read before it is written
     out = torch.full((T, Hq, D), 7.0, dtype=BF16, device="cuda")
     lse = torch.full((T, Hq), 7.0, device="cuda")
     sbg.cache_attention(q, cache, table, ints(lens), window=window, scale=scale, workspace=ws,
                         row_starts=None if rs is None else ints(starts), out=out, lse_out=lse)
+    assert T == 0 or not ws[:COUNTERS].any()     # left as it was found
     ref, rl, err, lerr = attention_reference(q, cache, table, lens, starts, scale, window)
     got, gl = out.double().cpu(), lse.double().cpu()
     none = torch.isnan(rl)
