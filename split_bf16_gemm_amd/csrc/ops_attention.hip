@@ -37,6 +37,8 @@
 // adds to the counter, and who finds the others' additions reads with device-scope
 // loads.  No cache is written back or invalidated, and nobody waits for another
 // workgroup.  Counters are zero between calls: who joins clears them.
+#include <type_traits>
+
 #include "ops_cache.cuh"
 
 namespace lowm {
@@ -48,9 +50,11 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
-constexpr int kGroupsLog = 9;                // workgroups: two to a CU
-constexpr int kGroups = 1 << kGroupsLog;
-constexpr int kJoin = 32;                    // places joined at once
+constexpr int kGroups = 512;                 // workgroups at most: two to a CU
+constexpr int kWideRows = 128;               // rows of a tile of attend_wide_kernel
+constexpr int kGroup = 16;                   // places joined at first
+constexpr int kJoin = kGroups / kGroup;      // and at most, groups of them
+constexpr int kJoinGroups = 1024;            // workgroups of join_kernel
 constexpr int kTileCost = 8;                 // what a tile costs beside its pages, in pages
 constexpr float kLift = 7.f;                 // log2 of what weights are scaled by, and how
 constexpr float kSlack = 8.f;                // far the largest may pass its reference
@@ -63,10 +67,13 @@ struct AttendArgs {
   uint16_t* out;
   float* lse;
   int* counts;       // [2][2 kGroups]: arrivals in a group of places, and of groups
+  int* notes;        // for join_kernel: [8] how many runs there are, [kGroups][8] a Note each
   float* sums;       // [2 kGroups][rows of a tile][D]
   float* stats;      // [2 kGroups][rows of a tile][2]: maximum, sum
   int64_t q_row, q_head;
   int Hq, G, window, rows;   // rows: of a tile
+  int groups_log;            // workgroups
+  int turn;                  // pages that a workgroup takes at a time
   float scale;               // times log2 e
 };
 
@@ -123,10 +130,10 @@ struct List {
       total += lane_value(upto, kWave - 1);
     }
   }
-  // Units of a workgroup's run: a multiple of its wavefronts.
-  __device__ __forceinline__ int64_t run() const {
-    const int64_t r = (total + kGroups - 1) >> kGroupsLog;
-    return (r + kWaves - 1) & ~(int64_t)(kWaves - 1);
+  // Units of a workgroup's run: whole turns.
+  __device__ __forceinline__ int64_t run(const AttendArgs& a) const {
+    const int64_t r = (total + (1 << a.groups_log) - 1) >> a.groups_log;
+    return (r + a.turn - 1) & ~(int64_t)(a.turn - 1);
   }
   // The sequence that unit u belongs to, and the first of its units.
   __device__ __forceinline__ int find(const AttendArgs& a, int64_t u, int64_t* start) const {
@@ -257,6 +264,25 @@ __device__ __forceinline__ void finish(const AttendArgs& a, const TileRows& rows
   if (a.lse && d == 0) a.lse[row] = (most + __builtin_amdgcn_logf(sum) - kLift) * kLn2;
 }
 
+// The sums of a tile that others have a part of, into their place: for a workgroup of
+// this launch, or for the next one.
+template <bool NOW>
+__device__ __forceinline__ void leave(const AttendArgs& a, int place, int r, int d, float most,
+                                      float sum, const f32x4& y) {
+  const int64_t row = (int64_t)place * a.rows + r;
+  if constexpr (!NOW) {
+    *reinterpret_cast<f32x4*>(a.sums + row * a.cache.D + d) = y;
+    if (d == 0) {
+      a.stats[2 * row] = most;
+      a.stats[2 * row + 1] = sum;
+    }
+    return;
+  }
+  put2(a.sums + row * a.cache.D + d, y[0], y[1]);
+  put2(a.sums + row * a.cache.D + d + 2, y[2], y[3]);
+  if (d == 0) put2(a.stats + 2 * row, most, sum);
+}
+
 // m places' sums joined: place i is of run w + i * step, of the tile that it begins
 // (w + i * step == w0) or of the one it continues.  To the rows, or to place 0.
 __device__ void join(const AttendArgs& a, const TileRows& rows, int64_t w0, int64_t w, int step,
@@ -281,16 +307,26 @@ __device__ void join(const AttendArgs& a, const TileRows& rows, int64_t w0, int6
     const float base = top == -__builtin_inff() ? 0.f : top;
     float all = 0.f;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int i = 0; i < m; ++i) {
-      const float* p = a.sums + at(i, r) * D + d;
-      const Two lo = get2(p), hi = get2(p + 2);
-      const float f = __builtin_amdgcn_exp2f(most[i * n + r] - base);
-      all += f * sum[i * n + r];
-      y[0] += f * lo.a;
-      y[1] += f * lo.b;
-      y[2] += f * hi.a;
-      y[3] += f * hi.b;
+    for (int i0 = 0; i0 < m; i0 += kGroup) {
+      Two lo[kGroup], hi[kGroup];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        const float* p = a.sums + at(i0 + i < m ? i0 + i : i0, r) * D + d;
+        lo[i] = get2(p);
+        hi[i] = get2(p + 2);
+      }
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        const int k = (i0 + i) * n + r;
+        const float f = i0 + i < m ? __builtin_amdgcn_exp2f(most[k] - base) : 0.f;
+        if (i0 + i < m) {
+          all += f * sum[k];
+          y[0] += f * lo[i].a;
+          y[1] += f * lo[i].b;
+          y[2] += f * hi[i].a;
+          y[3] += f * hi[i].b;
+        }
+      }
     }
     if (last) {
       finish(a, rows, r, d, top, all, y);
@@ -307,124 +343,139 @@ __device__ void join(const AttendArgs& a, const TileRows& rows, int64_t w0, int6
 // Keeps the loads above it above what follows.
 __device__ __forceinline__ void pin_loads() { asm volatile("" ::: "memory"); }
 
-// DP blocks of 64 elements of a head, all of them there (FULL) or not, RT blocks of 16
-// rows to a tile.
-template <int DP, bool FULL, int RT, bool E4M3>
-__global__ __launch_bounds__(kThreads, DP * RT <= 4 ? 2 : 1) void attend_kernel(AttendArgs a) {
-  constexpr int NT = 4 * DP;                // blocks of 16 elements
-  constexpr int kRows = 16 * RT;
-  constexpr int kPart = DP == 1 ? 4 : DP == 3 ? 6 : 8;   // joined through LDS at a time
-  static_assert(NT % kPart == 0, "whole parts");
-  constexpr int kPitch = 16 * kPart + 4;    // lanes' rows in distinct banks
-  __shared__ __align__(16) float joint[kWaves][kRows][kPitch];
-  __shared__ float joint_max[kWaves][kRows], joint_sum[kWaves][kRows];
-  __shared__ int arrived;
-  static_assert(sizeof(joint) >= 2 * kJoin * kRows * sizeof(float), "room to join");
+// What join_kernel needs to know of the tile that a run begins and others end.
+struct Note {
+  int parts;         // runs that have a part of it; 0: there is no such tile
+  TileRows rows;
+};
 
-  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, col = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-  const lowm_kv_cache& c = a.cache;
-  const int D = FULL ? 64 * DP : c.D, nt = FULL ? NT : D / 16;
+// A workgroup's run of the list, part of a tile after part of a tile.
+struct Walk {
+  List list;
+  int64_t run, w, u, end, start;   // its units are u .. end - 1; start: of sequence b
+  int b;
+  // the part of a tile at hand
+  Rows seq;
+  TileRows rows;
+  int first, pages_all;            // of the sequence: first page, and pages, of a tile
+  int page_at, pages;              // of those, this part's
+  int64_t first_page;              // unit of the tile's first page
+  int low, high;                   // positions of the tile's first and last row
+  bool noted;                      // whether the run's note is written, or there is no run
 
-  const List list(a);
-  const int64_t run = list.run();
-  // runs that have units, an eighth of them to each XCD: neighbours, which may share a
-  // head's pages, share an L2
-  const int64_t runs = (list.total + run - 1) / (run > 0 ? run : 1);
-  const int64_t w = (blockIdx.x % 8) * ((runs + 7) / 8) + blockIdx.x / 8;
-  if ((int64_t)blockIdx.x / 8 >= (runs + 7) / 8 || w >= runs) return;
-  int64_t u = w * run;
-  const int64_t end = u + run < list.total ? u + run : list.total;
-  int64_t start;
-  int b = list.find(a, u, &start);
-
-  while (u < end) {
-    const Share s(a, b);
-    if (u - start >= s.units) {
-      start += s.units;
-      ++b;
-      continue;
-    }
-    // a tile's units: kTileCost that stand for no page, then its pages
-    const int64_t tile_at = (u - start) / (s.pages + kTileCost);
-    const int from = (int)(u - start - tile_at * (s.pages + kTileCost));
-    const int64_t room = end - u;
-    const int units = s.pages + kTileCost - from < room ? s.pages + kTileCost - from : (int)room;
-    u += units;
-    const int page_at = from > kTileCost ? from - kTileCost : 0,
-              pages = from + units - kTileCost - page_at;
-    const int head = (int)(tile_at / s.tiles), tile = (int)(tile_at - (int64_t)head * s.tiles);
-    const int row0 = tile * kRows, last_row = s.rows.n * a.G - 1;
-    const TileRows rows{row0, last_row, head, s.rows.first};
-    if (pages <= 0) {
+  __device__ __forceinline__ explicit Walk(const AttendArgs& a) : list(a) {
+    run = list.run(a);
+    // runs that have units, an eighth of them to each XCD: neighbours, which may share a
+    // head's pages, share an L2
+    const int64_t runs = (list.total + run - 1) / (run > 0 ? run : 1);
+    w = (blockIdx.x % 8) * ((runs + 7) / 8) + blockIdx.x / 8;
+    u = w * run;
+    end = u + run < list.total ? u + run : list.total;
+    if ((int64_t)blockIdx.x / 8 >= (runs + 7) / 8) u = end;   // the next XCD's runs
+    noted = u >= end;
+    b = u < end ? list.find(a, u, &start) : 0;
+  }
+  // The next part that has pages; rows of sequences without any get their zeros here.
+  __device__ __forceinline__ bool next(const AttendArgs& a) {
+    while (u < end) {
+      const Share s(a, b);
+      if (u - start >= s.units) {
+        start += s.units;
+        ++b;
+        continue;
+      }
+      const int64_t tile_at = (u - start) / (s.pages + kTileCost);
+      const int64_t tile_start = start + tile_at * (s.pages + kTileCost);
+      const int from = (int)(u - tile_start);
+      const int64_t room = end - u;
+      const int units = s.pages + kTileCost - from < room ? s.pages + kTileCost - from : (int)room;
+      u += units;
+      page_at = from > kTileCost ? from - kTileCost : 0;
+      pages = from + units - kTileCost - page_at;
+      const int head = (int)(tile_at / s.tiles), tile = (int)(tile_at - (int64_t)head * s.tiles);
+      rows = TileRows{tile * a.rows, s.rows.n * a.G - 1, head, s.rows.first};
+      if (pages > 0) {
+        seq = s.rows;
+        first = s.first;
+        pages_all = s.pages;
+        first_page = tile_start + kTileCost;
+        const int last = rows.row0 + a.rows - 1 < rows.last_row ? rows.row0 + a.rows - 1
+                                                                 : rows.last_row;
+        low = seq.position(rows.row0 / a.G);
+        high = seq.position(last / a.G);
+        return true;
+      }
       // whoever has the first unit of a tile without pages writes its rows
-      if (s.pages == 0 && from == 0)
-        for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads)
-          if (row0 + i / (D / 4) <= last_row)
-            finish(a, rows, i / (D / 4), i % (D / 4) * 4, -__builtin_inff(), 0.f,
+      if (s.pages == 0 && from == 0) {
+        const int quads = a.cache.D / 4;
+        for (int i = threadIdx.x; i < a.rows * quads; i += blockDim.x)
+          if (rows.row0 + i / quads <= rows.last_row)
+            finish(a, rows, i / quads, i % quads * 4, -__builtin_inff(), 0.f,
                    f32x4{0.f, 0.f, 0.f, 0.f});
-      continue;
+      }
     }
-    // positions of the tile's first and last row: pages past the last are not seen
-    const int low = s.rows.position(row0 / a.G);
-    const int high = s.rows.position((row0 + kRows - 1 < last_row ? row0 + kRows - 1 : last_row) / a.G);
-    const int high_lo = a.window > 0 && high >= a.window ? high - a.window + 1 : 0;
-    const int seen = high < 0 ? 0 : high / LOWM_PAGE + 1 - s.first;
-    const int stop = page_at + pages < seen ? page_at + pages : seen;
-    const int* table = a.seq.table + b * a.seq.table_ld + s.first;
+    return false;
+  }
+  __device__ __forceinline__ const int* table(const AttendArgs& a) const {
+    return a.seq.table + b * a.seq.table_ld + first;
+  }
+  // Where this part stops for rows up to position `high`: pages past it are not seen.
+  __device__ __forceinline__ int stop(int high) const {
+    const int seen = high < 0 ? 0 : high / LOWM_PAGE + 1 - first;
+    return page_at + pages < seen ? page_at + pages : seen;
+  }
+  __device__ __forceinline__ bool whole() const { return page_at == 0 && pages == pages_all; }
+  __device__ __forceinline__ int place() const { return place_of(w, page_at > 0); }
 
-    ops_u32x4 keys[4][DP], vals[NT];
-    float k_scale = 0.f, v_scale = 0.f;
-    int page = -1, next_page = -1;
-    // The token of row r of score block i is 16 (r / 4) + 4 i + r % 4: then lane group
-    // g has tokens 16 g .. 16 g + 15, in the order of the values' bytes.
-    auto load_keys = [&]() {
-      page = next_page >= 0 && next_page < c.P ? next_page : -1;
-      const int64_t at = (int64_t)(page < 0 ? 0 : page) * c.H + head;
-      const uint8_t* p = static_cast<const uint8_t*>(c.k) + at * (LOWM_PAGE * D);
-      k_scale = c.k_scale[at];
-      v_scale = c.v_scale[at];
-#pragma unroll
-      for (int m = 0; m < DP; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int piece = 4 * m + g;
-          const uint8_t* x = p + (piece * LOWM_PAGE + 16 * (col >> 2) + 4 * i + (col & 3)) * 16;
-          keys[i][m] = ops_u32x4{0u, 0u, 0u, 0u};
-          if (FULL || m < DP - 1 || piece * 16 < D)
-            keys[i][m] = *reinterpret_cast<const ops_u32x4*>(x);
-        }
-      pin_loads();
-    };
-    auto load_vals = [&]() {
-      const uint8_t* p = static_cast<const uint8_t*>(c.v) +
-                         ((int64_t)(page < 0 ? 0 : page) * c.H + head) * (LOWM_PAGE * D);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (FULL || n < NT - 4 || n < nt)
-          vals[n] = __builtin_nontemporal_load(
-              reinterpret_cast<const ops_u32x4*>(p + (g * D + 16 * n + col) * 16));
-      pin_loads();
-    };
-    // the number of a page is read a turn before its keys
-    int at = page_at + wave;
-    if (at < stop) {
-      next_page = table[at];
-      load_keys();
-      next_page = table[at + kWaves < stop ? at + kWaves : at];
-    }
+  // Leaves the run's note: of the tile at hand if it begins here and ends elsewhere, in
+  // any case before the workgroup ends.
+  __device__ __forceinline__ void note(const AttendArgs& a, bool last_call) {
+    if (blockIdx.x == 0 && last_call && threadIdx.x == 0)
+      a.notes[0] = run > 0 ? (int)((list.total + run - 1) / run) : 0;
+    if (noted) return;
+    if (!last_call && (page_at > 0 || whole())) return;
+    noted = true;
+    if (threadIdx.x != 0) return;
+    Note n{0, rows};
+    if (!last_call) n.parts = (int)((first_page + pages_all - 1) / run - first_page / run) + 1;
+    *reinterpret_cast<Note*>(a.notes + 8 * (1 + w)) = n;
+  }
+  // After the sums of a part that is not whole are in their place: the runs that share
+  // the tile, in groups of kGroup, and then the groups.
+  __device__ __forceinline__ void share(const AttendArgs& a, int* arrived, float* lds) const {
+    const int64_t w0 = first_page / run;
+    const int n = (int)((first_page + pages_all - 1) / run - w0) + 1;
+    const int group = (int)(w - w0) / kGroup, groups = (n + kGroup - 1) / kGroup;
+    const int64_t leader = w0 + group * kGroup;
+    const int members = n - group * kGroup < kGroup ? n - group * kGroup : kGroup;
+    if (!arrive(a.counts + place_of(leader, group > 0), members, arrived)) return;
+    join(a, rows, w0, leader, 1, members, groups == 1, lds);
+    if (groups == 1) return;
+    if (arrive(a.counts + 2 * kGroups + place_of(w0, false), groups, arrived))
+      join(a, rows, w0, w0, kGroup, groups, true, lds);
+  }
+};
 
-    // rows: what they see, and their queries as the matrix operand
-    int see_lo[RT], see_hi[RT];
-    float unit[RT];
-    f16x8 q[RT][2 * DP];
+// Sixteen rows for each t: what they see, and their queries as the matrix operand.
+template <int DP, bool FULL, int RT>
+struct Queries {
+  int see_lo[RT], see_hi[RT];
+  float unit[RT];             // what a product of operands stands for, times log2 e
+  f16x8 q[RT][2 * DP];
+
+  // Rows row0 + 16 t + lane % 16 of the tile's sequence.
+  __device__ __forceinline__ Queries(const AttendArgs& a, const Walk& walk, int row0) {
+    const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, col = lane & 15;
+    const int D = a.cache.D;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const int r = row0 + 16 * t + col, in = r <= last_row ? r : last_row;
-      const int j = in / a.G, h = head * a.G + (in - j * a.G), pos = s.rows.position(j);
-      see_hi[t] = r <= last_row ? pos : -1;
+      const int r = row0 + 16 * t + col;
+      const int in = r <= walk.rows.last_row ? r : walk.rows.last_row;
+      const int j = in / a.G, h = walk.rows.head * a.G + (in - j * a.G);
+      const int pos = walk.seq.position(j);
+      see_hi[t] = r <= walk.rows.last_row ? pos : -1;
       see_lo[t] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-      const uint16_t* x = a.q + (s.rows.first + j) * a.q_row + h * a.q_head;
+      const uint16_t* x = a.q + (walk.seq.first + j) * a.q_row + h * a.q_head;
       ops_u32x4 raw[2 * DP];
       uint32_t top = 0;
 #pragma unroll
@@ -445,25 +496,30 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 4 ? 2 : 1) void attend_kernel(
       // 2^(14 - exponent of the largest), within what fp32 has; with the sign of the
       // scale, so that larger products are larger scores
       const int e = (int)(top >> 23), up = 127 + 14 - (e - 127);
-      const float lift = bits_float((uint32_t)(up < 1 ? 1 : up > 254 ? 254 : up) << 23);
-      const float signed_lift = a.scale < 0.f ? -lift : lift;
-      unit[t] = top < 0x7f800000u ? a.scale / signed_lift : __builtin_nanf("");
+      const float size = bits_float((uint32_t)(up < 1 ? 1 : up > 254 ? 254 : up) << 23);
+      const float lift = a.scale < 0.f ? -size : size;
+      unit[t] = top < 0x7f800000u ? a.scale / lift : __builtin_nanf("");
 #pragma unroll
       for (int m = 0; m < 2 * DP; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t w = raw[m][i];
-          q[t][m][2 * i] = (_Float16)(bf16_lo(w) * signed_lift);
-          q[t][m][2 * i + 1] = (_Float16)(bf16_hi(w) * signed_lift);
+          q[t][m][2 * i] = (_Float16)(bf16_lo(w) * lift);
+          q[t][m][2 * i + 1] = (_Float16)(bf16_hi(w) * lift);
         }
     }
+  }
+};
 
-    // Weights are e^(x + log vs - ref) 2^kLift with vs the page's scale of the values in
-    // units of the first page's, v0: they multiply the bytes as they are, and go into the
-    // sums o without another factor.  ref is the largest x + log vs so far, or up to
-    // kSlack less: the sums are scaled anew only when a page passes that.
-    float ref[RT], sum[RT], v0 = 0.f;
-    f32x4 o[RT][NT];
+// The softmax's state.  Weights are e^(x + log vs - ref) 2^kLift with vs the page's scale
+// of the values in units of the first page's, v0: they multiply the bytes as they are,
+// and go into the sums o without another factor.  ref is the largest x + log vs so far,
+// or up to kSlack less: the sums are scaled anew only when a page passes that.
+template <int NT, int RT>
+struct Softmax {
+  float ref[RT], sum[RT], v0 = 0.f;
+  f32x4 o[RT][NT];
+  __device__ __forceinline__ Softmax() {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       ref[t] = -__builtin_inff();
@@ -471,13 +527,203 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 4 ? 2 : 1) void attend_kernel(
 #pragma unroll
       for (int n = 0; n < NT; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+  }
+  // A page's products x to weights p, for its first `live` tokens from token0 on; masked:
+  // whether a row may not see some of them.
+  template <typename Q>
+  __device__ __forceinline__ void weigh(const Q& q, f32x4 (&x)[RT][4], f16x8 (&p)[RT][2],
+                                        bool masked, int live, int token0, float ks, float vs) {
+    const int g = (threadIdx.x & (kWave - 1)) >> 4;
+    // a scale of 0 (or one too small to be a number with a logarithm) leaves no value
+    const bool some = !(fabsf(vs) < 1.17549435e-38f);
+    if (v0 == 0.f && some && vs > 0.f && vs < __builtin_inff()) v0 = vs;
+    const float vs_here = some ? vs / (v0 == 0.f ? 1.f : v0) : 1.f,
+                log_vs = __builtin_amdgcn_logf(vs_here), per_vs = 1.f / vs_here;
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int token = token0 + 16 * g + 4 * i + e;
+            const bool sees = live > 0 && token >= q.see_lo[t] && token <= q.see_hi[t];
+            x[t][i][e] = sees ? x[t][i][e] : -__builtin_inff();
+          }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      // never 0, which would make NaN of the masked ones
+      float per = q.unit[t] * ks;
+      per = per == 0.f ? 1e-38f : per;
+      float here = x[t][0][0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) here = fmaxf(here, x[t][i][e]);
+      here = row_max(here);
+      // a row that sees none of the page is not touched by its scales
+      const bool none = here == -__builtin_inff();
+      here = here * per + log_vs;
+      per = none ? 1.f : per;
+      if (__any(here > ref[t] + kSlack)) {
+        const float now = here > ref[t] + kSlack ? here : ref[t];
+        const float keep = now == ref[t] ? 1.f : __builtin_amdgcn_exp2f(ref[t] - now);
+        ref[t] = now;
+        sum[t] *= keep;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[t][n] *= keep;
+      }
+      const float lift =
+          none ? 0.f : log_vs + kLift - (ref[t] == -__builtin_inff() ? 0.f : ref[t]);
+      float add = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][i][e], per, lift));
+          add += w;
+          p[t][i / 2][4 * (i % 2) + e] = (_Float16)w;
+        }
+      sum[t] += add * (none ? 1.f : per_vs);
+    }
+    if (!some) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) p[t][0] = p[t][1] = f16x8{};
+    }
+  }
+};
+
+// What lies behind a sequence may be any byte, a NaN of e4m3 among them: a piece of 16
+// tokens, of which `left` are there.
+__device__ __forceinline__ void clear_behind(ops_u32x4& v, int left) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = left - 4 * i;
+    v[i] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << 8 * n) - 1;
+  }
+}
+
+// The token of row r of score block i is 16 (r / 4) + 4 i + r % 4: then lane group g has
+// tokens 16 g .. 16 g + 15, in the order of the values' bytes.
+__device__ __forceinline__ int key_piece(int g, int col, int m, int i) {
+  return (4 * m + g) * LOWM_PAGE + 16 * (col >> 2) + 4 * i + (col & 3);
+}
+
+// One word for the whole wavefront by a vector load.  A scalar load would share the
+// counter of LDS accesses, and those would wait for it (first_lane() at its use makes it
+// one number again).
+template <typename T>
+__device__ __forceinline__ T load_apart(const T* p) {
+  uint32_t none = 0;
+  asm volatile("" : "+v"(none));
+  return p[none];
+}
+__device__ __forceinline__ int first_lane(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float first_lane(float v) {
+  return bits_float((uint32_t)__builtin_amdgcn_readfirstlane((int)float_bits(v)));
+}
+
+// A barrier for LDS alone: loads in flight stay so.
+__device__ __forceinline__ void meet_in_lds() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Whether the registers of two workgroups fit a CU; and whether they do with the queries
+// in LDS.
+constexpr bool queries_in_lds(int DP, int RT) { return DP == 2 && RT == 2; }
+constexpr bool two_to_a_cu(int DP, int RT) {
+  return DP * RT <= 2 || (DP == 3 && RT == 1) || (DP == 2 && RT == 2);
+}
+
+// DP blocks of 64 elements of a head, all of them there (FULL) or not, RT blocks of 16
+// rows to a tile.  Each wavefront takes every fourth page of the part.
+template <int DP, bool FULL, int RT, bool E4M3>
+__global__ __launch_bounds__(kThreads, two_to_a_cu(DP, RT) ? 2 : 1)
+void attend_kernel(AttendArgs a) {
+  constexpr int NT = 4 * DP;                // blocks of 16 elements
+  constexpr int kRows = 16 * RT;
+  constexpr int kPart = DP == 1 ? 4 : DP == 3 ? 6 : 8;   // joined through LDS at a time
+  static_assert(NT % kPart == 0, "whole parts");
+  constexpr int kPitch = 16 * kPart + 4;    // lanes' rows in distinct banks
+  __shared__ __align__(16) float joint[kWaves][kRows][kPitch];
+  __shared__ float joint_max[kWaves][kRows], joint_sum[kWaves][kRows];
+  __shared__ int arrived;
+  constexpr bool kInLds = queries_in_lds(DP, RT);
+  __shared__ f16x8 queries[kInLds ? RT : 1][kInLds ? 2 * DP : 1][kWave];
+  constexpr bool kNow = RT == 1;            // few rows are joined here, others by join_kernel
+  static_assert(!kNow || sizeof(joint) >= 2 * kJoin * kRows * sizeof(float), "room to join");
+
+  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, col = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const lowm_kv_cache& c = a.cache;
+  const int D = FULL ? 64 * DP : c.D, nt = FULL ? NT : D / 16;
+
+  Walk walk(a);
+  while (walk.next(a)) {
+    const int stop = walk.stop(walk.high), head = walk.rows.head;
+    const int high_lo = a.window > 0 && walk.high >= a.window ? walk.high - a.window + 1 : 0;
+    const int* table = walk.table(a);
+
+    ops_u32x4 keys[4][DP], vals[NT];
+    float k_scale = 0.f, v_scale = 0.f;
+    int page = -1, next_page = -1;
+    auto load_keys = [&](int next) {
+      page = first_lane(next_page);
+      page = page >= 0 && page < c.P ? page : -1;
+      const int64_t at = (int64_t)(page < 0 ? 0 : page) * c.H + head;
+      next_page = load_apart(table + next);
+      const ops_u32x4* p =
+          reinterpret_cast<const ops_u32x4*>(static_cast<const uint8_t*>(c.k) + at * (LOWM_PAGE * D));
+      k_scale = load_apart(c.k_scale + at);
+      v_scale = load_apart(c.v_scale + at);
+#pragma unroll
+      for (int m = 0; m < DP; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          keys[i][m] = ops_u32x4{0u, 0u, 0u, 0u};
+          if (FULL || m < DP - 1 || (4 * m + g) * 16 < D) keys[i][m] = p[key_piece(g, col, m, i)];
+        }
+      pin_loads();
+    };
+    // Values are read once: with the streaming hint (the keys' lines are shared by two
+    // loads each, and would be fetched twice: 2 x 131001 tokens 91 us, 95 with the hint
+    // on both, 102 on neither).
+    auto load_vals = [&]() {
+      const ops_u32x4* p = reinterpret_cast<const ops_u32x4*>(
+          static_cast<const uint8_t*>(c.v) +
+          ((int64_t)(page < 0 ? 0 : page) * c.H + head) * (LOWM_PAGE * D));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (!FULL && n >= NT - 4) vals[n] = ops_u32x4{0u, 0u, 0u, 0u};
+        if (FULL || n < NT - 4 || n < nt)
+          vals[n] = __builtin_nontemporal_load(p + g * D + 16 * n + col);
+      }
+      pin_loads();
+    };
+    // the number of a page is read a turn before its keys
+    int at = walk.page_at + wave;
+    if (at < stop) {
+      next_page = load_apart(table + at);
+      load_keys(at + kWaves < stop ? at + kWaves : at);
+    }
+    const Queries<DP, FULL, RT> rows(a, walk, walk.rows.row0);
+    if constexpr (kInLds) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int m = 0; m < 2 * DP; ++m)
+          if (m % kWaves == wave) queries[t][m][lane] = rows.q[t][m];
+      meet_in_lds();
+    }
+    Softmax<NT, RT> sm;
 
     for (; at < stop; at += kWaves) {
-      const int token0 = (s.first + at) * LOWM_PAGE;
+      const int token0 = (walk.first + at) * LOWM_PAGE;
       // tokens of the page that are there at all
-      int live = s.rows.len - token0;
+      int live = walk.seq.len - token0;
       live = page < 0 ? 0 : live < LOWM_PAGE ? live : LOWM_PAGE;
-      const float ks = live > 0 ? k_scale : 0.f, vs = live > 0 ? v_scale : 0.f;
+      const float ks = live > 0 ? first_lane(k_scale) : 0.f, vs = live > 0 ? first_lane(v_scale) : 0.f;
       load_vals();
 
       f32x4 x[RT][4];
@@ -485,118 +731,71 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 4 ? 2 : 1) void attend_kernel(
       for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // four operands are widened while the matrix unit takes the four before
+      f16x8 ops[2][4];
+      auto widen_keys = [&](int step) {
 #pragma unroll
-      for (int m = 0; m < DP; ++m)
+        for (int i = 0; i < 4; ++i)
+          ops[step % 2][i] = widen<E4M3>(keys[i][step / 2][step % 2 * 2],
+                                         keys[i][step / 2][step % 2 * 2 + 1]);
+      };
+      auto widen_vals = [&](int step) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f16x8 k0 = widen<E4M3>(keys[i][m][0], keys[i][m][1]),
-                      k1 = widen<E4M3>(keys[i][m][2], keys[i][m][3]);
+        for (int i = 0; i < 4; ++i)
+          ops[step % 2][i] = widen<E4M3>(vals[2 * step + i / 2][i % 2 * 2],
+                                         vals[2 * step + i / 2][i % 2 * 2 + 1]);
+      };
+      widen_keys(0);
 #pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            x[t][i] = product(k0, q[t][2 * m], x[t][i]);
-            x[t][i] = product(k1, q[t][2 * m + 1], x[t][i]);
-          }
-        }
+      for (int step = 0; step < 2 * DP; ++step) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (step + 1 < 2 * DP) widen_keys(step + 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+            x[t][i] = product(ops[step % 2][i], kInLds ? queries[t][step][lane] : rows.q[t][step],
+                              x[t][i]);
+      }
       if (at + kWaves < stop) {
-        load_keys();
-        next_page = table[at + 2 * kWaves < stop ? at + 2 * kWaves : at];
+        load_keys(at + 2 * kWaves < stop ? at + 2 * kWaves : at);
       }
-
-      // a scale of 0 (or one too small to be a number with a logarithm) leaves no value
-      const bool some = !(fabsf(vs) < 1.17549435e-38f);
-      if (v0 == 0.f && some && vs > 0.f && vs < __builtin_inff()) v0 = vs;
-      const float vs_here = some ? vs / (v0 == 0.f ? 1.f : v0) : 1.f,
-                  log_vs = __builtin_amdgcn_logf(vs_here), per_vs = 1.f / vs_here;
-
-      if (live < LOWM_PAGE || token0 + LOWM_PAGE - 1 > low || token0 < high_lo) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int token = token0 + 16 * g + 4 * i + e;
-              const bool sees = live > 0 && token >= see_lo[t] && token <= see_hi[t];
-              x[t][i][e] = sees ? x[t][i][e] : -__builtin_inff();
-            }
-      }
-
       f16x8 p[RT][2];
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        // never 0, which would make NaN of the masked ones
-        float per = unit[t] * ks;
-        per = per == 0.f ? 1e-38f : per;
-        float here = x[t][0][0];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) here = fmaxf(here, x[t][i][e]);
-        here = row_max(here);
-        // a row that sees none of the page is not touched by its scales
-        const bool none = here == -__builtin_inff();
-        here = here * per + log_vs;
-        per = none ? 1.f : per;
-        if (__any(here > ref[t] + kSlack)) {
-          const float now = here > ref[t] + kSlack ? here : ref[t];
-          const float keep = now == ref[t] ? 1.f : __builtin_amdgcn_exp2f(ref[t] - now);
-          ref[t] = now;
-          sum[t] *= keep;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) o[t][n] *= keep;
-        }
-        const float lift =
-            none ? 0.f : log_vs + kLift - (ref[t] == -__builtin_inff() ? 0.f : ref[t]);
-        float add = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][i][e], per, lift));
-            add += w;
-            p[t][i / 2][4 * (i % 2) + e] = (_Float16)w;
-          }
-        sum[t] += add * (none ? 1.f : per_vs);
-      }
-      if (!some) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t) p[t][0] = p[t][1] = f16x8{};
-      }
+      sm.weigh(rows, x, p,
+               live < LOWM_PAGE || token0 + LOWM_PAGE - 1 > walk.low || token0 < high_lo, live,
+               token0, ks, vs);
       if (E4M3 && live < LOWM_PAGE) {
-        // what lies behind the sequence may be any byte, a NaN among them
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int left = live - 16 * g - 4 * i;
-            const uint32_t mask = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << 8 * left) - 1;
-            vals[n][i] &= mask;
-          }
+        for (int n = 0; n < NT; ++n) clear_behind(vals[n], live - 16 * g);
       }
+      // (blocks past D are zeros)
+      widen_vals(0);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (!FULL && n >= NT - 4 && n >= nt) continue;
-        const f16x8 y0 = widen<E4M3>(vals[n][0], vals[n][1]),
-                    y1 = widen<E4M3>(vals[n][2], vals[n][3]);
+      for (int step = 0; step < NT / 2; ++step) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (step + 1 < NT / 2) widen_vals(step + 1);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          o[t][n] = product(y0, p[t][0], o[t][n]);
-          o[t][n] = product(y1, p[t][1], o[t][n]);
-        }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+              sm.o[t][2 * step + n] =
+                  product(ops[step % 2][2 * n + i], p[t][i], sm.o[t][2 * step + n]);
       }
     }
 
     // the four wavefronts' sums of the tile
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const float all = row_sum(sum[t]);
+      const float all = row_sum(sm.sum[t]);
       if (g == 0) {
-        joint_max[wave][16 * t + col] = ref[t];
+        joint_max[wave][16 * t + col] = sm.ref[t];
         joint_sum[wave][16 * t + col] = all;
       }
     }
-    const bool whole = page_at == 0 && pages == s.pages;
-    const int place = place_of(w, page_at > 0);
+    const bool whole = walk.whole();
+    const int place = walk.place();
 #pragma unroll
     for (int n0 = 0; n0 < NT; n0 += kPart) {
 #pragma unroll
@@ -604,11 +803,11 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 4 ? 2 : 1) void attend_kernel(
 #pragma unroll
         for (int n = 0; n < kPart; ++n)
           *reinterpret_cast<f32x4*>(&joint[wave][16 * t + col][16 * n + 4 * g]) =
-              o[t][n0 + n] * v0;
+              sm.o[t][n0 + n] * sm.v0;
       __syncthreads();
       for (int i = threadIdx.x; i < kRows * 4 * kPart; i += kThreads) {
         const int r = i / (4 * kPart), d4 = i % (4 * kPart), d = 16 * n0 + 4 * d4;
-        if (row0 + r > last_row || (!FULL && d >= D)) continue;
+        if (walk.rows.row0 + r > walk.rows.last_row || (!FULL && d >= D)) continue;
         float top = joint_max[0][r];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) top = fmaxf(top, joint_max[w][r]);
@@ -623,56 +822,324 @@ __global__ __launch_bounds__(kThreads, DP * RT <= 4 ? 2 : 1) void attend_kernel(
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] += f * z[e];
         }
-        if (whole) {
-          finish(a, rows, r, d, top, all, y);
-        } else {
-          const int64_t row = (int64_t)place * kRows + r;
-          put2(a.sums + row * D + d, y[0], y[1]);
-          put2(a.sums + row * D + d + 2, y[2], y[3]);
-          if (d == 0) put2(a.stats + 2 * row, top, all);
-        }
+        if (whole)
+          finish(a, walk.rows, r, d, top, all, y);
+        else
+          leave<kNow>(a, place, r, d, top, all, y);
       }
       __syncthreads();
     }
-    if (whole) continue;
+    if constexpr (kNow) {
+      if (!whole) walk.share(a, &arrived, &joint[0][0][0]);
+    } else {
+      walk.note(a, false);
+    }
+  }
+  if constexpr (!kNow) walk.note(a, true);
+}
 
-    // the runs that share the tile, in groups of kJoin, and then the groups
-    const int64_t first_page = start + tile_at * (s.pages + kTileCost) + kTileCost;
-    const int64_t w0 = first_page / run;
-    const int n = (int)((first_page + s.pages - 1) / run - w0) + 1;
-    const int group = (int)(w - w0) / kJoin, groups = (n + kJoin - 1) / kJoin;
-    const int64_t leader = w0 + group * kJoin;
-    const int members = n - group * kJoin < kJoin ? n - group * kJoin : kJoin;
-    if (!arrive(a.counts + place_of(leader, group > 0), members, &arrived)) continue;
-    float* lds = &joint[0][0][0];
-    join(a, rows, w0, leader, 1, members, groups == 1, lds);
-    if (groups == 1) continue;
-    if (arrive(a.counts + 2 * kGroups + place_of(w0, false), groups, &arrived))
-      join(a, rows, w0, w0, kJoin, groups, true, lds);
+// The same for many rows: 16 RT to each of WAVES wavefronts, all on the same page.  A
+// page becomes fp16 once, in LDS, a share by each wavefront, in the order in which the
+// matrix instructions take it (a lane's 16 bytes after another: no bank is hit twice);
+// the next two pages are on their way in registers meanwhile, and go into the other half
+// of the LDS in turn.  One barrier a page, which waits for LDS alone.
+template <int DP, bool FULL, int RT, int WAVES, bool E4M3>
+__global__ __launch_bounds__(kWave* WAVES, DP <= 2 || WAVES == 8 ? 2 : 1)
+void attend_wide_kernel(AttendArgs a) {
+  constexpr int NT = 4 * DP;
+  constexpr int kShare = 8 * DP / WAVES;   // pieces of a page to a wavefront
+  static_assert(8 * DP % WAVES == 0, "equal shares");
+  // keys of score block i and 64 elements m: 4 m + i; values of 16 elements n: 4 DP + n
+  __shared__ f16x8 stage[2][8 * DP][2][kWave];
+
+  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, col = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const lowm_kv_cache& c = a.cache;
+  const int D = FULL ? 64 * DP : c.D, nt = FULL ? NT : D / 16;
+
+  Walk walk(a);
+  while (walk.next(a)) {
+    const int stop = walk.stop(walk.high), head = walk.rows.head;
+    const int* table = walk.table(a);
+    // the wavefront's own rows
+    const int row0 = walk.rows.row0 + 16 * RT * wave;
+    const int last = row0 + 16 * RT - 1 < walk.rows.last_row ? row0 + 16 * RT - 1
+                                                             : walk.rows.last_row;
+    const bool mine = row0 <= walk.rows.last_row;
+    const int low = mine ? walk.seq.position(row0 / a.G) : -1,
+              high = mine ? walk.seq.position(last / a.G) : -1;
+    const int high_lo = a.window > 0 && high >= a.window ? high - a.window + 1 : 0;
+    const int low_lo = a.window > 0 && low >= a.window ? low - a.window + 1 : 0;
+
+    // Two pages are on their way, one for each half of the LDS: pieces wave + WAVES k.
+    ops_u32x4 raw[2][kShare];
+    struct Page {
+      float ks, vs;
+      int live;
+    } on_way[2] = {}, here = {};
+    int next_page = 0;
+    auto load = [&](auto half_c, int at) {
+      constexpr int half = decltype(half_c)::value;
+      const int page = first_lane(next_page);
+      const bool some = page >= 0 && page < c.P;
+      const int64_t from = (int64_t)(some ? page : 0) * c.H + head;
+      // the next page's number first: waiting for it is not waiting for what follows
+      next_page = load_apart(table + (at + 1 < stop ? at + 1 : at));
+      const ops_u32x4* pk = reinterpret_cast<const ops_u32x4*>(static_cast<const uint8_t*>(c.k) +
+                                                               from * (LOWM_PAGE * D));
+      const ops_u32x4* pv = reinterpret_cast<const ops_u32x4*>(static_cast<const uint8_t*>(c.v) +
+                                                               from * (LOWM_PAGE * D));
+      const int live = walk.seq.len - (walk.first + at) * LOWM_PAGE;
+      on_way[half].live = !some ? 0 : live < LOWM_PAGE ? live : LOWM_PAGE;
+      on_way[half].ks = load_apart(c.k_scale + from);
+      on_way[half].vs = load_apart(c.v_scale + from);
+#pragma unroll
+      for (int k = 0; k < kShare; ++k) {
+        const int piece = wave + WAVES * k;
+        const bool key = piece < 4 * DP;
+        const int m = piece / 4, n = piece - 4 * DP;
+        const bool there = FULL || (key ? (4 * m + g) * 16 < D : n < nt);
+        const ops_u32x4* x =
+            key ? pk + key_piece(g, col, m, piece % 4) : pv + g * D + 16 * n + col;
+        raw[half][k] = ops_u32x4{0u, 0u, 0u, 0u};
+        if (there) raw[half][k] = *x;
+      }
+      pin_loads();
+    };
+    auto put = [&](auto half_c) {
+      constexpr int half = decltype(half_c)::value;
+#pragma unroll
+      for (int k = 0; k < kShare; ++k) {
+        const int piece = wave + WAVES * k;
+        ops_u32x4 v = raw[half][k];
+        if (E4M3 && piece >= 4 * DP && on_way[half].live < LOWM_PAGE)
+          clear_behind(v, on_way[half].live - 16 * g);
+        stage[half][piece][0][lane] = widen<E4M3>(v[0], v[1]);
+        stage[half][piece][1][lane] = widen<E4M3>(v[2], v[3]);
+      }
+      here.live = on_way[half].live;
+      here.ks = first_lane(on_way[half].ks);
+      here.vs = first_lane(on_way[half].vs);
+    };
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, 1> odd{};
+    int at = walk.page_at;
+    if (at < stop) {
+      next_page = load_apart(table + at);
+      load(even, at);
+      if (at + 1 < stop) load(odd, at + 1);
+    }
+    const Queries<DP, FULL, RT> rows(a, walk, row0);
+    Softmax<NT, RT> sm;
+    if (at < stop) {
+      put(even);
+      if (at + 2 < stop) load(even, at + 2);
+      meet_in_lds();
+    }
+    auto turn = [&](auto half_c, auto other, int at) {
+      constexpr int half = decltype(half_c)::value;
+      const int token0 = (walk.first + at) * LOWM_PAGE;
+      // wavefronts whose rows do not see the page only pass it on
+      if (mine && token0 <= high && token0 + LOWM_PAGE > low_lo) {
+        f32x4 x[RT][4];
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // four operands are read while eight instructions take the four before
+        f16x8 ops[2][4];
+        auto read_keys = [&](int step) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ops[step % 2][i] = stage[half][step / 2 * 4 + i][step % 2][lane];
+        };
+        auto read_vals = [&](int step) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ops[step % 2][i] = stage[half][4 * DP + 2 * step + i / 2][i % 2][lane];
+        };
+        read_keys(0);
+#pragma unroll
+        for (int step = 0; step < 2 * DP; ++step) {
+          if (step + 1 < 2 * DP)
+            read_keys(step + 1);
+          else
+            read_vals(0);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+              x[t][i] = product(ops[step % 2][i], rows.q[t][step], x[t][i]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        const float ks = here.live > 0 ? here.ks : 0.f, vs = here.live > 0 ? here.vs : 0.f;
+        f16x8 p[RT][2];
+        sm.weigh(rows, x, p,
+                 here.live < LOWM_PAGE || token0 + LOWM_PAGE - 1 > low || token0 < high_lo,
+                 here.live, token0, ks, vs);
+        // (blocks past D are zeros)
+#pragma unroll
+        for (int step = 0; step < NT / 2; ++step) {
+          if (step + 1 < NT / 2) read_vals(step + 1);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int t = 0; t < RT; ++t)
+                sm.o[t][2 * step + n] =
+                    product(ops[step % 2][2 * n + i], p[t][i], sm.o[t][2 * step + n]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if (at + 1 < stop) {
+        put(other);
+        if (at + 3 < stop) load(other, at + 3);
+      }
+      meet_in_lds();
+    };
+    for (; at < stop; at += 2) {
+      turn(even, odd, at);
+      if (at + 1 < stop) turn(odd, even, at + 1);
+    }
+
+    const bool whole = walk.whole();
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const float all = row_sum(sm.sum[t]);
+      const int r = 16 * RT * wave + 16 * t + col;
+      if (walk.rows.row0 + r > walk.rows.last_row) continue;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (!FULL && n >= NT - 4 && n >= nt) continue;
+        const int d = 16 * n + 4 * g;
+        if (whole)
+          finish(a, walk.rows, r, d, sm.ref[t], all, sm.o[t][n] * sm.v0);
+        else
+          leave<false>(a, walk.place(), r, d, sm.ref[t], all, sm.o[t][n] * sm.v0);
+      }
+    }
+    walk.note(a, false);
+  }
+  walk.note(a, true);
+}
+
+// Joins the tiles that several runs have a part of, in the order of join().  Each
+// wavefront finds out which runs begin one, and takes 64 / lanes rows at a time.
+__global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
+  constexpr int kAhead = 16, kSets = kGroups / kWave;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int runs = a.notes[0];
+  uint64_t begun[kSets];
+  int tiles = 0;
+#pragma unroll
+  for (int k = 0; k < kSets; ++k) {
+    const int w = kWave * k + lane;
+    const int parts = reinterpret_cast<const Note*>(a.notes + 8 * (1 + w))->parts;
+    begun[k] = __ballot(w < runs && parts > 0);
+    tiles += __builtin_popcountll(begun[k]);
+  }
+  const int D = a.cache.D, lanes = D <= 64 ? 16 : D <= 128 ? 32 : 64;
+  const int per = a.rows * lanes / kWave;   // turns to a tile
+  const int d = lane % lanes * 4;
+  for (int item = blockIdx.x * kWaves + (int)threadIdx.x / kWave; item < tiles * per;
+       item += kWaves * gridDim.x) {
+    int skip = item / per;
+    int64_t w0 = 0;
+#pragma unroll
+    for (int k = 0; k < kSets; ++k) {
+      const int here = __builtin_popcountll(begun[k]);
+      if (skip >= 0 && skip < here) {
+        uint64_t left = begun[k];
+        for (int i = 0; i < skip; ++i) left &= left - 1;
+        w0 = kWave * k + __builtin_ctzll(left);
+      }
+      skip -= here;
+    }
+    const Note note = *reinterpret_cast<const Note*>(a.notes + 8 * (1 + w0));
+    const int n = note.parts, r = item % per * (kWave / lanes) + lane / lanes;
+    if (note.rows.row0 + r > note.rows.last_row || d >= D) continue;
+    float most = -__builtin_inff(), sum = 0.f;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      float top[kAhead], part[kAhead];
+      f32x4 z[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int in = i0 + i < n ? i0 + i : n - 1;
+        const int64_t row = (int64_t)place_of(w0 + in, in > 0) * a.rows + r;
+        top[i] = i0 + i < n ? a.stats[2 * row] : -__builtin_inff();
+        part[i] = a.stats[2 * row + 1];
+        z[i] = *reinterpret_cast<const f32x4*>(a.sums + row * D + d);
+      }
+      float now = most;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) now = fmaxf(now, top[i]);
+      const float base = now == -__builtin_inff() ? 0.f : now;
+      const float keep = __builtin_amdgcn_exp2f(most - base);
+      sum *= keep;
+      y *= keep;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float f = __builtin_amdgcn_exp2f(top[i] - base);
+        if (i0 + i < n) {
+          sum += f * part[i];
+          y += f * z[i];
+        }
+      }
+      most = now;
+    }
+    finish(a, note.rows, r, d, most, sum, y);
   }
 }
 
-template <int DP, bool FULL>
-const void* kernel_for(int rt, bool e4m3) {
-  if (rt == 1)
-    return e4m3 ? (const void*)&attend_kernel<DP, FULL, 1, true>
-                : (const void*)&attend_kernel<DP, FULL, 1, false>;
-  return e4m3 ? (const void*)&attend_kernel<DP, FULL, 2, true>
-              : (const void*)&attend_kernel<DP, FULL, 2, false>;
+// A sequence's rows of a key head, on average, choose the kernel: up to 16, 32 or 64, or
+// more.
+enum Kind { kFew = 16, kSome = 32, kMore = 64, kMany = kWideRows };
+Kind kind_for(int64_t T, int G, int B) {
+  const int64_t rows = T * G;
+  return rows <= (int64_t)B * kFew    ? kFew
+         : rows <= (int64_t)B * kSome ? kSome
+         : rows <= (int64_t)B * kMore ? kMore
+                                      : kMany;
 }
-const void* kernel_for(int D, int rt, bool e4m3) {
+// Wavefronts of a workgroup.  Past 128 elements a page's fp16 take more than half of the
+// LDS, and 16 rows to each of eight wavefronts keep two on each SIMD where 32 to each of
+// four would keep one.
+int waves_for(Kind k, int D) { return k == kMany && D > 128 ? 8 : 4; }
+template <int DP, bool FULL, bool E4M3>
+const void* kernel_for(Kind k) {
+  switch (k) {
+    case kFew: return (const void*)&attend_kernel<DP, FULL, 1, E4M3>;
+    case kSome: return (const void*)&attend_kernel<DP, FULL, 2, E4M3>;
+    case kMore: return (const void*)&attend_wide_kernel<DP, FULL, 1, 4, E4M3>;
+    default:
+      return (const void*)&attend_wide_kernel<DP, FULL, DP <= 2 ? 2 : 1, DP <= 2 ? 4 : 8, E4M3>;
+  }
+}
+template <int DP>
+const void* kernel_for(Kind k, bool full, bool e4m3) {
+  return full ? (e4m3 ? kernel_for<DP, true, true>(k) : kernel_for<DP, true, false>(k))
+              : (e4m3 ? kernel_for<DP, false, true>(k) : kernel_for<DP, false, false>(k));
+}
+const void* kernel_for(int D, Kind k, bool e4m3) {
   switch ((D + 63) / 64) {
-    case 1: return D == 64 ? kernel_for<1, true>(rt, e4m3) : kernel_for<1, false>(rt, e4m3);
-    case 2: return D == 128 ? kernel_for<2, true>(rt, e4m3) : kernel_for<2, false>(rt, e4m3);
-    case 3: return D == 192 ? kernel_for<3, true>(rt, e4m3) : kernel_for<3, false>(rt, e4m3);
-    default: return D == 256 ? kernel_for<4, true>(rt, e4m3) : kernel_for<4, false>(rt, e4m3);
+    case 1: return kernel_for<1>(k, D == 64, e4m3);
+    case 2: return kernel_for<2>(k, D == 128, e4m3);
+    case 3: return kernel_for<3>(k, D == 192, e4m3);
+    default: return kernel_for<4>(k, D == 256, e4m3);
   }
 }
 
-// Rows of a tile that a workspace has room for.
-int64_t room_rows(int T, int G) { return (int64_t)T * G <= 16 ? 16 : 32; }
+// Rows of the largest tile that T rows may take.
+int64_t room_rows(int T, int G) {
+  const int64_t rows = (int64_t)T * G;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : kWideRows;
+}
 size_t workspace_bytes(int T, int G, int D) {
-  return (size_t)(2 * kGroups * (2 * 4 + room_rows(T, G) * (D + 2) * 4));
+  return (size_t)(4 * (4 * kGroups + 8 * (1 + kGroups) + 2 * kGroups * room_rows(T, G) * (D + 2)));
 }
 
 int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
@@ -705,17 +1172,20 @@ int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
     for (int k = 0; k < i; ++k)
       if (meet(out[i], out[k])) return LOWM_ERR_INVALID_ARG;
   }
-  // Two blocks of rows to a tile where a sequence has more than one block, on average.
-  const int rt = room_rows(s.T, G) == 32 && (int64_t)s.T * G > (int64_t)s.B * 16 ? 2 : 1;
+  const Kind kind = kind_for(s.T, G, s.B);
   AttendArgs a{};
   a.cache = c;
   a.seq = s;
   a.q = static_cast<const uint16_t*>(u->q);
   a.out = static_cast<uint16_t*>(u->out);
   a.lse = u->lse;
-  a.rows = 16 * rt;
+  a.rows = kind;
+  // one workgroup to a CU where its registers and LDS leave no room for two
+  a.groups_log = kind >= kMore && c.D > 128 ? 8 : 9;
+  a.turn = kind >= kMore ? 1 : kWaves;
   a.counts = static_cast<int*>(u->workspace);
-  a.stats = static_cast<float*>(u->workspace) + 4 * kGroups;
+  a.notes = a.counts + 4 * kGroups;
+  a.stats = reinterpret_cast<float*>(a.notes + 8 * (1 + kGroups));
   a.sums = a.stats + 2 * kGroups * a.rows * 2;
   a.q_row = u->q_row;
   a.q_head = u->q_head;
@@ -724,8 +1194,12 @@ int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
   a.window = u->window;
   a.scale = u->scale * kLog2e;
   void* args[] = {&a};
-  return launched(hipLaunchKernel(kernel_for(c.D, rt, c.type == LOWM_E4M3), dim3(kGroups),
-                                  dim3(kThreads), args, 0, stream));
+  rc = launched(hipLaunchKernel(kernel_for(c.D, kind, c.type == LOWM_E4M3),
+                                dim3(1u << a.groups_log), dim3(kWave * waves_for(kind, c.D)), args,
+                                0, stream));
+  if (rc != LOWM_OK || kind == kFew) return rc;
+  return launched(hipLaunchKernel((const void*)&join_kernel,
+                                  dim3(kJoinGroups), dim3(kThreads), args, 0, stream));
 }
 
 }  // namespace
