@@ -72,82 +72,109 @@ struct AttendArgs {
   float* stats;      // [2 kGroups][rows of a tile][2]: maximum, sum
   int64_t q_row, q_head;
   int Hq, G, window, rows;   // rows: of a tile
-  int groups_log;            // workgroups
-  int turn;                  // pages that a workgroup takes at a time
+  int groups;                // workgroups
+  int turn;                  // pages that a workgroup takes at a time, a power of two
+  int small;                 // pages of a tile that a workgroup had better take alone
+  int most_log;              // log2 of the pages of a part, where tiles are cut by themselves
+  uint32_t g_magic, g_shift; // for division by G
   float scale;               // times log2 e
 };
 
-// A sequence's share of the list: its tiles, each kTileCost units that stand for no page,
-// then its pages.
+// x / G for x of 31 bits: G's reciprocal rounded up, so that no quotient is too small,
+// with enough bits that none is too large.
+struct Divisor {
+  uint32_t magic, shift;
+  explicit Divisor(int d) {
+    shift = 0;
+    while ((1 << shift) < d) ++shift;
+    magic = (uint32_t)(((1ull << (31 + shift)) + d - 1) / d);
+  }
+};
+__device__ __forceinline__ int by_g(const AttendArgs& a, int x) {
+  return a.G == 1 ? x : (int)(__umulhi((uint32_t)x, a.g_magic) >> (a.g_shift - 1));
+}
+
+// A sequence's share of the list.
 struct Share {
   Rows rows;
   int tiles;          // of a key head
   int first, pages;   // first page that a row may see; how many from there
-  int64_t units;
+  __device__ __forceinline__ Share() {}
   __device__ __forceinline__ Share(const AttendArgs& a, int b) {
     rows = rows_of(a.seq, b);
-    tiles = (rows.n * a.G + a.rows - 1) / a.rows;
+    tiles = (rows.n * a.G + a.rows - 1) / a.rows;   // a.rows: a power of two
     const int64_t most = (int64_t)a.seq.W * LOWM_PAGE;
     const int tokens = rows.len < most ? rows.len : (int)most;
     const int64_t from = (int64_t)rows.len - rows.n - a.window + 1;
     first = a.window > 0 && from > 0 ? (int)(from / LOWM_PAGE) : 0;
     pages = (tokens + LOWM_PAGE - 1) / LOWM_PAGE - first;
     if (pages < 0) pages = 0;
-    units = (int64_t)a.cache.H * tiles * (pages + kTileCost);
+  }
+  // The share of the wavefront's lane `from`.
+  __device__ __forceinline__ Share of_lane(int from) const {
+    auto get = [&](int v) { return __builtin_amdgcn_readlane(v, from); };
+    Share s;
+    s.rows = Rows{get(rows.first), get(rows.n), get(rows.len)};
+    s.tiles = get(tiles);
+    s.first = get(first);
+    s.pages = get(pages);
+    return s;
   }
 };
 
-__device__ __forceinline__ int64_t wave_scan64(int64_t v) {
-  uint64_t x = (uint64_t)v;
-  auto add = [&](auto move) {
-    const uint32_t lo = move((uint32_t)x), hi = move((uint32_t)(x >> 32));
-    x += (uint64_t)hi << 32 | lo;
-  };
-  add([](uint32_t w) { return lane_move<0x111, 0xf>(w); });
-  add([](uint32_t w) { return lane_move<0x112, 0xf>(w); });
-  add([](uint32_t w) { return lane_move<0x114, 0xf>(w); });
-  add([](uint32_t w) { return lane_move<0x118, 0xf>(w); });
-  add([](uint32_t w) { return lane_move<0x142, 0xa>(w); });
-  add([](uint32_t w) { return lane_move<0x143, 0xc>(w); });
-  return (int64_t)x;
-}
-__device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane),
-                 hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), lane);
-  return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
-// The whole list, as every wavefront sums it for itself, 64 sequences at a time.
+// The list: every sequence's tiles, head after head, and how they are cut into runs, one
+// to a workgroup.  Where there are workgroups enough, each tile is cut by itself
+// (`apart`): into parts of 2^per_log pages, a unit each, or none if it is small, and a
+// run is a unit.  Else a tile is kTileCost units that stand for no page and then its
+// pages, and all tiles are one list of equal runs, which may end inside a tile.  Every
+// wavefront works that out for itself, 64 sequences at a time.  The host sees to it that
+// 32 bits hold the units.
 struct List {
-  int64_t total;
-  int64_t own, upto;     // of sequence `lane`, and up to it (the only step of up to 64)
+  int total, run, per_log, small, lane;
+  bool apart;
+  Share own;                         // of sequence `lane` (of the last 64)
+  __device__ __forceinline__ int parts(int pages, int log) const {
+    const int alone = small > 1 << log ? small : 1 << log;
+    return pages <= alone ? 1 : (pages + (1 << log) - 1) >> log;
+  }
   __device__ __forceinline__ explicit List(const AttendArgs& a) {
-    const int lane = threadIdx.x & (kWave - 1);
-    total = 0;
+    lane = threadIdx.x & (kWave - 1);
+    small = a.small;
+    int units = 0, runs[2] = {};   // for parts of 8 and of 16 pages
+    float rows = 0.f;
     for (int at = 0; at < a.seq.B; at += kWave) {
-      own = at + lane < a.seq.B ? Share(a, at + lane).units : 0;
-      upto = wave_scan64(own);
-      total += lane_value(upto, kWave - 1);
+      own = Share(a, at + lane < a.seq.B ? at + lane : a.seq.B - 1);
+      const int tiles = at + lane < a.seq.B ? a.cache.H * own.tiles : 0;
+      auto all = [&](int v) { return __builtin_amdgcn_readlane(wave_scan(v), kWave - 1); };
+      units += all(tiles * (own.pages + kTileCost));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) runs[i] += all(tiles * parts(own.pages, 3 + i));
+      rows += wave_sum(at + lane < a.seq.B ? (float)own.rows.n : 0.f);
     }
+    // row_starts that fall may count rows twice, and more units than 32 bits hold
+    if (rows > 1.001f * (float)a.seq.T) units = runs[0] = 0;
+    per_log = runs[0] <= a.groups ? 3 : a.most_log;
+    apart = runs[per_log - 3] <= a.groups;
+    run = apart ? 1 : ((units + a.groups - 1) / a.groups + a.turn - 1) & ~(a.turn - 1);
+    total = apart ? runs[per_log - 3] : units;
   }
-  // Units of a workgroup's run: whole turns.
-  __device__ __forceinline__ int64_t run(const AttendArgs& a) const {
-    const int64_t r = (total + (1 << a.groups_log) - 1) >> a.groups_log;
-    return (r + a.turn - 1) & ~(int64_t)(a.turn - 1);
+  // Units from one tile to the next.
+  __device__ __forceinline__ int span(const Share& s) const {
+    return apart ? parts(s.pages, per_log) : s.pages + kTileCost;
   }
-  // The sequence that unit u belongs to, and the first of its units.
-  __device__ __forceinline__ int find(const AttendArgs& a, int64_t u, int64_t* start) const {
-    const int lane = threadIdx.x & (kWave - 1);
-    int64_t before = 0, mine = own, sum = upto;
+  // The sequence that unit u belongs to, the first of its units, and its share.
+  __device__ __forceinline__ int find(const AttendArgs& a, int u, int* start, Share* s) const {
+    int before = 0;
     for (int at = 0; at < a.seq.B; at += kWave) {
-      if (a.seq.B > kWave) {
-        mine = at + lane < a.seq.B ? Share(a, at + lane).units : 0;
-        sum = wave_scan64(mine);
-      }
-      const int64_t all = lane_value(sum, kWave - 1);
+      Share mine = own;
+      if (a.seq.B > kWave) mine = Share(a, at + lane < a.seq.B ? at + lane : a.seq.B - 1);
+      const int units = at + lane < a.seq.B ? a.cache.H * mine.tiles * span(mine) : 0;
+      const int sum = wave_scan(units);
+      const int all = __builtin_amdgcn_readlane(sum, kWave - 1);
       if (u - before < all) {
         const int first = __builtin_ctzll(__ballot(sum > u - before));
-        *start = before + lane_value(sum - mine, first);
+        *start = before + __builtin_amdgcn_readlane(sum - units, first);
+        *s = mine.of_lane(first);
         return at + first;
       }
       before += all;
@@ -159,7 +186,7 @@ struct List {
 
 // Where the unfinished sums of a tile that run w has a part of are: of the one tile that
 // an earlier run began, or of the one that this run begins and a later one ends.
-__device__ __forceinline__ int place_of(int64_t w, bool begun) { return 2 * (int)w + !begun; }
+__device__ __forceinline__ int place_of(int w, bool begun) { return 2 * w + !begun; }
 
 __device__ __forceinline__ float bits_float(uint32_t b) { return __builtin_bit_cast(float, b); }
 __device__ __forceinline__ uint32_t float_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
@@ -251,7 +278,7 @@ __device__ __forceinline__ bool arrive(int* count, int n, int* lds) {
 struct TileRows {
   int row0, last_row, head, first;   // first row of the tile, last of the sequence's
   __device__ __forceinline__ int64_t at(const AttendArgs& a, int r) const {
-    const int j = (row0 + r) / a.G;
+    const int j = by_g(a, row0 + r);
     return (int64_t)(first + j) * a.Hq + head * a.G + (row0 + r - j * a.G);
   }
 };
@@ -285,13 +312,13 @@ __device__ __forceinline__ void leave(const AttendArgs& a, int place, int r, int
 
 // m places' sums joined: place i is of run w + i * step, of the tile that it begins
 // (w + i * step == w0) or of the one it continues.  To the rows, or to place 0.
-__device__ void join(const AttendArgs& a, const TileRows& rows, int64_t w0, int64_t w, int step,
+__device__ void join(const AttendArgs& a, const TileRows& rows, int w0, int w, int step,
                      int m, bool last, float* lds) {
   const int n = rows.last_row - rows.row0 + 1 < a.rows ? rows.last_row - rows.row0 + 1 : a.rows;
   const int D = a.cache.D;
   float *most = lds, *sum = lds + kJoin * a.rows;
   auto at = [&](int i, int r) {
-    const int64_t run = w + (int64_t)i * step;
+    const int run = w + i * step;
     return (int64_t)place_of(run, run > w0) * a.rows + r;
   };
   for (int i = threadIdx.x; i < m * n; i += kThreads) {
@@ -351,102 +378,124 @@ struct Note {
 
 // A workgroup's run of the list, part of a tile after part of a tile.
 struct Walk {
-  List list;
-  int64_t run, w, u, end, start;   // its units are u .. end - 1; start: of sequence b
+  int total, run, per_log, w, u, end, start;   // its units are u .. end - 1; start: of b
+  bool apart;
   int b;
+  Share s;                         // of sequence b
   // the part of a tile at hand
-  Rows seq;
   TileRows rows;
-  int first, pages_all;            // of the sequence: first page, and pages, of a tile
-  int page_at, pages;              // of those, this part's
-  int64_t first_page;              // unit of the tile's first page
+  int page_at, pages;              // of the tile's pages, this part's
+  int w0, n;                       // the runs that share the tile: w0 .. w0 + n - 1
   int low, high;                   // positions of the tile's first and last row
   bool noted;                      // whether the run's note is written, or there is no run
 
-  __device__ __forceinline__ explicit Walk(const AttendArgs& a) : list(a) {
-    run = list.run(a);
+  __device__ __forceinline__ explicit Walk(const AttendArgs& a) {
+    const List list(a);
+    total = list.total;
+    run = list.run;
+    per_log = list.per_log;
+    apart = list.apart;
     // runs that have units, an eighth of them to each XCD: neighbours, which may share a
     // head's pages, share an L2
-    const int64_t runs = (list.total + run - 1) / (run > 0 ? run : 1);
-    w = (blockIdx.x % 8) * ((runs + 7) / 8) + blockIdx.x / 8;
+    const int runs = apart ? total : run > 0 ? (total + run - 1) / run : 0;
+    const int each = (runs + 7) / 8;
+    w = (blockIdx.x % 8) * each + blockIdx.x / 8;
     u = w * run;
-    end = u + run < list.total ? u + run : list.total;
-    if ((int64_t)blockIdx.x / 8 >= (runs + 7) / 8) u = end;   // the next XCD's runs
+    end = u + run < total ? u + run : total;
+    if ((int)blockIdx.x / 8 >= each || w >= runs) u = end = 0;
     noted = u >= end;
-    b = u < end ? list.find(a, u, &start) : 0;
+    if (u >= end) return;
+    b = list.find(a, u, &start, &s);
+    if (b >= a.seq.B) u = end;
+    if (apart) {
+      // the only part there is
+      const int span = list.span(s);
+      const int tile_at = (int)((uint32_t)(u - start) / (uint32_t)span);
+      const int part = u - start - tile_at * span;
+      w0 = w - part;
+      n = span;
+      page_at = part << per_log;
+      pages = n == 1 || s.pages - page_at < 1 << per_log ? s.pages - page_at : 1 << per_log;
+      take(a, tile_at);
+    }
+  }
+  // The tile's rows.
+  __device__ __forceinline__ void take(const AttendArgs& a, int tile_at) {
+    const int head = (int)((uint32_t)tile_at / (uint32_t)s.tiles), tile = tile_at - head * s.tiles;
+    rows = TileRows{tile * a.rows, s.rows.n * a.G - 1, head, s.rows.first};
+    const int last = rows.row0 + a.rows - 1 < rows.last_row ? rows.row0 + a.rows - 1 : rows.last_row;
+    low = s.rows.position(by_g(a, rows.row0));
+    high = s.rows.position(by_g(a, last));
+  }
+  __device__ __forceinline__ void zeros(const AttendArgs& a) const {
+    const int quads = a.cache.D / 4;
+    for (int i = threadIdx.x; i < a.rows * quads; i += blockDim.x)
+      if (rows.row0 + i / quads <= rows.last_row)
+        finish(a, rows, i / quads, i % quads * 4, -__builtin_inff(), 0.f, f32x4{0.f, 0.f, 0.f, 0.f});
   }
   // The next part that has pages; rows of sequences without any get their zeros here.
   __device__ __forceinline__ bool next(const AttendArgs& a) {
     while (u < end) {
-      const Share s(a, b);
-      if (u - start >= s.units) {
-        start += s.units;
-        ++b;
+      if (apart) {
+        ++u;
+        if (pages > 0) return true;
+        zeros(a);
+        return false;
+      }
+      const int span = s.pages + kTileCost;
+      if ((uint32_t)(u - start) >= (uint32_t)(a.cache.H * s.tiles * span)) {
+        start += a.cache.H * s.tiles * span;
+        if (++b >= a.seq.B) return false;
+        s = Share(a, b);
         continue;
       }
-      const int64_t tile_at = (u - start) / (s.pages + kTileCost);
-      const int64_t tile_start = start + tile_at * (s.pages + kTileCost);
-      const int from = (int)(u - tile_start);
-      const int64_t room = end - u;
-      const int units = s.pages + kTileCost - from < room ? s.pages + kTileCost - from : (int)room;
-      u += units;
+      const int tile_at = (int)((uint32_t)(u - start) / (uint32_t)span);
+      const int from = u - start - tile_at * span;
+      const int to = from + end - u < span ? from + end - u : span;
+      const int first_page = u - from + kTileCost;   // unit of the tile's first page
+      u += to - from;
       page_at = from > kTileCost ? from - kTileCost : 0;
-      pages = from + units - kTileCost - page_at;
-      const int head = (int)(tile_at / s.tiles), tile = (int)(tile_at - (int64_t)head * s.tiles);
-      rows = TileRows{tile * a.rows, s.rows.n * a.G - 1, head, s.rows.first};
+      pages = to - kTileCost - page_at;
+      take(a, tile_at);
       if (pages > 0) {
-        seq = s.rows;
-        first = s.first;
-        pages_all = s.pages;
-        first_page = tile_start + kTileCost;
-        const int last = rows.row0 + a.rows - 1 < rows.last_row ? rows.row0 + a.rows - 1
-                                                                 : rows.last_row;
-        low = seq.position(rows.row0 / a.G);
-        high = seq.position(last / a.G);
+        w0 = first_page / run;
+        n = (first_page + s.pages - 1) / run - w0 + 1;
         return true;
       }
       // whoever has the first unit of a tile without pages writes its rows
-      if (s.pages == 0 && from == 0) {
-        const int quads = a.cache.D / 4;
-        for (int i = threadIdx.x; i < a.rows * quads; i += blockDim.x)
-          if (rows.row0 + i / quads <= rows.last_row)
-            finish(a, rows, i / quads, i % quads * 4, -__builtin_inff(), 0.f,
-                   f32x4{0.f, 0.f, 0.f, 0.f});
-      }
+      if (s.pages == 0 && from == 0) zeros(a);
     }
     return false;
   }
   __device__ __forceinline__ const int* table(const AttendArgs& a) const {
-    return a.seq.table + b * a.seq.table_ld + first;
+    return a.seq.table + b * a.seq.table_ld + s.first;
   }
   // Where this part stops for rows up to position `high`: pages past it are not seen.
   __device__ __forceinline__ int stop(int high) const {
-    const int seen = high < 0 ? 0 : high / LOWM_PAGE + 1 - first;
+    const int seen = high < 0 ? 0 : high / LOWM_PAGE + 1 - s.first;
     return page_at + pages < seen ? page_at + pages : seen;
   }
-  __device__ __forceinline__ bool whole() const { return page_at == 0 && pages == pages_all; }
-  __device__ __forceinline__ int place() const { return place_of(w, page_at > 0); }
+  __device__ __forceinline__ bool whole() const { return n == 1; }
+  __device__ __forceinline__ int place() const { return place_of(w, w > w0); }
 
   // Leaves the run's note: of the tile at hand if it begins here and ends elsewhere, in
   // any case before the workgroup ends.
   __device__ __forceinline__ void note(const AttendArgs& a, bool last_call) {
     if (blockIdx.x == 0 && last_call && threadIdx.x == 0)
-      a.notes[0] = run > 0 ? (int)((list.total + run - 1) / run) : 0;
+      a.notes[0] = run > 0 ? (total + run - 1) / run : 0;
     if (noted) return;
-    if (!last_call && (page_at > 0 || whole())) return;
+    if (!last_call && (w > w0 || whole())) return;
     noted = true;
     if (threadIdx.x != 0) return;
-    Note n{0, rows};
-    if (!last_call) n.parts = (int)((first_page + pages_all - 1) / run - first_page / run) + 1;
-    *reinterpret_cast<Note*>(a.notes + 8 * (1 + w)) = n;
+    Note mine{0, rows};
+    if (!last_call) mine.parts = n;
+    *reinterpret_cast<Note*>(a.notes + 8 * (1 + w)) = mine;
   }
   // After the sums of a part that is not whole are in their place: the runs that share
   // the tile, in groups of kGroup, and then the groups.
   __device__ __forceinline__ void share(const AttendArgs& a, int* arrived, float* lds) const {
-    const int64_t w0 = first_page / run;
-    const int n = (int)((first_page + pages_all - 1) / run - w0) + 1;
-    const int group = (int)(w - w0) / kGroup, groups = (n + kGroup - 1) / kGroup;
-    const int64_t leader = w0 + group * kGroup;
+    const int group = (w - w0) / kGroup, groups = (n + kGroup - 1) / kGroup;
+    const int leader = w0 + group * kGroup;
     const int members = n - group * kGroup < kGroup ? n - group * kGroup : kGroup;
     if (!arrive(a.counts + place_of(leader, group > 0), members, arrived)) return;
     join(a, rows, w0, leader, 1, members, groups == 1, lds);
@@ -471,11 +520,11 @@ struct Queries {
     for (int t = 0; t < RT; ++t) {
       const int r = row0 + 16 * t + col;
       const int in = r <= walk.rows.last_row ? r : walk.rows.last_row;
-      const int j = in / a.G, h = walk.rows.head * a.G + (in - j * a.G);
-      const int pos = walk.seq.position(j);
+      const int j = by_g(a, in), h = walk.rows.head * a.G + (in - j * a.G);
+      const int pos = walk.s.rows.position(j);
       see_hi[t] = r <= walk.rows.last_row ? pos : -1;
       see_lo[t] = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-      const uint16_t* x = a.q + (walk.seq.first + j) * a.q_row + h * a.q_head;
+      const uint16_t* x = a.q + (walk.s.rows.first + j) * a.q_row + h * a.q_head;
       ops_u32x4 raw[2 * DP];
       uint32_t top = 0;
 #pragma unroll
@@ -719,9 +768,9 @@ void attend_kernel(AttendArgs a) {
     Softmax<NT, RT> sm;
 
     for (; at < stop; at += kWaves) {
-      const int token0 = (walk.first + at) * LOWM_PAGE;
+      const int token0 = (walk.s.first + at) * LOWM_PAGE;
       // tokens of the page that are there at all
-      int live = walk.seq.len - token0;
+      int live = walk.s.rows.len - token0;
       live = page < 0 ? 0 : live < LOWM_PAGE ? live : LOWM_PAGE;
       const float ks = live > 0 ? first_lane(k_scale) : 0.f, vs = live > 0 ? first_lane(v_scale) : 0.f;
       load_vals();
@@ -866,8 +915,8 @@ void attend_wide_kernel(AttendArgs a) {
     const int last = row0 + 16 * RT - 1 < walk.rows.last_row ? row0 + 16 * RT - 1
                                                              : walk.rows.last_row;
     const bool mine = row0 <= walk.rows.last_row;
-    const int low = mine ? walk.seq.position(row0 / a.G) : -1,
-              high = mine ? walk.seq.position(last / a.G) : -1;
+    const int low = mine ? walk.s.rows.position(by_g(a, row0)) : -1,
+              high = mine ? walk.s.rows.position(by_g(a, last)) : -1;
     const int high_lo = a.window > 0 && high >= a.window ? high - a.window + 1 : 0;
     const int low_lo = a.window > 0 && low >= a.window ? low - a.window + 1 : 0;
 
@@ -889,7 +938,7 @@ void attend_wide_kernel(AttendArgs a) {
                                                                from * (LOWM_PAGE * D));
       const ops_u32x4* pv = reinterpret_cast<const ops_u32x4*>(static_cast<const uint8_t*>(c.v) +
                                                                from * (LOWM_PAGE * D));
-      const int live = walk.seq.len - (walk.first + at) * LOWM_PAGE;
+      const int live = walk.s.rows.len - (walk.s.first + at) * LOWM_PAGE;
       on_way[half].live = !some ? 0 : live < LOWM_PAGE ? live : LOWM_PAGE;
       on_way[half].ks = load_apart(c.k_scale + from);
       on_way[half].vs = load_apart(c.v_scale + from);
@@ -938,7 +987,7 @@ void attend_wide_kernel(AttendArgs a) {
     }
     auto turn = [&](auto half_c, auto other, int at) {
       constexpr int half = decltype(half_c)::value;
-      const int token0 = (walk.first + at) * LOWM_PAGE;
+      const int token0 = (walk.s.first + at) * LOWM_PAGE;
       // wavefronts whose rows do not see the page only pass it on
       if (mine && token0 <= high && token0 + LOWM_PAGE > low_lo) {
         f32x4 x[RT][4];
@@ -1047,7 +1096,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
   for (int item = blockIdx.x * kWaves + (int)threadIdx.x / kWave; item < tiles * per;
        item += kWaves * gridDim.x) {
     int skip = item / per;
-    int64_t w0 = 0;
+    int w0 = 0;
 #pragma unroll
     for (int k = 0; k < kSets; ++k) {
       const int here = __builtin_popcountll(begun[k]);
@@ -1173,6 +1222,9 @@ int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
       if (meet(out[i], out[k])) return LOWM_ERR_INVALID_ARG;
   }
   const Kind kind = kind_for(s.T, G, s.B);
+  // units of the list (see List), at most
+  if ((rows / c.H / kind + s.B + 1) * c.H * (s.W + kTileCost + 64) > INT32_MAX / 2)
+    return LOWM_ERR_UNSUPPORTED;
   AttendArgs a{};
   a.cache = c;
   a.seq = s;
@@ -1181,8 +1233,13 @@ int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
   a.lse = u->lse;
   a.rows = kind;
   // one workgroup to a CU where its registers and LDS leave no room for two
-  a.groups_log = kind >= kMore && c.D > 128 ? 8 : 9;
+  a.groups = kind >= kMore && c.D > 128 ? kGroups / 2 : kGroups;
   a.turn = kind >= kMore ? 1 : kWaves;
+  a.small = kind >= kMore ? 8 : 12;
+  a.most_log = kind >= kMore ? 3 : 4;
+  const Divisor g(G);
+  a.g_magic = g.magic;
+  a.g_shift = g.shift;
   a.counts = static_cast<int*>(u->workspace);
   a.notes = a.counts + 4 * kGroups;
   a.stats = reinterpret_cast<float*>(a.notes + 8 * (1 + kGroups));
@@ -1195,7 +1252,7 @@ int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
   a.scale = u->scale * kLog2e;
   void* args[] = {&a};
   rc = launched(hipLaunchKernel(kernel_for(c.D, kind, c.type == LOWM_E4M3),
-                                dim3(1u << a.groups_log), dim3(kWave * waves_for(kind, c.D)), args,
+                                dim3((unsigned)a.groups), dim3(kWave * waves_for(kind, c.D)), args,
                                 0, stream));
   if (rc != LOWM_OK || kind == kFew) return rc;
   return launched(hipLaunchKernel((const void*)&join_kernel,

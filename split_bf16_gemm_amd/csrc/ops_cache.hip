@@ -57,7 +57,7 @@ __device__ __forceinline__ Touched page_of(const lowm_sequences& s, int P, int i
   }
   t.rows = rows_of(s, b);
   const Stretch all(s, t.rows);
-  if (nth >= all.pages()) return t;
+  if (nth < 0 || nth >= all.pages()) return t;
   const int p = all.lo / LOWM_PAGE + nth;
   t.begin = p * LOWM_PAGE;
   t.lo = all.lo > t.begin ? all.lo : t.begin;
