@@ -5,7 +5,9 @@
 //   read:    bf16(q s)
 //
 // A workgroup owns one head of one page, its keys or its values, so nothing it
-// reads or writes is another's.  A thread holds four tokens by eight elements:
+// reads or writes is another's: 256 threads for long rows of a sequence, a wavefront
+// where a page gets a token or two (61 sequences of one token: as many workgroups, a
+// quarter of the wavefronts to start).  A thread holds four tokens by eight elements:
 // keys go straight to their pieces of 16 elements, values are turned in LDS into
 // pieces of 16 tokens, whose rows of bytes are padded so that the lanes' words lie
 // in distinct banks.  A page that is being filled token by token keeps its bytes
@@ -17,7 +19,6 @@
 namespace lowm {
 namespace {
 
-constexpr int kThreads = 256;
 
 // The page of a sequence that a workgroup serves, by its number among the pages
 // that the call's rows touch.
@@ -72,7 +73,7 @@ __device__ __forceinline__ Touched page_of(const lowm_sequences& s, int P, int i
 __device__ __forceinline__ int turned(int D, int group, int d) {   // in words
   return (group * (D + D / 8) + d + d / 8) * 4;
 }
-constexpr int turned_words(int D) { return 4 * (D + D / 8) * 4; }
+inline int turned_words(int D) { return 4 * (D + D / 8) * 4; }
 
 struct Levels {
   float scale;
@@ -120,13 +121,14 @@ struct AppendArgs {
   int first_item;
 };
 
-// Q quads of four tokens by eight elements to a thread.
-template <int Q>
-__global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
+// Q items, each four tokens by eight elements, stay in a thread's registers; where a page
+// has more of them they are read a second time.
+template <int Q, int THREADS>
+__global__ __launch_bounds__(THREADS) void append_kernel(AppendArgs a) {
   const lowm_cache_append_args& u = a.u;
   const lowm_kv_cache& c = u.cache;
-  __shared__ uint32_t tops[kThreads / kWave];
-  __shared__ __align__(16) uint32_t turn[turned_words(128 * Q)];
+  __shared__ uint32_t tops[THREADS / kWave];
+  extern __shared__ __align__(16) uint32_t turn[];
   const Touched t = page_of(u.seq, c.P, a.first_item + (int)blockIdx.x, a.uniform_pages);
   if (t.page < 0) return;
   const int head = blockIdx.y, D = c.D, chunks = D / 8;
@@ -146,36 +148,42 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   const int first_quad = lo / 4, items = ((hi + 3) / 4 - first_quad) * chunks;
   Raw8 raw[Q][4];
   int tok[Q], el[Q];
+  auto load = [&](int first) {
 #pragma unroll
-  for (int i = 0; i < Q; ++i) {
-    const int at = (int)threadIdx.x + i * kThreads;
-    const int in = at < items ? at : 0;
-    tok[i] = (first_quad + in / chunks) * 4;
-    el[i] = in % chunks * 8;
+    for (int i = 0; i < Q; ++i) {
+      const int at = first + (int)threadIdx.x + i * THREADS;
+      const int in = at < items ? at : 0;
+      tok[i] = (first_quad + in / chunks) * 4;
+      el[i] = in % chunks * 8;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = tok[i] + j;
-      raw[i][j] = load8(x, (row0 + (k < lo ? lo : k >= hi ? hi - 1 : k)) * x_row + x_at + el[i], f32);
-    }
-  }
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < Q; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float v[8];
-      values8(raw[i][j], f32, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, v[e]) & 0x7fffffffu;
-        top = b > top ? b : top;   // repeated tokens change nothing
+      for (int j = 0; j < 4; ++j) {
+        const int k = tok[i] + j;
+        raw[i][j] =
+            load8(x, (row0 + (k < lo ? lo : k >= hi ? hi - 1 : k)) * x_row + x_at + el[i], f32);
       }
     }
+  };
+  uint32_t top = 0;
+  for (int first = 0; first < items; first += Q * THREADS) {
+    load(first);
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[8];
+        values8(raw[i][j], f32, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t b = __builtin_bit_cast(uint32_t, v[e]) & 0x7fffffffu;
+          top = b > top ? b : top;   // repeated tokens change nothing
+        }
+      }
+  }
   top = wave_umax(top);
   if ((threadIdx.x & (kWave - 1)) == 0) tops[threadIdx.x / kWave] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / kWave; ++w) top = tops[w] > top ? tops[w] : top;
+  for (int w = 0; w < THREADS / kWave; ++w) top = tops[w] > top ? tops[w] : top;
   float now = top < 0x7f800000u ? __builtin_bit_cast(float, top) / (e4m3 ? 448.f : 127.f)
                                 : __builtin_nanf("");
   if (lo > 0) now = before != before ? before : before > now ? before : now;
@@ -184,41 +192,55 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   const float ratio = grown ? before / now : 1.f;
   if (threadIdx.x == 0) *scale_at = now;
 
+  for (int first = 0; first < items; first += Q * THREADS) {
+    if (items > Q * THREADS) load(first);
 #pragma unroll
-  for (int i = 0; i < Q; ++i) {
-    if ((int)threadIdx.x + i * kThreads >= items) break;
-    uint32_t q[4][2];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float v[8];
-      values8(raw[i][j], f32, v);
-      q[j][0] = levels.of(v[0], v[1], v[2], v[3]);
-      q[j][1] = levels.of(v[4], v[5], v[6], v[7]);
-    }
-    if (!values) {
+    for (int i = 0; i < Q; ++i) {
+      if (first + (int)threadIdx.x + i * THREADS >= items) break;
+      uint32_t q[4][2];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int k = tok[i] + j;
-        if (k >= lo && k < hi)
-          *reinterpret_cast<ops_u32x2*>(out + (el[i] / 16 * LOWM_PAGE + k) * 16 + el[i] % 16) =
-              ops_u32x2{q[j][0], q[j][1]};
+        float v[8];
+        values8(raw[i][j], f32, v);
+        q[j][0] = levels.of(v[0], v[1], v[2], v[3]);
+        q[j][1] = levels.of(v[4], v[5], v[6], v[7]);
       }
-    } else {
+      if (!values) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint32_t w = 0;
+        for (int j = 0; j < 4; ++j) {
+          const int k = tok[i] + j;
+          if (k >= lo && k < hi)
+            *reinterpret_cast<ops_u32x2*>(out + (el[i] / 16 * LOWM_PAGE + k) * 16 + el[i] % 16) =
+                ops_u32x2{q[j][0], q[j][1]};
+        }
+      } else if (!grown && hi - lo == 1) {
+        // one more token of a page that keeps its scale: a byte an element
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w |= (q[j][e / 4] >> 8 * (e % 4) & 255u) << 8 * j;
-        turn[turned(D, tok[i] / 16, el[i] + e) + tok[i] % 16 / 4] = w;
+        for (int e = 0; e < 8; ++e) {
+          uint8_t b = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (tok[i] + j == lo) b = (uint8_t)(q[j][e / 4] >> 8 * (e % 4));
+          out[(lo / 16 * D + el[i] + e) * 16 + lo % 16] = b;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t w = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w |= (q[j][e / 4] >> 8 * (e % 4) & 255u) << 8 * j;
+          turn[turned(D, tok[i] / 16, el[i] + e) + tok[i] % 16 / 4] = w;
+        }
       }
     }
   }
+  if (values && !grown && hi - lo == 1) return;
 
   ops_u32x4* pieces = reinterpret_cast<ops_u32x4*>(out);
   if (!values) {
     if (grown) {
       // earlier tokens of the keys: a piece each
-      for (int at = threadIdx.x; at < D / 16 * lo; at += kThreads) {
+      for (int at = threadIdx.x; at < D / 16 * lo; at += THREADS) {
         const int p = at / lo * LOWM_PAGE + at % lo;
         ops_u32x4 w = pieces[p];
 #pragma unroll
@@ -231,7 +253,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   __syncthreads();
   // pieces of the values: whole ones are written, others are merged
   const int first = grown ? 0 : lo / 16;
-  for (int at = threadIdx.x; at < ((hi + 15) / 16 - first) * D; at += kThreads) {
+  for (int at = threadIdx.x; at < ((hi + 15) / 16 - first) * D; at += THREADS) {
     const int g = first + at / D, d = at % D;
     const int from = lo - 16 * g, to = hi - 16 * g;   // new tokens of the piece
     ops_u32x4 w = {0u, 0u, 0u, 0u};
@@ -258,11 +280,11 @@ struct ReadArgs {
   int first_item;
 };
 
-template <int Q>
-__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void read_kernel(ReadArgs a) {
   const lowm_cache_read_args& u = a.u;
   const lowm_kv_cache& c = u.cache;
-  __shared__ __align__(16) uint32_t turn[turned_words(128 * Q)];
+  extern __shared__ __align__(16) uint32_t turn[];
   const Touched t = page_of(u.seq, c.P, a.first_item + (int)blockIdx.x, a.uniform_pages);
   if (t.page < 0) return;
   const int head = blockIdx.y, D = c.D, chunks = D / 8;
@@ -284,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
     store8(out, ((row0 + k) * c.H + head) * D + d, false, x);
   };
   if (!values) {
-    for (int at = threadIdx.x; at < (hi - lo) * chunks; at += kThreads) {
+    for (int at = threadIdx.x; at < (hi - lo) * chunks; at += THREADS) {
       const int k = lo + at / chunks, d = at % chunks * 8;
       const ops_u32x2 w = *reinterpret_cast<const ops_u32x2*>(
           in + (d / 16 * LOWM_PAGE + k) * 16 + d % 16);
@@ -294,13 +316,13 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
   }
   const ops_u32x4* pieces = reinterpret_cast<const ops_u32x4*>(in);
   const int first = lo / 16;
-  for (int at = threadIdx.x; at < ((hi + 15) / 16 - first) * D; at += kThreads) {
+  for (int at = threadIdx.x; at < ((hi + 15) / 16 - first) * D; at += THREADS) {
     const int g = first + at / D, d = at % D;
     *reinterpret_cast<ops_u32x4*>(&turn[turned(D, g, d)]) = pieces[g * D + d];
   }
   __syncthreads();
   const int first_quad = lo / 4, items = ((hi + 3) / 4 - first_quad) * chunks;
-  for (int at = threadIdx.x; at < items; at += kThreads) {
+  for (int at = threadIdx.x; at < items; at += THREADS) {
     const int k = (first_quad + at / chunks) * 4, d = at % chunks * 8;
     uint32_t w[8];
 #pragma unroll
@@ -320,9 +342,10 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
 }
 
 // Page-by-head workgroups, keys and values: no more pages than rows, and no more
-// than the rows fill with two more for each sequence.
+// than the rows fill with two more for each sequence.  `one`: of a wavefront, for up to
+// two rows a sequence on average; `four`: of four.
 template <typename A>
-int launch_pages(const void* one, const void* two, A a, const lowm_sequences& s,
+int launch_pages(const void* one, const void* four, A a, const lowm_sequences& s,
                  const lowm_kv_cache& c, hipStream_t stream) {
   int64_t items;
   if (!s.row_starts) {
@@ -335,15 +358,17 @@ int launch_pages(const void* one, const void* two, A a, const lowm_sequences& s,
     items = (int64_t)s.T / LOWM_PAGE + 2 * (int64_t)s.B;
     if (items > s.T) items = s.T;
   }
-  const int64_t most = kMaxThreads / kThreads / (2 * c.H);
+  const bool few = s.T <= 2 * (int64_t)s.B;
+  const int threads = few ? kWave : 4 * kWave;
+  const int64_t most = kMaxThreads / threads / (2 * c.H);
   void* args[] = {&a};
   int rc = LOWM_OK;
   for (int64_t i = 0; i < items && rc == LOWM_OK; i += most) {
     a.first_item = (int)i;
-    rc = launched(hipLaunchKernel(c.D > 128 ? two : one,
+    rc = launched(hipLaunchKernel(few ? one : four,
                                   dim3((unsigned)(items - i < most ? items - i : most),
                                        (unsigned)c.H, 2),
-                                  dim3(kThreads), args, 0, stream));
+                                  dim3(threads), args, 4 * turned_words(c.D), stream));
   }
   return rc;
 }
@@ -372,7 +397,9 @@ int cache_append(const lowm_cache_append_args* u, hipStream_t stream) {
     if (cs.meets(x)) return LOWM_ERR_INVALID_ARG;
   for (const Span& x : cs.s)
     if (ss.meets(x)) return LOWM_ERR_INVALID_ARG;
-  return launch_pages((const void*)&append_kernel<1>, (const void*)&append_kernel<2>,
+  return launch_pages((const void*)&append_kernel<1, kWave>,
+                      c.D > 128 ? (const void*)&append_kernel<2, 4 * kWave>
+                                : (const void*)&append_kernel<1, 4 * kWave>,
                       AppendArgs{*u, 0, 0}, u->seq, c, stream);
 }
 
@@ -392,7 +419,7 @@ int cache_read(const lowm_cache_read_args* u, hipStream_t stream) {
   const SequenceSpans ss(u->seq);
   if (meet(k, v) || cs.meets(k) || cs.meets(v) || ss.meets(k) || ss.meets(v))
     return LOWM_ERR_INVALID_ARG;
-  return launch_pages((const void*)&read_kernel<1>, (const void*)&read_kernel<2>,
+  return launch_pages((const void*)&read_kernel<kWave>, (const void*)&read_kernel<4 * kWave>,
                       ReadArgs{*u, 0, 0}, u->seq, c, stream);
 }
 

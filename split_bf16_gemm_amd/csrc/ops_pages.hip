@@ -5,8 +5,9 @@
 // Whole numbers and copies.  Counting how often each page is used goes over the
 // table with one atomic addition an entry, whose order does not matter; which page
 // goes where is decided by one workgroup, from prefix sums over the rows and over
-// the pages in ascending order, so that the same tables give the same pages.  Then
-// all workgroups copy: a page of a layer is one run of bytes for the keys and one for
+// the pages in ascending order, so that the same tables give the same pages.  Small
+// tables go through that workgroup whole, with the counts in LDS, instead of three
+// launches (8 rows: 14.6 us, 8.x so).  Then all workgroups copy: a page of a layer is one run of bytes for the keys and one for
 // the values, in units of kUnit bytes.
 #include "ops_cache.cuh"
 
@@ -16,6 +17,8 @@ namespace {
 constexpr int kOne = 1024;            // threads of the workgroup that decides
 constexpr int kWaves = kOne / kWave;
 constexpr int kPer = 4;               // pages, or rows, to a thread and step
+constexpr int kSmallP = 4096;         // pages whose counts fit its LDS,
+constexpr int kSmallEntries = 16384;  // and entries of a table that it goes through alone
 constexpr int kUnit = 16384;          // bytes copied by a workgroup at a time
 
 // The workspace: 32-bit words.
@@ -66,13 +69,21 @@ __device__ __forceinline__ int held_of(const PagesArgs& a, int p) {
   return a.held && a.held[p] > 0 ? a.held[p] : 0;
 }
 
+// Uses of each page, and for forking who has it as an unfinished last page: in the
+// workspace and refs_out, or in LDS.
+struct Counts {
+  int *refs, *owner, *parts;
+};
+__device__ __forceinline__ void begin_page(const PagesArgs& a, const Counts& n, int p) {
+  n.refs[p] = held_of(a, p);
+  n.owner[p] = a.lens ? INT32_MAX : p;
+  n.parts[p] = 0;
+}
 __global__ __launch_bounds__(256) void pages_begin_kernel(PagesArgs a) {
+  const Counts n{a.refs, a.w.owner, a.w.parts};
   for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < a.cache.P;
-       p += (int64_t)gridDim.x * 256) {
-    a.refs[p] = held_of(a, (int)p);
-    a.w.owner[p] = a.lens ? INT32_MAX : (int)p;
-    a.w.parts[p] = 0;
-  }
+       p += (int64_t)gridDim.x * 256)
+    begin_page(a, n, (int)p);
 }
 
 // Whose pages row r takes, and how many tokens: what goes on with none, and what
@@ -93,34 +104,43 @@ struct Heir {
   }
 };
 
+// Entry w of row r.
+__device__ __forceinline__ void fork_entry(const PagesArgs& a, const Counts& n, const Heir& h,
+                                           int r, int w) {
+  int page = -1;
+  if (w < h.pages) {
+    page = a.table[(int64_t)h.parent * a.W + w];
+    if (page < 0 || page >= a.cache.P) page = -1;
+  }
+  a.table_out[(int64_t)r * a.W + w] = page;
+  if (page >= 0) {
+    atomicAdd(&n.refs[page], 1);
+    if (w == h.pages - 1 && h.len % LOWM_PAGE) {
+      atomicAdd(&n.parts[page], 1);
+      atomicMin(&n.owner[page], r);
+    }
+  }
+}
 // A workgroup to a row and a stretch of its entries.
 __global__ __launch_bounds__(256) void fork_rows_kernel(PagesArgs a) {
   const int r = blockIdx.x;
   const Heir h(a, r);
-  for (int w = blockIdx.y * 256 + threadIdx.x; w < a.W; w += gridDim.y * 256) {
-    int page = -1;
-    if (w < h.pages) {
-      page = a.table[(int64_t)h.parent * a.W + w];
-      if (page < 0 || page >= a.cache.P) page = -1;
-    }
-    a.table_out[(int64_t)r * a.W + w] = page;
-    if (page >= 0) {
-      atomicAdd(&a.refs[page], 1);
-      if (w == h.pages - 1 && h.len % LOWM_PAGE) {
-        atomicAdd(&a.w.parts[page], 1);
-        atomicMin(&a.w.owner[page], r);
-      }
-    }
-  }
+  const Counts n{a.refs, a.w.owner, a.w.parts};
+  for (int w = blockIdx.y * 256 + threadIdx.x; w < a.W; w += gridDim.y * 256)
+    fork_entry(a, n, h, r, w);
   if (blockIdx.y == 0 && threadIdx.x == 0) a.lens_out[r] = h.len;
 }
 
+__device__ __forceinline__ void count_entry(const PagesArgs& a, const Counts& n, int64_t i) {
+  const int page = a.table[i];
+  if (page >= 0 && page < a.cache.P) atomicAdd(&n.refs[page], 1);
+}
 __global__ __launch_bounds__(256) void count_kernel(PagesArgs a) {
-  const int64_t n = (int64_t)a.R * a.W;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int page = a.table[i];
-    if (page >= 0 && page < a.cache.P) atomicAdd(&a.refs[page], 1);
-  }
+  const int64_t entries = (int64_t)a.R * a.W;
+  const Counts n{a.refs, a.w.owner, a.w.parts};
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < entries;
+       i += (int64_t)gridDim.x * 256)
+    count_entry(a, n, i);
 }
 
 // Inclusive sums over the deciding workgroup, and the sum of all.
@@ -145,7 +165,7 @@ struct GroupScan {
   }
 };
 
-__global__ __launch_bounds__(kOne) void fork_decide_kernel(PagesArgs a) {
+__device__ void fork_decide(const PagesArgs& a, const Counts& c) {
   __shared__ int lds[2 * kWaves];
   __shared__ int sums[3];   // copies made, pages missing, table entries that were too few
   GroupScan scan{lds};
@@ -163,7 +183,7 @@ __global__ __launch_bounds__(kOne) void fork_decide_kernel(PagesArgs a) {
       int copy = 0, more = 0;
       if (h.len % LOWM_PAGE) {
         const int page = a.table_out[(int64_t)r * a.W + h.pages - 1];
-        copy = page >= 0 && !(a.w.owner[page] == r && a.refs[page] == a.w.parts[page]);
+        copy = page >= 0 && !(c.owner[page] == r && c.refs[page] == c.parts[page]);
       }
       if (h.on) {
         const int want = pages_for((int64_t)h.len + a.reserve);
@@ -186,7 +206,7 @@ __global__ __launch_bounds__(kOne) void fork_decide_kernel(PagesArgs a) {
     int n = 0, total;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      free[i] = p + i < P && a.refs[p + i] == 0;
+      free[i] = p + i < P && c.refs[p + i] == 0;
       n += free[i];
     }
     int at = found + scan(n, &total) - n;
@@ -211,10 +231,10 @@ __global__ __launch_bounds__(kOne) void fork_decide_kernel(PagesArgs a) {
     int missing = 0;
     if (copy) {
       const int old = row[h.pages - 1], page = at < found ? a.w.list[at] : -1;
-      atomicSub(&a.refs[old], 1);
+      atomicSub(&c.refs[old], 1);
       row[h.pages - 1] = page;
       if (page >= 0) {
-        atomicAdd(&a.refs[page], 1);
+        atomicAdd(&c.refs[page], 1);
         const int k = atomicAdd(&sums[0], 1);
         a.w.src[k] = old;
         a.w.dst[k] = page;
@@ -227,7 +247,7 @@ __global__ __launch_bounds__(kOne) void fork_decide_kernel(PagesArgs a) {
       const int page = at < found ? a.w.list[at] : -1;
       row[h.pages + i] = page;
       if (page >= 0)
-        atomicAdd(&a.refs[page], 1);
+        atomicAdd(&c.refs[page], 1);
       else
         ++missing;
     }
@@ -239,17 +259,38 @@ __global__ __launch_bounds__(kOne) void fork_decide_kernel(PagesArgs a) {
     a.result[0] = sums[1] + sums[2];
   }
 }
+__global__ __launch_bounds__(kOne) void fork_decide_kernel(PagesArgs a) {
+  fork_decide(a, Counts{a.refs, a.w.owner, a.w.parts});
+}
+// All of it but the copies, for tables and caches that the workgroup's LDS holds.
+__global__ __launch_bounds__(kOne) void fork_small_kernel(PagesArgs a) {
+  __shared__ int refs[kSmallP], owner[kSmallP], parts[kSmallP];
+  const Counts n{refs, owner, parts};
+  for (int p = threadIdx.x; p < a.cache.P; p += kOne) begin_page(a, n, p);
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.R * a.W; i += kOne) {
+    const int r = i / a.W, w = i - r * a.W;
+    const Heir h(a, r);
+    fork_entry(a, n, h, r, w);
+    if (w == 0) a.lens_out[r] = h.len;
+  }
+  __syncthreads();
+  fork_decide(a, n);
+  __syncthreads();
+  for (int p = threadIdx.x; p < a.cache.P; p += kOne) a.refs[p] = refs[p];
+}
+
 
 // The i-th lowest free page takes the i-th highest movable one while that is higher:
 // a free page p, the i-th, is taken if more than i movable ones lie above it, and a
 // movable one moves if more free ones lie below it than movable ones above.
-__global__ __launch_bounds__(kOne) void compact_decide_kernel(PagesArgs a) {
+__device__ void compact_decide(const PagesArgs& a, const Counts& c) {
   __shared__ int lds[2 * kWaves];
   __shared__ int top;
   GroupScan scan{lds};
   if (threadIdx.x == 0) top = 0;
   const int P = a.cache.P;
-  auto movable = [&](int64_t p) { return a.refs[p] > 0 && held_of(a, (int)p) == 0; };
+  auto movable = [&](int64_t p) { return c.refs[p] > 0 && held_of(a, (int)p) == 0; };
   int count = 0;
   for (int64_t p = threadIdx.x; p < P; p += kOne) count += movable(p);
   int all;
@@ -262,7 +303,7 @@ __global__ __launch_bounds__(kOne) void compact_decide_kernel(PagesArgs a) {
     int nf = 0, nm = 0, tf, tm;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      kind[i] = p + i >= P ? 0 : a.refs[p + i] == 0 ? 1 : movable(p + i) ? 2 : 0;
+      kind[i] = p + i >= P ? 0 : c.refs[p + i] == 0 ? 1 : movable(p + i) ? 2 : 0;
       if (kind[i] == 0 && p + i < P) highest = (int)p + i + 1;
       nf += kind[i] == 1;
       nm += kind[i] == 2;
@@ -293,9 +334,9 @@ __global__ __launch_bounds__(kOne) void compact_decide_kernel(PagesArgs a) {
   scan(moved, &pairs);   // its barrier is behind every store of a pair
   for (int i = threadIdx.x; i < pairs; i += kOne) {
     const int s = a.w.src[i], d = a.w.dst[i];
-    a.refs[d] = a.refs[s];
-    a.refs[s] = 0;
-    a.w.owner[s] = d;
+    c.refs[d] = c.refs[s];
+    c.refs[s] = 0;
+    c.owner[s] = d;
   }
   atomicMax(&top, highest);
   __syncthreads();
@@ -303,6 +344,22 @@ __global__ __launch_bounds__(kOne) void compact_decide_kernel(PagesArgs a) {
     a.w.count[0] = pairs;
     a.result[0] = pairs;
     a.result[1] = top;
+  }
+}
+__global__ __launch_bounds__(kOne) void compact_decide_kernel(PagesArgs a) {
+  compact_decide(a, Counts{a.refs, a.w.owner, a.w.parts});
+}
+__global__ __launch_bounds__(kOne) void compact_small_kernel(PagesArgs a) {
+  __shared__ int refs[kSmallP], owner[kSmallP], parts[kSmallP];
+  const Counts n{refs, owner, parts};
+  for (int p = threadIdx.x; p < a.cache.P; p += kOne) begin_page(a, n, p);
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.R * a.W; i += kOne) count_entry(a, n, i);
+  __syncthreads();
+  compact_decide(a, n);
+  for (int p = threadIdx.x; p < a.cache.P; p += kOne) {
+    a.refs[p] = refs[p];
+    a.w.owner[p] = owner[p];
   }
 }
 
@@ -360,6 +417,7 @@ unsigned blocks_for(int64_t n, int64_t per, int64_t most) {
   const int64_t b = (n + per - 1) / per;
   return (unsigned)(b < 1 ? 1 : b > most ? most : b);
 }
+bool is_small(int P, int64_t entries) { return P <= kSmallP && entries <= kSmallEntries; }
 int launch_copies(const PagesArgs& a, int64_t pairs, bool renumber, hipStream_t stream) {
   const lowm_kv_cache& c = a.cache;
   const int64_t units = ((int64_t)c.H * c.D * LOWM_PAGE + kUnit - 1) / kUnit;
@@ -432,6 +490,10 @@ int fork_pages(const lowm_fork_pages_args* u, hipStream_t stream) {
   a.R = u->R;
   a.W = u->W;
   a.reserve = u->reserve;
+  if (is_small(c.P, n)) {
+    rc = launch((const void*)&fork_small_kernel, dim3(1), kOne, a, false, stream);
+    return rc == LOWM_OK ? launch_copies(a, u->R, false, stream) : rc;
+  }
   rc = launch((const void*)&pages_begin_kernel, dim3(blocks_for(c.P, 256, 1024)), 256, a, false,
               stream);
   if (rc == LOWM_OK)
@@ -466,13 +528,17 @@ int compact_pages(const lowm_compact_pages_args* u, hipStream_t stream) {
   a.result = u->counts_out;
   a.R = u->R;
   a.W = u->W;
+  const int64_t most = n < c.P / 2 + 1 ? n : c.P / 2 + 1;
+  if (is_small(c.P, n)) {
+    rc = launch((const void*)&compact_small_kernel, dim3(1), kOne, a, false, stream);
+    return rc == LOWM_OK ? launch_copies(a, most, true, stream) : rc;
+  }
   rc = launch((const void*)&pages_begin_kernel, dim3(blocks_for(c.P, 256, 1024)), 256, a, false,
               stream);
   if (rc == LOWM_OK)
     rc = launch((const void*)&count_kernel, dim3(blocks_for(n, 1024, 1024)), 256, a, false, stream);
   if (rc == LOWM_OK)
     rc = launch((const void*)&compact_decide_kernel, dim3(1), kOne, a, false, stream);
-  const int64_t most = n < c.P / 2 + 1 ? n : c.P / 2 + 1;
   return rc == LOWM_OK ? launch_copies(a, most, true, stream) : rc;
 }
 

@@ -3,11 +3,12 @@
 //
 //   a = pos freq ;  (x, y) -> scale (x cos a - y sin a, x sin a + y cos a)
 //
-// Elementwise but for the angles, which all heads of a token share: a thread owns
-// eight pairs of a token, forms their sines and cosines once and goes through
-// heads with them, so few heads to a thread cost arithmetic and many leave lanes
-// idle (launch_rotary).  The angle is taken modulo a turn in fp64, where position
-// and frequency are exact to 2^-53, and goes to the fp32 sine in half turns.
+// Elementwise but for the angles, which all heads of a token share: a thread owns 16
+// elements of a token's heads, eight pairs or 16 that are only copied, forms their sines
+// and cosines once and goes through heads with them.  Few heads to a thread cost
+// arithmetic, many leave lanes idle (launch_rotary).  The angle is taken modulo a turn in
+// fp64, where position and frequency are exact to 2^-53, and goes to the fp32 sine in half
+// turns.
 #include "ops_cache.cuh"
 
 namespace lowm {
@@ -17,7 +18,7 @@ struct RotaryArgs {
   lowm_rotary_args u;
   int64_t first_token, tokens;   // of this launch
   int head_lanes;                // threads that share a token's heads
-  int pair_groups, groups;       // of eight pairs; with those of eight copied elements
+  int pair_groups, groups;       // of eight pairs; with those of 16 copied elements
   bool copy_q, copy_k;           // whether what is not turned has to be copied
 };
 
@@ -45,66 +46,58 @@ __device__ __forceinline__ void put(void* p, int64_t at, int n, const float (&v)
 template <bool F32, bool HALF>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
   const lowm_rotary_args& u = a.u;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int g = (int)(at % a.groups);
-  const int64_t th = at / a.groups;
-  const int lane = (int)(th % a.head_lanes);
-  const int64_t local = th / a.head_lanes;
+  // (fewer than 2^31 threads to a launch)
+  const uint32_t at = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t th = at / (uint32_t)a.groups, local = th / (uint32_t)a.head_lanes;
+  const int g = (int)(at - th * a.groups), lane = (int)(th - local * a.head_lanes);
   if (local >= a.tokens) return;
   const int64_t t = a.first_token + local;
   const int heads = u.Hq + u.Hk, pairs = u.R / 2;
-  auto row_of = [&](int h, const void** x, void** y, int64_t* from, int64_t* to) {
-    const bool q = h < u.Hq;
-    const int i = q ? h : h - u.Hq;
-    *x = q ? u.q : u.k;
-    *y = q ? u.q_out : u.k_out;
-    *from = t * (q ? u.q_row : u.k_row) + i * (q ? u.q_head : u.k_head);
-    *to = t * (q ? u.q_out_row : u.k_out_row) + i * (q ? u.q_out_head : u.k_out_head);
-  };
 
-  if (g >= a.pair_groups) {
-    // eight of the elements that are copied: those before the turned ones, then
-    // those behind them, groups of each apart
-    const int before = (u.first + 7) / 8, c = g - a.pair_groups;
-    const int d = c < before ? 8 * c : u.first + u.R + 8 * (c - before);
-    const int end = c < before ? u.first : u.D;
-    const int n = end - d < 8 ? end - d : 8;
-    for (int h = lane; h < heads; h += a.head_lanes) {
-      if (!(h < u.Hq ? a.copy_q : a.copy_k)) continue;
-      const void* x;
-      void* y;
-      int64_t from, to;
-      row_of(h, &x, &y, &from, &to);
-      float v[8];
-      take<F32>(x, from + d, n, v);
-      put<F32>(y, to + d, n, v);
-    }
-    return;
-  }
-
-  const int p0 = 8 * g, n = pairs - p0 < 8 ? pairs - p0 : 8;
-  const double pos = u.positions_bytes == 8
-                         ? (double)static_cast<const int64_t*>(u.positions)[t]
-                         : (double)static_cast<const int32_t*>(u.positions)[t];
+  // two runs of up to eight elements, at d0 and d1: n0 and n1 of them
+  const bool turn = g < a.pair_groups;
+  int d0, d1, n0, n1;
   float c[8], s[8];
+  if (turn) {
+    const int p0 = 8 * g, n = pairs - p0 < 8 ? pairs - p0 : 8;
+    d0 = u.first + (HALF ? p0 : 2 * p0);
+    d1 = HALF ? d0 + pairs : d0 + 8;
+    n0 = HALF ? n : 2 * n;
+    n1 = HALF ? n : 2 * n - 8;
+    const double pos = u.positions_bytes == 8
+                           ? (double)static_cast<const int64_t*>(u.positions)[t]
+                           : (double)static_cast<const int32_t*>(u.positions)[t];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const double half_turns = pos * u.freqs[p0 + (i < n ? i : 0)] * 0.31830988618379067154;
-    const float part = (float)(half_turns - 2.0 * rint(0.5 * half_turns));
-    float si, co;
-    sincospif(part, &si, &co);
-    c[i] = u.scale * co;
-    s[i] = u.scale * (u.flags & LOWM_ROTARY_INVERSE ? -si : si);
+    for (int i = 0; i < 8; ++i) {
+      const double half_turns = pos * u.freqs[p0 + (i < n ? i : 0)] * 0.31830988618379067154;
+      const float part = (float)(half_turns - 2.0 * rint(0.5 * half_turns));
+      float si, co;
+      sincospif(part, &si, &co);
+      c[i] = u.scale * co;
+      s[i] = u.scale * (u.flags & LOWM_ROTARY_INVERSE ? -si : si);
+    }
+  } else {
+    // those before the turned ones, then those behind them, groups of each apart
+    const int before = (u.first + 15) / 16, k = g - a.pair_groups;
+    d0 = k < before ? 16 * k : u.first + u.R + 16 * (k - before);
+    d1 = d0 + 8;
+    n0 = (k < before ? u.first : u.D) - d0;
+    n1 = n0 - 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = s[i] = 0.f;
   }
-  const int d0 = u.first + (HALF ? p0 : 2 * p0);
-  const int d1 = HALF ? d0 + pairs : d0 + 8;
-  const int n0 = HALF ? n : 2 * n, n1 = HALF ? n : 2 * n - 8;
-#pragma unroll 2
+  if (n0 > 8) n0 = 8;
+  if (n1 > 8) n1 = 8;
+
+#pragma unroll 4
   for (int h = lane; h < heads; h += a.head_lanes) {
-    const void* x;
-    void* y;
-    int64_t from, to;
-    row_of(h, &x, &y, &from, &to);
+    const bool q = h < u.Hq;
+    if (!turn && !(q ? a.copy_q : a.copy_k)) continue;
+    const int i = q ? h : h - u.Hq;
+    const void* x = q ? u.q : u.k;
+    void* y = q ? u.q_out : u.k_out;
+    const int64_t from = t * (q ? u.q_row : u.k_row) + i * (q ? u.q_head : u.k_head);
+    const int64_t to = t * (q ? u.q_out_row : u.k_out_row) + i * (q ? u.q_out_head : u.k_out_head);
     float v[8], w[8], v2[8], w2[8];
     take<F32>(x, from + d0, n0, v);
     take<F32>(x, from + d1, n1, w);
@@ -123,6 +116,11 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
         w2[2 * i + 1] = w[2 * i] * s[4 + i] + w[2 * i + 1] * c[4 + i];
       }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v2[i] = turn ? v2[i] : v[i];
+      w2[i] = turn ? w2[i] : w[i];
+    }
     put<F32>(y, to + d0, n0, v2);
     put<F32>(y, to + d1, n1, w2);
   }
@@ -133,7 +131,7 @@ int launch_rotary(RotaryArgs a, hipStream_t stream) {
   const int pairs = u.R / 2, heads = u.Hq + u.Hk;
   a.pair_groups = (pairs + 7) / 8;
   a.groups = a.pair_groups + ((a.copy_q || a.copy_k)
-                                  ? (u.first + 7) / 8 + (u.D - u.first - u.R + 7) / 8
+                                  ? (u.first + 15) / 16 + (u.D - u.first - u.R + 15) / 16
                                   : 0);
   // As many threads to a token's heads as fill the GPU with 8 wavefronts to a CU.
   const int64_t per = (int64_t)u.T * a.groups;
