@@ -75,6 +75,7 @@ struct AttendArgs {
   int groups;                // workgroups
   int turn;                  // pages that a workgroup takes at a time, a power of two
   int small;                 // pages of a tile that a workgroup had better take alone
+  int lone;                  // units to a workgroup from which half as many take them
   int most_log;              // log2 of the pages of a part, where tiles are cut by themselves
   uint32_t g_magic, g_shift; // for division by G
   float scale;               // times log2 e
@@ -155,7 +156,9 @@ struct List {
     if (rows > 1.001f * (float)a.seq.T) units = runs[0] = 0;
     per_log = runs[0] <= a.groups ? 3 : a.most_log;
     apart = runs[per_log - 3] <= a.groups;
-    run = apart ? 1 : ((units + a.groups - 1) / a.groups + a.turn - 1) & ~(a.turn - 1);
+    // long runs do better with one to a CU
+    const int groups = units / a.lone >= a.groups ? a.groups / 2 : a.groups;
+    run = apart ? 1 : ((units + groups - 1) / groups + a.turn - 1) & ~(a.turn - 1);
     total = apart ? runs[per_log - 3] : units;
   }
   // Units from one tile to the next.
@@ -1232,11 +1235,15 @@ int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
   a.out = static_cast<uint16_t*>(u->out);
   a.lse = u->lse;
   a.rows = kind;
-  // one workgroup to a CU where its registers and LDS leave no room for two
-  a.groups = kind >= kMore && c.D > 128 ? kGroups / 2 : kGroups;
+  // One workgroup to a CU streams best (2 x 131001 tokens 89 us; 92 with two), and is all
+  // that fits where a page takes more than half of the LDS; two where tiles are many and
+  // short (64 sequences of 300 tokens, 512 tiles: 11.3 us; 21.7 with one), or rows many.
+  const int64_t tiles = (int64_t)c.H * (s.B < s.T ? s.B : s.T);
+  a.groups = (kind >= kMore ? c.D <= 128 : tiles > 128) ? kGroups : kGroups / 2;
   a.turn = kind >= kMore ? 1 : kWaves;
   a.small = kind >= kMore ? 8 : 12;
   a.most_log = kind >= kMore ? 3 : 4;
+  a.lone = kind < kMore && a.groups == kGroups ? 24 : 1 << 20;
   const Divisor g(G);
   a.g_magic = g.magic;
   a.g_shift = g.shift;

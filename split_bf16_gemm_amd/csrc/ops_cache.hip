@@ -8,9 +8,9 @@
 // reads or writes is another's: 256 threads for long rows of a sequence, a wavefront
 // where a page gets a token or two (61 sequences of one token: as many workgroups, a
 // quarter of the wavefronts to start).  A thread holds four tokens by eight elements:
-// keys go straight to their pieces of 16 elements, values are turned in LDS into
-// pieces of 16 tokens, whose rows of bytes are padded so that the lanes' words lie
-// in distinct banks.  A page that is being filled token by token keeps its bytes
+// the bytes meet in LDS, values turned into pieces of 16 tokens, padded so that the
+// lanes' words lie in distinct banks, and go from there to memory in whole pieces, one
+// after another.  A page that is being filled token by token keeps its bytes
 // and its scale until a token is larger than all before it; only then are the
 // earlier ones rounded again, to the new step, which is at most half a step off
 // for each time the scale has grown.
@@ -74,6 +74,11 @@ __device__ __forceinline__ int turned(int D, int group, int d) {   // in words
   return (group * (D + D / 8) + d + d / 8) * 4;
 }
 inline int turned_words(int D) { return 4 * (D + D / 8) * 4; }
+
+// Keys in LDS: the page's pieces, one more for every 64 of them.
+__device__ __forceinline__ int key_words(int chunk, int token) {
+  return (chunk * (LOWM_PAGE + 1) + token) * 4;
+}
 
 struct Levels {
   float scale;
@@ -190,6 +195,7 @@ __global__ __launch_bounds__(THREADS) void append_kernel(AppendArgs a) {
   const Levels levels(now, e4m3);
   const bool grown = lo > 0 && now > before;   // not where it is NaN
   const float ratio = grown ? before / now : 1.f;
+  const bool one = hi - lo == 1;   // token: it needs no detour
   if (threadIdx.x == 0) *scale_at = now;
 
   for (int first = 0; first < items; first += Q * THREADS) {
@@ -209,11 +215,14 @@ __global__ __launch_bounds__(THREADS) void append_kernel(AppendArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int k = tok[i] + j;
-          if (k >= lo && k < hi)
-            *reinterpret_cast<ops_u32x2*>(out + (el[i] / 16 * LOWM_PAGE + k) * 16 + el[i] % 16) =
-                ops_u32x2{q[j][0], q[j][1]};
+          const ops_u32x2 w = {q[j][0], q[j][1]};
+          if (k < lo || k >= hi) continue;
+          if (one)
+            *reinterpret_cast<ops_u32x2*>(out + (el[i] / 16 * LOWM_PAGE + k) * 16 + el[i] % 16) = w;
+          else
+            *reinterpret_cast<ops_u32x2*>(&turn[key_words(el[i] / 16, k) + el[i] % 16 / 4]) = w;
         }
-      } else if (!grown && hi - lo == 1) {
+      } else if (!grown && one) {
         // one more token of a page that keeps its scale: a byte an element
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -234,7 +243,7 @@ __global__ __launch_bounds__(THREADS) void append_kernel(AppendArgs a) {
       }
     }
   }
-  if (values && !grown && hi - lo == 1) return;
+  if (!grown && one) return;
 
   ops_u32x4* pieces = reinterpret_cast<ops_u32x4*>(out);
   if (!values) {
@@ -247,6 +256,12 @@ __global__ __launch_bounds__(THREADS) void append_kernel(AppendArgs a) {
         for (int i = 0; i < 4; ++i) w[i] = again4(w[i], e4m3, ratio);
         pieces[p] = w;
       }
+    }
+    if (one) return;
+    __syncthreads();
+    for (int at = threadIdx.x; at < D / 16 * LOWM_PAGE; at += THREADS) {
+      const int chunk = at / LOWM_PAGE, k = at % LOWM_PAGE;
+      if (k >= lo && k < hi) pieces[at] = *reinterpret_cast<ops_u32x4*>(&turn[key_words(chunk, k)]);
     }
     return;
   }
