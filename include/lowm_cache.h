@@ -26,8 +26,8 @@
  *
  * so element d of token t of a page is byte [d / 16][t][d % 16] of its keys and
  * [t / 16][d][t % 16] of its values, and stands for that byte, as int8 or as e4m3
- * (1 sign, 4 exponent, 3 mantissa bits, bias 7, no infinity), times the scale.  D is
- * a multiple of 16 up to LOWM_CACHE_MAX_D.
+ * (1 sign, 4 exponent, 3 mantissa bits, bias 7, no infinity), times the scale, which
+ * is not negative.  D is a multiple of 16 up to LOWM_CACHE_MAX_D.
  *
  * Sequences.  Row b of `table` [B][table_ld] (int32) lists the pages of sequence b
  * in order, and lens[b] (int32) counts its tokens, those of the call itself
@@ -180,8 +180,9 @@ int lowm_cache_read(const lowm_cache_read_args* args, void* stream);
  * last one) are not written.
  *
  * Sums and softmax statistics are fp32.  The matrix products take fp16: a row of
- * q scaled by a power of two, the bytes as they are (both exact but for elements
- * below 2^-29 of their row's largest), and e^(x - max), rounded to 11 bits.
+ * q scaled by a power of two, the bytes as they are (both exact but for elements of q
+ * below 2^-28 of their row's largest), and the weights e^(x - max), rounded to 11 bits
+ * (below 2^-21 of the largest to a multiple of 2^-32 of it).
  * The same inputs give the same bits.
  *
  * The workspace (lowm_cache_attention_workspace_bytes, 256-byte aligned) is zeroed once
@@ -208,7 +209,8 @@ size_t lowm_cache_attention_workspace_bytes(int T, int Hq, int H, int D);
 
 /* Errors as lowm_cache_append; Hq no multiple of H, window < 0:
  * LOWM_ERR_INVALID_ARG; q, its strides or out not 16-byte, workspace not 256-byte
- * aligned: LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
+ * aligned, T Hq past 2^31 - 1, H (T Hq / (16 H) + B) (W + 72) past 2^30 (a tenth as many
+ * rows where there are more than 32 to a key head): LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
  * LOWM_ERR_WORKSPACE. */
 int lowm_cache_attention(const lowm_cache_attention_args* args, void* stream);
 

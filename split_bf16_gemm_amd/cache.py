@@ -26,26 +26,76 @@ from . import ops
 PAGE = 64          # tokens of a page
 ROTARY_INTERLEAVED, ROTARY_INVERSE = 1, 2
 
-_declared = False
+_vp, _i, _l, _f, _size = ops._vp, ops._i, ops._l, ops._f, ops._size
 
 
-def _library():
-    """liblowm.so with the workspace sizes of lowm_cache.h declared."""
-    global _declared
-    lib = ops.library()
-    if not _declared:
-        i = ctypes.c_int32
-        lib.lib.lowm_cache_attention_workspace_bytes.argtypes = [i, i, i, i]
-        lib.lib.lowm_cache_attention_workspace_bytes.restype = ctypes.c_size_t
-        lib.lib.lowm_pages_workspace_bytes.argtypes = [i, i, i]
-        lib.lib.lowm_pages_workspace_bytes.restype = ctypes.c_size_t
-        _declared = True
-    return lib
+# The argument structs of lowm_cache.h.
+class KvCacheArg(ctypes.Structure):
+    _fields_ = ops._fields(("k v k_scale v_scale", _vp), ("P H D type layers", _i))
+
+
+class SequencesArg(ctypes.Structure):
+    _fields_ = ops._fields(("table lens row_starts", _vp), ("table_ld", _l), ("B W T", _i))
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = ops._fields(
+        ("q k q_out k_out positions freqs", _vp),
+        ("q_row q_head k_row k_head q_out_row q_out_head k_out_row k_out_head", _l),
+        ("T Hq Hk D R first type positions_bytes flags", _i), ("scale", _f))
+
+
+class CacheAppendArgs(ctypes.Structure):
+    _fields_ = [("cache", KvCacheArg), ("seq", SequencesArg),
+                *ops._fields(("k v", _vp), ("k_row k_head v_row v_head", _l), ("type", _i))]
+
+
+class CacheReadArgs(ctypes.Structure):
+    _fields_ = [("cache", KvCacheArg), ("seq", SequencesArg), *ops._fields(("k_out v_out", _vp))]
+
+
+class CacheAttentionArgs(ctypes.Structure):
+    _fields_ = [("cache", KvCacheArg), ("seq", SequencesArg),
+                *ops._fields(("q out lse workspace", _vp), ("workspace_bytes", _size),
+                             ("q_row q_head", _l), ("Hq window", _i), ("scale", _f))]
+
+
+class ForkPagesArgs(ctypes.Structure):
+    _fields_ = [("cache", KvCacheArg),
+                *ops._fields(("table lens parents held table_out lens_out refs_out missing_out "
+                              "workspace", _vp), ("workspace_bytes", _size),
+                             ("R W reserve", _i))]
+
+
+class CompactPagesArgs(ctypes.Structure):
+    _fields_ = [("cache", KvCacheArg),
+                *ops._fields(("table held table_out refs_out counts_out workspace", _vp),
+                             ("workspace_bytes", _size), ("R W", _i))]
+
+
+_lib = None
+
+
+def library():
+    """liblowm.so with the entry points of lowm_cache.h declared."""
+    global _lib
+    if _lib is None:
+        lib = ops.library()
+        c = lib.lib
+        for name in ("rotary", "cache_append", "cache_read", "cache_attention", "fork_pages",
+                     "compact_pages"):
+            getattr(c, f"lowm_{name}").argtypes = [_vp, _vp]
+        c.lowm_cache_attention_workspace_bytes.argtypes = [_i, _i, _i, _i]
+        c.lowm_cache_attention_workspace_bytes.restype = _size
+        c.lowm_pages_workspace_bytes.argtypes = [_i, _i, _i]
+        c.lowm_pages_workspace_bytes.restype = _size
+        _lib = lib
+    return _lib
 
 
 class KVCache(NamedTuple):
-    """Keys and values of one layer, a byte an element (int8 or e4m3) with a scale for each
-    page of 64 tokens and head; or of several layers, with a first dimension more.
+    """Keys and values of one layer, a byte an element (int8 or e4m3) with a scale, not negative,
+    for each page of 64 tokens and head; or of several layers, with a first dimension more.
 
     Element d of token t of page p and head h is k[p, h, d // 16, t, d % 16] * k_scale[p, h]
     and v[p, h, t // 16, d, t % 16] * v_scale[p, h]."""
@@ -139,7 +189,7 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
         (ROTARY_INTERLEAVED if layout == "interleaved" else 0) | (ROTARY_INVERSE if inverse else 0),
         scale, ops._stream(stream, dev))
     if rc:
-        ops.library().check(rc)
+        library().check(rc)
     return q_out, k_out
 
 
@@ -154,7 +204,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.
     rc = (ops._calls or ops._native()).cache_append(
         k, v, *cache, table, lens, row_starts, ops._stream(stream, k.device))
     if rc:
-        ops.library().check(rc)
+        library().check(rc)
 
 
 def cache_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, *,
@@ -173,7 +223,7 @@ def cache_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, *,
     rc = (ops._calls or ops._native()).cache_read(
         k_out, v_out, *cache, table, lens, row_starts, ops._stream(stream, dev))
     if rc:
-        ops.library().check(rc)
+        library().check(rc)
     return k_out, v_out
 
 
@@ -181,7 +231,7 @@ def make_cache_attention_workspace(T: int, q_heads: int, heads: int, head_dim: i
                                    device="cuda") -> Optional[torch.Tensor]:
     """A zeroed workspace of cache_attention for T rows (None for sizes it rejects); it serves
     any sizes that need no more bytes, one call at a time, but no other operator."""
-    n = _library().lib.lowm_cache_attention_workspace_bytes(T, q_heads, heads, head_dim)
+    n = library().lib.lowm_cache_attention_workspace_bytes(T, q_heads, heads, head_dim)
     return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
 
@@ -204,7 +254,7 @@ def cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
         q, *cache, table, lens, row_starts, out, lse_out, workspace, window,
         q.shape[-1] ** -0.5 if scale is None else scale, ops._stream(stream, dev))
     if rc:
-        ops.library().check(rc)
+        library().check(rc)
     return out, lse_out
 
 
@@ -212,7 +262,7 @@ def make_pages_workspace(rows: int, width: int, pages: int,
                          device="cuda") -> Optional[torch.Tensor]:
     """A workspace of fork_pages and compact_pages for tables [rows, width] and caches of that
     many pages (None for sizes they reject); it needs no clearing and serves one call at a time."""
-    n = _library().lib.lowm_pages_workspace_bytes(rows, width, pages)
+    n = library().lib.lowm_pages_workspace_bytes(rows, width, pages)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
@@ -240,7 +290,7 @@ def fork_pages(cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
     rc = (ops._calls or ops._native()).fork_pages(
         *cache, table, lens, parents, held, *outs, workspace, reserve, ops._stream(stream, dev))
     if rc:
-        ops.library().check(rc)
+        library().check(rc)
     return tuple(outs)
 
 
@@ -257,5 +307,5 @@ def compact_pages(cache: KVCache, table: torch.Tensor, *, held: Optional[torch.T
     rc = (ops._calls or ops._native()).compact_pages(
         *cache, table, held, *outs, workspace, ops._stream(stream, dev))
     if rc:
-        ops.library().check(rc)
+        library().check(rc)
     return tuple(outs)

@@ -28,7 +28,7 @@ import pytest
 import torch
 
 import split_bf16_gemm_amd as sbg
-from split_bf16_gemm_amd import ops
+from split_bf16_gemm_amd import cache as cache_ops
 from split_bf16_gemm_amd.cache import PAGE
 
 U = 2.0 ** -24
@@ -1001,55 +1001,24 @@ def test_tensors_that_do_not_fit_are_refused():
             pytest.fail(f"call {i} was not refused")
 
 
-def test_c_abi_refuses(monkeypatch):
+def test_c_abi_refuses():
     """The checks of the C ABI itself, with addresses that are never followed."""
     import ctypes as ct
 
-    class Cache(ct.Structure):
-        _fields_ = ops._fields(("k v k_scale v_scale", ct.c_void_p),
-                               ("P H D type layers", ct.c_int32))
-
-    class Sequences(ct.Structure):
-        _fields_ = ops._fields(("table lens row_starts", ct.c_void_p), ("table_ld", ct.c_int64),
-                               ("B W T", ct.c_int32))
-
-    class Append(ct.Structure):
-        _fields_ = [("cache", Cache), ("seq", Sequences),
-                    *ops._fields(("k v", ct.c_void_p), ("k_row k_head v_row v_head", ct.c_int64),
-                                 ("type", ct.c_int32))]
-
-    class Attention(ct.Structure):
-        _fields_ = [("cache", Cache), ("seq", Sequences),
-                    *ops._fields(("q out lse workspace", ct.c_void_p), ("bytes", ct.c_size_t),
-                                 ("q_row q_head", ct.c_int64), ("Hq window", ct.c_int32),
-                                 ("scale", ct.c_float))]
-
-    class Rotary(ct.Structure):
-        _fields_ = ops._fields(
-            ("q k q_out k_out positions freqs", ct.c_void_p),
-            ("q_row q_head k_row k_head q_out_row q_out_head k_out_row k_out_head", ct.c_int64),
-            ("T Hq Hk D R first type positions_bytes flags", ct.c_int32), ("scale", ct.c_float))
-
-    class Fork(ct.Structure):
-        _fields_ = [("cache", Cache),
-                    *ops._fields(("table lens parents held table_out lens_out refs_out "
-                                  "missing_out workspace", ct.c_void_p), ("bytes", ct.c_size_t),
-                                 ("R W reserve", ct.c_int32))]
-
-    lib = ops.library().lib
+    lib = cache_ops.library().lib
     INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -3
     at = lambda i: (1 << 40) + (i << 32)  # noqa: E731
 
     def cache(**kw):
-        return Cache(**{**dict(k=at(0), v=at(1), k_scale=at(2), v_scale=at(3), P=4, H=2, D=64,
+        return cache_ops.KvCacheArg(**{**dict(k=at(0), v=at(1), k_scale=at(2), v_scale=at(3), P=4, H=2, D=64,
                                type=2, layers=1), **kw})
 
     def seq(**kw):
-        return Sequences(**{**dict(table=at(4), lens=at(5), row_starts=None, table_ld=3, B=2, W=3,
+        return cache_ops.SequencesArg(**{**dict(table=at(4), lens=at(5), row_starts=None, table_ld=3, B=2, W=3,
                                    T=2), **kw})
 
     def append(c=None, s=None, **kw):
-        a = Append(cache=c or cache(), seq=s or seq(),
+        a = cache_ops.CacheAppendArgs(cache=c or cache(), seq=s or seq(),
                    **{**dict(k=at(6), v=at(7), k_row=128, k_head=64, v_row=128, v_head=64, type=0),
                       **kw})
         return lib.lowm_cache_append(ct.byref(a), None)
@@ -1073,12 +1042,11 @@ def test_c_abi_refuses(monkeypatch):
         assert got == want
 
     size = lib.lowm_cache_attention_workspace_bytes
-    size.argtypes, size.restype = [ct.c_int32] * 4, ct.c_size_t
 
     def attend(c=None, s=None, **kw):
-        a = Attention(cache=c or cache(), seq=s or seq(),
+        a = cache_ops.CacheAttentionArgs(cache=c or cache(), seq=s or seq(),
                       **{**dict(q=at(6), out=at(7), lse=at(8), workspace=at(9),
-                                bytes=size(2, 8, 2, 64), q_row=512, q_head=64, Hq=8, window=0,
+                                workspace_bytes=size(2, 8, 2, 64), q_row=512, q_head=64, Hq=8, window=0,
                                 scale=1.0), **kw})
         return lib.lowm_cache_attention(ct.byref(a), None)
 
@@ -1089,16 +1057,18 @@ def test_c_abi_refuses(monkeypatch):
         (INVALID, attend(q=None)), (INVALID, attend(out=None)), (UNSUPPORTED, attend(q=at(6) + 2)),
         (UNSUPPORTED, attend(out=at(7) + 8)), (UNSUPPORTED, attend(lse=at(8) + 1)),
         (UNSUPPORTED, attend(q_head=68)), (INVALID, attend(q_row=64)),
-        (WORKSPACE, attend(workspace=None)), (WORKSPACE, attend(bytes=size(2, 8, 2, 64) - 1)),
+        (WORKSPACE, attend(workspace=None)), (WORKSPACE, attend(workspace_bytes=size(2, 8, 2, 64) - 1)),
         (UNSUPPORTED, attend(workspace=at(9) + 128)), (INVALID, attend(out=at(6))),
         (INVALID, attend(lse=at(7))), (INVALID, attend(workspace=at(0))),
         (INVALID, attend(out=at(4))), (UNSUPPORTED, attend(Hq=2048, q_row=2048 * 64)),
         (INVALID, attend(c=cache(layers=3))), (INVALID, lib.lowm_cache_attention(None, None)),
+        (UNSUPPORTED, attend(s=seq(T=1 << 20, B=1, W=65536, table_ld=65536),
+                             workspace_bytes=size(1 << 20, 8, 2, 64), workspace=at(12))),
     ]:
         assert got == want
 
     def rotary(**kw):
-        a = Rotary(**{**dict(q=at(0), k=at(1), q_out=at(2), k_out=at(3), positions=at(4),
+        a = cache_ops.RotaryArgs(**{**dict(q=at(0), k=at(1), q_out=at(2), k_out=at(3), positions=at(4),
                              freqs=at(5), q_row=256, q_head=64, k_row=64, k_head=64,
                              q_out_row=256, q_out_head=64, k_out_row=64, k_out_head=64, T=2, Hq=4,
                              Hk=1, D=64, R=64, first=0, type=0, positions_bytes=8, flags=0,
@@ -1122,13 +1092,12 @@ def test_c_abi_refuses(monkeypatch):
         assert got == want
 
     room = lib.lowm_pages_workspace_bytes
-    room.argtypes, room.restype = [ct.c_int32] * 3, ct.c_size_t
 
     def fork(c=None, **kw):
-        a = Fork(cache=c or cache(layers=3),
+        a = cache_ops.ForkPagesArgs(cache=c or cache(layers=3),
                  **{**dict(table=at(4), lens=at(5), parents=None, held=None, table_out=at(6),
                            lens_out=at(7), refs_out=at(8), missing_out=at(9), workspace=at(10),
-                           bytes=room(4, 3, 4), R=4, W=3, reserve=1), **kw})
+                           workspace_bytes=room(4, 3, 4), R=4, W=3, reserve=1), **kw})
         return lib.lowm_fork_pages(ct.byref(a), None)
 
     assert room(0, 1, 1) == room(1, 0, 1) == room(1, 1, 0) == room(4097, 1, 1) == 0
@@ -1138,7 +1107,7 @@ def test_c_abi_refuses(monkeypatch):
         (UNSUPPORTED, fork(R=4097)), (UNSUPPORTED, fork(W=65537)),
         (UNSUPPORTED, fork(c=cache(P=(1 << 24) + 1))), (UNSUPPORTED, fork(held=at(11) + 2)),
         (UNSUPPORTED, fork(reserve=65536 * 64 + 1)), (WORKSPACE, fork(workspace=None)),
-        (WORKSPACE, fork(bytes=room(4, 3, 4) - 1)), (UNSUPPORTED, fork(workspace=at(10) + 4)),
+        (WORKSPACE, fork(workspace_bytes=room(4, 3, 4) - 1)), (UNSUPPORTED, fork(workspace=at(10) + 4)),
         (INVALID, fork(table_out=at(4))), (INVALID, fork(lens_out=at(5))),
         (INVALID, fork(refs_out=at(6))), (INVALID, fork(missing_out=at(0))),
         (INVALID, fork(table=at(1))), (INVALID, fork(held=at(8))),
