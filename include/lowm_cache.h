@@ -209,8 +209,8 @@ size_t lowm_cache_attention_workspace_bytes(int T, int Hq, int H, int D);
 
 /* Errors as lowm_cache_append; Hq no multiple of H, window < 0:
  * LOWM_ERR_INVALID_ARG; q, its strides or out not 16-byte, workspace not 256-byte
- * aligned, T Hq past 2^31 - 1, H (T Hq / (16 H) + B) (W + 72) past 2^30 (a tenth as many
- * rows where there are more than 32 to a key head): LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
+ * aligned, T Hq past 2^31 - 1, H (T Hq / (H R) + B + 1) (W + 72) past 2^30 - 1 with R =
+ * 16, 32, 64 or 128 where T Hq is up to 16, 32 or 64 H B or more: LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
  * LOWM_ERR_WORKSPACE. */
 int lowm_cache_attention(const lowm_cache_attention_args* args, void* stream);
 

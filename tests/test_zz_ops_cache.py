@@ -399,7 +399,7 @@ def attention_reference(q, cache, table, lens, starts, scale, window):
                 lse[t, h] = torch.logsumexp(x, 0)
                 w = torch.exp(x - lse[t, h])
                 out[t, h] = w @ vv
-                E = scale * (D + 3) * U * (kk.abs() @ q[t, h].abs())
+                E = abs(scale) * (D + 3) * U * (kk.abs() @ q[t, h].abs())
                 E = E + 4 * U * (x.max() - x) + 4 * U * x.abs()
                 n_sum = (64 + len(pages) * 4 + 16) * U
                 off = 2 * E + (w @ E) + 2.0 ** -11 + n_sum
@@ -464,6 +464,14 @@ ATTENTIONS = [
     (9, 3, 160, torch.int8, [190], [30], 0),
     (24, 8, 176, FP8, [65, 200], [1, 1], 0),
     (3, 1, 240, torch.int8, [100, 320], [4, 33], 33),
+    (16, 2, 128, torch.int8, [2000, 100], [20, 30], 0),
+    (8, 2, 64, FP8, [1500], [40], 0),
+    (8, 2, 192, FP8, [900, 70], [33, 20], 0),
+    (16, 2, 256, torch.int8, [1200], [25], 200),
+    (8, 1, 128, torch.int8, [3000, 64], [6, 8], 0),
+    (8, 1, 192, torch.int8, [600], [8], 70),
+    (4, 1, 256, FP8, [500], [6], 0),
+    (10, 2, 128, FP8, [20000], [26], 0),
 ]
 
 
@@ -487,9 +495,13 @@ def test_attention(case):
     # heads first in memory
     q2 = q.transpose(0, 1).contiguous().transpose(0, 1)
     ws = sbg.make_cache_attention_workspace(T, Hq, H, D)
-    third, none = sbg.cache_attention(q2, cache, table, ints(lens), row_starts=ints(starts),
-                                      window=window, workspace=ws)
+    wide_table = torch.full((len(lens), table.shape[1] + 5), 1 << 30, dtype=I32, device="cuda")
+    wide_table[:, :table.shape[1]] = table
+    third, none = sbg.cache_attention(q2, cache, wide_table[:, :table.shape[1]], ints(lens),
+                                      row_starts=ints(starts), window=window, workspace=ws)
     assert torch.equal(third, out) and none is None
+    # larger products are smaller scores
+    check_attention(q, cache, table, lens, starts, window=window, scale=-0.05, ws=ws)
 
 
 @gpu
@@ -586,8 +598,14 @@ def test_attention_long_and_shared(G):
     table = tables(g, P, lens)
     starts = [0, *itertools.accumulate(new)]
     q = randn(g, sum(new), H * G, D, std=2.0)
-    check_attention(q, cache, table, lens, starts)
-    check_attention(q, cache, table, lens, starts, window=5000)
+    ws = sbg.make_cache_attention_workspace(sum(new), H * G, H, D)
+    out, lse = check_attention(q, cache, table, lens, starts, ws=ws)
+    check_attention(q, cache, table, lens, starts, window=5000, ws=ws)
+    # whoever joins the parts, the bits are the same
+    for _ in range(5):
+        again, lse2 = sbg.cache_attention(q, cache, table, ints(lens), row_starts=ints(starts),
+                                          workspace=ws, lse_out=torch.empty_like(lse))
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
 
 
 @gpu
@@ -628,6 +646,53 @@ def test_attention_many_sequences():
     starts = [0, *itertools.accumulate(new)]
     q = randn(g, sum(new) + 3, 4, D)
     check_attention(q, cache, tables(g, P, lens), lens, starts)
+
+
+@gpu
+@pytest.mark.parametrize("G", [1, 8, 40])
+def test_attention_row_starts_that_fall(G):
+    """Rows counted twice: nothing is written, and nothing else is touched."""
+    g = gen(27)
+    cache = random_cache(g, 4, 2, 32)
+    table, lens = ints([[0, 1], [2, 3], [1, 0], [3, 2]]), ints([100, 128, 70, 128])
+    q = randn(g, 12, 2 * G, 32)
+    ws = sbg.make_cache_attention_workspace(12, 2 * G, 2, 32)
+    out, lse = torch.full_like(q, 5.0), torch.full((12, 2 * G), 5.0, device="cuda")
+    for starts in ([0, 12, 0, 12, 12], [3, 12, -5, 1 << 30, 12]):
+        sbg.cache_attention(q, cache, table, lens, row_starts=ints(starts), workspace=ws, out=out,
+                            lse_out=lse)
+        assert (out == 5).all() and (lse == 5).all() and not ws[:COUNTERS].any()
+
+
+@gpu
+def test_two_captured_calls_share_a_workspace():
+    """Graphs of two shapes over one workspace, replayed in turn with eager calls between."""
+    g = gen(28)
+    cache = random_cache(g, 40, 2, 64)
+    shapes = [(1, [900]), (20, [1500, 70]), (3, [64, 64, 200])]
+    runs = []
+    ws = sbg.make_cache_attention_workspace(40, 16, 2, 64)
+    for n, lens in shapes:
+        T = n * len(lens)
+        table, q = tables(g, 40, lens), randn(g, T, 16, 64)
+        out, lse, L = torch.empty_like(q), torch.empty(T, 16, device="cuda"), ints(lens)
+
+        def call(q=q, table=table, L=L, out=out, lse=lse):
+            sbg.cache_attention(q, cache, table, L, workspace=ws, out=out, lse_out=lse)
+
+        call()
+        want = (out.clone(), lse.clone())
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((graph, call, out, lse, want))
+    for i in range(12):
+        graph, call, out, lse, want = runs[i % 3]
+        out.fill_(3.0)
+        graph.replay() if i % 4 else call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
 # ---------------------------------------------------------------------------------------------
