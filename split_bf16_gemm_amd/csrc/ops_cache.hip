@@ -36,13 +36,14 @@ __device__ __forceinline__ Touched page_of(const lowm_sequences& s, int P, int i
   if (!s.row_starts) {
     b = item / uniform_pages;
     nth = item % uniform_pages;
+    t.rows = rows_of(s, b);
   } else {
     // every wavefront looks for itself, 64 sequences at a time
     const int lane = threadIdx.x & (kWave - 1);
     b = -1;
     for (int at = 0; at < s.B; at += kWave) {
-      int n = 0;
-      if (at + lane < s.B) n = Stretch(s, rows_of(s, at + lane)).pages();
+      const Rows mine = rows_of(s, at + lane < s.B ? at + lane : s.B - 1);
+      const int n = at + lane < s.B ? Stretch(s, mine).pages() : 0;
       const int sum = wave_scan(n);
       const int total = __builtin_amdgcn_readlane(sum, kWave - 1);
       if (item - nth < total) {
@@ -50,13 +51,15 @@ __device__ __forceinline__ Touched page_of(const lowm_sequences& s, int P, int i
         const int first = __builtin_ctzll(past);
         b = at + first;
         nth = item - nth - __builtin_amdgcn_readlane(sum - n, first);
+        t.rows = Rows{__builtin_amdgcn_readlane(mine.first, first),
+                      __builtin_amdgcn_readlane(mine.n, first),
+                      __builtin_amdgcn_readlane(mine.len, first)};
         break;
       }
       nth += total;
     }
     if (b < 0) return t;
   }
-  t.rows = rows_of(s, b);
   const Stretch all(s, t.rows);
   if (nth < 0 || nth >= all.pages()) return t;
   const int p = all.lo / LOWM_PAGE + nth;
@@ -320,20 +323,38 @@ __global__ __launch_bounds__(THREADS) void read_kernel(ReadArgs a) {
     for (int i = 0; i < 4; ++i) x[4 + i] = p[i] * scale;
     store8(out, ((row0 + k) * c.H + head) * D + d, false, x);
   };
+  // several loads at a time: a loop's next load would wait for the store before it
+  constexpr int kAhead = 4;
   if (!values) {
-    for (int at = threadIdx.x; at < (hi - lo) * chunks; at += THREADS) {
-      const int k = lo + at / chunks, d = at % chunks * 8;
-      const ops_u32x2 w = *reinterpret_cast<const ops_u32x2*>(
-          in + (d / 16 * LOWM_PAGE + k) * 16 + d % 16);
-      store(k, d, w[0], w[1]);
+    const int items = (hi - lo) * chunks;
+    for (int first = threadIdx.x; first < items; first += kAhead * THREADS) {
+      ops_u32x2 w[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int at = first + i * THREADS < items ? first + i * THREADS : first;
+        const int k = lo + at / chunks, d = at % chunks * 8;
+        w[i] = *reinterpret_cast<const ops_u32x2*>(in + (d / 16 * LOWM_PAGE + k) * 16 + d % 16);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int at = first + i * THREADS;
+        if (at < items) store(lo + at / chunks, at % chunks * 8, w[i][0], w[i][1]);
+      }
     }
     return;
   }
   const ops_u32x4* pieces = reinterpret_cast<const ops_u32x4*>(in);
-  const int first = lo / 16;
-  for (int at = threadIdx.x; at < ((hi + 15) / 16 - first) * D; at += THREADS) {
-    const int g = first + at / D, d = at % D;
-    *reinterpret_cast<ops_u32x4*>(&turn[turned(D, g, d)]) = pieces[g * D + d];
+  const int first_piece = lo / 16 * D, all = (hi + 15) / 16 * D;
+  for (int first = first_piece + threadIdx.x; first < all; first += kAhead * THREADS) {
+    ops_u32x4 w[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      w[i] = pieces[first + i * THREADS < all ? first + i * THREADS : first];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int at = first + i * THREADS;
+      if (at < all) *reinterpret_cast<ops_u32x4*>(&turn[turned(D, at / D, at % D)]) = w[i];
+    }
   }
   __syncthreads();
   const int first_quad = lo / 4, items = ((hi + 3) / 4 - first_quad) * chunks;
