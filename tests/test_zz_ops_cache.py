@@ -588,6 +588,28 @@ def test_attention_magnitudes():
 
 
 @gpu
+@pytest.mark.parametrize("case", [
+    # Hq, H, D, kind, lens, new rows, window
+    (8, 1, 64, torch.int8, [900], [700], 100),
+    (8, 1, 128, FP8, [513, 70], [513, 70], 0),
+    (4, 1, 192, torch.int8, [700], [650], 70),
+    (2, 2, 64, torch.int8, [600, 3000], [90, 30], 65),
+    (2, 2, 96, FP8, [400, 3000], [1, 40], 500),
+    (32, 8, 16, torch.int8, [1100], [1000], 0),
+    (32, 8, 16, FP8, [1100, 64], [1000, 3], 700),
+], ids=lambda c: f"h{c[0]}_{c[1]}_d{c[2]}_n{c[5][0]}_w{c[6]}")
+def test_attention_of_whole_prompts(case):
+    """Rows of many tiles, which see more and more pages, or through a window ever others."""
+    Hq, H, D, kind, lens, new, window = case
+    g = gen(41, Hq, D, window)
+    P = sum(-(-n // PAGE) for n in lens) + 2
+    cache = random_cache(g, P, H, D, kind)
+    starts = [0, *itertools.accumulate(new)]
+    q = randn(g, sum(new) + 2, Hq, D, std=1.5)
+    check_attention(q, cache, tables(g, P, lens), lens, starts, window=window)
+
+
+@gpu
 @pytest.mark.parametrize("G", [1, 3, 16, 40])
 def test_attention_long_and_shared(G):
     """Sequences cut over many workgroups beside short ones; the rows of several tiles."""
