@@ -3,40 +3,45 @@
 //
 //   x_t = scale q . k_t ;  out = sum_t e^(x_t - lse) v_t ;  lse = log sum_t e^x_t
 //
-// One pass over the pages with a running maximum and sum, in one launch.  Bound by HBM
-// for few rows: a byte of the cache is read once for up to 32 rows of a key head.
+// One pass over the pages with a running maximum and sum.  Bound by HBM for few rows, where
+// a byte of the cache is read once for all rows of a key head (2 x 131001 tokens, 64 heads on
+// 8 of 128, e4m3: 90 us, 6.0 TB/s); by the matrix unit and the vector unit beside it for many
+// (1024 rows over 8192 tokens, the same heads: 302 us, 850 TFLOP/s of 1470 that a large
+// product reaches); by round trips where the work is small (640 tokens: 9.5 us).
 //
-// Layout.  Up to 16 RT rows of one key head (a token's query heads that share it,
-// token after token) are a tile.  A wavefront takes a page of 64 tokens at a time:
-// S^T = K Q^T by v_mfma_f32_16x16x32_f16, tokens as the 16 rows of the result and
-// query rows as its columns, so that a lane holds 16 scores of one query row and all
-// softmax state is one number a lane.  The tokens of the four score blocks are dealt
-// so that a lane's scores are, in order, what the second product O^T = V^T P^T wants
-// of that lane: scores go from one matrix instruction to the other without leaving
-// their lane.  The cache's layout is what the two products read: a load of 16 bytes a
-// lane takes 16 elements of a token's key, or 16 tokens of a value's element, whole
-// lines at a time and straight into registers.  The next page's keys load while this
-// page's scores are worked on, its values while the keys multiply.
+// Layout.  Rows of one key head (a token's query heads that share it, token after token)
+// are taken in tiles, blocks of 16 to a wavefront.  S^T = K Q^T by
+// v_mfma_f32_16x16x32_f16, 64 tokens of a page as the rows of four results and query rows
+// as their columns, so that a lane holds 16 scores of one query row and all softmax state
+// is one number a lane.  The tokens of the four score blocks are dealt so that a lane's
+// scores are, in order, what the second product O^T = V^T P^T wants of that lane: scores
+// go from one matrix instruction to the other without leaving their lane.  The cache's
+// layout is what the two products read: a load of 16 bytes a lane takes 16 elements of a
+// token's key, or 16 tokens of a value's element, whole lines at a time.
+//
+// Up to 32 rows (attend_kernel) each wavefront has pages of its own, straight into
+// registers: the next page's keys load while this page's scores are worked on, its values
+// while the keys multiply.  With more (attend_wide_kernel) all wavefronts of a workgroup take
+// the same page, each for other rows, and it becomes fp16 once, in LDS.
 //
 // Bytes become fp16 exactly (an int8 by two byte permutations to 1024 + 128 + b and a
-// packed subtraction).  A row of q is scaled by a power of two to just below 2^15; e^(x
-// - max of the page) by 2^14, so that fp16 keeps what is within 2^-28 of a page's
-// largest; the scale of the values and the page's distance to the running maximum are
-// one factor on the page's fp32 result.
+// packed subtraction).  A row of q is scaled by a power of two to just below 2^15.  Weights
+// are 2^7 e^(x - ref), ref at most 2^8 below the largest, so that fp16 keeps all 11 bits of
+// what is within 2^-21 of it and sums are seldom scaled anew; the scale of a page's values
+// is part of the exponent.
 //
-// Work.  The pages of all sequences, heads and tiles are one list that is cut into
-// equal runs, one to a workgroup, whatever the lengths are; they are read on the
-// device.  A tile counts as kTileCost pages more than it has, so that many short
-// sequences are spread like one long one.  A run has at most two tiles that others
-// share, its first and its last, and leaves its sums of them in two places of its own
-// in the workspace; the last of a tile's runs to arrive at its counter joins them, in the
-// order of the pages, so that the bits do not depend on who that is.
+// Work is cut on the device, whatever the lengths are (List, Walk).  Runs of the list have
+// at most two tiles that others share, their first and their last, and leave their sums of
+// them in two places of their own in the workspace; they are joined in the order of the
+// pages, so that the bits do not depend on who does it.
 //
-// The exchange.  Sums go to the workspace with device-scope stores, which pass the
+// The join, for few rows: sums go to the workspace with device-scope stores, which pass the
 // XCDs' own caches; a workgroup waits until its stores are acknowledged there and then
-// adds to the counter, and who finds the others' additions reads with device-scope
+// adds to the tile's counter, and who finds all the others' additions reads with device-scope
 // loads.  No cache is written back or invalidated, and nobody waits for another
-// workgroup.  Counters are zero between calls: who joins clears them.
+// workgroup.  Counters are zero between calls: who joins clears them.  Sums of more rows
+// are too many to pass the caches (64 KB of a part of 128 rows of 128): a second launch,
+// join_kernel, reads them, and finds the tiles in notes that the first one leaves.
 #include <type_traits>
 
 #include "ops_cache.cuh"
@@ -74,10 +79,6 @@ struct AttendArgs {
   int Hq, G, window, rows;   // rows: of a tile
   int most_pages;            // that a tile's rows may see together through the window
   int groups;                // workgroups
-  int turn;                  // pages that a workgroup takes at a time, a power of two
-  int small;                 // pages of a tile that a workgroup had better take alone
-  int lone;                  // units to a workgroup from which half as many take them
-  int most_log;              // log2 of the pages of a part, where tiles are cut by themselves
   uint32_t g_magic, g_shift; // for division by G
   float scale;               // times log2 e
 };
@@ -134,18 +135,27 @@ struct Share {
 // pages, and all tiles are one list of equal runs, which may end inside a tile.  Every
 // wavefront works that out for itself, 64 sequences at a time.  The host sees to it that
 // 32 bits hold the units.
+//
+// A workgroup of attend_kernel takes four pages at a time, one of attend_wide_kernel (WIDE)
+// one.  WIDE, parts of less than 8 pages pay while up to kFine workgroups leave sums (64 rows over 1024 tokens, 16 tiles: 21 us in parts of
+// 2 pages, 29 in parts of 8; 512 rows over themselves, 128 tiles: 27 whole, 35 in parts of 4).
+template <bool WIDE>
 struct List {
-  int total, run, per_log, small, lane;
+  static constexpr int kTurn = WIDE ? 1 : kWaves;
+  static constexpr int kLogs = WIDE ? 3 : 2, kLeast = WIDE ? 1 : 3;   // log2 of a part's pages
+  static constexpr int kSmall = WIDE ? 0 : 12;      // pages of a tile that is not cut
+  static constexpr int kFine = WIDE ? 128 : kGroups;   // runs at most for parts not the largest
+  static constexpr int kLone = 24;   // units to a workgroup from which half as many take them
+  int total, run, per_log, lane;
   bool apart;
   Share own;                         // of sequence `lane` (of the last 64)
   __device__ __forceinline__ int parts(int pages, int log) const {
-    const int alone = small > 1 << log ? small : 1 << log;
+    const int alone = kSmall > 1 << log ? kSmall : 1 << log;
     return pages <= alone ? 1 : (pages + (1 << log) - 1) >> log;
   }
   __device__ __forceinline__ explicit List(const AttendArgs& a) {
     lane = threadIdx.x & (kWave - 1);
-    small = a.small;
-    int units = 0, runs[2] = {};   // for parts of 8 and of 16 pages
+    int units = 0, runs[kLogs] = {};   // for parts of 2^kLeast pages, of twice as many ..
     float rows = 0.f;
     for (int at = 0; at < a.seq.B; at += kWave) {
       own = Share(a, at + lane < a.seq.B ? at + lane : a.seq.B - 1);
@@ -153,17 +163,25 @@ struct List {
       auto all = [&](int v) { return __builtin_amdgcn_readlane(wave_scan(v), kWave - 1); };
       units += all(tiles * (own.pages + kTileCost));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) runs[i] += all(tiles * parts(own.pages, 3 + i));
+      for (int i = 0; i < kLogs; ++i) runs[i] += all(tiles * parts(own.pages, kLeast + i));
       rows += wave_sum(at + lane < a.seq.B ? (float)own.rows.n : 0.f);
     }
     // row_starts that fall may count rows twice, and more units than 32 bits hold
     if (rows > 1.001f * (float)a.seq.T) units = runs[0] = 0;
-    per_log = runs[0] <= a.groups ? 3 : a.most_log;
-    apart = runs[per_log - 3] <= a.groups;
+    apart = false;
+    per_log = 0;
+    total = units;
+#pragma unroll
+    for (int i = kLogs - 1; i >= 0; --i) {
+      if (runs[i] > a.groups || (i < kLogs - 1 && runs[i] > kFine)) continue;
+      apart = true;
+      per_log = kLeast + i;
+      total = runs[i];
+    }
     // long runs do better with one to a CU
-    const int groups = units / a.lone >= a.groups ? a.groups / 2 : a.groups;
-    run = apart ? 1 : ((units + groups - 1) / groups + a.turn - 1) & ~(a.turn - 1);
-    total = apart ? runs[per_log - 3] : units;
+    const bool half = !WIDE && a.groups == kGroups && units / kLone >= kGroups;
+    const int groups = half ? kGroups / 2 : a.groups;
+    run = apart ? 1 : ((units + groups - 1) / groups + kTurn - 1) & ~(kTurn - 1);
   }
   // Units from one tile to the next.
   __device__ __forceinline__ int span(const Share& s) const {
@@ -384,6 +402,7 @@ struct Note {
 };
 
 // A workgroup's run of the list, part of a tile after part of a tile.
+template <bool WIDE>
 struct Walk {
   int total, run, per_log, w, u, end, start;   // its units are u .. end - 1; start: of b
   bool apart;
@@ -398,7 +417,7 @@ struct Walk {
   bool noted;                      // whether the run's note is written, or there is no run
 
   __device__ __forceinline__ explicit Walk(const AttendArgs& a) {
-    const List list(a);
+    const List<WIDE> list(a);
     total = list.total;
     run = list.run;
     per_log = list.per_log;
@@ -420,19 +439,20 @@ struct Walk {
       const int span = list.span(s);
       const int tile_at = (int)((uint32_t)(u - start) / (uint32_t)span);
       const int part = u - start - tile_at * span;
-      w0 = w - part;
-      n = span;
-      page_at = part << per_log;
-      pages = n == 1 || s.pages - page_at < 1 << per_log ? s.pages - page_at : 1 << per_log;
       take(a, tile_at);
+      w0 = w - part;
+      page_at = part << per_log;
+      pages = span == 1 || s.pages - page_at < 1 << per_log ? s.pages - page_at : 1 << per_log;
+      n = span == 1 ? 1 : (seen() + (1 << per_log) - 1) >> per_log;
+      if (part >= n) u = end;   // no row of the tile sees these pages
     }
   }
   // The tile's rows and first page.  Without a window later rows see more pages, so that
   // tiles are taken from both ends in turn, and equal runs have equal work in them (8192
-  // rows over themselves, 64 heads on 8 of 128: 2045 us in order, 1256 so).
+  // rows over themselves, 64 heads on 8 of 128: 2045 us in order, 1243 so).
   __device__ __forceinline__ void take(const AttendArgs& a, int tile_at) {
     const int head = (int)((uint32_t)tile_at / (uint32_t)s.tiles), nth = tile_at - head * s.tiles;
-    const int tile = a.window > 0 ? nth : nth % 2 ? s.tiles - 1 - nth / 2 : nth / 2;
+    const int tile = !WIDE || a.window > 0 ? nth : nth % 2 ? s.tiles - 1 - nth / 2 : nth / 2;
     rows = TileRows{tile * a.rows, s.rows.n * a.G - 1, head, s.rows.first};
     const int last = rows.row0 + a.rows - 1 < rows.last_row ? rows.row0 + a.rows - 1 : rows.last_row;
     low = s.rows.position(by_g(a, rows.row0));
@@ -471,8 +491,9 @@ struct Walk {
       pages = to - kTileCost - page_at;
       take(a, tile_at);
       if (pages > 0) {
+        if (page_at >= seen()) continue;
         w0 = first_page / run;
-        n = (first_page + s.pages - 1) / run - w0 + 1;
+        n = (first_page + seen() - 1) / run - w0 + 1;
         return true;
       }
       // whoever has the first unit of a tile without pages writes its rows
@@ -483,11 +504,21 @@ struct Walk {
   __device__ __forceinline__ const int* table(const AttendArgs& a) const {
     return a.seq.table + b * a.seq.table_ld + first;
   }
-  // Where this part stops: pages past it are not seen.
-  __device__ __forceinline__ int stop() const {
+  // The tile's pages that a row of it may see: how many are left from its first one on
+  // (none, or less, where a window begins past the table).
+  __device__ __forceinline__ int left() const {
     const int past = high < 0 ? 0 : high / LOWM_PAGE + 1;
-    const int seen = (past < s.end ? past : s.end) - first;
-    return page_at + pages < seen ? page_at + pages : seen;
+    return (past < s.end ? past : s.end) - first;
+  }
+  // That, but one at least, which is somebody's part, and no more than the list has; for few
+  // rows, all of which see about the same, what the list has.
+  __device__ __forceinline__ int seen() const {
+    if (!WIDE) return s.pages;
+    return left() > 1 ? left() < s.pages ? left() : s.pages : 1;
+  }
+  // Where this part stops: no page past it is read.
+  __device__ __forceinline__ int stop() const {
+    return page_at + pages < left() ? page_at + pages : left();
   }
   __device__ __forceinline__ bool whole() const { return n == 1; }
   __device__ __forceinline__ int place() const { return place_of(w, w > w0); }
@@ -527,7 +558,8 @@ struct Queries {
   f16x8 q[RT][2 * DP];
 
   // Rows row0 + 16 t + lane % 16 of the tile's sequence.
-  __device__ __forceinline__ Queries(const AttendArgs& a, const Walk& walk, int row0) {
+  template <typename W>
+  __device__ __forceinline__ Queries(const AttendArgs& a, const W& walk, int row0) {
     const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, col = lane & 15;
     const int D = a.cache.D;
 #pragma unroll
@@ -722,7 +754,7 @@ void attend_kernel(AttendArgs a) {
   const lowm_kv_cache& c = a.cache;
   const int D = FULL ? 64 * DP : c.D, nt = FULL ? NT : D / 16;
 
-  Walk walk(a);
+  Walk<false> walk(a);
   while (walk.next(a)) {
     const int stop = walk.stop(), head = walk.rows.head;
     const int high_lo = a.window > 0 && walk.high >= a.window ? walk.high - a.window + 1 : 0;
@@ -920,7 +952,7 @@ void attend_wide_kernel(AttendArgs a) {
   const lowm_kv_cache& c = a.cache;
   const int D = FULL ? 64 * DP : c.D, nt = FULL ? NT : D / 16;
 
-  Walk walk(a);
+  Walk<true> walk(a);
   while (walk.next(a)) {
     const int stop = walk.stop(), head = walk.rows.head;
     const int* table = walk.table(a);
@@ -1089,10 +1121,11 @@ void attend_wide_kernel(AttendArgs a) {
   walk.note(a, true);
 }
 
+__host__ __device__ inline int join_lanes(int D) { return D <= 64 ? 16 : D <= 128 ? 32 : 64; }
 // Joins the tiles that several runs have a part of, in the order of join().  Each
 // wavefront finds out which runs begin one, and takes 64 / lanes rows at a time.
 __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
-  constexpr int kAhead = 16, kSets = kGroups / kWave;
+  constexpr int kSets = kGroups / kWave;
   const int lane = threadIdx.x & (kWave - 1);
   const int runs = a.notes[0];
   uint64_t begun[kSets];
@@ -1104,7 +1137,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
     begun[k] = __ballot(w < runs && parts > 0);
     tiles += __builtin_popcountll(begun[k]);
   }
-  const int D = a.cache.D, lanes = D <= 64 ? 16 : D <= 128 ? 32 : 64;
+  const int D = a.cache.D, lanes = join_lanes(D);
   const int per = a.rows * lanes / kWave;   // turns to a tile
   const int d = lane % lanes * 4;
   for (int item = blockIdx.x * kWaves + (int)threadIdx.x / kWave; item < tiles * per;
@@ -1126,34 +1159,42 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
     if (note.rows.row0 + r > note.rows.last_row || d >= D) continue;
     float most = -__builtin_inff(), sum = 0.f;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
-      float top[kAhead], part[kAhead];
-      f32x4 z[kAhead];
+    auto fold = [&](auto ahead_c) {
+      constexpr int ahead = decltype(ahead_c)::value;
+      for (int i0 = 0; i0 < n; i0 += ahead) {
+        float top[ahead], part[ahead];
+        f32x4 z[ahead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int in = i0 + i < n ? i0 + i : n - 1;
-        const int64_t row = (int64_t)place_of(w0 + in, in > 0) * a.rows + r;
-        top[i] = i0 + i < n ? a.stats[2 * row] : -__builtin_inff();
-        part[i] = a.stats[2 * row + 1];
-        z[i] = *reinterpret_cast<const f32x4*>(a.sums + row * D + d);
-      }
-      float now = most;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) now = fmaxf(now, top[i]);
-      const float base = now == -__builtin_inff() ? 0.f : now;
-      const float keep = __builtin_amdgcn_exp2f(most - base);
-      sum *= keep;
-      y *= keep;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const float f = __builtin_amdgcn_exp2f(top[i] - base);
-        if (i0 + i < n) {
-          sum += f * part[i];
-          y += f * z[i];
+        for (int i = 0; i < ahead; ++i) {
+          const int in = i0 + i < n ? i0 + i : n - 1;
+          const int64_t row = (int64_t)place_of(w0 + in, in > 0) * a.rows + r;
+          top[i] = i0 + i < n ? a.stats[2 * row] : -__builtin_inff();
+          part[i] = a.stats[2 * row + 1];
+          z[i] = *reinterpret_cast<const f32x4*>(a.sums + row * D + d);
         }
+        float now = most;
+#pragma unroll
+        for (int i = 0; i < ahead; ++i) now = fmaxf(now, top[i]);
+        const float base = now == -__builtin_inff() ? 0.f : now;
+        const float keep = __builtin_amdgcn_exp2f(most - base);
+        sum *= keep;
+        y *= keep;
+#pragma unroll
+        for (int i = 0; i < ahead; ++i) {
+          const float f = __builtin_amdgcn_exp2f(top[i] - base);
+          if (i0 + i < n) {
+            sum += f * part[i];
+            y += f * z[i];
+          }
+        }
+        most = now;
       }
-      most = now;
-    }
+    };
+    // (most tiles of a prompt have two parts or three)
+    if (n <= 4)
+      fold(std::integral_constant<int, 4>{});
+    else
+      fold(std::integral_constant<int, 16>{});
     finish(a, note.rows, r, d, most, sum, y);
   }
 }
@@ -1251,10 +1292,6 @@ int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
   // short (64 sequences of 300 tokens, 512 tiles: 11.3 us; 21.7 with one), or rows many.
   const int64_t tiles = (int64_t)c.H * (s.B < s.T ? s.B : s.T);
   a.groups = (kind >= kMore ? c.D <= 128 : tiles > 128) ? kGroups : kGroups / 2;
-  a.turn = kind >= kMore ? 1 : kWaves;
-  a.small = kind >= kMore ? 8 : 12;
-  a.most_log = kind >= kMore ? 3 : 4;
-  a.lone = kind < kMore && a.groups == kGroups ? 24 : 1 << 20;
   // positions p to p + (rows + G - 2) / G of a tile's rows, and the window before p
   const int64_t most = ((int64_t)u->window + (a.rows + G - 2) / G + LOWM_PAGE - 2) / LOWM_PAGE + 1;
   a.most_pages = u->window > 0 && most < INT32_MAX ? (int)most : INT32_MAX;
@@ -1276,8 +1313,11 @@ int cache_attention(const lowm_cache_attention_args* u, hipStream_t stream) {
                                 dim3((unsigned)a.groups), dim3(kWave * waves_for(kind, c.D)), args,
                                 0, stream));
   if (rc != LOWM_OK || kind == kFew) return rc;
+  const int64_t joins = (rows / c.H / kind + (s.B < s.T ? s.B : s.T)) * c.H *
+                        (kind * join_lanes(c.D) / kWave) / kWaves;
   return launched(hipLaunchKernel((const void*)&join_kernel,
-                                  dim3(kJoinGroups), dim3(kThreads), args, 0, stream));
+                                  dim3((unsigned)(joins < kJoinGroups ? joins : kJoinGroups)),
+                                  dim3(kThreads), args, 0, stream));
 }
 
 }  // namespace

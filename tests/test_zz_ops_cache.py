@@ -610,6 +610,20 @@ def test_attention_of_whole_prompts(case):
 
 
 @gpu
+@pytest.mark.parametrize("Hq,H,window", [(8, 1, 100), (8, 1, 0), (2, 2, 70), (32, 8, 130)])
+def test_attention_of_prompts_past_their_table(Hq, H, window):
+    """Tables of fewer pages than the sequences have: later rows see what there is, or, through a
+    window, nothing."""
+    g = gen(42, Hq, window)
+    D, P, lens, new = 32, 40, [900, 500, 64], [700, 300, 64]
+    cache = random_cache(g, P, H, D, FP8)
+    table = tables(g, P, lens)[:, :5].contiguous()
+    starts = [0, *itertools.accumulate(new)]
+    q = randn(g, sum(new), Hq, D, std=1.5)
+    check_attention(q, cache, table, lens, starts, window=window)
+
+
+@gpu
 @pytest.mark.parametrize("G", [1, 3, 16, 40])
 def test_attention_long_and_shared(G):
     """Sequences cut over many workgroups beside short ones; the rows of several tiles."""
