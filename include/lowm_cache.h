@@ -182,7 +182,7 @@ int lowm_cache_read(const lowm_cache_read_args* args, void* stream);
  * Sums and softmax statistics are fp32.  The matrix products take fp16: a row of
  * q scaled by a power of two, the bytes as they are (both exact but for elements of q
  * below 2^-28 of their row's largest), and the weights e^(x - max), rounded to 11 bits
- * (below 2^-21 of the largest to a multiple of 2^-32 of it).
+ * (below 2^-21 of the largest to a multiple of 2^-31 of it, or of less).
  * The same inputs give the same bits.
  *
  * The workspace (lowm_cache_attention_workspace_bytes, 256-byte aligned) is zeroed once
@@ -210,8 +210,8 @@ size_t lowm_cache_attention_workspace_bytes(int T, int Hq, int H, int D);
 /* Errors as lowm_cache_append; Hq no multiple of H, window < 0:
  * LOWM_ERR_INVALID_ARG; q, its strides or out not 16-byte, workspace not 256-byte
  * aligned, T Hq past 2^31 - 1, H (T Hq / (H R) + B + 1) (W + 72) past 2^30 - 1 with R =
- * 16, 32, 64 or 128 where T Hq is up to 16, 32 or 64 H B or more: LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small:
- * LOWM_ERR_WORKSPACE. */
+ * 16, 32, 64 or 128 where T Hq is up to 16, 32 or 64 H B or more:
+ * LOWM_ERR_UNSUPPORTED; a workspace that is missing or too small: LOWM_ERR_WORKSPACE. */
 int lowm_cache_attention(const lowm_cache_attention_args* args, void* stream);
 
 /*

@@ -7,9 +7,9 @@
 // goes where is decided by one workgroup, from prefix sums over the rows and over
 // the pages in ascending order, so that the same tables give the same pages.  Small
 // tables go through that workgroup whole, with the counts in LDS, instead of three
-// launches (8 rows: 14.6 us, 8.2 so).  Then all workgroups copy: a page of a layer is one run of bytes for the keys and one for
-// the values, in units of kUnit bytes, past the caches (355 pages of 786 KB 118 us, 4.75
-// TB/s; 127 through them).
+// launches (8 rows: 14.6 us, 8.2 so).  Then all workgroups copy: a page of a layer is one
+// run of bytes for the keys and one for the values, in units of kUnit bytes, past the caches
+// (355 pages of 786 KB 118 us, 4.75 TB/s; 127 through them).
 #include "ops_cache.cuh"
 
 namespace lowm {
@@ -280,7 +280,6 @@ __global__ __launch_bounds__(kOne) void fork_small_kernel(PagesArgs a) {
   __syncthreads();
   for (int p = threadIdx.x; p < a.cache.P; p += kOne) a.refs[p] = refs[p];
 }
-
 
 // The i-th lowest free page takes the i-th highest movable one while that is higher:
 // a free page p, the i-th, is taken if more than i movable ones lie above it, and a
