@@ -151,9 +151,10 @@ typedef struct lowm_cache_append_args {
 
 /* Errors, of this call and the next two: NULL operand, T or B or W < 0, a size < 1,
  * an unknown type, T no multiple of B where row_starts is NULL, a stride < 0 or rows of
- * k, v or q that overlap, an output that overlaps another operand: LOWM_ERR_INVALID_ARG; D not a multiple of 16 or past
- * LOWM_CACHE_MAX_D, B or heads past their limits, k or v of the cache not 16-byte
- * (another pointer: element) aligned: LOWM_ERR_UNSUPPORTED.  T == 0 does nothing. */
+ * k, v or q that overlap, an output that overlaps another operand:
+ * LOWM_ERR_INVALID_ARG; D not a multiple of 16 or past LOWM_CACHE_MAX_D, B or heads
+ * past their limits, k or v of the cache not 16-byte (another pointer: element)
+ * aligned: LOWM_ERR_UNSUPPORTED.  T == 0 does nothing. */
 int lowm_cache_append(const lowm_cache_append_args* args, void* stream);
 
 /* The rows' keys and values as bf16 (byte times scale, rounded once), [T, H, D]
