@@ -34,9 +34,9 @@
  * included.  The call's rows lie one sequence after another: sequence b has rows
  * row_starts[b] .. row_starts[b + 1] - 1 of T (row_starts int32 [B + 1], not
  * falling), or T / B each where row_starts is NULL; row j of n stands at position
- * lens[b] - n + j.  What cannot be is left out, not followed: a position below 0
- * or past the table's width, a page number outside 0 .. P - 1, rows outside
- * 0 .. T - 1.
+ * lens[b] - n + j, n and j by the bounds as they are given.  What cannot be is left
+ * out, not followed, and moves nothing else: a position below 0 or past the table's
+ * width, a page number outside 0 .. P - 1, rows outside 0 .. T - 1.
  */
 #ifndef LOWM_CACHE_H
 #define LOWM_CACHE_H

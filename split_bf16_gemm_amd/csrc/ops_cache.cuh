@@ -103,23 +103,25 @@ struct SequenceSpans {
 // A sequence's rows in the call and where they stand.
 struct Rows {
   int first, n;      // rows first .. first + n - 1 of the call
-  int len;           // tokens of the sequence
+  int len;           // tokens of the sequence, up to the last of these rows
   __device__ __forceinline__ int position(int j) const { return len - n + j; }
 };
 __device__ __forceinline__ Rows rows_of(const lowm_sequences& s, int b) {
   Rows r;
+  int past = 0;   // rows behind the call's last: they are left out, each with its token
   if (s.row_starts) {
     int lo = s.row_starts[b], hi = s.row_starts[b + 1];
+    past = hi > s.T ? hi - s.T : 0;
     lo = lo < 0 ? 0 : lo > s.T ? s.T : lo;
-    hi = hi < lo ? lo : hi > s.T ? s.T : hi;
+    hi -= past;
     r.first = lo;
-    r.n = hi - lo;
+    r.n = hi < lo ? 0 : hi - lo;
   } else {
     r.n = s.T / s.B;
     r.first = b * r.n;
   }
   const int len = s.lens[b];
-  r.len = len < 0 ? 0 : len;
+  r.len = len > past ? len - past : 0;
   return r;
 }
 
