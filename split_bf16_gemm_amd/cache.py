@@ -212,12 +212,19 @@ def cache_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, *,
                k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
                stream=None):
     """(k, v) [T, H, D] bf16: the rows' keys and values as the cache holds them.  T is that of
-    the outputs, or ``rows``, or one row a sequence; rows that are left out are not written."""
+    the outputs, or ``rows``; without row_starts one row a sequence where neither is given.  Rows
+    that are left out are not written."""
     dev = cache.k.device
-    T = rows if rows is not None else table.shape[0]
-    shape = (T, cache.k.shape[1], cache.v.shape[3])
     if k_out is None:
-        k_out = ops._empty(shape if v_out is None else v_out.shape, torch.bfloat16, dev, stream)
+        if v_out is not None:
+            shape = v_out.shape
+        else:
+            if rows is None and row_starts is not None:
+                raise ValueError("with row_starts, cache_read needs rows or outputs: how many "
+                                 "rows there are is only known on the GPU")
+            T = rows if rows is not None else table.shape[0]
+            shape = (T, cache.k.shape[1], cache.v.shape[3])
+        k_out = ops._empty(shape, torch.bfloat16, dev, stream)
     if v_out is None:
         v_out = ops._empty(k_out.shape, torch.bfloat16, dev, stream)
     rc = (ops._calls or ops._native()).cache_read(

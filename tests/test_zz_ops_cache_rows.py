@@ -85,3 +85,16 @@ def test_attention_of_rows_past_the_last(case, G):
         bound = err + (ref.abs() + err) * HALF[BF16]
         assert bool(((got - ref).abs() <= bound)[some].all())
         assert bool(((gl - rl).abs() <= lerr)[some].all())
+
+
+def test_read_with_bounds_needs_the_number_of_rows():
+    """How many rows row_starts counts is on the GPU: one row a sequence would be a guess, and a
+    silent one, as rows past the last are left out.  (Refused before any tensor is looked at.)"""
+    c = sbg.make_kv_cache(4, 1, 16, device="cpu")
+    table, lens, starts = ints([[0], [1]], "cpu"), ints([9, 9], "cpu"), ints([0, 3, 7], "cpu")
+    with pytest.raises(ValueError, match="rows"):
+        sbg.cache_read(c, table, lens, row_starts=starts)
+    out = torch.empty(7, 1, 16, dtype=BF16)
+    for given in (dict(rows=7), dict(k_out=out), dict(v_out=out)):
+        with pytest.raises(ValueError, match="GPU"):
+            sbg.cache_read(c, table, lens, row_starts=starts, **given)
