@@ -73,7 +73,7 @@ struct AttendArgs {
   float* lse;
   int* counts;       // [2][2 kGroups]: arrivals in a group of places, and of groups
   int* notes;        // for join_kernel: [8] how many runs there are, [kGroups][8] a Note each
-  float* sums;       // [2 kGroups][rows of a tile][D]
+  float* sums;       // [2 kGroups][rows of a tile][D]: averages of the values so far
   float* stats;      // [2 kGroups][rows of a tile][2]: maximum, sum
   int64_t q_row, q_head;
   int Hq, G, window, rows;   // rows: of a tile
@@ -307,16 +307,56 @@ struct TileRows {
     return (int64_t)(first + j) * a.Hq + head * a.G + (row0 + r - j * a.G);
   }
 };
+// 1 / the sum of a row's weights, to one unit in the last place; of one that saw nothing, 0.
+__device__ __forceinline__ float over(float sum) {
+  return sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum);
+}
+// y: a row's outputs, the average of the values that it saw, which is no larger than they
+// are (weights times values would be: 2^20 times and more).  So are those of a part.
 __device__ __forceinline__ void finish(const AttendArgs& a, const TileRows& rows, int r, int d,
                                        float most, float sum, const f32x4& y) {
   const int64_t row = rows.at(a, r);
-  const float k = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<ops_u32x2*>(a.out + row * a.cache.D + d) =
-      ops_u32x2{pack_bf16(y[0] * k, y[1] * k), pack_bf16(y[2] * k, y[3] * k)};
+      ops_u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
   if (a.lse && d == 0) a.lse[row] = (most + __builtin_amdgcn_logf(sum) - kLift) * kLn2;
 }
 
-// The sums of a tile that others have a part of, into their place: for a workgroup of
+// Averages of the values of several parts, which saw weights of these sums in units of
+// e^most each, given the largest of those units.  A part counts for its factor
+// e^(its most - top) times its sum over all of them.  Where a factor nears the end of
+// fp32's range (`far`) the values, which may be as large, take it as two halves.
+struct Joined {
+  float base;
+  __device__ __forceinline__ explicit Joined(float top)
+      : base(top == -__builtin_inff() ? 0.f : top) {}
+  __device__ __forceinline__ float factor(float most) const {
+    return __builtin_amdgcn_exp2f(most - base);
+  }
+  __device__ __forceinline__ float half(float most) const {
+    return __builtin_amdgcn_exp2f(0.5f * (most - base));
+  }
+  __device__ __forceinline__ bool far(float most) const {
+    return most - base < -100.f && most != -__builtin_inff();
+  }
+};
+__device__ __forceinline__ void add_part(f32x4& y, const f32x4& z, float k) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] += z[e] * k;
+}
+__device__ __forceinline__ void add_part(f32x4& y, const f32x4& z, float half, float share) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] += z[e] * half * share;
+}
+// Over the 16 lanes of a row of them.
+template <typename Op>
+__device__ __forceinline__ float lanes_reduce(float v, Op op) {
+  v = op(v, bits_float(lane_move<0x128, 0xf>(float_bits(v))));   // row_ror 8, 4, 2, 1
+  v = op(v, bits_float(lane_move<0x124, 0xf>(float_bits(v))));
+  v = op(v, bits_float(lane_move<0x122, 0xf>(float_bits(v))));
+  return op(v, bits_float(lane_move<0x121, 0xf>(float_bits(v))));
+}
+
+// What a tile that others have a part of has so far, into its place: for a workgroup of
 // this launch, or for the next one.
 template <bool NOW>
 __device__ __forceinline__ void leave(const AttendArgs& a, int place, int r, int d, float most,
@@ -341,23 +381,42 @@ __device__ void join(const AttendArgs& a, const TileRows& rows, int w0, int w, i
                      int m, bool last, float* lds) {
   const int n = rows.last_row - rows.row0 + 1 < a.rows ? rows.last_row - rows.row0 + 1 : a.rows;
   const int D = a.cache.D;
-  float *most = lds, *sum = lds + kJoin * a.rows;
+  float *half = lds, *share = lds + kJoin * a.rows;    // of part i and row r: i * n + r
+  float *tops = lds + 2 * kJoin * a.rows, *sums = tops + a.rows;
   auto at = [&](int i, int r) {
     const int run = w + i * step;
     return (int64_t)place_of(run, run > w0) * a.rows + r;
   };
-  for (int i = threadIdx.x; i < m * n; i += kThreads) {
-    const Two v = get2(a.stats + 2 * at(i / n, i % n));
-    most[i] = v.a;
-    sum[i] = v.b;
+  // 16 lanes to each of up to 16 rows
+  static_assert(kThreads == 16 * kGroup && kGroup == 16 && kJoin <= 2 * kGroup, "all rows at once");
+  const int row = threadIdx.x / kGroup, lane = threadIdx.x % kGroup;
+  if (row < n) {
+    Two part[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      part[k] = lane + kGroup * k < m ? get2(a.stats + 2 * at(lane + kGroup * k, row))
+                                      : Two{-__builtin_inff(), 0.f};
+    const float top =
+        lanes_reduce(fmaxf(part[0].a, part[1].a), [](float x, float y) { return fmaxf(x, y); });
+    const Joined join(top);
+    const float h[2] = {join.half(part[0].a), join.half(part[1].a)};
+    const float all = lanes_reduce(h[0] * h[0] * part[0].b + h[1] * h[1] * part[1].b,
+                                   [](float x, float y) { return x + y; });
+    const float inverse = over(all);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (lane + kGroup * k < m) {
+        half[(lane + kGroup * k) * n + row] = h[k];
+        share[(lane + kGroup * k) * n + row] = h[k] * (part[k].b * inverse);
+      }
+    if (lane == 0) {
+      tops[row] = top;
+      sums[row] = all;
+    }
   }
   __syncthreads();
   for (int item = threadIdx.x; item < n * (D / 4); item += kThreads) {
     const int r = item / (D / 4), d = item % (D / 4) * 4;
-    float top = -__builtin_inff();
-    for (int i = 0; i < m; ++i) top = fmaxf(top, most[i * n + r]);
-    const float base = top == -__builtin_inff() ? 0.f : top;
-    float all = 0.f;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
     for (int i0 = 0; i0 < m; i0 += kGroup) {
       Two lo[kGroup], hi[kGroup];
@@ -370,23 +429,17 @@ __device__ void join(const AttendArgs& a, const TileRows& rows, int w0, int w, i
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
         const int k = (i0 + i) * n + r;
-        const float f = i0 + i < m ? __builtin_amdgcn_exp2f(most[k] - base) : 0.f;
-        if (i0 + i < m) {
-          all += f * sum[k];
-          y[0] += f * lo[i].a;
-          y[1] += f * lo[i].b;
-          y[2] += f * hi[i].a;
-          y[3] += f * hi[i].b;
-        }
+        if (i0 + i < m)
+          add_part(y, f32x4{lo[i].a, lo[i].b, hi[i].a, hi[i].b}, half[k], share[k]);
       }
     }
     if (last) {
-      finish(a, rows, r, d, top, all, y);
+      finish(a, rows, r, d, tops[r], sums[r], y);
     } else {
       float* p = a.sums + at(0, r) * D + d;
       put2(p, y[0], y[1]);
       put2(p + 2, y[2], y[3]);
-      if (d == 0) put2(a.stats + 2 * at(0, r), top, all);
+      if (d == 0) put2(a.stats + 2 * at(0, r), tops[r], sums[r]);
     }
   }
   __syncthreads();
@@ -623,6 +676,15 @@ struct Softmax {
       for (int n = 0; n < NT; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
   }
+  // What makes the sums o[t] averages of the values, given the sum of a row's weights.
+  __device__ __forceinline__ float to_average(int t, float all) {
+    const float k = over(all);
+    if (__builtin_expect(!(v0 < 0x1p-60f), 1)) return k * v0;
+    // in two steps, or the factor could be subnormal
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[t][n] *= k;
+    return v0;
+  }
   // A page's products x to weights p, for its first `live` tokens from token0 on; masked:
   // whether a row may not see some of them.
   template <typename Q>
@@ -747,7 +809,7 @@ void attend_kernel(AttendArgs a) {
   constexpr bool kInLds = queries_in_lds(DP, RT);
   __shared__ f16x8 queries[kInLds ? RT : 1][kInLds ? 2 * DP : 1][kWave];
   constexpr bool kNow = RT == 1;            // few rows are joined here, others by join_kernel
-  static_assert(!kNow || sizeof(joint) >= 2 * kJoin * kRows * sizeof(float), "room to join");
+  static_assert(!kNow || sizeof(joint) >= 2 * (kJoin + 1) * kRows * sizeof(float), "room to join");
 
   const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
@@ -880,10 +942,12 @@ void attend_kernel(AttendArgs a) {
       }
     }
 
-    // the four wavefronts' sums of the tile
+    // the four wavefronts' parts of the tile
+    float to_average[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const float all = row_sum(sm.sum[t]);
+      to_average[t] = sm.to_average(t, all);
       if (g == 0) {
         joint_max[wave][16 * t + col] = sm.ref[t];
         joint_sum[wave][16 * t + col] = all;
@@ -898,7 +962,7 @@ void attend_kernel(AttendArgs a) {
 #pragma unroll
         for (int n = 0; n < kPart; ++n)
           *reinterpret_cast<f32x4*>(&joint[wave][16 * t + col][16 * n + 4 * g]) =
-              sm.o[t][n0 + n] * sm.v0;
+              sm.o[t][n0 + n] * to_average[t];
       __syncthreads();
       for (int i = threadIdx.x; i < kRows * 4 * kPart; i += kThreads) {
         const int r = i / (4 * kPart), d4 = i % (4 * kPart), d = 16 * n0 + 4 * d4;
@@ -906,16 +970,27 @@ void attend_kernel(AttendArgs a) {
         float top = joint_max[0][r];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) top = fmaxf(top, joint_max[w][r]);
-        const float base = top == -__builtin_inff() ? 0.f : top;
-        float all = 0.f;
+        const Joined join(top);
+        float k[kWaves], all = 0.f;
+        bool far = false;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const float most = joint_max[w][r];
+          k[w] = join.factor(most) * joint_sum[w][r];
+          all += k[w];
+          far |= join.far(most);
+        }
+        const float inverse = over(all);
         f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          const float f = __builtin_amdgcn_exp2f(joint_max[w][r] - base);
-          all += f * joint_sum[w][r];
           const f32x4 z = *reinterpret_cast<const f32x4*>(&joint[w][r][4 * d4]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] += f * z[e];
+          if (__builtin_expect(!far, 1)) {
+            add_part(y, z, k[w] * inverse);
+          } else {
+            const float h = join.half(joint_max[w][r]);
+            add_part(y, z, h, h * (joint_sum[w][r] * inverse));
+          }
         }
         if (whole)
           finish(a, walk.rows, r, d, top, all, y);
@@ -1103,7 +1178,7 @@ void attend_wide_kernel(AttendArgs a) {
     const bool whole = walk.whole();
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const float all = row_sum(sm.sum[t]);
+      const float all = row_sum(sm.sum[t]), to_average = sm.to_average(t, all);
       const int r = 16 * RT * wave + 16 * t + col;
       if (walk.rows.row0 + r > walk.rows.last_row) continue;
 #pragma unroll
@@ -1111,9 +1186,9 @@ void attend_wide_kernel(AttendArgs a) {
         if (!FULL && n >= NT - 4 && n >= nt) continue;
         const int d = 16 * n + 4 * g;
         if (whole)
-          finish(a, walk.rows, r, d, sm.ref[t], all, sm.o[t][n] * sm.v0);
+          finish(a, walk.rows, r, d, sm.ref[t], all, sm.o[t][n] * to_average);
         else
-          leave<false>(a, walk.place(), r, d, sm.ref[t], all, sm.o[t][n] * sm.v0);
+          leave<false>(a, walk.place(), r, d, sm.ref[t], all, sm.o[t][n] * to_average);
       }
     }
     walk.note(a, false);
@@ -1175,19 +1250,37 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
         float now = most;
 #pragma unroll
         for (int i = 0; i < ahead; ++i) now = fmaxf(now, top[i]);
-        const float base = now == -__builtin_inff() ? 0.f : now;
-        const float keep = __builtin_amdgcn_exp2f(most - base);
-        sum *= keep;
-        y *= keep;
+        const Joined join(now);
+        // (the sum so far is 0 where the loop begins)
+        bool far = join.far(most);
+        const float before = join.factor(most) * sum;
+        float all = before;
 #pragma unroll
         for (int i = 0; i < ahead; ++i) {
-          const float f = __builtin_amdgcn_exp2f(top[i] - base);
-          if (i0 + i < n) {
-            sum += f * part[i];
-            y += f * z[i];
+          far |= join.far(top[i]);
+          part[i] *= join.factor(top[i]);   // (of parts past the last: 0)
+          all += part[i];
+        }
+        const float inverse = over(all);
+        if (__builtin_expect(!far, 1)) {
+          y *= before * inverse;
+#pragma unroll
+          for (int i = 0; i < ahead; ++i) add_part(y, z[i], part[i] * inverse);
+        } else {
+          const float h = join.half(most);
+          f32x4 x = {0.f, 0.f, 0.f, 0.f};
+          add_part(x, y, h, h * (sum * inverse));
+          for (int i = i0; i < n && i < i0 + ahead; ++i) {
+            // (read again, rather than kept in registers for this)
+            const int64_t row = (int64_t)place_of(w0 + i, i > 0) * a.rows + r;
+            const float h = join.half(a.stats[2 * row]);
+            add_part(x, *reinterpret_cast<const f32x4*>(a.sums + row * D + d), h,
+                     h * (a.stats[2 * row + 1] * inverse));
           }
+          y = x;
         }
         most = now;
+        sum = all;
       }
     };
     // (most tiles of a prompt have two parts or three)
