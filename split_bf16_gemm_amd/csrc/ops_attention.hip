@@ -660,17 +660,26 @@ struct Queries {
 };
 
 // The softmax's state.  Weights are e^(x + log vs - ref) 2^kLift with vs the page's scale
-// of the values in units of the first page's, v0: they multiply the bytes as they are,
-// and go into the sums o without another factor.  ref is the largest x + log vs so far,
-// or up to kSlack less: the sums are scaled anew only when a page passes that.
+// of the values in units of 2^unit, the first page's exponent: they multiply the bytes as
+// they are, and go into the sums o without another factor.  ref is the largest x + log vs
+// so far, or up to kSlack less: the sums are scaled anew only when a page passes that.
+//
+// The sum of the weights has them without vs, in units of e^low, low being to x what ref is
+// to x + log vs: a page's weights count for 2^(ref - low - log vs) times as much there.
+// Scales may lie anywhere in fp32's range; where a page's is so small that its values are
+// nothing beside those that a row has seen (kNothing), or 0, its weights are taken in units
+// of e^low and its values as 0.
+constexpr float kNothing = 90.f;
 template <int NT, int RT>
 struct Softmax {
-  float ref[RT], sum[RT], v0 = 0.f;
+  static constexpr int kNoUnit = 1000;
+  float ref[RT], low[RT], sum[RT];
+  int unit = kNoUnit;
   f32x4 o[RT][NT];
   __device__ __forceinline__ Softmax() {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      ref[t] = -__builtin_inff();
+      ref[t] = low[t] = -__builtin_inff();
       sum[t] = 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -678,12 +687,15 @@ struct Softmax {
   }
   // What makes the sums o[t] averages of the values, given the sum of a row's weights.
   __device__ __forceinline__ float to_average(int t, float all) {
-    const float k = over(all);
-    if (__builtin_expect(!(v0 < 0x1p-60f), 1)) return k * v0;
-    // in two steps, or the factor could be subnormal
+    const float k = over(all), none = -__builtin_inff();
+    const float up = ref[t] == none ? none : ref[t] - low[t] + (float)unit;
+    if (__builtin_expect(!__any(up > 60.f || (up < -60.f && up > none)), 1))
+      return k * __builtin_amdgcn_exp2f(up);
+    // in steps, or the factor could be subnormal, or infinite
+    const float half = __builtin_amdgcn_exp2f(0.5f * up);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) o[t][n] *= k;
-    return v0;
+    for (int n = 0; n < NT; ++n) o[t][n] = o[t][n] * k * half;
+    return half;
   }
   // A page's products x to weights p, for its first `live` tokens from token0 on; masked:
   // whether a row may not see some of them.
@@ -691,11 +703,11 @@ struct Softmax {
   __device__ __forceinline__ void weigh(const Q& q, f32x4 (&x)[RT][4], f16x8 (&p)[RT][2],
                                         bool masked, int live, int token0, float ks, float vs) {
     const int g = (threadIdx.x & (kWave - 1)) >> 4;
-    // a scale of 0 (or one too small to be a number with a logarithm) leaves no value
-    const bool some = !(fabsf(vs) < 1.17549435e-38f);
-    if (v0 == 0.f && some && vs > 0.f && vs < __builtin_inff()) v0 = vs;
-    const float vs_here = some ? vs / (v0 == 0.f ? 1.f : v0) : 1.f,
-                log_vs = __builtin_amdgcn_logf(vs_here), per_vs = 1.f / vs_here;
+    const int exponent = __builtin_amdgcn_frexp_expf(vs);
+    if (unit == kNoUnit && vs > 0.f) unit = exponent;
+    const float log_vs =
+        (float)(exponent - unit) + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(vs));
+    const float not_nan = vs - vs;   // 0, or NaN, which the rows that see the page get
     if (masked) {
 #pragma unroll
       for (int t = 0; t < RT; ++t)
@@ -711,7 +723,7 @@ struct Softmax {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       // never 0, which would make NaN of the masked ones
-      float per = q.unit[t] * ks;
+      float per = __builtin_fmaf(q.unit[t], ks, not_nan);
       per = per == 0.f ? 1.17549435e-38f : per;
       float here = x[t][0][0];
 #pragma unroll
@@ -721,18 +733,23 @@ struct Softmax {
       here = row_max(here);
       // a row that sees none of the page is not touched by its scales
       const bool none = here == -__builtin_inff();
-      here = here * per + log_vs;
+      here *= per;
       per = none ? 1.f : per;
-      if (__any(here > ref[t] + kSlack)) {
-        const float now = here > ref[t] + kSlack ? here : ref[t];
+      const float value = here + log_vs;
+      if (__any(value > ref[t] + kSlack || here > low[t] + kSlack)) {
+        const float now = value > ref[t] + kSlack ? value : ref[t];
         const float keep = now == ref[t] ? 1.f : __builtin_amdgcn_exp2f(ref[t] - now);
         ref[t] = now;
-        sum[t] *= keep;
 #pragma unroll
         for (int n = 0; n < NT; ++n) o[t][n] *= keep;
+        const float most = here > low[t] + kSlack ? here : low[t];
+        sum[t] *= most == low[t] ? 1.f : __builtin_amdgcn_exp2f(low[t] - most);
+        low[t] = most;
       }
-      const float lift =
-          none ? 0.f : log_vs + kLift - (ref[t] == -__builtin_inff() ? 0.f : ref[t]);
+      const float apart = ref[t] - low[t] - log_vs;
+      // (also where ref is -infinity: a scale of 0)
+      const bool nothing = !none && !(apart <= kNothing);
+      const float lift = none ? 0.f : kLift + (nothing ? -low[t] : log_vs - ref[t]);
       float add = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -742,11 +759,9 @@ struct Softmax {
           add += w;
           p[t][i / 2][4 * (i % 2) + e] = (_Float16)w;
         }
-      sum[t] += add * (none ? 1.f : per_vs);
-    }
-    if (!some) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) p[t][0] = p[t][1] = f16x8{};
+      sum[t] += add * (none || nothing ? 1.f : __builtin_amdgcn_exp2f(apart));
+      if (__builtin_expect(__any(nothing), 0))
+        if (nothing) p[t][0] = p[t][1] = f16x8{};
     }
   }
 };
@@ -949,7 +964,7 @@ void attend_kernel(AttendArgs a) {
       const float all = row_sum(sm.sum[t]);
       to_average[t] = sm.to_average(t, all);
       if (g == 0) {
-        joint_max[wave][16 * t + col] = sm.ref[t];
+        joint_max[wave][16 * t + col] = sm.low[t];
         joint_sum[wave][16 * t + col] = all;
       }
     }
@@ -1186,9 +1201,9 @@ void attend_wide_kernel(AttendArgs a) {
         if (!FULL && n >= NT - 4 && n >= nt) continue;
         const int d = 16 * n + 4 * g;
         if (whole)
-          finish(a, walk.rows, r, d, sm.ref[t], all, sm.o[t][n] * to_average);
+          finish(a, walk.rows, r, d, sm.low[t], all, sm.o[t][n] * to_average);
         else
-          leave<false>(a, walk.place(), r, d, sm.ref[t], all, sm.o[t][n] * to_average);
+          leave<false>(a, walk.place(), r, d, sm.low[t], all, sm.o[t][n] * to_average);
       }
     }
     walk.note(a, false);
