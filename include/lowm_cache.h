@@ -231,7 +231,10 @@ int lowm_cache_attention(const lowm_cache_attention_args* args, void* stream);
  * lowest row, its copy before its reserve.  Pages past a row's n are given up:
  * freeing a sequence is a parent outside the rows.  Where pages run out, or the
  * table is too narrow, a row gets -1 there, a copy does not take place, and
- * missing counts them.
+ * missing counts them.  What is then appended there is lost, and is not seen later:
+ * a row that goes on with an unfinished last page that the table does not give is
+ * counted by every call, until that page is full (the next one is reserved as
+ * usual) or the row ends.
  *
  * parents NULL: every row its own.  held (int32 [P], NULL: none): pages with a
  * value > 0 are in use by others and stay untouched.  refs' [P] counts the rows'

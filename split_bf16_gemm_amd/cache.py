@@ -288,8 +288,10 @@ def fork_pages(cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
     it and the others get copies (in every layer of ``cache``), and a row that goes on gets pages
     for ``reserve`` more tokens.  New pages are the lowest that are in no row and not held (held
     int32 [P]: pages with a value > 0 are someone else's).  refs [P] counts the uses of each page.
-    missing [1] counts the pages that were not to be had (-1 in the table).  ``outs``: four
-    tensors to write into, none of them an input."""
+    missing [1] counts the pages that were not to be had (-1 in the table); tokens appended there
+    are lost, and as long as such a page is a row's unfinished last one every call counts it.  A
+    row that ended has length 0, and begins anew from there: add a step's token to the lengths of
+    those that go on only.  ``outs``: four tensors to write into, none of them an input."""
     dev = table.device
     if outs is None:
         outs = (_ints(table.shape, dev, stream), _ints(lens.shape, dev, stream),

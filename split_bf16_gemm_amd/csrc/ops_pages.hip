@@ -168,7 +168,7 @@ struct GroupScan {
 
 __device__ void fork_decide(const PagesArgs& a, const Counts& c) {
   __shared__ int lds[2 * kWaves];
-  __shared__ int sums[3];   // copies made, pages missing, table entries that were too few
+  __shared__ int sums[3];   // copies made, pages missing, others that a row cannot have
   GroupScan scan{lds};
   if (threadIdx.x < 3) sums[threadIdx.x] = 0;
   __syncthreads();
@@ -185,6 +185,8 @@ __device__ void fork_decide(const PagesArgs& a, const Counts& c) {
       if (h.len % LOWM_PAGE) {
         const int page = a.table_out[(int64_t)r * a.W + h.pages - 1];
         copy = page >= 0 && !(c.owner[page] == r && c.refs[page] == c.parts[page]);
+        // nothing holds the tokens that it should have: a new page would show others
+        if (page < 0) atomicAdd(&sums[2], 1);
       }
       if (h.on) {
         const int want = pages_for((int64_t)h.len + a.reserve);
