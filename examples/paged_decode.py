@@ -13,8 +13,9 @@ Per step, for one token of each beam:
         x        = x + gemm(y, Wo)
 
 The step is captured into a HIP graph once and replayed with other inputs, parents and lengths;
-every buffer and workspace is made beforehand.  Now and then compact_pages moves the pages in
-use together.  Weights are random.
+every buffer and workspace is made beforehand.  A beam whose parent is -1 ends: it has no tokens,
+its pages are free and its row of the result is x as it came, until it goes on as another's or
+its own.  Now and then compact_pages moves the pages in use together.  Weights are random.
 """
 from __future__ import annotations
 
@@ -54,6 +55,7 @@ class PagedDecode:
         self.forked = (torch.empty_like(self.table), torch.empty_like(self.lens),
                        torch.empty(pages, dtype=torch.int32, device=device),
                        torch.zeros(1, dtype=torch.int32, device=device))
+        self.missing = torch.zeros(1, dtype=torch.int32, device=device)     # over all steps
         self.x = torch.zeros(beams, hidden, dtype=torch.bfloat16, device=device)
         self.attended = torch.zeros(layers, beams, heads, head_dim, dtype=torch.bfloat16,
                                     device=device)
@@ -69,8 +71,10 @@ class PagedDecode:
         sbg.fork_pages(self.cache, self.table, self.lens, self.parents, reserve=1,
                        workspace=self.ws_pages, outs=self.forked)
         self.table.copy_(self.forked[0])
+        self.missing.add_(self.forked[3])
         self.positions.copy_(self.forked[1])
-        torch.add(self.forked[1], 1, out=self.lens)
+        # a token for every beam that goes on
+        torch.add(self.forked[1], self.parents.ge(0), out=self.lens)
         x = self.x
         for i, (wqkv, wo) in enumerate(self.weights):
             layer = self.cache.layer(i)
@@ -86,6 +90,7 @@ class PagedDecode:
     def reset(self):
         self.table.fill_(-1)
         self.lens.zero_()
+        self.missing.zero_()
         self.parents.copy_(torch.arange(self.shape[0]))
 
     def capture(self) -> torch.cuda.CUDAGraph:
@@ -121,16 +126,21 @@ def main():
                       torch.float8_e4m3fn if args.e4m3 else torch.int8)
     graph = run.capture()
     g = torch.Generator().manual_seed(1)
+    parents = torch.arange(args.beams)
     for i in range(args.steps):
         run.x.copy_(torch.randn(args.beams, args.hidden, generator=g).to(torch.bfloat16))
-        run.parents.copy_(torch.randint(0, args.beams, (args.beams,), generator=g)
-                          if i % 10 == 9 else torch.arange(args.beams))
+        # each goes on, and where beams are reordered, as another, anew (as one that has ended), or
+        # not at all
+        parents = torch.arange(args.beams).where(parents >= 0, -1)
+        if i % 10 == 9:
+            parents = torch.randint(-1, args.beams, (args.beams,), generator=g)
+        run.parents.copy_(parents)
         graph.replay()
         if i % 40 == 39:
             print(f"step {i + 1}: pages in use end at {run.compact()}")
     torch.cuda.synchronize()
     print(f"{args.steps} steps, lengths {run.lens.tolist()}, missing pages "
-          f"{int(run.forked[3])}, output norm {run.result.float().norm():.3f}")
+          f"{int(run.missing)}, output norm {run.result.float().norm():.3f}")
 
 
 if __name__ == "__main__":
