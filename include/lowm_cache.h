@@ -178,7 +178,10 @@ int lowm_cache_read(const lowm_cache_read_args* args, void* stream);
  * out [T, Hq, D] bf16 dense, lse fp32 [T, Hq] where not NULL.  A row that sees
  * nothing has out 0 and lse -infinity; tokens on a page that the table does not
  * give (a number outside 0 .. P - 1) are not seen.  Rows of no sequence (behind the
- * last one) are not written.
+ * last one) are not written.  What no row of a sequence sees may hold anything; but an
+ * e4m3 NaN (lowm_cache_append writes none) among the values of a token that one of its
+ * rows sees may reach that element of its other rows in the call too, and a page's scale
+ * is every row's that sees a token of the page.
  *
  * Sums and softmax statistics are fp32.  The matrix products take fp16: a row of
  * q scaled by a power of two, the bytes as they are (both exact but for elements of q

@@ -573,6 +573,10 @@ struct Walk {
   __device__ __forceinline__ int stop() const {
     return page_at + pages < left() ? page_at + pages : left();
   }
+  // The first token that a row at a position sees.
+  __device__ __forceinline__ int window_of(const AttendArgs& a, int position) const {
+    return a.window > 0 && position >= a.window ? position - a.window + 1 : 0;
+  }
   __device__ __forceinline__ bool whole() const { return n == 1; }
   __device__ __forceinline__ int place() const { return place_of(w, w > w0); }
 
@@ -775,6 +779,14 @@ __device__ __forceinline__ void clear_behind(ops_u32x4& v, int left) {
     v[i] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << 8 * n) - 1;
   }
 }
+// And so may what lies before every row's window: the first `gone` of a piece.
+__device__ __forceinline__ void clear_before(ops_u32x4& v, int gone) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = gone - 4 * i;
+    v[i] &= n >= 4 ? 0u : n <= 0 ? ~0u : ~((1u << 8 * n) - 1);
+  }
+}
 
 // The token of row r of score block i is 16 (r / 4) + 4 i + r % 4: then lane group g has
 // tokens 16 g .. 16 g + 15, in the order of the values' bytes.
@@ -834,7 +846,7 @@ void attend_kernel(AttendArgs a) {
   Walk<false> walk(a);
   while (walk.next(a)) {
     const int stop = walk.stop(), head = walk.rows.head;
-    const int high_lo = a.window > 0 && walk.high >= a.window ? walk.high - a.window + 1 : 0;
+    const int high_lo = walk.window_of(a, walk.high), low_lo = walk.window_of(a, walk.low);
     const int* table = walk.table(a);
 
     ops_u32x4 keys[4][DP], vals[NT];
@@ -939,6 +951,10 @@ void attend_kernel(AttendArgs a) {
       if (E4M3 && live < LOWM_PAGE) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) clear_behind(vals[n], live - 16 * g);
+      }
+      if (E4M3 && token0 < low_lo) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) clear_before(vals[n], low_lo - token0 - 16 * g);
       }
       // (blocks past D are zeros)
       widen_vals(0);
@@ -1053,14 +1069,14 @@ void attend_wide_kernel(AttendArgs a) {
     const bool mine = row0 <= walk.rows.last_row;
     const int low = mine ? walk.s.rows.position(by_g(a, row0)) : -1,
               high = mine ? walk.s.rows.position(by_g(a, last)) : -1;
-    const int high_lo = a.window > 0 && high >= a.window ? high - a.window + 1 : 0;
-    const int low_lo = a.window > 0 && low >= a.window ? low - a.window + 1 : 0;
+    const int high_lo = walk.window_of(a, high), low_lo = walk.window_of(a, low);
+    const int tile_lo = walk.window_of(a, walk.low);
 
     // Two pages are on their way, one for each half of the LDS: pieces wave + WAVES k.
     ops_u32x4 raw[2][kShare];
     struct Page {
       float ks, vs;
-      int live;
+      int live, gone;   // tokens that are there, and those before every row's window
     } on_way[2] = {}, here = {};
     int next_page = 0;
     auto load = [&](auto half_c, int at) {
@@ -1076,6 +1092,7 @@ void attend_wide_kernel(AttendArgs a) {
                                                                from * (LOWM_PAGE * D));
       const int live = walk.s.rows.len - (walk.first + at) * LOWM_PAGE;
       on_way[half].live = !some ? 0 : live < LOWM_PAGE ? live : LOWM_PAGE;
+      on_way[half].gone = tile_lo - (walk.first + at) * LOWM_PAGE;
       on_way[half].ks = load_apart(c.k_scale + from);
       on_way[half].vs = load_apart(c.v_scale + from);
 #pragma unroll
@@ -1099,6 +1116,8 @@ void attend_wide_kernel(AttendArgs a) {
         ops_u32x4 v = raw[half][k];
         if (E4M3 && piece >= 4 * DP && on_way[half].live < LOWM_PAGE)
           clear_behind(v, on_way[half].live - 16 * g);
+        if (E4M3 && piece >= 4 * DP && on_way[half].gone > 0)
+          clear_before(v, on_way[half].gone - 16 * g);
         stage[half][piece][0][lane] = widen<E4M3>(v[0], v[1]);
         stage[half][piece][1][lane] = widen<E4M3>(v[2], v[3]);
       }
