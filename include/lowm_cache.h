@@ -183,10 +183,15 @@ int lowm_cache_read(const lowm_cache_read_args* args, void* stream);
  * rows sees may reach that element of its other rows in the call too, and a page's scale
  * is every row's that sees a token of the page.
  *
- * Sums and softmax statistics are fp32.  The matrix products take fp16: a row of
- * q scaled by a power of two, the bytes as they are (both exact but for elements of q
- * below 2^-28 of their row's largest), and the weights e^(x - max), rounded to 11 bits
- * (below 2^-21 of the largest to a multiple of 2^-31 of it, or of less).
+ * Sums and softmax statistics are fp32, and a page's value scale may be any that is
+ * finite, however far from another's.  The matrix products take fp16: a row of q scaled
+ * by a power of two, the bytes as they are (both exact but for elements of q below 2^-28
+ * of their row's largest), and each token's weight e^(x - lse) times its page's value
+ * scale, rounded to 11 bits, or, below 2^-21 of the largest such product that the row
+ * sees, to a multiple of 2^-31 of that, or of less.  So with w the weights, s the scales,
+ * b the values' bytes and v = s b, an element of out is off by at most 2^-11 sum w |v| +
+ * 2^-32 max (w s) sum |b| before it is rounded to bf16, beside fp32's own roundings: where
+ * a page of much larger scale holds zeros in an element, little may be left of the others'.
  * The same inputs give the same bits.
  *
  * The workspace (lowm_cache_attention_workspace_bytes, 256-byte aligned) is zeroed once
