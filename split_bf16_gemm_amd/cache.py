@@ -138,7 +138,9 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str =
                 slowed by factor and the fastest not at all
     "by_parts"  pairs that turn fewer than ``low`` times over original_length slowed by factor,
                 those that turn more than ``high`` times kept, the others in between, linearly
-                in their turns
+                in their turns (a model's own low and high belong here: with a ramp in turns
+                often 1 and 4; the defaults 1 and 32 are common with a ramp in the pair's index,
+                which this is not)
     """
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError(f"rotary_dim must be even and positive, not {rotary_dim}")

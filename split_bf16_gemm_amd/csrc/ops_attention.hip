@@ -5,9 +5,11 @@
 //
 // One pass over the pages with a running maximum and sum.  Bound by HBM for few rows, where
 // a byte of the cache is read once for all rows of a key head (2 x 131001 tokens, 64 heads on
-// 8 of 128, e4m3: 90 us, 6.0 TB/s); by the matrix unit and the vector unit beside it for many
-// (1024 rows over 8192 tokens, the same heads: 302 us, 850 TFLOP/s of 1470 that a large
-// product reaches); by round trips where the work is small (640 tokens: 9.5 us).
+// 8 of 128, e4m3: 96 us, 5.6 TB/s, inputs changing from call to call); by the matrix unit and
+// the vector unit, which hardly overlap, for many (1024 rows over 8192 tokens, the same heads:
+// 296 to 303 us, 850 TFLOP/s and more of 1470 that a large product reaches; matrix
+// instructions take 38 % of a SIMD's cycles, others 48 %); by round trips where the work is
+// small (640 tokens: 9.5 us).
 //
 // Layout.  Rows of one key head (a token's query heads that share it, token after token)
 // are taken in tiles, blocks of 16 to a wavefront.  S^T = K Q^T by
@@ -26,14 +28,15 @@
 //
 // Bytes become fp16 exactly (an int8 by two byte permutations to 1024 + 128 + b and a
 // packed subtraction).  A row of q is scaled by a power of two to just below 2^15.  Weights
-// are 2^7 e^(x - ref), ref at most 2^8 below the largest, so that fp16 keeps all 11 bits of
-// what is within 2^-21 of it and sums are seldom scaled anew; the scale of a page's values
-// is part of the exponent.
+// are taken times the scale of their page's values, which is part of the exponent, as
+// 2^7 e^(x + log vs - ref), ref at most 8 (as a power of two) below the largest: fp16 keeps
+// all 11 bits of what is within 2^-21 of that, and sums are seldom scaled anew.
 //
 // Work is cut on the device, whatever the lengths are (List, Walk).  Runs of the list have
-// at most two tiles that others share, their first and their last, and leave their sums of
-// them in two places of their own in the workspace; they are joined in the order of the
-// pages, so that the bits do not depend on who does it.
+// at most two tiles that others share, their first and their last, and leave what they have
+// of them (a row's average of the values, its weights' sum and largest score) in two places
+// of their own in the workspace; they are joined in the order of the pages, so that the
+// bits do not depend on who does it.
 //
 // The join, for few rows: sums go to the workspace with device-scope stores, which pass the
 // XCDs' own caches; a workgroup waits until its stores are acknowledged there and then
@@ -143,7 +146,9 @@ template <bool WIDE>
 struct List {
   static constexpr int kTurn = WIDE ? 1 : kWaves;
   static constexpr int kLogs = WIDE ? 3 : 2, kLeast = WIDE ? 1 : 3;   // log2 of a part's pages
-  static constexpr int kSmall = WIDE ? 0 : 12;      // pages of a tile that is not cut
+  // Pages of a tile that is not cut (10 to 12 pages 9.7 us, 11 in parts of 8; 19 pages 12.5 whole, 11
+  // in parts).
+  static constexpr int kSmall = WIDE ? 0 : 12;
   static constexpr int kFine = WIDE ? 128 : kGroups;   // runs at most for parts not the largest
   static constexpr int kLone = 24;   // units to a workgroup from which half as many take them
   int total, run, per_log, lane;

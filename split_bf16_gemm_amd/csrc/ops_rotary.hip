@@ -7,7 +7,7 @@
 // elements of a token's heads, eight pairs or 16 that are only copied, forms their sines
 // and cosines once and goes through heads with them.  Few heads to a thread cost
 // arithmetic, many leave lanes idle (launch_rotary).  Bound by HBM (8192 tokens of 72 heads of
-// 128, half of each turned: 66 us, 4.6 TB/s read and written, a large copy 5.0), one token by
+// 128, half of each turned: 66 to 71 us, 4.3 to 4.6 TB/s read and written, a large copy 5.0), one token by
 // its chain of position, angle and sine (4.0 us).  The angle is taken modulo a turn in
 // fp64, where position and frequency are exact to 2^-53, and goes to the fp32 sine in half
 // turns.
